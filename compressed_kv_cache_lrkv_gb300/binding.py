@@ -25,7 +25,10 @@ EXPORTED = ["lrkv_abi_version", "lrkv_status_string", "lrkv_last_error", "lrkv_c
             "lrkv_append_layers", "lrkv_decode_layers",
             "lrkv_prefill_workspace_bytes", "lrkv_prefill", "lrkv_prefill_fused", "lrkv_mla_cache_block_bytes", "lrkv_mla_append",
             "lrkv_mla_decode_workspace_bytes", "lrkv_mla_decode", "lrkv_train_forward", "lrkv_train_workspace_bytes",
-            "lrkv_train_backward"]
+            "lrkv_train_backward", "lrkv_quant_row_bytes", "lrkv_quant_block_bytes", "lrkv_cache_quantize",
+            "lrkv_cache_dequantize", "lrkv_decode_quant_workspace_bytes", "lrkv_decode_quant",
+            "lrkv_decode_quant_partials", "lrkv_decode_shared_workspace_bytes", "lrkv_decode_shared",
+            "lrkv_prefix_partials"]
 STATIC_WS_BYTES = 16 << 20  # LRKV_STATIC_WS_BYTES
 
 
@@ -55,6 +58,10 @@ class MlaDims(ctypes.Structure):
 class Cache(ctypes.Structure):
     _fields_ = [("sK", ctypes.c_void_p), ("sV", ctypes.c_void_p), ("zK", ctypes.c_void_p), ("zV", ctypes.c_void_p),
                 ("num_blocks", ctypes.c_int32)]
+
+
+class QuantCacheStruct(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
 
 
 _lib = None
@@ -116,6 +123,26 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.lrkv_mla_decode_workspace_bytes.argtypes = [P(MlaDims), i32]
     lib.lrkv_mla_decode.restype = ctypes.c_int
     lib.lrkv_mla_decode.argtypes = [P(MlaDims), vp, vp, i32, vp, i32, vp, i32, vp, vp, sz, vp, vp]
+    for f in (lib.lrkv_quant_row_bytes, lib.lrkv_quant_block_bytes):
+        f.restype, f.argtypes = sz, [P(Dims)]
+    lib.lrkv_cache_quantize.restype = ctypes.c_int
+    lib.lrkv_cache_quantize.argtypes = [P(Dims), i32, P(Cache), vp, P(QuantCacheStruct), vp, vp, vp]
+    lib.lrkv_cache_dequantize.restype = ctypes.c_int
+    lib.lrkv_cache_dequantize.argtypes = [P(Dims), i32, P(QuantCacheStruct), vp, P(Cache), vp, vp, vp]
+    lib.lrkv_decode_quant_workspace_bytes.restype = sz
+    lib.lrkv_decode_quant_workspace_bytes.argtypes = [P(Dims), i32]
+    lib.lrkv_decode_quant.restype = ctypes.c_int
+    lib.lrkv_decode_quant.argtypes = [P(Dims), vp, vp, vp, P(QuantCacheStruct), vp, i32, vp, i32, vp, vp, sz, vp, vp]
+    lib.lrkv_decode_quant_partials.restype = ctypes.c_int
+    lib.lrkv_decode_quant_partials.argtypes = [P(Dims), vp, vp, P(QuantCacheStruct), vp, i32, vp, i32, vp, vp, sz, vp,
+                                               vp]
+    lib.lrkv_decode_shared_workspace_bytes.restype = sz
+    lib.lrkv_decode_shared_workspace_bytes.argtypes = [P(Dims), i32, i32]
+    lib.lrkv_decode_shared.restype = ctypes.c_int
+    lib.lrkv_decode_shared.argtypes = [P(Dims), vp, vp, vp, P(Cache), vp, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp,
+                                       vp]
+    lib.lrkv_prefix_partials.restype = ctypes.c_int
+    lib.lrkv_prefix_partials.argtypes = [P(Dims), vp, vp, P(Cache), vp, i32, vp, i32, vp, vp, sz, vp, vp]
     _lib = lib
     return lib
 
@@ -309,6 +336,113 @@ def lrkv_decode_layers(dims: Dims, q, BK, BV, cache: LayeredCache, block_table, 
                                    _ptr(out), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
                                    _ptr(status), _stream(stream))
     _check(rc, "lrkv_decode_layers")
+
+
+class QuantCache:
+    """One layer's quantised rows: uint8 [num_blocks, 64, quant_row_bytes(dims)]."""
+
+    def __init__(self, rows):
+        self.rows = rows
+        self.num_blocks = int(rows.shape[0])
+
+    @classmethod
+    def empty(cls, dims: Dims, num_blocks: int, device="cuda"):
+        return cls(torch.empty((num_blocks, 64, quant_row_bytes(dims)), dtype=torch.uint8, device=device))
+
+    def struct(self, dims: Dims) -> QuantCacheStruct:
+        if self.rows.numel() != self.num_blocks * quant_block_bytes(dims):
+            raise ValueError(f"quantised rows {tuple(self.rows.shape)}: expected [num_blocks, 64, "
+                             f"{quant_row_bytes(dims)}] for these dims")
+        return QuantCacheStruct(_ptr(self.rows), self.num_blocks)
+
+
+def quant_row_bytes(dims: Dims) -> int:
+    return int(load().lrkv_quant_row_bytes(ctypes.byref(dims)))
+
+
+def quant_block_bytes(dims: Dims) -> int:
+    return int(load().lrkv_quant_block_bytes(ctypes.byref(dims)))
+
+
+def decode_quant_workspace_bytes(dims: Dims, batch: int) -> int:
+    return int(load().lrkv_decode_quant_workspace_bytes(ctypes.byref(dims), batch))
+
+
+def decode_shared_workspace_bytes(dims: Dims, batch: int, max_prefix_blocks: int) -> int:
+    return int(load().lrkv_decode_shared_workspace_bytes(ctypes.byref(dims), batch, max_prefix_blocks))
+
+
+def lrkv_cache_quantize(dims: Dims, cache: PagedCache, bf16_slots, qcache: QuantCache, quant_slots, status=None,
+                        stream=None):
+    """Rows bf16_slots [n] of the bf16 pools -> rows quant_slots [n] of the quantised cache."""
+    c, qc = cache.struct(), qcache.struct(dims)
+    rc = load().lrkv_cache_quantize(ctypes.byref(dims), _same_length(bf16_slots, quant_slots), ctypes.byref(c),
+                                    _ptr(bf16_slots), ctypes.byref(qc), _ptr(quant_slots), _ptr(status),
+                                    _stream(stream))
+    _check(rc, "lrkv_cache_quantize")
+
+
+def lrkv_cache_dequantize(dims: Dims, qcache: QuantCache, quant_slots, cache: PagedCache, bf16_slots, status=None,
+                          stream=None):
+    """Rows quant_slots [n] of the quantised cache -> rows bf16_slots [n] of the bf16 pools (exact)."""
+    c, qc = cache.struct(), qcache.struct(dims)
+    rc = load().lrkv_cache_dequantize(ctypes.byref(dims), _same_length(bf16_slots, quant_slots), ctypes.byref(qc),
+                                      _ptr(quant_slots), ctypes.byref(c), _ptr(bf16_slots), _ptr(status),
+                                      _stream(stream))
+    _check(rc, "lrkv_cache_dequantize")
+
+
+def _same_length(a, b) -> int:
+    if int(a.shape[0]) != int(b.shape[0]):
+        raise ValueError(f"slot arrays of {int(a.shape[0])} and {int(b.shape[0])} rows")
+    return int(a.shape[0])
+
+
+def lrkv_decode_quant(dims: Dims, q, BK, BV, qcache: QuantCache, block_table, seq_lens, out, workspace, status=None,
+                      stream=None):
+    """lrkv_decode over quantised rows: q [B, H, d_h] -> out [B, H, d_h]."""
+    qc = qcache.struct(dims)
+    rc = load().lrkv_decode_quant(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(qc),
+                                  _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(q.shape[0]),
+                                  _ptr(out), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                  _ptr(status), _stream(stream))
+    _check(rc, "lrkv_decode_quant")
+
+
+def lrkv_decode_quant_partials(dims: Dims, q, BK, qcache: QuantCache, block_table, seq_lens, partials, workspace,
+                               status=None, stream=None):
+    """lrkv_decode_partials over quantised rows: -> partials [B, H, d_h + r + 2] fp32."""
+    qc = qcache.struct(dims)
+    rc = load().lrkv_decode_quant_partials(ctypes.byref(dims), _ptr(q), _ptr(BK), ctypes.byref(qc),
+                                           _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
+                                           int(q.shape[0]), _ptr(partials), _ptr(workspace),
+                                           int(workspace.numel() * workspace.element_size()), _ptr(status),
+                                           _stream(stream))
+    _check(rc, "lrkv_decode_quant_partials")
+
+
+def lrkv_decode_shared(dims: Dims, q, BK, BV, cache: PagedCache, prefix_blocks, prefix_len, block_table, seq_lens, out,
+                       workspace, status=None, stream=None):
+    """Decode of a batch that shares a prefix: prefix_blocks [max_prefix_blocks], prefix_len [1]; the sequences' own
+    tokens in block_table, seq_lens (0 allowed): q [B, H, d_h] -> out [B, H, d_h]."""
+    c = cache.struct()
+    rc = load().lrkv_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(c),
+                                   _ptr(prefix_blocks), int(prefix_blocks.shape[0]), _ptr(prefix_len),
+                                   _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(q.shape[0]),
+                                   _ptr(out), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                   _ptr(status), _stream(stream))
+    _check(rc, "lrkv_decode_shared")
+
+
+def lrkv_prefix_partials(dims: Dims, q, BK, cache: PagedCache, prefix_blocks, prefix_len, partials, workspace,
+                         status=None, stream=None):
+    """Decode partials of the whole batch over the shared prefix: -> partials [B, H, d_h + r + 2] fp32."""
+    c = cache.struct()
+    rc = load().lrkv_prefix_partials(ctypes.byref(dims), _ptr(q), _ptr(BK), ctypes.byref(c), _ptr(prefix_blocks),
+                                     int(prefix_blocks.shape[0]), _ptr(prefix_len), int(q.shape[0]), _ptr(partials),
+                                     _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                     _ptr(status), _stream(stream))
+    _check(rc, "lrkv_prefix_partials")
 
 
 def lrkv_prefill(dims: Dims, q, BK, BV, cache: PagedCache, block_table, q_start, out, workspace=None, status=None,

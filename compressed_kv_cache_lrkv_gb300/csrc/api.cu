@@ -13,6 +13,8 @@
 
 #include "kernels.h"
 #include "mla.h"
+#include "prefix.h"
+#include "quant.h"
 #include "train.h"
 
 namespace {
@@ -375,6 +377,39 @@ size_t lrkv_decode_workspace_bytes(const lrkv_dims* dims, int32_t batch) {
     return lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, decode_ranges(dims, di.sms));
 }
 
+// The prefix of lrkv_decode_shared / lrkv_prefix_partials.
+struct SharedPrefix {
+    const int32_t* blocks;
+    int32_t max_blocks;
+    const int32_t* len;
+};
+
+// Scan of the prefix (q~ is in p.d.qt) and the merge with the sequences' own partials, if any.
+static lrkv_status prefix_launch(lrkv::PrefixArgs& p, const lrkv_dims* dims, const lrkv_cache* cache,
+                                 const SharedPrefix& prefix, int suffix, int nsplit, void* ws, cudaStream_t st,
+                                 const char* what) {
+    p.sK = static_cast<const uint16_t*>(cache->sK);
+    p.sV = static_cast<const uint16_t*>(cache->sV);
+    p.zK = static_cast<const uint16_t*>(cache->zK);
+    p.zV = static_cast<const uint16_t*>(cache->zV);
+    p.blocks = prefix.blocks;
+    p.len = prefix.len;
+    p.max_blocks = prefix.max_blocks;
+    p.suffix = suffix;
+    p.nsplit = nsplit;
+    lrkv::prefix_carve_workspace(&p, ws, dims->d_h, dims->r);
+    cudaError_t e = lrkv::launch_prefix_scan(p, dims->d_h, dims->r, dims->d_rope, st);
+    if (e == cudaSuccess) e = lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st);
+    return cuda_status(e, what);
+}
+
+static lrkv_status check_prefix(const lrkv_dims* dims, const SharedPrefix& p) {
+    if (p.max_blocks < 1 || (long long)p.max_blocks * dims->block_size > (1LL << 30))
+        return fail(LRKV_ERR_INVALID_ARG, "max_prefix_blocks %d", p.max_blocks);
+    if (!p.blocks || !p.len) return fail(LRKV_ERR_INVALID_ARG, "prefix_blocks or prefix_len is NULL");
+    return LRKV_OK;
+}
+
 // Shared body of lrkv_decode (q~ = q B^K computed here, output B^V-projected), lrkv_decode_fused
 // (q~ given by the caller, output [o_s | o_z] / l), lrkv_decode_layers (several layers) and
 // lrkv_decode_partials (partials instead of an output: q~ computed, no B^V).
@@ -383,7 +418,7 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
                                const lrkv_cache* cache, const int32_t* block_table, int32_t max_blocks_per_seq,
                                const int32_t* seq_lens, int32_t batch, void* out, void* workspace,
                                size_t workspace_bytes, uint32_t* status_dev, void* stream,
-                               float* partials = nullptr) {
+                               float* partials = nullptr, const SharedPrefix* prefix = nullptr) {
     const bool fused = q_tilde != nullptr;
     const char* what = partials ? "lrkv_decode_partials launch"
                                 : fused ? "lrkv_decode_fused launch" : "lrkv_decode launch";
@@ -437,11 +472,15 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
         a.ls_zK = ls->zK;
         a.ls_zV = ls->zV;
     }
+    if (prefix && (s = check_prefix(dims, *prefix)) != LRKV_OK) return s;
     DeviceInfo di;
     if ((s = device_info(&di)) != LRKV_OK) return s;
     const int nvb = num_layers * batch;
     const int nranges = decode_ranges(dims, di.sms);
-    const size_t need = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, nvb, nranges);
+    const size_t scan_bytes = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, nvb, nranges);
+    const int psplits = prefix ? lrkv::prefix_splits(dims->H, dims->r, batch, prefix->max_blocks, di.sms) : 0;
+    const size_t need =
+        scan_bytes + (prefix ? lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, psplits) : 0);
     if (!workspace || ((uintptr_t)workspace & 255u))
         return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
@@ -491,6 +530,17 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
     a.scale_log2 = logit_scale(dims) * 1.4426950408889634f;
     lrkv::decode_carve_workspace(&a, workspace, dims->H, dims->d_h, dims->r, nvb, nranges);
     a.nhg = nhg;
+    if (prefix) {
+        a.no_combine = 1;
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        cudaError_t e = lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms,
+                                            di.smem_optin, st);
+        if (e != cudaSuccess) return cuda_status(e, "lrkv_decode_shared launch");
+        lrkv::PrefixArgs p{};
+        p.d = a;
+        return prefix_launch(p, dims, cache, *prefix, 1, psplits, static_cast<uint8_t*>(workspace) + scan_bytes, st,
+                             "lrkv_decode_shared launch");
+    }
     return cuda_status(lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms,
                                            di.smem_optin,
                                            static_cast<cudaStream_t>(stream)),
@@ -547,6 +597,207 @@ lrkv_status lrkv_decode_merge(const lrkv_dims* dims, int32_t num_parts, const fl
                                                  dims->d_h, dims->r, static_cast<uint16_t*>(out), status_dev,
                                                  static_cast<cudaStream_t>(stream)),
                        "lrkv_decode_merge launch");
+}
+
+size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t max_prefix_blocks) {
+    if (check_dims(dims) != LRKV_OK || batch < 0 || max_prefix_blocks < 1) return 0;
+    DeviceInfo di;
+    if (device_info(&di) != LRKV_OK) return 0;
+    const int ns = lrkv::prefix_splits(dims->H, dims->r, batch, max_prefix_blocks, di.sms);
+    return lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, decode_ranges(dims, di.sms)) +
+           lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, ns);
+}
+
+lrkv_status lrkv_decode_shared(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                               const lrkv_cache* cache, const int32_t* prefix_blocks, int32_t max_prefix_blocks,
+                               const int32_t* prefix_len, const int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t batch, void* out, void* workspace,
+                               size_t workspace_bytes, uint32_t* status_dev, void* stream) {
+    const SharedPrefix prefix{prefix_blocks, max_prefix_blocks, prefix_len};
+    return decode_impl(dims, 1, nullptr, q, nullptr, BK, BV, cache, block_table, max_blocks_per_seq, seq_lens, batch,
+                       out, workspace, workspace_bytes, status_dev, stream, nullptr, &prefix);
+}
+
+lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const void* BK, const lrkv_cache* cache,
+                                 const int32_t* prefix_blocks, int32_t max_prefix_blocks, const int32_t* prefix_len,
+                                 int32_t batch, float* partials, void* workspace, size_t workspace_bytes,
+                                 uint32_t* status_dev, void* stream) {
+    lrkv_status s = check_dims(dims);
+    if (s != LRKV_OK) return s;
+    if ((s = check_cache(cache)) != LRKV_OK) return s;
+    if (batch < 0 || batch > 65535) return fail(LRKV_ERR_INVALID_ARG, "batch %d (0..65535)", batch);
+    if (batch == 0) return ok();
+    LRKV_REQUIRE_PTR(q);
+    LRKV_REQUIRE_PTR(BK);
+    LRKV_REQUIRE_PTR(partials);
+    const SharedPrefix prefix{prefix_blocks, max_prefix_blocks, prefix_len};
+    if ((s = check_prefix(dims, prefix)) != LRKV_OK) return s;
+    DeviceInfo di;
+    if ((s = device_info(&di)) != LRKV_OK) return s;
+    const int nranges = decode_ranges(dims, di.sms);
+    const size_t scan_bytes = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, nranges);
+    const int ns = lrkv::prefix_splits(dims->H, dims->r, batch, max_prefix_blocks, di.sms);
+    const size_t need = scan_bytes + lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, ns);
+    if (!workspace || ((uintptr_t)workspace & 255u))
+        return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(LRKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    lrkv::PrefixArgs p{};
+    p.d.q = static_cast<const uint16_t*>(q);
+    p.d.BK = static_cast<const uint16_t*>(BK);
+    p.d.part_out = partials;
+    p.d.status = status_dev;
+    p.d.B = batch;
+    p.d.H = dims->H;
+    p.d.layers = 1;
+    p.d.num_blocks = cache->num_blocks;
+    p.d.scale_log2 = logit_scale(dims) * 1.4426950408889634f;
+    lrkv::decode_carve_workspace(&p.d, workspace, dims->H, dims->d_h, dims->r, batch, nranges);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = lrkv::launch_decode_absorb(p.d, dims->d_h, dims->r, dims->d_rope, st);
+    if (e != cudaSuccess) return cuda_status(e, "lrkv_prefix_partials launch");
+    return prefix_launch(p, dims, cache, prefix, 0, ns, static_cast<uint8_t*>(workspace) + scan_bytes, st,
+                         "lrkv_prefix_partials launch");
+}
+
+// ------------------------------------------------------------------ quantised cache
+static lrkv_status check_quant_cache(const lrkv_quant_cache* c) {
+    if (!c) return fail(LRKV_ERR_INVALID_ARG, "quantised cache is NULL");
+    if (!c->rows) return fail(LRKV_ERR_INVALID_ARG, "quantised rows pointer is NULL");
+    if (!aligned16(c->rows)) return fail(LRKV_ERR_INVALID_ARG, "quantised rows pointer not 16-byte aligned");
+    if (c->num_blocks < 1 || c->num_blocks > (1 << 24))
+        return fail(LRKV_ERR_INVALID_ARG, "num_blocks %d outside [1, 2^24]", c->num_blocks);
+    return LRKV_OK;
+}
+
+size_t lrkv_quant_row_bytes(const lrkv_dims* dims) {
+    if (check_dims(dims) != LRKV_OK) return 0;
+    return (size_t)lrkv::quant_layout(dims->d_h, dims->d_rope, dims->H, dims->r).row_bytes;
+}
+
+size_t lrkv_quant_block_bytes(const lrkv_dims* dims) { return lrkv_quant_row_bytes(dims) * 64; }
+
+static lrkv_status quant_store(bool write, const lrkv_dims* dims, int32_t n_tok, const lrkv_cache* cache,
+                               const int32_t* bf16_slots, const lrkv_quant_cache* qcache, const int32_t* quant_slots,
+                               uint32_t* status_dev, void* stream) {
+    lrkv_status s = check_dims(dims);
+    if (s != LRKV_OK) return s;
+    if ((s = check_cache(cache)) != LRKV_OK) return s;
+    if ((s = check_quant_cache(qcache)) != LRKV_OK) return s;
+    if (n_tok < 0) return fail(LRKV_ERR_INVALID_ARG, "n_tok %d < 0", n_tok);
+    if (n_tok == 0) return ok();
+    if (!bf16_slots || !quant_slots) return fail(LRKV_ERR_INVALID_ARG, "bf16_slots or quant_slots is NULL");
+    lrkv::QuantStoreArgs a{};
+    a.sK = static_cast<uint16_t*>(cache->sK);
+    a.sV = static_cast<uint16_t*>(cache->sV);
+    a.zK = static_cast<uint16_t*>(cache->zK);
+    a.zV = static_cast<uint16_t*>(cache->zV);
+    a.rows = static_cast<uint8_t*>(qcache->rows);
+    a.bf_slots = bf16_slots;
+    a.q_slots = quant_slots;
+    a.status = status_dev;
+    a.n = n_tok;
+    a.bf_nslots = (long long)cache->num_blocks * dims->block_size;
+    a.q_nslots = (long long)qcache->num_blocks * dims->block_size;
+    a.q = lrkv::quant_layout(dims->d_h, dims->d_rope, dims->H, dims->r);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return write ? cuda_status(lrkv::launch_cache_quantize(a, st), "lrkv_cache_quantize launch")
+                 : cuda_status(lrkv::launch_cache_dequantize(a, st), "lrkv_cache_dequantize launch");
+}
+
+lrkv_status lrkv_cache_quantize(const lrkv_dims* dims, int32_t n_tok, const lrkv_cache* cache,
+                                const int32_t* bf16_slots, const lrkv_quant_cache* qcache,
+                                const int32_t* quant_slots, uint32_t* status_dev, void* stream) {
+    return quant_store(true, dims, n_tok, cache, bf16_slots, qcache, quant_slots, status_dev, stream);
+}
+
+lrkv_status lrkv_cache_dequantize(const lrkv_dims* dims, int32_t n_tok, const lrkv_quant_cache* qcache,
+                                  const int32_t* quant_slots, const lrkv_cache* cache, const int32_t* bf16_slots,
+                                  uint32_t* status_dev, void* stream) {
+    return quant_store(false, dims, n_tok, cache, bf16_slots, qcache, quant_slots, status_dev, stream);
+}
+
+size_t lrkv_decode_quant_workspace_bytes(const lrkv_dims* dims, int32_t batch) {
+    if (check_dims(dims) != LRKV_OK || batch < 0) return 0;
+    DeviceInfo di;
+    if (device_info(&di) != LRKV_OK) return 0;
+    return lrkv::quant_decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, decode_ranges(dims, di.sms));
+}
+
+// Shared body of lrkv_decode_quant (out) and lrkv_decode_quant_partials (partials, no B^V).
+static lrkv_status decode_quant_impl(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                                     const lrkv_quant_cache* qcache, const int32_t* block_table,
+                                     int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, void* out,
+                                     float* partials, void* workspace, size_t workspace_bytes, uint32_t* status_dev,
+                                     void* stream) {
+    lrkv_status s = check_dims(dims);
+    if (s != LRKV_OK) return s;
+    if ((s = check_quant_cache(qcache)) != LRKV_OK) return s;
+    if (batch < 0 || batch > 65535) return fail(LRKV_ERR_INVALID_ARG, "batch %d (0..65535)", batch);
+    if (batch == 0) return ok();
+    if (max_blocks_per_seq < 1 || (long long)max_blocks_per_seq * dims->block_size > (1LL << 30))
+        return fail(LRKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", max_blocks_per_seq);
+    if ((long long)batch * max_blocks_per_seq * dims->block_size >= (1LL << 34))
+        return fail(LRKV_ERR_INVALID_ARG, "batch x max_blocks_per_seq x block_size = %lld (below 2^34)",
+                    (long long)batch * max_blocks_per_seq * dims->block_size);
+    LRKV_REQUIRE_PTR(q);
+    LRKV_REQUIRE_PTR(BK);
+    if (partials) {
+        LRKV_REQUIRE_PTR(partials);
+    } else {
+        LRKV_REQUIRE_PTR(BV);
+        LRKV_REQUIRE_PTR(out);
+    }
+    if (!block_table || !seq_lens) return fail(LRKV_ERR_INVALID_ARG, "block_table or seq_lens is NULL");
+    DeviceInfo di;
+    if ((s = device_info(&di)) != LRKV_OK) return s;
+    const int nranges = decode_ranges(dims, di.sms);
+    const size_t need = lrkv::quant_decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, nranges);
+    if (!workspace || ((uintptr_t)workspace & 255u))
+        return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(LRKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    lrkv::QuantDecodeArgs a{};
+    a.rows = static_cast<const uint8_t*>(qcache->rows);
+    a.q = lrkv::quant_layout(dims->d_h, dims->d_rope, dims->H, dims->r);
+    a.d.q = static_cast<const uint16_t*>(q);
+    a.d.BK = static_cast<const uint16_t*>(BK);
+    a.d.BV = static_cast<const uint16_t*>(BV);
+    a.d.part_out = partials;
+    a.d.block_table = block_table;
+    a.d.seq_lens = seq_lens;
+    a.d.status = status_dev;
+    a.d.out = static_cast<uint16_t*>(out);
+    a.d.B = batch;
+    a.d.H = dims->H;
+    a.d.layers = 1;
+    a.d.nhg = 1;
+    a.d.max_pages = max_blocks_per_seq;
+    a.d.num_blocks = qcache->num_blocks;
+    a.d.nranges = nranges;
+    a.d.wait_ns = decode_wait_limit_ns();
+    a.d.scale_log2 = logit_scale(dims) * 1.4426950408889634f;
+    return cuda_status(lrkv::launch_quant_decode(a, workspace, dims->d_h, dims->r, dims->d_rope, di.sms,
+                                                 di.smem_optin, static_cast<cudaStream_t>(stream)),
+                       partials ? "lrkv_decode_quant_partials launch" : "lrkv_decode_quant launch");
+}
+
+lrkv_status lrkv_decode_quant(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                              const lrkv_quant_cache* qcache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                              const int32_t* seq_lens, int32_t batch, void* out, void* workspace,
+                              size_t workspace_bytes, uint32_t* status_dev, void* stream) {
+    return decode_quant_impl(dims, q, BK, BV, qcache, block_table, max_blocks_per_seq, seq_lens, batch, out, nullptr,
+                             workspace, workspace_bytes, status_dev, stream);
+}
+
+lrkv_status lrkv_decode_quant_partials(const lrkv_dims* dims, const void* q, const void* BK,
+                                       const lrkv_quant_cache* qcache, const int32_t* block_table,
+                                       int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch,
+                                       float* partials, void* workspace, size_t workspace_bytes,
+                                       uint32_t* status_dev, void* stream) {
+    if (!partials) return fail(LRKV_ERR_INVALID_ARG, "partials is NULL");
+    return decode_quant_impl(dims, q, BK, nullptr, qcache, block_table, max_blocks_per_seq, seq_lens, batch, nullptr,
+                             partials, workspace, workspace_bytes, status_dev, stream);
 }
 
 size_t lrkv_prefill_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t Tq) {

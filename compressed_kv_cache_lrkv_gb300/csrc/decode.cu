@@ -964,7 +964,7 @@ static cudaError_t launch_decode_t(const CUtensorMap& tK, const CUtensorMap& tV,
             }
             e = launch_decode_tc_split<R>(tK, tV, a, grid, decode_tc_smem_bytes(p.nslot, p.stage_bytes), !a.qt_in,
                                           stream);
-            if (e != cudaSuccess) return e;
+            if (e != cudaSuccess || a.no_combine) return e;
             return launch_combine<D_H, R>(a, nvb, sms, stream);
         }
     }
@@ -979,8 +979,27 @@ static cudaError_t launch_decode_t(const CUtensorMap& tK, const CUtensorMap& tV,
         if (e != cudaSuccess) return e;
         e = launch_pdl(split, dim3(grid), dim3(p.threads), p.smem_bytes, stream, tK, tV, tZK, tZV, a);
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.no_combine) return e;
     return launch_combine<D_H, R>(a, nvb, sms, stream);
+}
+
+cudaError_t launch_decode_absorb(const DecodeArgs& a, int D_H, int R, int D_R, cudaStream_t stream) {
+    const dim3 grid(a.H, a.layers * a.B);
+#define LRKV_ABS(DH, RR)                                                                                          \
+    if (D_H == DH && R == RR)                                                                                     \
+        return D_R == 0 ? launch_pdl(decode_absorb_kernel<DH, RR, 0>, grid, dim3(256), 0, stream, a)              \
+                        : launch_pdl(decode_absorb_kernel<DH, RR, 64>, grid, dim3(256), 0, stream, a);
+    LRKV_ABS(64, 8) LRKV_ABS(64, 16) LRKV_ABS(64, 32) LRKV_ABS(128, 8) LRKV_ABS(128, 16) LRKV_ABS(128, 32)
+#undef LRKV_ABS
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode_combine(const DecodeArgs& a, int D_H, int R, int sms, cudaStream_t stream) {
+#define LRKV_CMB(DH, RR) \
+    if (D_H == DH && R == RR) return launch_combine<DH, RR>(a, a.layers * a.B, sms, stream);
+    LRKV_CMB(64, 8) LRKV_CMB(64, 16) LRKV_CMB(64, 32) LRKV_CMB(128, 8) LRKV_CMB(128, 16) LRKV_CMB(128, 32)
+#undef LRKV_CMB
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_decode(const CUtensorMap& tK, const CUtensorMap& tV, const CUtensorMap& tZK,

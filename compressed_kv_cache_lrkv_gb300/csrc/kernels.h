@@ -56,6 +56,7 @@ struct DecodeArgs {
     int pmax;          // partial slots per head in the workspace (layers * B * nhg + nranges)
     float scale_log2;  // softmax scale * log2(e)
     unsigned long long wait_ns;  // limit of the split kernel's pipeline waits (a debugging aid may shorten it)
+    int no_combine;   // 1: stop after the scan (its partials are merged by the caller's own kernel)
     // Partials out (a token-range split of the sequences): when set, the combine writes each
     // (sequence, head)'s merged, unnormalised [acc_s | acc_z | m | l] ([B][H][D_H + R + 2],
     // m in the log2 domain) here instead of out, and no B^V is read.
@@ -105,6 +106,10 @@ void decode_carve_workspace(DecodeArgs* a, void* ws, int H, int D_H, int R, int 
 cudaError_t launch_decode(const CUtensorMap& tK, const CUtensorMap& tV, const CUtensorMap& tZK,
                           const CUtensorMap& tZV, DecodeArgs a, int D_H, int R, int D_R, int sms, int smem_limit,
                           cudaStream_t stream);
+
+// The absorb kernel alone (q~ = q B^K into a.qt), and the combine alone.
+cudaError_t launch_decode_absorb(const DecodeArgs& a, int D_H, int R, int D_R, cudaStream_t stream);
+cudaError_t launch_decode_combine(const DecodeArgs& a, int D_H, int R, int sms, cudaStream_t stream);
 
 // The split-K scan on the tensor cores (H = 128, d_h = 128, no positional key, one head group):
 // launched in place of the CUDA-core scan by launch_decode; smem_bytes from decode_tc_smem_bytes.

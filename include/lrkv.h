@@ -295,6 +295,110 @@ lrkv_status lrkv_decode_layers(const lrkv_dims* dims, int32_t num_layers, const 
                                int32_t batch, void* out, void* workspace, size_t workspace_bytes,
                                uint32_t* status_dev, void* stream);
 
+/* ======================================================================
+ * Quantised cache: the same pages with 8 bits a value.
+ *
+ * A token's row holds its four parts s^K (d_h + d_rope values), s^V (d_h), z^K (H r) and z^V (H r)
+ * in blocks of 32 consecutive values (a part's last block may be shorter), each with one scale
+ * 2^k.  With amax the block's largest magnitude,
+ *     k = floor(log2 amax) - 6 (at least -126),   q_i = min(127, max(-127, rint(x_i / 2^k)))
+ * (rint: nearest, ties to even), so |x_i - q_i 2^k| <= 2^(k-1) <= 2^-7 amax for amax >= 2^-120, and
+ * q_i 2^k is exact in bf16.  A block that holds a NaN or an infinity reads as NaN throughout.
+ *   row : [s^K | s^V | z^K, padded to 16 | z^V, padded to 16 | scales of s^K, s^V, z^K, z^V], bytes;
+ *         a value's byte is q_i + 128, a block's scale byte k + 127 (255: NaN block; 0: zeros, as
+ *         in memory that was cleared); padded to an odd number of 16-byte units
+ *   rows: [num_blocks][block_size][lrkv_quant_row_bytes()]
+ * The row is 1.03 bytes a value instead of 2.  Block tables, slots and lengths are as for the
+ * bf16 pools; the same dims as for lrkv_decode are supported (r = 32 with any H).
+ * ====================================================================== */
+typedef struct lrkv_quant_cache {
+    void* rows;          /* device pointer, 16-byte aligned */
+    int32_t num_blocks;
+} lrkv_quant_cache;
+
+/* Bytes of one token's row, and of one page (block_size rows); 0 for unsupported dims. */
+size_t lrkv_quant_row_bytes(const lrkv_dims* dims);
+size_t lrkv_quant_block_bytes(const lrkv_dims* dims);
+
+/*
+ * lrkv_cache_quantize -- write n_tok rows of a quantised cache from rows of bf16 pools (those a
+ *   lrkv_append has just written, or whole pages that move to 8 bits).
+ * lrkv_cache_dequantize -- read n_tok rows back into bf16 pools (exactly: no rounding).
+ *   Row i is moved between token slot bf16_slots[i] of `cache` and token slot quant_slots[i] of
+ *   `qcache`.
+ *   bf16_slots, quant_slots [n_tok] int32 (device); where either is negative the row is skipped;
+ *     one at or beyond its cache's num_blocks * block_size sets LRKV_DEV_BAD_SLOT and skips it.
+ *     The slots written by a call must differ from one another: of two rows written to one slot
+ *     any mixture may remain.
+ *   Slots that are not named keep their contents.  n_tok == 0 is a no-op.
+ */
+lrkv_status lrkv_cache_quantize(const lrkv_dims* dims, int32_t n_tok, const lrkv_cache* cache,
+                                const int32_t* bf16_slots, const lrkv_quant_cache* qcache,
+                                const int32_t* quant_slots, uint32_t* status_dev, void* stream);
+lrkv_status lrkv_cache_dequantize(const lrkv_dims* dims, int32_t n_tok, const lrkv_quant_cache* qcache,
+                                  const int32_t* quant_slots, const lrkv_cache* cache, const int32_t* bf16_slots,
+                                  uint32_t* status_dev, void* stream);
+
+/* Workspace bytes of the two decode calls below for `batch` sequences on the CURRENT device. */
+size_t lrkv_decode_quant_workspace_bytes(const lrkv_dims* dims, int32_t batch);
+
+/*
+ * lrkv_decode_quant -- lrkv_decode over a quantised cache: the same formulas on the values q_i 2^k
+ *   that the rows stand for, read as they are (nothing is dequantised into memory).
+ * lrkv_decode_quant_partials -- its lrkv_decode_partials: per (sequence, head) the unnormalised
+ *   state over this cache's tokens, for lrkv_decode_merge (e.g. old tokens here, the newest ones
+ *   or a shared prefix in bf16 pools).
+ *   Arguments, lengths, errors and status bits are those of lrkv_decode / lrkv_decode_partials with
+ *   `qcache` in place of the pools; workspace of lrkv_decode_quant_workspace_bytes(dims, batch)
+ *   bytes, 256-byte aligned.  The latents' products take q~ and the probabilities in fp16 (11
+ *   significant bits, scaled by powers of two so that nothing overflows) and sum in fp32.
+ */
+lrkv_status lrkv_decode_quant(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                              const lrkv_quant_cache* qcache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                              const int32_t* seq_lens, int32_t batch, void* out, void* workspace,
+                              size_t workspace_bytes, uint32_t* status_dev, void* stream);
+lrkv_status lrkv_decode_quant_partials(const lrkv_dims* dims, const void* q, const void* BK,
+                                       const lrkv_quant_cache* qcache, const int32_t* block_table,
+                                       int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch,
+                                       float* partials, void* workspace, size_t workspace_bytes,
+                                       uint32_t* status_dev, void* stream);
+
+/* ======================================================================
+ * Shared prefix: one decode step of a batch whose sequences begin with the same tokens.
+ *
+ * The prefix's rows sit once in the cache, in pages listed by prefix_blocks; each sequence goes on
+ * in pages of its own (block_table, seq_lens, as for lrkv_decode; a length may be 0).  Softmax
+ * attention over both is the log-sum-exp merge of the two parts' states, so the prefix is read
+ * once for all sequences, whose queries share its products on the tensor cores.
+ * ====================================================================== */
+
+/* Workspace bytes of the two calls below for `batch` sequences and prefixes of up to
+ * max_prefix_blocks pages, on the CURRENT device. */
+size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t max_prefix_blocks);
+
+/*
+ * lrkv_decode_shared -- out_h = softmax attention (Eqs. (6)-(7)) over the prefix_len[0] tokens of the
+ *   prefix followed by the sequence's own seq_lens[b] tokens.
+ *   prefix_blocks [max_prefix_blocks] int32 (device) pages of the prefix, in order
+ *   prefix_len    [1] int32 (device), in [0, max_prefix_blocks * block_size]; 0: no prefix
+ *   Everything else as for lrkv_decode, except that seq_lens[b] may be 0.  A prefix_len or length
+ *   outside its range, or no token at all, sets LRKV_DEV_BAD_SEQLEN and writes zeros (a bad
+ *   prefix_len: for all sequences).  A page id of the prefix outside [0, num_blocks) sets
+ *   LRKV_DEV_BAD_BLOCK and its tokens are left out.  Rows behind the prefix's last token may hold
+ *   any bits.  A NaN or infinity among the prefix's rows may reach all heads of the batch.
+ * lrkv_prefix_partials -- the prefix's part alone, as lrkv_decode_partials returns it (for
+ *   lrkv_decode_merge with the partials of other caches); prefix_len 0 gives empty partials.
+ */
+lrkv_status lrkv_decode_shared(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                               const lrkv_cache* cache, const int32_t* prefix_blocks, int32_t max_prefix_blocks,
+                               const int32_t* prefix_len, const int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, int32_t batch, void* out, void* workspace,
+                               size_t workspace_bytes, uint32_t* status_dev, void* stream);
+lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const void* BK, const lrkv_cache* cache,
+                                 const int32_t* prefix_blocks, int32_t max_prefix_blocks, const int32_t* prefix_len,
+                                 int32_t batch, float* partials, void* workspace, size_t workspace_bytes,
+                                 uint32_t* status_dev, void* stream);
+
 /* Workspace bytes lrkv_prefill needs (0 today; kept so callers size it). */
 size_t lrkv_prefill_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t Tq);
 

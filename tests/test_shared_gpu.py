@@ -1,0 +1,209 @@
+"""Decode of a batch that shares a prefix, against attention in 64 bits over the prefix and the
+sequence's own tokens."""
+import pytest
+import torch
+
+from attn64 import attend64, check
+
+pytestmark = pytest.mark.gpu
+
+from compressed_kv_cache_lrkv_gb300 import binding as b  # noqa: E402
+
+BAD_BLOCK, BAD_SEQLEN = b.DEV_BAD_BLOCK, b.DEV_BAD_SEQLEN
+
+
+class Case:
+    """Pools with NaN in every row that no token uses."""
+
+    def __init__(self, seed, H, d_h, r, d_rope, P, lens, cap=0, num_splits=0):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        self.H, self.d_h, self.r, self.d_rope, self.P, self.lens = H, d_h, r, d_rope, P, list(lens)
+        B = len(lens)
+        self.dims = b.make_dims(H, d_h, r, H * d_h, d_rope=d_rope, num_splits=num_splits)
+        pp, pages = (P + 63) // 64, [(n + 63) // 64 for n in lens]
+        nb = pp + sum(pages) + 2
+        ids = torch.randperm(nb, generator=g, device="cuda").int()
+        self.blocks = torch.full((max(1, pp) + cap,), -1, dtype=torch.int32, device="cuda")
+        self.blocks[:pp] = ids[:pp]
+        self.bt = torch.full((B, max(1, max(pages))), -1, dtype=torch.int32, device="cuda")
+        at = pp
+        for i, p in enumerate(pages):
+            self.bt[i, :p] = ids[at:at + p]
+            at += p
+        mk = lambda *s: torch.randn(nb, 64, *s, generator=g, device="cuda").to(torch.bfloat16)
+        pools = [mk(d_h + d_rope), mk(d_h), mk(H, r), mk(H, r)]
+        self.pslots = self.at(self.blocks, P)
+        self.slots = [self.at(self.bt[i], n) for i, n in enumerate(lens)]
+        used = torch.zeros(nb * 64, dtype=torch.bool, device="cuda")
+        for s in [self.pslots] + self.slots:
+            used[s] = True
+        for t in pools:
+            t.view(nb * 64, -1)[~used] = float("nan")
+        self.cache = b.PagedCache(*pools)
+        self.q = torch.randn(B, H, d_h + d_rope, generator=g, device="cuda").to(torch.bfloat16)
+        fk = lambda: (torch.randn(H, d_h, r, generator=g, device="cuda") * r ** -0.5).to(torch.bfloat16)
+        self.BK, self.BV = fk(), fk()
+        self.sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.pl = torch.tensor([P], dtype=torch.int32, device="cuda")
+        self.st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.ws = b.alloc_workspace(b.decode_shared_workspace_bytes(self.dims, B, int(self.blocks.shape[0])))
+        self.ws.fill_(255)
+        self.out = torch.full((B, H, d_h), float("nan"), dtype=torch.bfloat16, device="cuda")
+
+    def at(self, pages, n):
+        t = torch.arange(n, device="cuda")
+        return pages[t // 64].long() * 64 + t % 64
+
+    def run(self, stream=None):
+        b.lrkv_decode_shared(self.dims, self.q, self.BK, self.BV, self.cache, self.blocks, self.pl, self.bt, self.sl,
+                             self.out, self.ws, status=self.st, stream=stream)
+        return self.out
+
+    def parts(self, i):
+        s = torch.cat([self.pslots, self.slots[i]])
+        k, v, zk, zv = self.cache.tensors()
+        f = lambda t: t.view(-1, *t.shape[2:])[s].double()
+        return f(k), f(v), f(zk), f(zv)
+
+    def verify(self, out=None, seqs=None, what="decode_shared", rel_max=5e-3):
+        out = self.out if out is None else out
+        seqs = range(len(self.lens)) if seqs is None else seqs
+        for i in seqs:
+            # probabilities and q~ are rounded to bf16 for the tensor cores
+            want, bound = attend64(self.q[i].double(), self.BK.double(), self.BV.double(), self.parts(i), self.d_rope,
+                                   eps_p=2.0 ** -8, eps_qt=2.0 ** -8)
+            check(out[i], want, bound, f"{what} P={self.P} sequence {i} of {self.lens[i]}", rel_max)
+
+
+CASES = [
+    (1, 64, 8, 0, 1, [0]), (1, 128, 32, 64, 300, [1, 0, 70]), (3, 64, 8, 0, 63, [5, 0]), (8, 64, 16, 0, 64, [64, 1, 0, 9]),
+    (8, 64, 16, 0, 65, [2] * 5), (9, 64, 32, 0, 129, [33]), (5, 128, 8, 64, 1000, [100] * 7),
+    (16, 128, 16, 0, 2000, list(range(0, 33))), (32, 128, 16, 0, 4100, [17] * 16), (32, 128, 32, 0, 777, [1] * 33),
+    (20, 64, 16, 64, 200, [3] * 130), (40, 128, 8, 0, 500, [0] * 9), (128, 128, 16, 64, 640, [50, 0, 1]),
+    (128, 64, 8, 0, 100, [10] * 20), (100, 128, 32, 0, 320, [7, 8]), (128, 128, 32, 0, 192, [66, 2]),
+    (2, 128, 16, 0, 9000, [1, 2, 3]),
+]
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,P,lens", CASES,
+                         ids=[f"H{c[0]}_dh{c[1]}_r{c[2]}_rope{c[3]}_P{c[4]}_B{len(c[5])}" for c in CASES])
+def test_matches_64_bits(H, d_h, r, d_rope, P, lens):
+    c = Case(H + r + P, H, d_h, r, d_rope, P, lens)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify()
+
+
+def test_no_prefix():
+    """prefix_len 0: the sequences' own tokens alone; a sequence without any gets zeros and a status bit."""
+    c = Case(1, 8, 64, 16, 0, 0, [100, 3])
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify()
+    c = Case(2, 8, 64, 16, 0, 0, [100, 0])
+    c.run()
+    assert int(c.st.item()) == BAD_SEQLEN and (c.out[1] == 0).all()
+    c.verify(seqs=[0])
+
+
+def test_table_longer_than_the_prefix():
+    c = Case(3, 16, 128, 16, 0, 200, [10, 0], cap=300)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify()
+
+
+def test_bad_lengths_and_pages():
+    for bad in (-1, 257):
+        c = Case(4, 8, 64, 16, 0, 200, [10, 0])
+        c.pl.fill_(bad)
+        c.run()
+        assert int(c.st.item()) == BAD_SEQLEN and (c.out == 0).all()
+    c = Case(5, 8, 64, 16, 0, 200, [10, 20, 30])
+    c.sl[1] = 65
+    c.sl[2] = -1
+    c.run()
+    assert int(c.st.item()) == BAD_SEQLEN and (c.out[1:] == 0).all()
+    c.verify(seqs=[0])
+    for bad in (-1, 10 ** 6):
+        c = Case(6, 8, 64, 16, 0, 200, [10, 0])
+        c.blocks[1] = bad
+        c.run()
+        assert int(c.st.item()) == BAD_BLOCK
+        c.pslots = torch.cat([c.pslots[:64], c.pslots[128:]])
+        c.verify()
+
+
+def test_sharp_and_flat_logits():
+    c = Case(7, 16, 128, 16, 0, 1500, [40] * 20)
+    c.q[:10] *= 20
+    c.q[10:15] = 0
+    c.run()
+    c.verify(rel_max=1.0)  # (logits 20 times as large magnify q~'s rounding: the bound says by how much)
+
+
+def test_prefix_partials_join_other_caches():
+    """A prefix in bf16 pages, old own tokens in 8 bits, the newest in bf16: three partials, one merge."""
+    H, d_h, r, P = 16, 128, 16, 500
+    lens = [100, 30, 64, 1]
+    c = Case(8, H, d_h, r, 0, P, lens)
+    B = len(lens)
+    qc = b.QuantCache.empty(c.dims, c.cache.num_blocks)
+    old = [64, 0, 64, 0]
+    slots = torch.cat([s[:n] for s, n in zip(c.slots, old)]).int()
+    b.lrkv_cache_quantize(c.dims, c.cache, slots, qc, slots, status=c.st)
+    b.lrkv_cache_dequantize(c.dims, qc, slots, c.cache, slots, status=c.st)  # what the 8-bit rows stand for
+    parts = torch.full((3, B, H, d_h + r + 2), float("nan"), device="cuda")
+    ws = b.alloc_workspace(max(b.decode_workspace_bytes(c.dims, B), b.decode_quant_workspace_bytes(c.dims, B)))
+    b.lrkv_prefix_partials(c.dims, c.q, c.BK, c.cache, c.blocks, c.pl, parts[0], c.ws, status=c.st)
+    b.lrkv_decode_quant_partials(c.dims, c.q, c.BK, qc, c.bt, torch.tensor(old, device="cuda").int(), parts[1], ws,
+                                 status=c.st)
+    new_bt = torch.full_like(c.bt, -1)
+    new_bt[0, 0], new_bt[1, 0], new_bt[3, 0] = c.bt[0, 1], c.bt[1, 0], c.bt[3, 0]
+    b.lrkv_decode_partials(c.dims, c.q, c.BK, c.cache, new_bt, torch.tensor([36, 30, 0, 1], device="cuda").int(),
+                           parts[2], ws, status=c.st)
+    b.lrkv_decode_merge(c.dims, parts, c.BV, c.out, status=c.st)
+    assert int(c.st.item()) == 0
+    c.verify(what="joined partials")
+    # an empty prefix: empty partials, no status bit
+    c.pl.fill_(0)
+    b.lrkv_prefix_partials(c.dims, c.q, c.BK, c.cache, c.blocks, c.pl, parts[0], c.ws, status=c.st)
+    assert int(c.st.item()) == 0
+    assert torch.isneginf(parts[0, :, :, -2]).all() and (parts[0, :, :, -1] == 0).all()
+    assert (parts[0, :, :, :-2] == 0).all()
+
+
+def test_captured_and_replayed():
+    c = Case(9, 32, 128, 16, 0, 1000, [30, 0, 64, 5])
+    c.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run()
+    c.out.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    c.verify()
+    c.P, c.lens = 129, [1, 0, 9, 5]
+    c.pl.fill_(c.P)
+    c.sl.copy_(torch.tensor(c.lens, dtype=torch.int32))
+    c.pslots = c.pslots[:c.P]
+    c.slots = [s[:n] for s, n in zip(c.slots, c.lens)]
+    graph.replay()
+    torch.cuda.synchronize()
+    c.verify()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c.out.fill_(float("nan"))
+    side.wait_stream(torch.cuda.current_stream())
+    c.run(stream=side)
+    side.synchronize()
+    c.verify()
+
+
+def test_runs_are_bitwise_repeatable():
+    c = Case(10, 32, 128, 32, 0, 3001, [100] * 16)
+    first = c.run().clone()
+    for _ in range(5):
+        assert torch.equal(c.run(), first)
