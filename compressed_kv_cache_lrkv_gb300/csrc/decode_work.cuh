@@ -42,7 +42,9 @@ __host__ __device__ constexpr int decode_stage_stride(int W) { return (W % 16 ==
 // computes the plan before the first load of the CTA is issued, and a 64-bit division is a
 // long dependent software sequence on the GPU.  floor(c T / n) is formed as c (T / n) +
 // floor(c (T mod n) / n), whose product c (T mod n) < n^2 fits in 32 unsigned bits.
-struct Work {
+// GRAN: tokens per granule (8 unless the scan's tiles are longer).
+template <int GRAN>
+struct WorkT {
     const int32_t* g;  // lengths in global memory
     const int* s;      // shared-memory copy of the first kSeqCache
     int B, layers, cap, nranges;
@@ -60,7 +62,7 @@ struct Work {
     // Granules of sequence b, or 0 when its length is outside [1, cap].
     __device__ __forceinline__ int gran_b(int b) const {
         const int L = len(b);
-        return (L >= 1 && L <= cap) ? (L + kGran - 1) / kGran : 0;
+        return (L >= 1 && L <= cap) ? (L + GRAN - 1) / GRAN : 0;
     }
     __device__ __forceinline__ int gran(int vb) const { return gran_b(vb % B); }
     __device__ __forceinline__ int total() const { return Tb * layers; }
@@ -173,6 +175,8 @@ struct Work {
     __device__ __forceinline__ int work_items() const { return pieces ? per_layer_pieces * layers : nranges; }
 };
 
+using Work = WorkT<kGran>;
+
 // This CTA's walk over its segments: (virtual sequence, granule range in it, partial slot).
 struct SegWalk {
     int item;            // current piece or range
@@ -186,7 +190,8 @@ struct SegWalk {
         vb = 0;
         vstart = 0;
     }
-    __device__ __forceinline__ bool next(const Work& w, int* vb_out, int* g0, int* g1, int* slot) {
+    template <class W>
+    __device__ __forceinline__ bool next(const W& w, int* vb_out, int* g0, int* g1, int* slot) {
         if (w.pieces) {
             if (item >= w.work_items()) return false;
             w.piece(item, vb_out, g0, g1);
