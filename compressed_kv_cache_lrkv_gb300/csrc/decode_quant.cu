@@ -7,8 +7,9 @@
 // A row is half as many bytes as in bf16, so a scan at the memory's pace has half the time per
 // value, and each value must first be widened.  All products are therefore fed to the tensor
 // cores (mma.sync m16n8k16), the latents' too, straight from the row bytes:
-//   - a byte u = q + 128 becomes fp16 by one byte permute (two values 1024 + u at a time, exact) and
-//     one packed subtraction of 1152;
+//   - a byte u = q + 128 becomes fp16 by one byte permute (two values 1024 + u at a time, exact);
+//     the offset 1152 = 1024 + 128 leaves the sums again as -1152 sum q~ (in the K sums' start) and
+//     -1152 sum w (one product with a constant A per tile);
 //   - tokens are the M of the logits' product (A = 16 tokens x 16 features, B = features x 8
 //     heads) and the K of the values' (A = features x 16 tokens, B = 16 tokens x 8 heads), so both
 //     leave a thread the same two heads and the probabilities pass from one to the other by a
@@ -18,11 +19,11 @@
 //   - scales: one per (token, head's block) multiplies the K sums in fp32; the V weights are
 //     w_t = 2^(s_t + k_t - mz) in fp16 with a running maximum mz of their own, so tokens whose
 //     scales differ by any power of two lose nothing but what is small beside the largest;
-//   - the shared rows s^K, s^V (used by all heads) are widened to bf16 once per 16 tokens by two
+//   - the shared rows s^K, s^V (used by all heads) are widened to bf16 once per 16 tokens by
 //     converter warps (q_i 2^k is exact in bf16).
 // Warps of a CTA: consumers (NT x 8 heads each, NG groups taking 16-token tiles in turn), one
 // producer (bulk copies of whole rows, which lie contiguous within a page, into a ring of
-// stages), one or two converters; connected by mbarriers only, so they drift freely.  One CTA per
+// stages), three or four converters; connected by mbarriers only, so they drift freely.  One CTA per
 // SM; the work is cut as in the bf16 decode (decode_work.cuh).
 #include <cuda_fp16.h>
 
@@ -34,6 +35,13 @@ namespace lrkv {
 
 namespace {
 
+#ifndef MOST1
+#define MOST1 8
+#endif
+constexpr int kConsumers1 = MOST1, kConverters1 = 3;  // one tile of 8 heads per consumer warp
+constexpr int kConsumers2 = 8, kConverters2 = 3;  // two
+constexpr int kThreads1 = (kConsumers1 + 1 + kConverters1) * 32;
+constexpr int kThreads2 = (kConsumers2 + 1 + kConverters2) * 32;
 constexpr int kMaxWalkers = 16;   // warps of a CTA at most
 constexpr float kLazy = 8.0f;     // maxima are raised when exceeded by this much (log2 units)
 
@@ -41,9 +49,6 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
-    asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0], %1; }" ::"r"(bar), "r"(n) : "memory");
 }
 
 // D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
@@ -61,13 +66,14 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 // Two bytes of x, chosen by sel (0x4140: bytes 0, 1; 0x4342: 2, 3; 0x4240: 0, 2; 0x4341: 1, 3), as
-// fp16 values byte - 128: the fp16 with high byte 0x64 and low byte u is 1024 + u.
+// fp16 values 1024 + byte: the fp16 with high byte 0x64 and low byte u.
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel) {
     uint32_t v;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(v) : "r"(x), "r"(0x64646464u), "r"(sel));
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&v), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&h);
+    return v;
 }
+constexpr float kByteOffset = 1152.0f;          // 1024 + u = q + 1152
+constexpr uint32_t kMinusOffset2 = 0xe480e480u;  // fp16 (-1152, -1152)
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
@@ -78,6 +84,15 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
+// Values q_i 2^k of two bytes (b0, b1 of [b0, 0, b1, 0]) as bf16, s2 = (2^k, 2^k): with the low seven
+// bits in its mantissa bf16 holds 128 + u mod 128, from which 256 or, where the byte's top bit is
+// set, 128 is taken; both steps and the product are exact.
+__device__ __forceinline__ uint32_t bytes_bf16(uint32_t v, __nv_bfloat162 s2) {
+    const uint32_t lo = (v & 0x007f007fu) | 0x43004300u, hi = (v & 0x00800080u) ^ 0x43804380u;
+    const __nv_bfloat162 r = __hmul2(
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi)), s2);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -86,14 +101,32 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Scale of a block: 2^(e - 127); NaN for byte 255, zero for 0 (a cleared row).
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == 255 ? 0x7fc00000u : e << 23); }
 
+// try_wait that may sleep in hardware for some microseconds before it reports failure: a waiting warp
+// then takes few issue slots from the others.
+__device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait of a whole warp; false (with the abort flag set) once it, or any other, gave up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
                                           uint64_t limit_ns) {
     if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-    const bool ok = mbar_wait_for(bar, parity, status, limit_ns);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    *abort_flag = 1;
-    return false;
+    if (__all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (__all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) {
+            set_status(status, LRKV_DEV_TIMEOUT);
+            *abort_flag = 1;
+            return false;
+        }
+    }
 }
 
 struct QuantPlan {
@@ -112,7 +145,7 @@ struct QuantScanArgs {
 };
 
 // One warp's walk over the CTA's segments.
-struct Walker {
+struct alignas(16) Walker {
     SegWalk walk;
     int valid, vb, g0, g1, slot;
     template <class W>
@@ -120,7 +153,7 @@ struct Walker {
         valid = walk.next(w, &vb, &g0, &g1, &slot);
     }
 };
-static_assert(sizeof(Walker) <= 48, "walker");
+static_assert(sizeof(Walker) == 48, "walkers are an array in shared memory with the work plan behind it");
 
 // Row stride (floats) of a head in the staging of the group merge: 4 mod 16, so that the four head
 // pairs and eight columns of a warp's store fall on different banks.
@@ -130,7 +163,7 @@ __host__ __device__ constexpr int merge_stride(int W) { return W % 16 == 0 ? W +
 __host__ __device__ constexpr int cb_stride(int D_K, int D_H) { return (D_K + D_H) * 2 + 16; }
 
 template <int D_H, int R, int D_R, int NT, int TOK>
-__global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(const QuantScanArgs args) {
+__global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan_kernel(const QuantScanArgs args) {
     constexpr int D_K = D_H + D_R, W = D_H + R, WS = merge_stride(W);
     constexpr int SB = cb_stride(D_K, D_H);
     constexpr int NKK = D_K / 16;
@@ -138,6 +171,8 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
     constexpr int NCH = 8 * R / 16;                // chunks of a tile of 8 heads
     constexpr int TPP = kBlockSize / TOK;          // tiles per page
     using WorkQ = WorkT<TOK>;
+    static_assert(sizeof(WorkQ) <= 96 && alignof(WorkQ) <= 16, "room for the plan in shared memory");
+    static_assert(kThreads1 <= 32 * kMaxWalkers && kThreads2 <= 32 * kMaxWalkers, "walkers");
     const DecodeArgs& a = args.a.d;
     const QuantLayout& ql = args.a.q;
     const QuantPlan& p = args.p;
@@ -166,10 +201,10 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
     if (threadIdx.x == 0) {
         for (int i = 0; i < nslot; ++i) {
             mbar_init(smem_u32(full + i), 1);
-            mbar_init(smem_u32(empty + i), ST * (p.nwh + 1));
+            mbar_init(smem_u32(empty + i), NCW + p.ncv);
         }
         for (int i = 0; i < ncb; ++i) {
-            mbar_init(smem_u32(cfull + i), 1);
+            mbar_init(smem_u32(cfull + i), p.ncv);
             mbar_init(smem_u32(cempty + i), p.nwh);
         }
         mbar_init(smem_u32(merged), NCW);
@@ -193,9 +228,9 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
     __syncwarp();
 
     // Tile indices below count the CTA's tiles from its first (u) and its stages (k), alike in all
-    // warps.  Every warp waits for every stage in turn (not only for those with a tile of its
-    // own), and a widened tile's slot always belongs to the same group and converter (ncb is a
-    // multiple of both counts), so nobody can mistake one round of a barrier for another.
+    // warps.  Every consumer and converter waits for and releases every stage in turn (not only those
+    // with a tile of its own), and a widened tile's slot always belongs to the same group and converter
+    // (ncb is a multiple of both counts), so nobody can miss a round of a barrier or take one for another.
     if (warp == NCW) {
         // ---------------------------------------------------------------- producer
         const uint64_t pol = policy_evict_first();
@@ -228,8 +263,6 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
                     ok = warp_wait(smem_u32(empty + slot), (k / nslot - 1) & 1, abort_flag, a.status, a.wait_ns);
                 ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
                 if (ok && lane == 0) {
-                    // tiles the segment leaves out of the stage count as consumed
-                    if (e - f < ST) mbar_arrive_n(smem_u32(empty + slot), (ST - (e - f)) * (p.nwh + 1));
                     if (blk < 0 || blk >= a.num_blocks) {
                         set_status(a.status, LRKV_DEV_BAD_BLOCK);
                         meta[slot] = 0;
@@ -267,7 +300,6 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
                 bool ok = warp_wait(smem_u32(full + slot), (k / nslot) & 1, abort_flag, a.status, a.wait_ns);
                 const int f = max(g0, s * ST), e = min(g1, (s + 1) * ST);
                 for (int t = f; t < e; ++t, ++u) {
-                    if (u % p.ncv != cv) continue;
                     const int cb = u % ncb;
                     if (ok && u >= ncb)
                         ok = warp_wait(smem_u32(cempty + cb), (u / ncb - 1) & 1, abort_flag, a.status, a.wait_ns);
@@ -277,38 +309,30 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
                         const uint32_t src = ring + slot * p.stage_bytes + (t - s * ST) * TOK * RB;
                         const uint32_t dst = cbuf + cb * p.cb_bytes;
 #pragma unroll 4
-                        for (int i = lane; i < TOK * U; i += 32) {
+                        for (int i = cv * 32 + lane; i < TOK * U; i += p.ncv * 32) {
                             const int row = i / U, c = i - row * U;
                             const uint32_t ra = src + row * RB;
-                            uint32_t x0, x1;
-                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x0), "=r"(x1) : "r"(ra + c * 8));
+                            uint32_t x[2], o[4];
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(ra + c * 8));
                             const uint32_t sb = lds8(ra + ql.off_sc + (c >> 2));
-                            const float sc = scale_of(sb);
-                            uint32_t o[4];
+                            // the scale twice in bf16 (NaN for byte 255); zero for tokens behind the end (their
+                            // probabilities are 0, and 0 x NaN is not)
+                            uint32_t s2 = sb == 255 ? 0x7fc07fc0u : sb * 0x00800080u;
+                            s2 = row < nvalid ? s2 : 0u;
+                            const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&s2);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t x = j < 2 ? x0 : x1;
-                                uint32_t lo, hi;  // 2^23 + u
-                                asm("prmt.b32 %0, %1, %2, %3;" : "=r"(lo) : "r"(x), "r"(0x4b000000u), "r"(0x7540u + (j & 1) * 2));
-                                asm("prmt.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(x), "r"(0x4b000000u), "r"(0x7541u + (j & 1) * 2));
-                                o[j] = pack_bf16x2((__uint_as_float(lo) - 8388736.0f) * sc,
-                                                   (__uint_as_float(hi) - 8388736.0f) * sc);
-                            }
-                            // tokens behind the end: zeros (their probabilities are 0, and 0 x NaN is not)
-                            const bool live = row < nvalid;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) o[j] = live ? o[j] : 0u;
+                            for (int j = 0; j < 4; ++j)
+                                o[j] = bytes_bf16(__byte_perm(x[j >> 1], 0u, j & 1 ? 0x4342 : 0x4140), sc);
                             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * SB + c * 16),
                                          "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                                          : "memory");
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(cfull + cb));
-                        mbar_arrive(smem_u32(empty + slot));
-                    }
+                    if (lane == 0) mbar_arrive(smem_u32(cfull + cb));
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(empty + slot));
             }
             __syncwarp();
             if (lane == 0) wk.advance(*work);
@@ -321,9 +345,7 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
         const int g = lane >> 2, tq = lane & 3;
         const int nct = NCW * 32;
         const int g8 = TOK == 16 ? g + 8 : g;        // rows 8..15 of a tile of 8 tokens: masked copies of 0..7
-        // chunk c of tile nt belongs to heads of this grid: its latents end at the row's H r values
-        const int zlim = (ql.HR + 15) >> 4;          // 16-byte chunks of z^K (z^V) in a row
-        const int zc0 = h0 * R / 16;
+        const int zc0 = h0 * R / 16;                 // this warp's first 16-byte chunk of a row's latents
         pdl_wait();  // q~ written by the absorb kernel
         int k = 0, u = 0;
         while (wk.valid) {
@@ -332,6 +354,7 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
             // Queries as B fragments (features x heads, head h0 + 8 nt + g in this lane's column)
             uint32_t qb[NKK][NT][2];
             uint32_t qz[NZC][NT][2];
+            float ci[NT][2];  // start of the latent logits' sums
             float fz[NT][2];  // power of two that q~ was divided by, for heads 2 tq, 2 tq + 1 of each tile
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -371,6 +394,21 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
                 }
                 fz[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * tq);
                 fz[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * tq + 4);
+                // the products take 1152 + q for q: the sums start from -1152 sum q~ (as rounded).  (Against
+                // a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of it, more than
+                // q~ has.)
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < NZC; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qz[c][nt][i]));
+                        sum += x.x + x.y;
+                    }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                ci[nt][0] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq);
+                ci[nt][1] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
             }
             float o[D_H / 16][NT][4], oz[NZC][NT][4];
             float m[NT][2], mz[NT][2], l[NT][2];
@@ -408,7 +446,7 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) c[nt][i] = cz[nt][i] = 0.f;
+                            for (int i = 0; i < 4; ++i) c[nt][i] = cz[nt][i] = 0.f;  // (every cz is set below)
                         {
                             const int r16 = TOK == 16 ? lane & 15 : lane & 7;
                             const uint32_t ad = cv + r16 * SB + (lane >> 4) * 16;
@@ -420,22 +458,29 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
                                 for (int nt = 0; nt < NT; ++nt) mma_16816(c[nt], af, qb[kk][nt][0], qb[kk][nt][1]);
                             }
                         }
-                        // --- latent logits q~ . z^K, head by head
+                        // --- latent logits q~ . z^K, chunk by chunk of 16 bytes: of a product with all eight
+                        // heads' q~ only the columns of the chunk's own head (r = 8: two heads) are kept.  (Heads
+                        // past the last read whatever follows in shared memory: finite, and never stored.)
                         {
                             const uint32_t z0 = row0 + g * RB + ql.off_zK + zc0 * 16 + tq * 4;
                             const uint32_t z1 = row0 + g8 * RB + ql.off_zK + zc0 * 16 + tq * 4;
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int ch = 0; ch < NCH; ++ch) {
-                                    const int cc = nt * NCH + ch;
-                                    if (zc0 + cc < zlim) {
-                                        const uint32_t x0 = lds32(z0 + cc * 16), x1 = lds32(z1 + cc * 16);
-                                        const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
-                                        const int zc = R == 32 ? ch & 1 : 0;
-                                        mma_16816_f16(cz[nt], bytes_f16(x0, 0x4140), bytes_f16(x1, 0x4140),
-                                                      bytes_f16(x0, 0x4342), bytes_f16(x1, 0x4342),
-                                                      mine ? qz[zc][nt][0] : 0u, mine ? qz[zc][nt][1] : 0u);
+                                for (int j = 0; j < NCH / NZC; ++j) {
+                                    float d[4] = {ci[nt][0], ci[nt][1], ci[nt][0], ci[nt][1]};
+#pragma unroll
+                                    for (int zc = 0; zc < NZC; ++zc) {
+                                        const int at = (nt * NCH + j * NZC + zc) * 16;
+                                        const uint32_t x0 = lds32(z0 + at), x1 = lds32(z1 + at);
+                                        mma_16816_f16(d, bytes_f16(x0, 0x4140), bytes_f16(x1, 0x4140),
+                                                      bytes_f16(x0, 0x4342), bytes_f16(x1, 0x4342), qz[zc][nt][0],
+                                                      qz[zc][nt][1]);
+                                    }
+                                    if (tq == (R == 8 ? j : j >> 1)) {
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i)
+                                            if (R == 8 || (i & 1) == (j & 1)) cz[nt][i] = d[i];
                                     }
                                 }
                         }
@@ -528,36 +573,38 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
                         // elements are pairs of features, row g of A takes the even one, row g + 8 the odd one
                         {
                             const int r16 = TOK == 16 ? lane & 15 : lane & 7;
-                            const uint32_t zr = row0 + r16 * RB + ql.off_zV;
+                            const uint32_t zr = row0 + r16 * RB + ql.off_zV + (zc0 + (lane >> 4)) * 16;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
+                                // the offset 1152 of the bytes' products, taken off tile by tile (so that the
+                                // sums never grow with it)
+#pragma unroll
+                                for (int zc = 0; zc < NZC; ++zc)
+                                    mma_16816_f16(oz[zc][nt], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
+                                                  wb[nt][0], wb[nt][1]);
 #pragma unroll
                                 for (int c2 = 0; c2 < NCH; c2 += 2) {
-                                    const int cc = zc0 + nt * NCH + c2;
-                                    if (cc < zlim) {
-                                        uint32_t x[4];
-                                        ldmatrix_x4_trans(zr + min(cc + (lane >> 4), zlim - 1) * 16, x[0], x[1], x[2],
-                                                          x[3]);
+                                    uint32_t x[4];
+                                    ldmatrix_x4_trans(zr + (nt * NCH + c2) * 16, x[0], x[1], x[2], x[3]);
 #pragma unroll
-                                        for (int w = 0; w < 2; ++w) {
-                                            const int ch = c2 + w;
-                                            const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
-                                            const int zc = R == 32 ? ch & 1 : 0;
-                                            mma_16816_f16(oz[zc][nt], bytes_f16(x[2 * w], 0x4240),
-                                                          bytes_f16(x[2 * w], 0x4341), bytes_f16(x[2 * w + 1], 0x4240),
-                                                          bytes_f16(x[2 * w + 1], 0x4341), mine ? wb[nt][0] : 0u,
-                                                          mine ? wb[nt][1] : 0u);
-                                        }
+                                    for (int w = 0; w < 2; ++w) {
+                                        const int ch = c2 + w;
+                                        const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
+                                        const int zc = R == 32 ? ch & 1 : 0;
+                                        mma_16816_f16(oz[zc][nt], bytes_f16(x[2 * w], 0x4240),
+                                                      bytes_f16(x[2 * w], 0x4341), bytes_f16(x[2 * w + 1], 0x4240),
+                                                      bytes_f16(x[2 * w + 1], 0x4341), mine ? wb[nt][0] : 0u,
+                                                      mine ? wb[nt][1] : 0u);
                                     }
                                 }
+                            }
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(empty + slot));
-                        mbar_arrive(smem_u32(cempty + cb));
-                    }
+                    if (lane == 0) mbar_arrive(smem_u32(cempty + cb));
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(empty + slot));
             }
             // --- this group's state over the segment
 #pragma unroll
@@ -659,14 +706,16 @@ __global__ void __launch_bounds__(NT == 1 ? 480 : 352, 1) quant_scan_kernel(cons
     pdl_trigger();  // the combine waits for this grid's end
 }
 
+// Tokens of a tile.
+int tile_tokens(int H, int R) { return R == 32 && H > 96 ? 8 : 16; }
+
 template <int D_H, int R, int D_R>
 bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
-    // More than 96 heads take two tiles of 8 heads per warp (12 warps of one tile do not cover
-    // them); a row of more than 97 heads of r = 32 is so long that two stages of 16 do not fit:
-    // tiles of 8 tokens there.
-    p->nt = H > 96 ? 2 : 1;
-    const int tok = (p->nt == 2 && R == 32) ? 8 : 16;
-    const int most = p->nt == 2 ? 8 : 12;  // consumer warps
+    p->nt = H > 8 * kConsumers1 ? 2 : 1;
+    // a row of more than 96 heads of r = 32 is so long that two stages of 16 tokens do not fit
+    const int tok = tile_tokens(H, R);
+    const int most = p->nt == 2 ? kConsumers2 : kConsumers1;
+    p->ncv = p->nt == 2 ? kConverters2 : kConverters1;
     p->nwh = (H + 8 * p->nt - 1) / (8 * p->nt);
     const int ng_most = most / p->nwh > 1 ? most / p->nwh : 1;
     p->cb_bytes = tok * cb_stride(D_H + D_R, D_H);
@@ -692,7 +741,6 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
                 p->ng = ng;
                 p->ncb = ncb;
                 p->nslot = nslot;
-                p->ncv = ncb % 2 == 0 ? 2 : 1;
                 p->threads = (p->nwh * ng + 1 + p->ncv) * 32;
                 p->smem_bytes = nslot * p->stage_bytes + ncb * p->cb_bytes + fixed(nslot, ncb);
                 return true;
@@ -703,13 +751,16 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
 template <int D_H, int R, int D_R>
 cudaError_t launch_t(QuantScanArgs& x, int sms, int smem_limit, cudaStream_t stream) {
     if (!make_plan<D_H, R, D_R>(&x.p, x.a.q, x.a.d.H, smem_limit)) return cudaErrorInvalidConfiguration;
-    constexpr int TOK2 = R == 32 ? 8 : 16;
-    auto kern = x.p.nt == 1 ? quant_scan_kernel<D_H, R, D_R, 1, 16> : quant_scan_kernel<D_H, R, D_R, 2, TOK2>;
+    const int tok = tile_tokens(x.a.d.H, R);
+    auto kern = x.p.nt == 1 ? quant_scan_kernel<D_H, R, D_R, 1, 16> : quant_scan_kernel<D_H, R, D_R, 2, 16>;
+    if constexpr (R == 32) {
+        if (tok == 8) kern = quant_scan_kernel<D_H, R, D_R, 2, 8>;
+    }
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, x.p.smem_bytes);
     if (e != cudaSuccess) return e;
     // a pipeline drain and refill at a sequence boundary costs about as long as streaming 128 KB through
     // one SM (in granules of the plan)
-    const int gran = (x.p.nt == 2 ? TOK2 : 16) * x.a.q.row_bytes;
+    const int gran = tok * x.a.q.row_bytes;
     x.a.d.bubble = ((128 << 10) + gran - 1) / gran;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(x.a.d.nranges < sms ? x.a.d.nranges : sms);
