@@ -19,13 +19,16 @@
 //   - scales: one per (token, head's block) multiplies the K sums in fp32; the V weights are
 //     w_t = 2^(s_t + k_t - mz) in fp16 with a running maximum mz of their own, so tokens whose
 //     scales differ by any power of two lose nothing but what is small beside the largest;
-//   - the shared rows s^K, s^V (used by all heads) are widened to bf16 once per 16 tokens by
-//     converter warps (q_i 2^k is exact in bf16).
+//   - s^K enters the logits in the same way, 32 features (a block) at a time; s^V, whose sums over
+//     tokens cannot be scaled afterwards, is widened to bf16 (q_i 2^k is exact) once per 16 tokens
+//     by converter warps.
 // Warps of a CTA: consumers (NT x 8 heads each, NG groups taking 16-token tiles in turn), one
 // producer (bulk copies of whole rows, which lie contiguous within a page, into a ring of
-// stages), three or four converters; connected by mbarriers only, so they drift freely.  One CTA per
+// stages), three converters; connected by mbarriers only, so they drift freely.  One CTA per
 // SM; the work is cut as in the bf16 decode (decode_work.cuh).
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "decode_work.cuh"
 #include "lrkv_internal.cuh"
@@ -35,14 +38,12 @@ namespace lrkv {
 
 namespace {
 
-#ifndef MOST1
-#define MOST1 8
-#endif
-constexpr int kConsumers1 = MOST1, kConverters1 = 3;  // one tile of 8 heads per consumer warp
-constexpr int kConsumers2 = 8, kConverters2 = 3;  // two
-constexpr int kThreads1 = (kConsumers1 + 1 + kConverters1) * 32;
-constexpr int kThreads2 = (kConsumers2 + 1 + kConverters2) * 32;
-constexpr int kMaxWalkers = 16;   // warps of a CTA at most
+// Consumer warps at most, and converters: 12 warps with the producer, so that a thread may hold 168
+// registers.  (12 consumers in 16 warps of 128 registers measured 76 us instead of 72 on the
+// long-context case and 79 instead of 73 on the ragged one.)
+constexpr int kConsumers = 8, kConverters = 3;
+constexpr int kThreads = (kConsumers + 1 + kConverters) * 32;
+constexpr int kMaxWalkers = 12;   // warps of a CTA at most
 constexpr float kLazy = 8.0f;     // maxima are raised when exceeded by this much (log2 units)
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -101,6 +102,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // Scale of a block: 2^(e - 127); NaN for byte 255, zero for 0 (a cleared row).
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e == 255 ? 0x7fc00000u : e << 23); }
 
+// Byte i of x as a scale, NaN blocks apart.
+__device__ __forceinline__ float byte_scale(uint32_t x, int i) {
+    return __uint_as_float(__byte_perm(x, 0u, 0x0444 | (i << 12)) >> 1);
+}
+
 // try_wait that may sleep in hardware for some microseconds before it reports failure: a waiting warp
 // then takes few issue slots from the others.
 __device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
@@ -111,6 +117,12 @@ __device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
         : "r"(bar), "r"(parity), "r"(20000u)
         : "memory");
     return ok != 0;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Bounded wait of a whole warp; false (with the abort flag set) once it, or any other, gave up.
@@ -132,9 +144,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 struct QuantPlan {
     int nt;                      // tiles of 8 heads per consumer warp
     int nwh, ng;                 // consumer warps over the heads, groups
-    int ncv;                     // converter warps
     int st;                      // tiles (of TOK tokens) per stage
-    int nslot, ncb;              // stages of the ring, widened tiles
+    int nslot, ncb;              // stages of the ring, widened tiles (one or two per group)
     int stage_bytes, cb_bytes;
     int threads, smem_bytes;
 };
@@ -159,20 +170,20 @@ static_assert(sizeof(Walker) == 48, "walkers are an array in shared memory with 
 // pairs and eight columns of a warp's store fall on different banks.
 __host__ __device__ constexpr int merge_stride(int W) { return W % 16 == 0 ? W + 4 : W + 12; }
 
-// Row stride (bytes) of a widened tile [s^K | s^V] in bf16: an odd number of 16-byte units.
-__host__ __device__ constexpr int cb_stride(int D_K, int D_H) { return (D_K + D_H) * 2 + 16; }
+// Row stride (bytes) of a widened tile of s^V in bf16: an odd number of 16-byte units.
+__host__ __device__ constexpr int cb_stride(int D_H) { return D_H * 2 + 16; }
 
 template <int D_H, int R, int D_R, int NT, int TOK>
-__global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan_kernel(const QuantScanArgs args) {
+__global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScanArgs args) {
     constexpr int D_K = D_H + D_R, W = D_H + R, WS = merge_stride(W);
-    constexpr int SB = cb_stride(D_K, D_H);
+    constexpr int SB = cb_stride(D_H);
     constexpr int NKK = D_K / 16;
     constexpr int NZC = R > 16 ? R / 16 : 1;       // 16-byte chunks of a head's latents (r = 8: of two heads')
     constexpr int NCH = 8 * R / 16;                // chunks of a tile of 8 heads
     constexpr int TPP = kBlockSize / TOK;          // tiles per page
     using WorkQ = WorkT<TOK>;
     static_assert(sizeof(WorkQ) <= 96 && alignof(WorkQ) <= 16, "room for the plan in shared memory");
-    static_assert(kThreads1 <= 32 * kMaxWalkers && kThreads2 <= 32 * kMaxWalkers, "walkers");
+    static_assert(kThreads <= 32 * kMaxWalkers, "walkers");
     const DecodeArgs& a = args.a.d;
     const QuantLayout& ql = args.a.q;
     const QuantPlan& p = args.p;
@@ -187,11 +198,11 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
     const uint32_t ring = smem_u32(smem);
     const uint32_t cbuf = ring + nslot * p.stage_bytes;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + nslot * p.stage_bytes + ncb * p.cb_bytes);
-    uint64_t* full = bars;
-    uint64_t* empty = full + nslot;
-    uint64_t* cfull = empty + nslot;
-    uint64_t* cempty = cfull + ncb;
-    uint64_t* merged = cempty + ncb;
+    uint64_t* full = bars;               // a stage's rows have landed
+    uint64_t* empty = full + nslot;      // every warp is done with the stage
+    uint64_t* vfull = empty + nslot;     // a tile's s^V widened
+    uint64_t* vempty = vfull + ncb;      // and read by its group
+    uint64_t* merged = vempty + ncb;
     int* meta = reinterpret_cast<int*>(merged + 2);
     volatile int* abort_flag = meta + nslot;
     int* slc = meta + ((nslot + 1 + 3) & ~3);
@@ -201,11 +212,11 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
     if (threadIdx.x == 0) {
         for (int i = 0; i < nslot; ++i) {
             mbar_init(smem_u32(full + i), 1);
-            mbar_init(smem_u32(empty + i), NCW + p.ncv);
+            mbar_init(smem_u32(empty + i), NCW + kConverters);
         }
         for (int i = 0; i < ncb; ++i) {
-            mbar_init(smem_u32(cfull + i), p.ncv);
-            mbar_init(smem_u32(cempty + i), p.nwh);
+            mbar_init(smem_u32(vfull + i), kConverters);
+            mbar_init(smem_u32(vempty + i), p.nwh);
         }
         mbar_init(smem_u32(merged), NCW);
         *abort_flag = 0;
@@ -227,14 +238,16 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
     }
     __syncwarp();
 
-    // Tile indices below count the CTA's tiles from its first (u) and its stages (k), alike in all
-    // warps.  Every consumer and converter waits for and releases every stage in turn (not only those
-    // with a tile of its own), and a widened tile's slot always belongs to the same group and converter
-    // (ncb is a multiple of both counts), so nobody can miss a round of a barrier or take one for another.
+    // All roles walk the same tiles in the same order.  Tile u (counted over the CTA) belongs to group
+    // u mod ng and is widened into that group's buffer; every consumer and converter waits for and
+    // releases every stage in turn, also those without a tile of its own, so nobody can miss a round of
+    // a barrier or take one for another.  Ring positions and phases are counted along (a division by
+    // a run-time count costs as much as a chunk's product).
     if (warp == NCW) {
         // ---------------------------------------------------------------- producer
         const uint64_t pol = policy_evict_first();
-        int k = 0, segs = 0, issued = 0;
+        int slot = 0, issued = 0, segs = 0;
+        uint32_t phase = 1;  // parity of the round before this one of a slot's `empty`
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1;
             if (lane == 0 && g0 == 0) {
@@ -250,34 +263,41 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
             const int32_t* bt = a.block_table + (size_t)b * a.max_pages;
             const int last_page = (g1 - 1) / TPP;
             int page0 = g0 / TPP, ids = page0 + lane <= last_page ? bt[page0 + lane] : -1;
-            for (int s = g0 / ST; s <= (g1 - 1) / ST; ++s, ++k) {
-                const int slot = k % nslot;
-                const int f = max(g0, s * ST), e = min(g1, (s + 1) * ST);
+            for (int f = g0; f < g1;) {
+                const int e = min(g1, (f | (ST - 1)) + 1);  // stages are aligned in the sequence
                 const int page = f / TPP;
                 if (page - page0 >= 32) {
                     page0 = page;
                     ids = page0 + lane <= last_page ? bt[page0 + lane] : -1;
                 }
                 const int blk = __shfl_sync(0xffffffffu, ids, page - page0);
-                if (ok && k >= nslot)
-                    ok = warp_wait(smem_u32(empty + slot), (k / nslot - 1) & 1, abort_flag, a.status, a.wait_ns);
+                if (ok && issued >= nslot)
+                    ok = warp_wait(smem_u32(empty + slot), phase, abort_flag, a.status, a.wait_ns);
                 ok = ok && !__any_sync(0xffffffffu, *abort_flag != 0);
-                if (ok && lane == 0) {
-                    if (blk < 0 || blk >= a.num_blocks) {
-                        set_status(a.status, LRKV_DEV_BAD_BLOCK);
-                        meta[slot] = 0;
-                        mbar_arrive(smem_u32(full + slot));
-                    } else {
-                        meta[slot] = 1;
-                        const uint32_t bytes = (uint32_t)(e - f) * TOK * RB;
-                        mbar_arrive_expect_tx(smem_u32(full + slot), bytes);
-                        bulk_load_hint(ring + slot * p.stage_bytes + (f - s * ST) * TOK * RB,
-                                       args.a.rows + ((size_t)blk * kBlockSize + (f % TPP) * TOK) * RB, bytes,
-                                       smem_u32(full + slot), pol);
+                if (ok) {
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(full + slot);
+                        if (blk < 0 || blk >= a.num_blocks) {
+                            set_status(a.status, LRKV_DEV_BAD_BLOCK);
+                            meta[slot] = 0;
+                            mbar_arrive(bar);
+                        } else {
+                            meta[slot] = 1;
+                            const uint32_t bytes = (uint32_t)(e - f) * TOK * RB;
+                            mbar_arrive_expect_tx(bar, bytes);
+                            bulk_load_hint(ring + slot * p.stage_bytes,
+                                           args.a.rows + ((size_t)blk * kBlockSize + (f % TPP) * TOK) * RB, bytes, bar,
+                                           pol);
+                        }
+                    }
+                    ++issued;
+                    if (++slot == nslot) {
+                        slot = 0;
+                        phase ^= 1;
                     }
                 }
-                if (ok) issued = k + 1;
                 __syncwarp();
+                f = e;
             }
             ++segs;
             if (lane == 0) wk.advance(*work);
@@ -290,31 +310,33 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
     } else if (warp > NCW) {
         // ---------------------------------------------------------------- converters
         const int cv = warp - NCW - 1;
-        constexpr int U = (D_K + D_H) / 8;  // 8-value units of a row
-        int k = 0, u = 0;
+        int slot = 0, cb = 0, tiles = 0;
+        uint32_t phase = 0, cphase = 1;
+        constexpr int U = D_H / 8;  // 8-value units of a row's s^V
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1;
             const int L = b < kSeqCache ? slc[b] : a.seq_lens[b];
-            for (int s = g0 / ST; s <= (g1 - 1) / ST; ++s, ++k) {
-                const int slot = k % nslot;
-                bool ok = warp_wait(smem_u32(full + slot), (k / nslot) & 1, abort_flag, a.status, a.wait_ns);
-                const int f = max(g0, s * ST), e = min(g1, (s + 1) * ST);
-                for (int t = f; t < e; ++t, ++u) {
-                    const int cb = u % ncb;
-                    if (ok && u >= ncb)
-                        ok = warp_wait(smem_u32(cempty + cb), (u / ncb - 1) & 1, abort_flag, a.status, a.wait_ns);
-                    if (!ok) continue;
-                    if (meta[slot]) {
-                        const int nvalid = min(TOK, L - t * TOK);
-                        const uint32_t src = ring + slot * p.stage_bytes + (t - s * ST) * TOK * RB;
-                        const uint32_t dst = cbuf + cb * p.cb_bytes;
-#pragma unroll 4
-                        for (int i = cv * 32 + lane; i < TOK * U; i += p.ncv * 32) {
+            for (int f = g0; f < g1;) {
+                const int e = min(g1, (f | (ST - 1)) + 1);
+                bool ok = warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
+                const int have = meta[slot];
+                uint32_t src = ring + slot * p.stage_bytes;
+                for (int t = f; t < e; ++t, src += TOK * RB) {
+                    const uint32_t dst = cbuf + cb * p.cb_bytes;
+                    const int nvalid = min(TOK, L - t * TOK);
+                    if (ok && tiles >= ncb) ok = warp_wait(smem_u32(vempty + cb), cphase, abort_flag, a.status, a.wait_ns);
+                    if (ok && have) {
+#pragma unroll
+                        for (int i0 = 0; i0 < TOK * U; i0 += kConverters * 32) {
+                            const int i = i0 + cv * 32 + lane;
+                            if ((TOK * U) % (kConverters * 32) != 0 && i >= TOK * U) continue;
                             const int row = i / U, c = i - row * U;
                             const uint32_t ra = src + row * RB;
                             uint32_t x[2], o[4];
-                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(ra + c * 8));
-                            const uint32_t sb = lds8(ra + ql.off_sc + (c >> 2));
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                         : "=r"(x[0]), "=r"(x[1])
+                                         : "r"(ra + D_K + c * 8));
+                            const uint32_t sb = lds8(ra + ql.off_sc + D_K / kQuantBlock + (c >> 2));
                             // the scale twice in bf16 (NaN for byte 255); zero for tokens behind the end (their
                             // probabilities are 0, and 0 x NaN is not)
                             uint32_t s2 = sb == 255 ? 0x7fc07fc0u : sb * 0x00800080u;
@@ -329,10 +351,19 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(cfull + cb));
+                    if (lane == 0 && ok) mbar_arrive(smem_u32(vfull + cb));
+                    ++tiles;
+                    if (++cb == ncb) {
+                        cb = 0;
+                        cphase ^= 1;
+                    }
                 }
-                __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(empty + slot));
+                if (++slot == nslot) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                f = e;
             }
             __syncwarp();
             if (lane == 0) wk.advance(*work);
@@ -344,32 +375,52 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
         const int h0 = wh * NT * 8;                  // first head of this warp
         const int g = lane >> 2, tq = lane & 3;
         const int nct = NCW * 32;
-        const int g8 = TOK == 16 ? g + 8 : g;        // rows 8..15 of a tile of 8 tokens: masked copies of 0..7
-        const int zc0 = h0 * R / 16;                 // this warp's first 16-byte chunk of a row's latents
+        const int g8 = TOK == 16 ? 8 * RB : 0;       // rows 8..15 of a tile of 8 tokens: masked copies of 0..7
+        // Offsets of this lane's bytes in a tile of rows: latents of token g for the logits, of token
+        // lane mod 16 for the values (transposed loads), scale bytes of heads 2 tq, 2 tq + 1.
+        const int zk_off = g * RB + ql.off_zK + h0 * R + tq * 4;
+        const int zv_off = (TOK == 16 ? lane & 15 : lane & 7) * RB + ql.off_zV + h0 * R + (lane >> 4) * 16;
+        int sc_off[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                sc_off[nt][e] = g * RB + ql.off_sc + ql.nb_sK + ql.nb_sV +
+                                min(((h0 + nt * 8 + 2 * tq + e) * R) / kQuantBlock, ql.nb_z - 1);
+        constexpr int NSE = R == 32 ? 2 : 1;         // scales of the two heads (r <= 16: one block for both)
+        const int sk_off = g * RB + tq * 4;          // s^K bytes of token g
+        const int cv_off = (TOK == 16 ? (lane & 7) + ((lane >> 4) << 3) : lane & 7) * SB + ((lane >> 3) & 1) * 16;
         pdl_wait();  // q~ written by the absorb kernel
-        int k = 0, u = 0;
+        int slot = 0, until = grp;  // until: tiles before this group's next
+        int cb = grp;               // and its widened tile
+        uint32_t phase = 0, cphase = 0;
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1, pslot = wk.slot;
             const int L = b < kSeqCache ? slc[b] : a.seq_lens[b];
-            // Queries as B fragments (features x heads, head h0 + 8 nt + g in this lane's column)
+            // Queries and q~ as B fragments (features x heads, head h0 + 8 nt + g in this lane's column),
+            // fp16, both divided by the power of two that brings the head's largest magnitude into [1, 2).
+            // This lane holds features 4 tq .. 4 tq + 3 of each chunk of 16 (the order of the A fragments).
             uint32_t qb[NKK][NT][2];
             uint32_t qz[NZC][NT][2];
             float ci[NT][2];  // start of the latent logits' sums
-            float fz[NT][2];  // power of two that q~ was divided by, for heads 2 tq, 2 tq + 1 of each tile
+            float fz[NT][2];  // the power of two times the softmax scale, for heads 2 tq, 2 tq + 1 of each tile
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int h = h0 + nt * 8 + g;
                 const bool live = h < H;
-                const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + ((size_t)b * H + (live ? h : 0)) * D_K);
+                const uint16_t* q = a.q + ((size_t)b * H + (live ? h : 0)) * D_K + tq * 4;
+                float mx = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < NKK; ++kk) {
-                    qb[kk][nt][0] = live ? q[kk * 8 + tq] : 0u;
-                    qb[kk][nt][1] = live ? q[kk * 8 + 4 + tq] : 0u;
+                    const uint2 x = *reinterpret_cast<const uint2*>(q + kk * 16);
+                    qb[kk][nt][0] = live ? x.x : 0u;
+                    qb[kk][nt][1] = live ? x.y : 0u;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qb[kk][nt][i])), fabsf(bf16hi(qb[kk][nt][i]))));
                 }
-                // q~: this lane holds features 4 tq .. 4 tq + 3 of each chunk (the A fragments' order), scaled
-                // by the power of two that brings the head's largest magnitude into [1, 2)
                 const float* qt = a.qt + ((size_t)b * H + (live ? h : 0)) * R;
-                float v[NZC][4], mx = 0.f;
+                float v[NZC][4];
 #pragma unroll
                 for (int c = 0; c < NZC; ++c) {
                     const int f0 = R == 8 ? (tq * 4) & 7 : c * 16 + tq * 4;
@@ -388,13 +439,11 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
                 const float inv = __uint_as_float((254u - ex) << 23);
                 const float fac = __uint_as_float(ex << 23);
 #pragma unroll
-                for (int c = 0; c < NZC; ++c) {
-                    qz[c][nt][0] = pack_f16x2(v[c][0] * inv, v[c][1] * inv);
-                    qz[c][nt][1] = pack_f16x2(v[c][2] * inv, v[c][3] * inv);
-                }
-                fz[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * tq);
-                fz[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * tq + 4);
-                // the products take 1152 + q for q: the sums start from -1152 sum q~ (as rounded).  (Against
+                for (int kk = 0; kk < NKK; ++kk)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qb[kk][nt][i] = pack_f16x2(bf16lo(qb[kk][nt][i]) * inv, bf16hi(qb[kk][nt][i]) * inv);
+                // The products take 1152 + q for q: the sums start from -1152 sum q~ (as rounded).  (Against
                 // a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of it, more than
                 // q~ has.)
                 float sum = 0.f;
@@ -402,13 +451,17 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
                 for (int c = 0; c < NZC; ++c)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
+                        qz[c][nt][i] = pack_f16x2(v[c][2 * i] * inv, v[c][2 * i + 1] * inv);
                         const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qz[c][nt][i]));
                         sum += x.x + x.y;
                     }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                ci[nt][0] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq);
-                ci[nt][1] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq + 4);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    fz[nt][e] = __shfl_sync(0xffffffffu, fac, 8 * tq + 4 * e) * a.scale_log2;
+                    ci[nt][e] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq + 4 * e);
+                }
             }
             float o[D_H / 16][NT][4], oz[NZC][NT][4];
             float m[NT][2], mz[NT][2], l[NT][2];
@@ -424,95 +477,117 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
                     l[nt][e] = 0.f;
                 }
             }
-            for (int s = g0 / ST; s <= (g1 - 1) / ST; ++s, ++k) {
-                const int slot = k % nslot;
-                bool ok = warp_wait(smem_u32(full + slot), (k / nslot) & 1, abort_flag, a.status, a.wait_ns);
-                const int f = max(g0, s * ST), e1 = min(g1, (s + 1) * ST);
+            for (int f = g0; f < g1;) {
+                const int e1 = min(g1, (f | (ST - 1)) + 1);
+                bool ok = warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
                 const int have = meta[slot];
+                const uint32_t stage = ring + slot * p.stage_bytes;
 #pragma unroll 1
-                for (int t = f; t < e1; ++t, ++u) {
-                    if (u % p.ng != grp) continue;
-                    const int cb = u % ncb;
-                    if (ok) ok = warp_wait(smem_u32(cfull + cb), (u / ncb) & 1, abort_flag, a.status, a.wait_ns);
-                    if (!ok) continue;
-                    if (have) {
-                        const int nvalid = min(TOK, L - t * TOK);
-                        const uint32_t row0 = ring + slot * p.stage_bytes + (t - s * ST) * TOK * RB;
-                        const uint32_t cv = cbuf + cb * p.cb_bytes;
-                        const bool in0 = g < nvalid, in1 = TOK == 16 && g + 8 < nvalid;
-
-                        // --- shared logits [q | q^R] . [s^K | k^R]: 16 tokens x 8 heads
-                        float c[NT][4], cz[NT][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) c[nt][i] = cz[nt][i] = 0.f;  // (every cz is set below)
-                        {
-                            const int r16 = TOK == 16 ? lane & 15 : lane & 7;
-                            const uint32_t ad = cv + r16 * SB + (lane >> 4) * 16;
-#pragma unroll
-                            for (int kk = 0; kk < NKK; ++kk) {
-                                uint32_t af[4];
-                                ldmatrix_x4(ad + kk * 32, af[0], af[1], af[2], af[3]);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) mma_16816(c[nt], af, qb[kk][nt][0], qb[kk][nt][1]);
-                            }
+                for (; until < e1 - f; until += p.ng) {
+                    const uint32_t row0 = stage + until * TOK * RB;
+                    const int nvalid = L - (f + until) * TOK;
+                    const bool in0 = g < nvalid, in1 = TOK == 16 && g + 8 < nvalid;
+                    bool nan0 = false, nan1 = false;  // a block of s^K is a NaN block (tokens g, g + 8)
+                    float c[NT][4];
+                    if (ok && have) {
+                        // --- shared logits [q | q^R] . [s^K | k^R], block by block of 32 features: 16 tokens x 8
+                        // heads; the offset leaves by a product with a constant A
+                        constexpr int NBK = D_K / kQuantBlock;
+                        uint32_t sc0[2], sc1[2];  // scale bytes of the blocks
+                        sc0[0] = lds32(row0 + g * RB + ql.off_sc);
+                        sc1[0] = lds32(row0 + g * RB + g8 + ql.off_sc);
+                        if (NBK > 4) {
+                            sc0[1] = lds32(row0 + g * RB + ql.off_sc + 4);
+                            sc1[1] = lds32(row0 + g * RB + g8 + ql.off_sc + 4);
                         }
-                        // --- latent logits q~ . z^K, chunk by chunk of 16 bytes: of a product with all eight
-                        // heads' q~ only the columns of the chunk's own head (r = 8: two heads) are kept.  (Heads
-                        // past the last read whatever follows in shared memory: finite, and never stored.)
-                        {
-                            const uint32_t z0 = row0 + g * RB + ql.off_zK + zc0 * 16 + tq * 4;
-                            const uint32_t z1 = row0 + g8 * RB + ql.off_zK + zc0 * 16 + tq * 4;
+#pragma unroll
+                        for (int i = 0; i < (NBK + 3) / 4; ++i) {
+                            constexpr uint32_t mask = NBK % 4 == 0 ? 0x80808080u : 0x00008080u;  // (64, 192: two blocks)
+                            const uint32_t mk = i == NBK / 4 || NBK < 4 ? mask : 0x80808080u;
+                            nan0 |= ((~sc0[i] - 0x01010101u) & sc0[i] & mk) != 0;  // a byte is 255
+                            nan1 |= ((~sc1[i] - 0x01010101u) & sc1[i] & mk) != 0;
+                        }
+#pragma unroll
+                        for (int bl = 0; bl < NBK; ++bl) {
+                            float d[NT][4];
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+#pragma unroll
+                            for (int kk = 2 * bl; kk < 2 * bl + 2; ++kk) {
+                                const uint32_t x0 = lds32(row0 + sk_off + kk * 16);
+                                const uint32_t x1 = lds32(row0 + sk_off + g8 + kk * 16);
+                                const uint32_t a0 = bytes_f16(x0, 0x4140), a1 = bytes_f16(x1, 0x4140),
+                                               a2 = bytes_f16(x0, 0x4342), a3 = bytes_f16(x1, 0x4342);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma_16816_f16(d[nt], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
+                                                  qb[kk][nt][0], qb[kk][nt][1]);
+                                    mma_16816_f16(d[nt], a0, a1, a2, a3, qb[kk][nt][0], qb[kk][nt][1]);
+                                }
+                            }
+                            const float f0 = byte_scale(sc0[bl >> 2], bl & 3), f1 = byte_scale(sc1[bl >> 2], bl & 3);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int j = 0; j < NCH / NZC; ++j) {
-                                    float d[4] = {ci[nt][0], ci[nt][1], ci[nt][0], ci[nt][1]};
-#pragma unroll
-                                    for (int zc = 0; zc < NZC; ++zc) {
-                                        const int at = (nt * NCH + j * NZC + zc) * 16;
-                                        const uint32_t x0 = lds32(z0 + at), x1 = lds32(z1 + at);
-                                        mma_16816_f16(d, bytes_f16(x0, 0x4140), bytes_f16(x1, 0x4140),
-                                                      bytes_f16(x0, 0x4342), bytes_f16(x1, 0x4342), qz[zc][nt][0],
-                                                      qz[zc][nt][1]);
-                                    }
-                                    if (tq == (R == 8 ? j : j >> 1)) {
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i)
-                                            if (R == 8 || (i & 1) == (j & 1)) cz[nt][i] = d[i];
-                                    }
-                                }
+                                for (int i = 0; i < 4; ++i)
+                                    c[nt][i] = bl == 0 ? d[nt][i] * (i < 2 ? f0 : f1) : fmaf(d[nt][i], i < 2 ? f0 : f1, c[nt][i]);
                         }
-                        // --- logits s (log2 units) and s + k of the z^V scales; element i: token g (+ 8 for
-                        // i >= 2), head 2 tq + (i & 1)
-                        float sv[NT][4], sw[NT][4];
-                        bool raise = false;
+                    }
+                    if (ok) ok = warp_wait(smem_u32(vfull + cb), cphase, abort_flag, a.status, a.wait_ns);
+                    const uint32_t cvv = cbuf + cb * p.cb_bytes + cv_off;
+                    if (ok && have) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt) {
+                            // --- latent logits q~ . z^K, chunk by chunk of 16 bytes: of a product with all eight
+                            // heads' q~ only the columns of the chunk's own head (r = 8: two heads) are kept.
+                            // (Heads past the last read whatever follows in shared memory: finite, never stored.)
+                            float cz[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int j = 0; j < NCH / NZC; ++j) {
+                                float d[4] = {ci[nt][0], ci[nt][1], ci[nt][0], ci[nt][1]};
+#pragma unroll
+                                for (int zc = 0; zc < NZC; ++zc) {
+                                    const uint32_t at = row0 + zk_off + (nt * NCH + j * NZC + zc) * 16;
+                                    const uint32_t x0 = lds32(at), x1 = lds32(at + g8);
+                                    mma_16816_f16(d, bytes_f16(x0, 0x4140), bytes_f16(x1, 0x4140), bytes_f16(x0, 0x4342),
+                                                  bytes_f16(x1, 0x4342), qz[zc][nt][0], qz[zc][nt][1]);
+                                }
+                                const bool mine = tq == (R == 8 ? j : j >> 1);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (R == 8 || (i & 1) == (j & 1)) cz[i] = mine ? d[i] : cz[i];
+                            }
+                            // --- logits s (log2 units) and s + k, 2^k the scale of z^V; element i: token g (+ 8 for
+                            // i >= 2), head 2 tq + (i & 1)
+                            float sv[4], sw[4], ks[2][2], kv[2][2];
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                                for (int e = 0; e < NSE; ++e) {
+                                    const uint32_t sa = row0 + sc_off[nt][e] + hf * g8;
+                                    const uint32_t kb = lds8(sa);
+                                    ks[hf][e] = scale_of((hf ? nan1 : nan0) ? 255u : kb);
+                                    // log2 of the scale: -infinity of a cleared row, +infinity of a NaN block, whose
+                                    // weight then becomes infinity - infinity
+                                    kv[hf][e] = lg2_approx(__uint_as_float(lds8(sa + ql.nb_z) << 23));
+                                }
+                            float over = -INFINITY;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int e = i & 1;
-                                const int blk = min(((h0 + nt * 8 + 2 * tq + e) * R) / kQuantBlock, ql.nb_z - 1);
-                                const uint32_t sa = row0 + (i < 2 ? g : g8) * RB + ql.off_sc + ql.nb_sK + ql.nb_sV + blk;
-                                const uint32_t bk = lds8(sa), bv = lds8(sa + ql.nb_z);
-                                const float s =
-                                    fmaf(cz[nt][i] * fz[nt][e], scale_of(bk), c[nt][i]) * a.scale_log2;
-                                // exponent of the scale: a NaN block's is NaN, a cleared row's -infinity
-                                const float ke = bv == 255 ? __uint_as_float(0x7fc00000u)
-                                                           : bv == 0 ? -INFINITY : (float)((int)bv - 127);
-                                const bool in = i < 2 ? in0 : in1;
-                                sv[nt][i] = in ? s : -INFINITY;
-                                sw[nt][i] = in ? s + ke : -INFINITY;
-                                raise |= sv[nt][i] > m[nt][e] + kLazy || sw[nt][i] > mz[nt][e] + kLazy;
+                                const int e = i & 1, es = e & (NSE - 1), hf = i >> 1;
+                                const float s = fmaf(cz[i], ks[hf][es], c[nt][i]) * fz[nt][e];
+                                const bool in = hf ? in1 : in0;
+                                sv[i] = in ? s : -INFINITY;
+                                sw[i] = in ? s + kv[hf][es] : -INFINITY;
+                                over = fmaxf(over, fmaxf(sv[i] - m[nt][e], sw[i] - mz[nt][e]));
                             }
-                        // maxima are the same in the eight lanes that share two heads, and raised together
-                        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            // Maxima are the same in the eight lanes that share two heads, and raised together,
+                            // by all heads of the tile, once some logit lies more than 2^8 above.  (At the start
+                            // they are -infinity; -infinity - -infinity is a NaN, which fmaxf passes over.)
+                            if (__any_sync(0xffffffffu, over > kLazy)) {
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    float x = fmaxf(sv[nt][e], sv[nt][2 + e]), y = fmaxf(sw[nt][e], sw[nt][2 + e]);
+                                    float x = fmaxf(sv[e], sv[2 + e]), y = fmaxf(sw[e], sw[2 + e]);
 #pragma unroll
                                     for (int d = 4; d < 32; d <<= 1) {
                                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -536,75 +611,70 @@ __global__ void __launch_bounds__(NT == 1 ? kThreads1 : kThreads2, 1) quant_scan
                                         oz[i][nt][2 + e] *= az;
                                     }
                                 }
-                        }
-                        // --- p = 2^(s - m) and w = 2^(s + k - mz), transposed into B fragments
-                        uint32_t pb[NT][2], wb[NT][2];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                            }
+                            // --- p = 2^(s - m) and w = 2^(s + k - mz), transposed into B fragments
                             float pp[4], ww[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int e = i & 1;
                                 const bool in = i < 2 ? in0 : in1;
-                                pp[i] = in ? ex2_approx(sv[nt][i] - m[nt][e]) : 0.f;
-                                // (mz is -infinity as long as every block of the head was all zeros)
-                                ww[i] = in && sw[nt][i] != -INFINITY ? ex2_approx(sw[nt][i] - mz[nt][e]) : 0.f;
+                                pp[i] = in ? ex2_approx(sv[i] - m[nt][e]) : 0.f;
+                                // (mz is -infinity as long as every row of the block was a cleared one)
+                                ww[i] = sw[i] == -INFINITY ? 0.f : ex2_approx(sw[i] - mz[nt][e]);
                             }
                             l[nt][0] += pp[0] + pp[2];
                             l[nt][1] += pp[1] + pp[3];
-                            pb[nt][0] = movmatrix_trans(pack_bf16x2(pp[0], pp[1]));
-                            pb[nt][1] = movmatrix_trans(pack_bf16x2(pp[2], pp[3]));
-                            wb[nt][0] = movmatrix_trans(pack_f16x2(ww[0], ww[1]));
-                            wb[nt][1] = movmatrix_trans(pack_f16x2(ww[2], ww[3]));
-                        }
-                        // --- shared values: O^T (d x heads) += s^V^T . P
-                        {
-                            const int r16 = TOK == 16 ? (lane & 7) + ((lane >> 4) << 3) : lane & 7;
-                            const uint32_t ad = cv + r16 * SB + D_K * 2 + ((lane >> 3) & 1) * 16;
+                            const uint32_t pb0 = movmatrix_trans(pack_bf16x2(pp[0], pp[1]));
+                            const uint32_t pb1 = movmatrix_trans(pack_bf16x2(pp[2], pp[3]));
+                            const uint32_t wb0 = movmatrix_trans(pack_f16x2(ww[0], ww[1]));
+                            const uint32_t wb1 = movmatrix_trans(pack_f16x2(ww[2], ww[3]));
+                            // --- shared values: O^T (d x heads) += s^V^T . P
 #pragma unroll
                             for (int i = 0; i < D_H / 16; ++i) {
                                 uint32_t af[4];
-                                ldmatrix_x4_trans(ad + i * 32, af[0], af[1], af[2], af[3]);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) mma_16816(o[i][nt], af, pb[nt][0], pb[nt][1]);
+                                ldmatrix_x4_trans(cvv + i * 32, af[0], af[1], af[2], af[3]);
+                                mma_16816(o[i][nt], af, pb0, pb1);
                             }
-                        }
-                        // --- latent values, two 16-byte chunks at a time: rows of the transposed 16-bit
-                        // elements are pairs of features, row g of A takes the even one, row g + 8 the odd one
-                        {
-                            const int r16 = TOK == 16 ? lane & 15 : lane & 7;
-                            const uint32_t zr = row0 + r16 * RB + ql.off_zV + (zc0 + (lane >> 4)) * 16;
+                            // --- latent values, two 16-byte chunks at a time: rows of the transposed 16-bit
+                            // elements are pairs of features, row g of A takes the even one, row g + 8 the odd
+                            // one.  The offset 1152 of the bytes' products is taken off tile by tile (so that the
+                            // sums never grow with it).
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                // the offset 1152 of the bytes' products, taken off tile by tile (so that the
-                                // sums never grow with it)
+                            for (int zc = 0; zc < NZC; ++zc)
+                                mma_16816_f16(oz[zc][nt], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2, wb0,
+                                              wb1);
 #pragma unroll
-                                for (int zc = 0; zc < NZC; ++zc)
-                                    mma_16816_f16(oz[zc][nt], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
-                                                  wb[nt][0], wb[nt][1]);
+                            for (int c2 = 0; c2 < NCH; c2 += 2) {
+                                uint32_t x[4];
+                                ldmatrix_x4_trans(row0 + zv_off + (nt * NCH + c2) * 16, x[0], x[1], x[2], x[3]);
 #pragma unroll
-                                for (int c2 = 0; c2 < NCH; c2 += 2) {
-                                    uint32_t x[4];
-                                    ldmatrix_x4_trans(zr + (nt * NCH + c2) * 16, x[0], x[1], x[2], x[3]);
-#pragma unroll
-                                    for (int w = 0; w < 2; ++w) {
-                                        const int ch = c2 + w;
-                                        const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
-                                        const int zc = R == 32 ? ch & 1 : 0;
-                                        mma_16816_f16(oz[zc][nt], bytes_f16(x[2 * w], 0x4240),
-                                                      bytes_f16(x[2 * w], 0x4341), bytes_f16(x[2 * w + 1], 0x4240),
-                                                      bytes_f16(x[2 * w + 1], 0x4341), mine ? wb[nt][0] : 0u,
-                                                      mine ? wb[nt][1] : 0u);
-                                    }
+                                for (int w = 0; w < 2; ++w) {
+                                    const int ch = c2 + w;
+                                    const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
+                                    const int zc = R == 32 ? ch & 1 : 0;
+                                    mma_16816_f16(oz[zc][nt], bytes_f16(x[2 * w], 0x4240), bytes_f16(x[2 * w], 0x4341),
+                                                  bytes_f16(x[2 * w + 1], 0x4240), bytes_f16(x[2 * w + 1], 0x4341),
+                                                  mine ? wb0 : 0u, mine ? wb1 : 0u);
                                 }
                             }
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(cempty + cb));
+                    if (lane == 0 && ok) mbar_arrive(smem_u32(vempty + cb));
+                    cb += p.ng;
+                    if (cb >= ncb) {
+                        cb = grp;
+                        cphase ^= 1;
+                    }
                 }
+                until -= e1 - f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(empty + slot));
+                if (++slot == nslot) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                f = e1;
             }
             // --- this group's state over the segment
 #pragma unroll
@@ -711,14 +781,13 @@ int tile_tokens(int H, int R) { return R == 32 && H > 96 ? 8 : 16; }
 
 template <int D_H, int R, int D_R>
 bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
-    p->nt = H > 8 * kConsumers1 ? 2 : 1;
+    p->nt = H > 8 * kConsumers ? 2 : 1;
     // a row of more than 96 heads of r = 32 is so long that two stages of 16 tokens do not fit
     const int tok = tile_tokens(H, R);
-    const int most = p->nt == 2 ? kConsumers2 : kConsumers1;
-    p->ncv = p->nt == 2 ? kConverters2 : kConverters1;
+    const int most = kConsumers;
     p->nwh = (H + 8 * p->nt - 1) / (8 * p->nt);
     const int ng_most = most / p->nwh > 1 ? most / p->nwh : 1;
-    p->cb_bytes = tok * cb_stride(D_H + D_R, D_H);
+    p->cb_bytes = tok * cb_stride(D_H);
     const int WS = merge_stride(D_H + R);
     const int tile = tok * q.row_bytes;
     // tiles per stage: a copy instruction costs its thread some 60 to 80 ns, so short rows are brought a page
@@ -727,8 +796,8 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
     while (p->st * tok < kBlockSize && p->st * tile * 2 <= 28 << 10) p->st *= 2;
     p->stage_bytes = p->st * tile;
     auto fixed = [&](int nslot, int ncb) {
-        return (2 * nslot + 2 * ncb + 2) * 8 + ((nslot + 1 + 3) & ~3) * 4 + kSeqCache * 4 + kMaxWalkers * (int)sizeof(Walker) +
-               96 + 128;
+        return (2 * nslot + 2 * ncb + 2) * 8 + ((nslot + 1 + 3) & ~3) * 4 + kSeqCache * 4 +
+               kMaxWalkers * (int)sizeof(Walker) + 96 + 128;
     };
     for (int want = 3; want >= 2; --want)          // stages at least
         for (int ng = ng_most; ng >= 1; --ng)
@@ -741,7 +810,7 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
                 p->ng = ng;
                 p->ncb = ncb;
                 p->nslot = nslot;
-                p->threads = (p->nwh * ng + 1 + p->ncv) * 32;
+                p->threads = (p->nwh * ng + 1 + kConverters) * 32;
                 p->smem_bytes = nslot * p->stage_bytes + ncb * p->cb_bytes + fixed(nslot, ncb);
                 return true;
             }
