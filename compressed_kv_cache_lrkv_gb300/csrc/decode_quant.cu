@@ -22,7 +22,7 @@
 //   - s^K enters the logits in the same way, 32 features (a block) at a time; s^V, whose sums over
 //     tokens cannot be scaled afterwards, is widened to bf16 (q_i 2^k is exact) once per 16 tokens
 //     by converter warps.
-// Warps of a CTA: consumers (NT x 8 heads each, NG groups taking 16-token tiles in turn), one
+// Warps of a CTA: consumers (8 heads each, ng groups taking 16-token tiles in turn), one
 // producer (bulk copies of whole rows, which lie contiguous within a page, into a ring of
 // stages), three converters; connected by mbarriers only, so they drift freely.  One CTA per
 // SM; the work is cut as in the bf16 decode (decode_work.cuh).
@@ -38,12 +38,12 @@ namespace lrkv {
 
 namespace {
 
-// Consumer warps at most, and converters: 12 warps with the producer, so that a thread may hold 168
-// registers.  (12 consumers in 16 warps of 128 registers measured 76 us instead of 72 on the
-// long-context case and 79 instead of 73 on the ragged one.)
-constexpr int kConsumers = 8, kConverters = 3;
-constexpr int kThreads = (kConsumers + 1 + kConverters) * 32;
-constexpr int kMaxWalkers = 12;   // warps of a CTA at most
+// Consumer warps at most: 8 (12 warps with the converters and the producer, so that a thread may hold
+// 168 registers) for up to 64 heads, 16 (20 warps, 96 registers) for more.  Measured for 128 heads of
+// r = 16: two tiles of 8 heads per warp in 12 warps 107 us, one in 20 warps 97; for 32 heads of r = 32
+// 16 consumers are slower, as every tile in work holds a stage of the ring: 58 us with 8, 81 with 16.
+constexpr int kConverters = 3;
+constexpr int kMaxWalkers = 20;   // warps of a CTA at most
 constexpr float kLazy = 8.0f;     // maxima are raised when exceeded by this much (log2 units)
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -55,15 +55,14 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 // D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
 __device__ __forceinline__ void mma_16816_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 // Two bytes of x, chosen by sel (0x4140: bytes 0, 1; 0x4342: 2, 3; 0x4240: 0, 2; 0x4341: 1, 3), as
@@ -75,15 +74,12 @@ __device__ __forceinline__ uint32_t bytes_f16(uint32_t x, uint32_t sel) {
 }
 constexpr float kByteOffset = 1152.0f;          // 1024 + u = q + 1152
 constexpr uint32_t kMinusOffset2 = 0xe480e480u;  // fp16 (-1152, -1152)
+// Plain loads from shared memory (the compiler may batch them, but not move them over a wait).
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
+    return *static_cast<const uint32_t*>(__cvta_shared_to_generic(a));
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
+    return *static_cast<const uint8_t*>(__cvta_shared_to_generic(a));
 }
 // Values q_i 2^k of two bytes (b0, b1 of [b0, 0, b1, 0]) as bf16, s2 = (2^k, 2^k): with the low seven
 // bits in its mantissa bf16 holds 128 + u mod 128, from which 256 or, where the byte's top bit is
@@ -128,10 +124,10 @@ __device__ __forceinline__ float lg2_approx(float x) {
 // Bounded wait of a whole warp; false (with the abort flag set) once it, or any other, gave up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
                                           uint64_t limit_ns) {
-    if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
     if (__all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
         if (__all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
         if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) {
             set_status(status, LRKV_DEV_TIMEOUT);
@@ -142,10 +138,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 struct QuantPlan {
-    int nt;                      // tiles of 8 heads per consumer warp
-    int nwh, ng;                 // consumer warps over the heads, groups
+    int cw;                      // consumer warps the kernel is built for
+    int nwh, ng;                 // consumer warps over the heads (8 each), groups
     int st;                      // tiles (of TOK tokens) per stage
-    int nslot, ncb;              // stages of the ring, widened tiles (one or two per group)
+    int own_stages;              // 1: a stage is one tile, and a slot of the ring always the same group's
+    int nslot, ncb;              // stages of the ring, widened tiles (one to three per group)
     int stage_bytes, cb_bytes;
     int threads, smem_bytes;
 };
@@ -173,17 +170,18 @@ __host__ __device__ constexpr int merge_stride(int W) { return W % 16 == 0 ? W +
 // Row stride (bytes) of a widened tile of s^V in bf16: an odd number of 16-byte units.
 __host__ __device__ constexpr int cb_stride(int D_H) { return D_H * 2 + 16; }
 
-template <int D_H, int R, int D_R, int NT, int TOK>
-__global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScanArgs args) {
+template <int D_H, int R, int D_R, int CW, int TOK>
+__global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_kernel(const QuantScanArgs args) {
     constexpr int D_K = D_H + D_R, W = D_H + R, WS = merge_stride(W);
     constexpr int SB = cb_stride(D_H);
     constexpr int NKK = D_K / 16;
     constexpr int NZC = R > 16 ? R / 16 : 1;       // 16-byte chunks of a head's latents (r = 8: of two heads')
     constexpr int NCH = 8 * R / 16;                // chunks of a tile of 8 heads
     constexpr int TPP = kBlockSize / TOK;          // tiles per page
+    constexpr int kUnroll = CW == 8 ? 8 : 4;       // of the loops over chunks (96 registers: 4)
     using WorkQ = WorkT<TOK>;
     static_assert(sizeof(WorkQ) <= 96 && alignof(WorkQ) <= 16, "room for the plan in shared memory");
-    static_assert(kThreads <= 32 * kMaxWalkers, "walkers");
+    static_assert(CW + 1 + kConverters <= kMaxWalkers, "walkers");
     const DecodeArgs& a = args.a.d;
     const QuantLayout& ql = args.a.q;
     const QuantPlan& p = args.p;
@@ -212,10 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
     if (threadIdx.x == 0) {
         for (int i = 0; i < nslot; ++i) {
             mbar_init(smem_u32(full + i), 1);
-            mbar_init(smem_u32(empty + i), NCW + kConverters);
+            mbar_init(smem_u32(empty + i), (p.own_stages ? p.nwh : NCW) + kConverters);
         }
         for (int i = 0; i < ncb; ++i) {
-            mbar_init(smem_u32(vfull + i), kConverters);
+            mbar_init(smem_u32(vfull + i), 1);
             mbar_init(smem_u32(vempty + i), p.nwh);
         }
         mbar_init(smem_u32(merged), NCW);
@@ -239,10 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
     __syncwarp();
 
     // All roles walk the same tiles in the same order.  Tile u (counted over the CTA) belongs to group
-    // u mod ng and is widened into that group's buffer; every consumer and converter waits for and
-    // releases every stage in turn, also those without a tile of its own, so nobody can miss a round of
-    // a barrier or take one for another.  Ring positions and phases are counted along (a division by
-    // a run-time count costs as much as a chunk's product).
+    // u mod ng and is widened into buffer u mod ncb (ncb a multiple of ng), each buffer by one converter.
+    // Every converter waits for and releases every stage in turn, also those without a tile of its own,
+    // and so does every consumer unless each slot of the ring belongs to one group: nobody can then miss
+    // a round of a barrier or take one for another.  Ring positions and phases are counted along (a
+    // division by a run-time count costs as much as a chunk's product).
     if (warp == NCW) {
         // ---------------------------------------------------------------- producer
         const uint64_t pol = policy_evict_first();
@@ -310,9 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
     } else if (warp > NCW) {
         // ---------------------------------------------------------------- converters
         const int cv = warp - NCW - 1;
-        int slot = 0, cb = 0, tiles = 0;
-        uint32_t phase = 0, cphase = 1;
         constexpr int U = D_H / 8;  // 8-value units of a row's s^V
+        int slot = 0, cb = 0;
+        bool first = true;          // the buffers' first round: nothing to wait for
+        uint32_t phase = 0, cphase = 1;
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1;
             const int L = b < kSeqCache ? slc[b] : a.seq_lens[b];
@@ -322,42 +322,43 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
                 const int have = meta[slot];
                 uint32_t src = ring + slot * p.stage_bytes;
                 for (int t = f; t < e; ++t, src += TOK * RB) {
-                    const uint32_t dst = cbuf + cb * p.cb_bytes;
-                    const int nvalid = min(TOK, L - t * TOK);
-                    if (ok && tiles >= ncb) ok = warp_wait(smem_u32(vempty + cb), cphase, abort_flag, a.status, a.wait_ns);
-                    if (ok && have) {
+                    if (cb % kConverters == cv) {
+                        const uint32_t dst = cbuf + cb * p.cb_bytes;
+                        const int nvalid = L - t * TOK;
+                        if (ok && !first) ok = warp_wait(smem_u32(vempty + cb), cphase, abort_flag, a.status, a.wait_ns);
+                        if (ok && have) {
+#pragma unroll 8
+                            for (int i0 = 0; i0 < TOK * U; i0 += 32) {
+                                const int i = i0 + lane;
+                                const int row = i / U, c = i - row * U;
+                                const uint32_t ra = src + row * RB;
+                                uint32_t x[2], o[4];
+                                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                             : "=r"(x[0]), "=r"(x[1])
+                                             : "r"(ra + D_K + c * 8));
+                                const uint32_t sb = lds8(ra + ql.off_sc + D_K / kQuantBlock + (c >> 2));
+                                // the scale twice in bf16 (NaN for byte 255); zero for tokens behind the end
+                                // (their probabilities are 0, and 0 x NaN is not)
+                                uint32_t s2 = sb == 255 ? 0x7fc07fc0u : sb * 0x00800080u;
+                                s2 = row < nvalid ? s2 : 0u;
+                                const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&s2);
 #pragma unroll
-                        for (int i0 = 0; i0 < TOK * U; i0 += kConverters * 32) {
-                            const int i = i0 + cv * 32 + lane;
-                            if ((TOK * U) % (kConverters * 32) != 0 && i >= TOK * U) continue;
-                            const int row = i / U, c = i - row * U;
-                            const uint32_t ra = src + row * RB;
-                            uint32_t x[2], o[4];
-                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                         : "=r"(x[0]), "=r"(x[1])
-                                         : "r"(ra + D_K + c * 8));
-                            const uint32_t sb = lds8(ra + ql.off_sc + D_K / kQuantBlock + (c >> 2));
-                            // the scale twice in bf16 (NaN for byte 255); zero for tokens behind the end (their
-                            // probabilities are 0, and 0 x NaN is not)
-                            uint32_t s2 = sb == 255 ? 0x7fc07fc0u : sb * 0x00800080u;
-                            s2 = row < nvalid ? s2 : 0u;
-                            const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                o[j] = bytes_bf16(__byte_perm(x[j >> 1], 0u, j & 1 ? 0x4342 : 0x4140), sc);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * SB + c * 16),
-                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                         : "memory");
+                                for (int j = 0; j < 4; ++j)
+                                    o[j] = bytes_bf16(__byte_perm(x[j >> 1], 0u, j & 1 ? 0x4342 : 0x4140), sc);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + row * SB + c * 16),
+                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]));
+                            }
                         }
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(smem_u32(vfull + cb));
                     }
-                    __syncwarp();
-                    if (lane == 0 && ok) mbar_arrive(smem_u32(vfull + cb));
-                    ++tiles;
                     if (++cb == ncb) {
                         cb = 0;
                         cphase ^= 1;
+                        first = false;
                     }
                 }
+                __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(empty + slot));
                 if (++slot == nslot) {
                     slot = 0;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
     } else {
         // ---------------------------------------------------------------- consumers
         const int grp = warp / p.nwh, wh = warp - grp * p.nwh;
-        const int h0 = wh * NT * 8;                  // first head of this warp
+        const int h0 = wh * 8;                  // first head of this warp
         const int g = lane >> 2, tq = lane & 3;
         const int nct = NCW * 32;
         const int g8 = TOK == 16 ? 8 * RB : 0;       // rows 8..15 of a tile of 8 tokens: masked copies of 0..7
@@ -380,13 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
         // lane mod 16 for the values (transposed loads), scale bytes of heads 2 tq, 2 tq + 1.
         const int zk_off = g * RB + ql.off_zK + h0 * R + tq * 4;
         const int zv_off = (TOK == 16 ? lane & 15 : lane & 7) * RB + ql.off_zV + h0 * R + (lane >> 4) * 16;
-        int sc_off[NT][2];
+        int sc_off[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                sc_off[nt][e] = g * RB + ql.off_sc + ql.nb_sK + ql.nb_sV +
-                                min(((h0 + nt * 8 + 2 * tq + e) * R) / kQuantBlock, ql.nb_z - 1);
+        for (int e = 0; e < 2; ++e)
+            sc_off[e] = g * RB + ql.off_sc + ql.nb_sK + ql.nb_sV +
+                        min(((h0 + 2 * tq + e) * R) / kQuantBlock, ql.nb_z - 1);
         constexpr int NSE = R == 32 ? 2 : 1;         // scales of the two heads (r <= 16: one block for both)
         const int sk_off = g * RB + tq * 4;          // s^K bytes of token g
         const int cv_off = (TOK == 16 ? (lane & 7) + ((lane >> 4) << 3) : lane & 7) * SB + ((lane >> 3) & 1) * 16;
@@ -397,88 +396,91 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1, pslot = wk.slot;
             const int L = b < kSeqCache ? slc[b] : a.seq_lens[b];
-            // Queries and q~ as B fragments (features x heads, head h0 + 8 nt + g in this lane's column),
+            // Queries and q~ as B fragments (features x heads, head h0 + g in this lane's column),
             // fp16, both divided by the power of two that brings the head's largest magnitude into [1, 2).
             // This lane holds features 4 tq .. 4 tq + 3 of each chunk of 16 (the order of the A fragments).
-            uint32_t qb[NKK][NT][2];
-            uint32_t qz[NZC][NT][2];
-            float ci[NT][2];  // start of the latent logits' sums
-            float fz[NT][2];  // the power of two times the softmax scale, for heads 2 tq, 2 tq + 1 of each tile
+            uint32_t qb[NKK][2];
+            uint32_t qz[NZC][2];
+            float ci[2];  // start of the latent logits' sums
+            float fz[2];  // the power of two times the softmax scale, for heads 2 tq, 2 tq + 1 of each tile
+            const int h = h0 + g;
+            const bool live = h < H;
+            const uint16_t* q = a.q + ((size_t)b * H + (live ? h : 0)) * D_K + tq * 4;
+            float mx = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int h = h0 + nt * 8 + g;
-                const bool live = h < H;
-                const uint16_t* q = a.q + ((size_t)b * H + (live ? h : 0)) * D_K + tq * 4;
-                float mx = 0.f;
+            for (int kk = 0; kk < NKK; ++kk) {
+                const uint2 x = *reinterpret_cast<const uint2*>(q + kk * 16);
+                qb[kk][0] = live ? x.x : 0u;
+                qb[kk][1] = live ? x.y : 0u;
 #pragma unroll
-                for (int kk = 0; kk < NKK; ++kk) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(q + kk * 16);
-                    qb[kk][nt][0] = live ? x.x : 0u;
-                    qb[kk][nt][1] = live ? x.y : 0u;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qb[kk][nt][i])), fabsf(bf16hi(qb[kk][nt][i]))));
-                }
-                const float* qt = a.qt + ((size_t)b * H + (live ? h : 0)) * R;
-                float v[NZC][4];
-#pragma unroll
-                for (int c = 0; c < NZC; ++c) {
-                    const int f0 = R == 8 ? (tq * 4) & 7 : c * 16 + tq * 4;
-                    const float4 x = *reinterpret_cast<const float4*>(qt + f0);
-                    const bool mine = live && (R != 8 || (tq >> 1) == (g & 1));
-                    v[c][0] = mine ? x.x : 0.f;
-                    v[c][1] = mine ? x.y : 0.f;
-                    v[c][2] = mine ? x.z : 0.f;
-                    v[c][3] = mine ? x.w : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[c][i]));
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-                const float inv = __uint_as_float((254u - ex) << 23);
-                const float fac = __uint_as_float(ex << 23);
-#pragma unroll
-                for (int kk = 0; kk < NKK; ++kk)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        qb[kk][nt][i] = pack_f16x2(bf16lo(qb[kk][nt][i]) * inv, bf16hi(qb[kk][nt][i]) * inv);
-                // The products take 1152 + q for q: the sums start from -1152 sum q~ (as rounded).  (Against
-                // a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of it, more than
-                // q~ has.)
-                float sum = 0.f;
-#pragma unroll
-                for (int c = 0; c < NZC; ++c)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        qz[c][nt][i] = pack_f16x2(v[c][2 * i] * inv, v[c][2 * i + 1] * inv);
-                        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qz[c][nt][i]));
-                        sum += x.x + x.y;
-                    }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    fz[nt][e] = __shfl_sync(0xffffffffu, fac, 8 * tq + 4 * e) * a.scale_log2;
-                    ci[nt][e] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq + 4 * e);
-                }
+                for (int i = 0; i < 2; ++i)
+                    mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qb[kk][i])), fabsf(bf16hi(qb[kk][i]))));
             }
-            float o[D_H / 16][NT][4], oz[NZC][NT][4];
-            float m[NT][2], mz[NT][2], l[NT][2];
+            const float* qt = a.qt + ((size_t)b * H + (live ? h : 0)) * R;
+            float v[NZC][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int c = 0; c < NZC; ++c) {
+                const int f0 = R == 8 ? (tq * 4) & 7 : c * 16 + tq * 4;
+                const float4 x = *reinterpret_cast<const float4*>(qt + f0);
+                const bool mine = live && (R != 8 || (tq >> 1) == (g & 1));
+                v[c][0] = mine ? x.x : 0.f;
+                v[c][1] = mine ? x.y : 0.f;
+                v[c][2] = mine ? x.z : 0.f;
+                v[c][3] = mine ? x.w : 0.f;
 #pragma unroll
-                for (int i = 0; i < D_H / 16; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[c][i]));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
+            const float inv = __uint_as_float((254u - ex) << 23);
+            const float fac = __uint_as_float(ex << 23);
 #pragma unroll
-                for (int i = 0; i < NZC; ++i) oz[i][nt][0] = oz[i][nt][1] = oz[i][nt][2] = oz[i][nt][3] = 0.f;
+            for (int kk = 0; kk < NKK; ++kk)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    m[nt][e] = mz[nt][e] = -INFINITY;
-                    l[nt][e] = 0.f;
+                for (int i = 0; i < 2; ++i)
+                    qb[kk][i] = pack_f16x2(bf16lo(qb[kk][i]) * inv, bf16hi(qb[kk][i]) * inv);
+            // The products take 1152 + q for q: the sums start from -1152 sum q~ (as rounded).  (Against
+            // a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of it, more than
+            // q~ has.)
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < NZC; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    qz[c][i] = pack_f16x2(v[c][2 * i] * inv, v[c][2 * i + 1] * inv);
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qz[c][i]));
+                    sum += x.x + x.y;
                 }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                fz[e] = __shfl_sync(0xffffffffu, fac, 8 * tq + 4 * e) * a.scale_log2;
+                ci[e] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq + 4 * e);
+            }
+            float o[D_H / 16][4], oz[NZC][4];
+            float m[2], mz[2], l[2];
+#pragma unroll
+            for (int i = 0; i < D_H / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NZC; ++i) oz[i][0] = oz[i][1] = oz[i][2] = oz[i][3] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m[e] = mz[e] = -INFINITY;
+                l[e] = 0.f;
             }
             for (int f = g0; f < g1;) {
                 const int e1 = min(g1, (f | (ST - 1)) + 1);
+                if (p.own_stages && until > 0) {  // another group's stage
+                    --until;
+                    if (++slot == nslot) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                    ++f;
+                    continue;
+                }
                 bool ok = warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
                 const int have = meta[slot];
                 const uint32_t stage = ring + slot * p.stage_bytes;
@@ -488,8 +490,16 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
                     const int nvalid = L - (f + until) * TOK;
                     const bool in0 = g < nvalid, in1 = TOK == 16 && g + 8 < nvalid;
                     bool nan0 = false, nan1 = false;  // a block of s^K is a NaN block (tokens g, g + 8)
-                    float c[NT][4];
+                    float c[4];
+                    uint32_t kb[2][2], vb[2][2];  // scale bytes of z^K and z^V: token g (+ 8), head 2 tq (+ 1)
                     if (ok && have) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int e = 0; e < NSE; ++e) {
+                                kb[hf][e] = lds8(row0 + sc_off[e] + hf * g8);
+                                vb[hf][e] = lds8(row0 + sc_off[e] + hf * g8 + ql.nb_z);
+                            }
                         // --- shared logits [q | q^R] . [s^K | k^R], block by block of 32 features: 16 tokens x 8
                         // heads; the offset leaves by a product with a constant A
                         constexpr int NBK = D_K / kQuantBlock;
@@ -509,156 +519,145 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
                         }
 #pragma unroll
                         for (int bl = 0; bl < NBK; ++bl) {
-                            float d[NT][4];
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                             for (int kk = 2 * bl; kk < 2 * bl + 2; ++kk) {
                                 const uint32_t x0 = lds32(row0 + sk_off + kk * 16);
                                 const uint32_t x1 = lds32(row0 + sk_off + g8 + kk * 16);
                                 const uint32_t a0 = bytes_f16(x0, 0x4140), a1 = bytes_f16(x1, 0x4140),
                                                a2 = bytes_f16(x0, 0x4342), a3 = bytes_f16(x1, 0x4342);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma_16816_f16(d[nt], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
-                                                  qb[kk][nt][0], qb[kk][nt][1]);
-                                    mma_16816_f16(d[nt], a0, a1, a2, a3, qb[kk][nt][0], qb[kk][nt][1]);
-                                }
+                                mma_16816_f16(d, kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
+                                              qb[kk][0], qb[kk][1]);
+                                mma_16816_f16(d, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
                             }
                             const float f0 = byte_scale(sc0[bl >> 2], bl & 3), f1 = byte_scale(sc1[bl >> 2], bl & 3);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    c[nt][i] = bl == 0 ? d[nt][i] * (i < 2 ? f0 : f1) : fmaf(d[nt][i], i < 2 ? f0 : f1, c[nt][i]);
+                                    c[i] = bl == 0 ? d[i] * (i < 2 ? f0 : f1) : fmaf(d[i], i < 2 ? f0 : f1, c[i]);
                         }
                     }
-                    if (ok) ok = warp_wait(smem_u32(vfull + cb), cphase, abort_flag, a.status, a.wait_ns);
                     const uint32_t cvv = cbuf + cb * p.cb_bytes + cv_off;
                     if (ok && have) {
+                        // --- latent logits q~ . z^K, chunk by chunk of 16 bytes: of a product with all eight
+                        // heads' q~ only the columns of the chunk's own head (r = 8: two heads) are kept.
+                        // (Heads past the last read whatever follows in shared memory: finite, never stored.)
+                        float cz[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll kUnroll
+                        for (int j = 0; j < NCH / NZC; ++j) {
+                            float d[4] = {ci[0], ci[1], ci[0], ci[1]};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            // --- latent logits q~ . z^K, chunk by chunk of 16 bytes: of a product with all eight
-                            // heads' q~ only the columns of the chunk's own head (r = 8: two heads) are kept.
-                            // (Heads past the last read whatever follows in shared memory: finite, never stored.)
-                            float cz[4] = {0.f, 0.f, 0.f, 0.f};
+                            for (int zc = 0; zc < NZC; ++zc) {
+                                const uint32_t at = row0 + zk_off + (j * NZC + zc) * 16;
+                                const uint32_t x0 = lds32(at), x1 = lds32(at + g8);
+                                mma_16816_f16(d, bytes_f16(x0, 0x4140), bytes_f16(x1, 0x4140), bytes_f16(x0, 0x4342),
+                                              bytes_f16(x1, 0x4342), qz[zc][0], qz[zc][1]);
+                            }
+                            const bool mine = tq == (R == 8 ? j : j >> 1);
 #pragma unroll
-                            for (int j = 0; j < NCH / NZC; ++j) {
-                                float d[4] = {ci[nt][0], ci[nt][1], ci[nt][0], ci[nt][1]};
+                            for (int i = 0; i < 4; ++i)
+                                if (R == 8 || (i & 1) == (j & 1)) cz[i] = mine ? d[i] : cz[i];
+                        }
+                        // --- logits s (log2 units) and s + k, 2^k the scale of z^V; element i: token g (+ 8 for
+                        // i >= 2), head 2 tq + (i & 1)
+                        float sv[4], sw[4], ks[2][2], kv[2][2];
 #pragma unroll
-                                for (int zc = 0; zc < NZC; ++zc) {
-                                    const uint32_t at = row0 + zk_off + (nt * NCH + j * NZC + zc) * 16;
-                                    const uint32_t x0 = lds32(at), x1 = lds32(at + g8);
-                                    mma_16816_f16(d, bytes_f16(x0, 0x4140), bytes_f16(x1, 0x4140), bytes_f16(x0, 0x4342),
-                                                  bytes_f16(x1, 0x4342), qz[zc][nt][0], qz[zc][nt][1]);
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int e = 0; e < NSE; ++e) {
+                                ks[hf][e] = scale_of((hf ? nan1 : nan0) ? 255u : kb[hf][e]);
+                                // log2 of the scale: -infinity of a cleared row, +infinity of a NaN block, whose
+                                // weight then becomes infinity - infinity
+                                kv[hf][e] = lg2_approx(__uint_as_float(vb[hf][e] << 23));
+                            }
+                        float over = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = i & 1, es = e & (NSE - 1), hf = i >> 1;
+                            const float s = fmaf(cz[i], ks[hf][es], c[i]) * fz[e];
+                            const bool in = hf ? in1 : in0;
+                            sv[i] = in ? s : -INFINITY;
+                            sw[i] = in ? s + kv[hf][es] : -INFINITY;
+                            over = fmaxf(over, fmaxf(sv[i] - m[e], sw[i] - mz[e]));
+                        }
+                        // Maxima are the same in the eight lanes that share two heads, and raised together,
+                        // by all heads of the tile, once some logit lies more than 2^8 above.  (At the start
+                        // they are -infinity; -infinity - -infinity is a NaN, which fmaxf passes over.)
+                        if (__any_sync(0xffffffffu, over > kLazy)) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x = fmaxf(sv[e], sv[2 + e]), y = fmaxf(sw[e], sw[2 + e]);
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) {
+                                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
                                 }
-                                const bool mine = tq == (R == 8 ? j : j >> 1);
+                                x = fmaxf(x, m[e]);
+                                y = fmaxf(y, mz[e]);
+                                const float al = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - x);
+                                const float az = mz[e] == -INFINITY ? 0.f : ex2_approx(mz[e] - y);
+                                m[e] = x;
+                                mz[e] = y;
+                                l[e] *= al;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (R == 8 || (i & 1) == (j & 1)) cz[i] = mine ? d[i] : cz[i];
-                            }
-                            // --- logits s (log2 units) and s + k, 2^k the scale of z^V; element i: token g (+ 8 for
-                            // i >= 2), head 2 tq + (i & 1)
-                            float sv[4], sw[4], ks[2][2], kv[2][2];
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                                for (int e = 0; e < NSE; ++e) {
-                                    const uint32_t sa = row0 + sc_off[nt][e] + hf * g8;
-                                    const uint32_t kb = lds8(sa);
-                                    ks[hf][e] = scale_of((hf ? nan1 : nan0) ? 255u : kb);
-                                    // log2 of the scale: -infinity of a cleared row, +infinity of a NaN block, whose
-                                    // weight then becomes infinity - infinity
-                                    kv[hf][e] = lg2_approx(__uint_as_float(lds8(sa + ql.nb_z) << 23));
+                                for (int i = 0; i < D_H / 16; ++i) {
+                                    o[i][e] *= al;
+                                    o[i][2 + e] *= al;
                                 }
-                            float over = -INFINITY;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int e = i & 1, es = e & (NSE - 1), hf = i >> 1;
-                                const float s = fmaf(cz[i], ks[hf][es], c[nt][i]) * fz[nt][e];
-                                const bool in = hf ? in1 : in0;
-                                sv[i] = in ? s : -INFINITY;
-                                sw[i] = in ? s + kv[hf][es] : -INFINITY;
-                                over = fmaxf(over, fmaxf(sv[i] - m[nt][e], sw[i] - mz[nt][e]));
-                            }
-                            // Maxima are the same in the eight lanes that share two heads, and raised together,
-                            // by all heads of the tile, once some logit lies more than 2^8 above.  (At the start
-                            // they are -infinity; -infinity - -infinity is a NaN, which fmaxf passes over.)
-                            if (__any_sync(0xffffffffu, over > kLazy)) {
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    float x = fmaxf(sv[e], sv[2 + e]), y = fmaxf(sw[e], sw[2 + e]);
-#pragma unroll
-                                    for (int d = 4; d < 32; d <<= 1) {
-                                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                                    }
-                                    x = fmaxf(x, m[nt][e]);
-                                    y = fmaxf(y, mz[nt][e]);
-                                    const float al = m[nt][e] == -INFINITY ? 0.f : ex2_approx(m[nt][e] - x);
-                                    const float az = mz[nt][e] == -INFINITY ? 0.f : ex2_approx(mz[nt][e] - y);
-                                    m[nt][e] = x;
-                                    mz[nt][e] = y;
-                                    l[nt][e] *= al;
-#pragma unroll
-                                    for (int i = 0; i < D_H / 16; ++i) {
-                                        o[i][nt][e] *= al;
-                                        o[i][nt][2 + e] *= al;
-                                    }
-#pragma unroll
-                                    for (int i = 0; i < NZC; ++i) {
-                                        oz[i][nt][e] *= az;
-                                        oz[i][nt][2 + e] *= az;
-                                    }
-                                }
-                            }
-                            // --- p = 2^(s - m) and w = 2^(s + k - mz), transposed into B fragments
-                            float pp[4], ww[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int e = i & 1;
-                                const bool in = i < 2 ? in0 : in1;
-                                pp[i] = in ? ex2_approx(sv[i] - m[nt][e]) : 0.f;
-                                // (mz is -infinity as long as every row of the block was a cleared one)
-                                ww[i] = sw[i] == -INFINITY ? 0.f : ex2_approx(sw[i] - mz[nt][e]);
-                            }
-                            l[nt][0] += pp[0] + pp[2];
-                            l[nt][1] += pp[1] + pp[3];
-                            const uint32_t pb0 = movmatrix_trans(pack_bf16x2(pp[0], pp[1]));
-                            const uint32_t pb1 = movmatrix_trans(pack_bf16x2(pp[2], pp[3]));
-                            const uint32_t wb0 = movmatrix_trans(pack_f16x2(ww[0], ww[1]));
-                            const uint32_t wb1 = movmatrix_trans(pack_f16x2(ww[2], ww[3]));
-                            // --- shared values: O^T (d x heads) += s^V^T . P
-#pragma unroll
-                            for (int i = 0; i < D_H / 16; ++i) {
-                                uint32_t af[4];
-                                ldmatrix_x4_trans(cvv + i * 32, af[0], af[1], af[2], af[3]);
-                                mma_16816(o[i][nt], af, pb0, pb1);
-                            }
-                            // --- latent values, two 16-byte chunks at a time: rows of the transposed 16-bit
-                            // elements are pairs of features, row g of A takes the even one, row g + 8 the odd
-                            // one.  The offset 1152 of the bytes' products is taken off tile by tile (so that the
-                            // sums never grow with it).
-#pragma unroll
-                            for (int zc = 0; zc < NZC; ++zc)
-                                mma_16816_f16(oz[zc][nt], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2, wb0,
-                                              wb1);
-#pragma unroll
-                            for (int c2 = 0; c2 < NCH; c2 += 2) {
-                                uint32_t x[4];
-                                ldmatrix_x4_trans(row0 + zv_off + (nt * NCH + c2) * 16, x[0], x[1], x[2], x[3]);
-#pragma unroll
-                                for (int w = 0; w < 2; ++w) {
-                                    const int ch = c2 + w;
-                                    const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
-                                    const int zc = R == 32 ? ch & 1 : 0;
-                                    mma_16816_f16(oz[zc][nt], bytes_f16(x[2 * w], 0x4240), bytes_f16(x[2 * w], 0x4341),
-                                                  bytes_f16(x[2 * w + 1], 0x4240), bytes_f16(x[2 * w + 1], 0x4341),
-                                                  mine ? wb0 : 0u, mine ? wb1 : 0u);
+                                for (int i = 0; i < NZC; ++i) {
+                                    oz[i][e] *= az;
+                                    oz[i][2 + e] *= az;
                                 }
                             }
                         }
+                        // --- p = 2^(s - m) and w = 2^(s + k - mz), transposed into B fragments
+                        float pp[4], ww[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = i & 1;
+                            const bool in = i < 2 ? in0 : in1;
+                            pp[i] = in ? ex2_approx(sv[i] - m[e]) : 0.f;
+                            // (mz is -infinity as long as every row of the block was a cleared one)
+                            ww[i] = sw[i] == -INFINITY ? 0.f : ex2_approx(sw[i] - mz[e]);
+                        }
+                        l[0] += pp[0] + pp[2];
+                        l[1] += pp[1] + pp[3];
+                        const uint32_t pb0 = movmatrix_trans(pack_bf16x2(pp[0], pp[1]));
+                        const uint32_t pb1 = movmatrix_trans(pack_bf16x2(pp[2], pp[3]));
+                        const uint32_t wb0 = movmatrix_trans(pack_f16x2(ww[0], ww[1]));
+                        const uint32_t wb1 = movmatrix_trans(pack_f16x2(ww[2], ww[3]));
+                        // --- shared values: O^T (d x heads) += s^V^T . P
+                        ok = warp_wait(smem_u32(vfull + cb), cphase, abort_flag, a.status, a.wait_ns);
+#pragma unroll
+                        for (int i = 0; i < D_H / 16; ++i) {
+                            uint32_t af[4];
+                            ldmatrix_x4_trans(cvv + i * 32, af[0], af[1], af[2], af[3]);
+                            mma_16816(o[i], af, pb0, pb1);
+                        }
+                        // --- latent values, two 16-byte chunks at a time: rows of the transposed 16-bit
+                        // elements are pairs of features, row g of A takes the even one, row g + 8 the odd
+                        // one.  The offset 1152 of the bytes' products is taken off tile by tile (so that the
+                        // sums never grow with it).
+#pragma unroll
+                        for (int zc = 0; zc < NZC; ++zc)
+                            mma_16816_f16(oz[zc], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2, wb0,
+                                          wb1);
+#pragma unroll kUnroll
+                        for (int c2 = 0; c2 < NCH; c2 += 2) {
+                            uint32_t x[4];
+                            ldmatrix_x4_trans(row0 + zv_off + c2 * 16, x[0], x[1], x[2], x[3]);
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                const int ch = c2 + w;
+                                const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
+                                const int zc = R == 32 ? ch & 1 : 0;
+                                mma_16816_f16(oz[zc], bytes_f16(x[2 * w], 0x4240), bytes_f16(x[2 * w], 0x4341),
+                                              bytes_f16(x[2 * w + 1], 0x4240), bytes_f16(x[2 * w + 1], 0x4341),
+                                              mine ? wb0 : 0u, mine ? wb1 : 0u);
+                            }
+                        }
                     }
+                    if (ok && !have) ok = warp_wait(smem_u32(vfull + cb), cphase, abort_flag, a.status, a.wait_ns);
                     __syncwarp();
                     if (lane == 0 && ok) mbar_arrive(smem_u32(vempty + cb));
                     cb += p.ng;
@@ -678,25 +677,23 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
             }
             // --- this group's state over the segment
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+                    for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
                     // the latents' sums brought to the probabilities' maximum
-                    const float fac = mz[nt][e] == -INFINITY ? 0.f : ex2_approx(mz[nt][e] - m[nt][e]);
+                    const float fac = mz[e] == -INFINITY ? 0.f : ex2_approx(mz[e] - m[e]);
 #pragma unroll
                     for (int i = 0; i < NZC; ++i) {
-                        oz[i][nt][e] *= fac;
-                        oz[i][nt][2 + e] *= fac;
+                        oz[i][e] *= fac;
+                        oz[i][2 + e] *= fac;
                     }
                     // a NaN sum is handed on as NaN values with a weight, not as an empty part
-                    if (l[nt][e] != l[nt][e]) {
-                        l[nt][e] = 1.f;
-                        if (!(fabsf(m[nt][e]) < INFINITY)) m[nt][e] = 0.f;
+                    if (l[e] != l[e]) {
+                        l[e] = 1.f;
+                        if (!(fabsf(m[e]) < INFINITY)) m[e] = 0.f;
 #pragma unroll
                         for (int i = 0; i < D_H / 16; ++i)
-                            o[i][nt][e] = o[i][nt][2 + e] = __uint_as_float(0x7fc00000u);
+                            o[i][e] = o[i][2 + e] = __uint_as_float(0x7fc00000u);
                     }
                 }
             const bool direct = p.ng == 1;
@@ -708,29 +705,27 @@ __global__ void __launch_bounds__(kThreads, 1) quant_scan_kernel(const QuantScan
             float* gacc = direct ? a.part_acc + (size_t)pslot * W : sacc + (size_t)grp * H * WS;
             if (!direct) named_bar(1, nct);  // every tile of the segment consumed: the ring is idle
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int h = h0 + nt * 8 + 2 * tq + e;
+                    const int h = h0 + 2 * tq + e;
                     if (h >= H) continue;
                     if (g == 0) {
-                        gml[h * hs_ml] = m[nt][e];
-                        gml[h * hs_ml + 1] = l[nt][e];
+                        gml[h * hs_ml] = m[e];
+                        gml[h * hs_ml + 1] = l[e];
                     }
                     float* dst = gacc + h * hs_acc;
 #pragma unroll
                     for (int i = 0; i < D_H / 16; ++i) {
-                        dst[i * 16 + g] = o[i][nt][e];
-                        dst[i * 16 + 8 + g] = o[i][nt][2 + e];
+                        dst[i * 16 + g] = o[i][e];
+                        dst[i * 16 + 8 + g] = o[i][2 + e];
                     }
                     if (R == 8) {
                         if ((g >> 2) == e)
-                            *reinterpret_cast<float2*>(dst + D_H + (g & 3) * 2) = make_float2(oz[0][nt][e], oz[0][nt][2 + e]);
+                            *reinterpret_cast<float2*>(dst + D_H + (g & 3) * 2) = make_float2(oz[0][e], oz[0][2 + e]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < NZC; ++i)
                             *reinterpret_cast<float2*>(dst + D_H + i * 16 + g * 2) =
-                                make_float2(oz[i][nt][e], oz[i][nt][2 + e]);
+                                make_float2(oz[i][e], oz[i][2 + e]);
                     }
                 }
             if (!direct) {
@@ -781,12 +776,11 @@ int tile_tokens(int H, int R) { return R == 32 && H > 96 ? 8 : 16; }
 
 template <int D_H, int R, int D_R>
 bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
-    p->nt = H > 8 * kConsumers ? 2 : 1;
+    p->cw = H > 64 ? 16 : 8;
     // a row of more than 96 heads of r = 32 is so long that two stages of 16 tokens do not fit
     const int tok = tile_tokens(H, R);
-    const int most = kConsumers;
-    p->nwh = (H + 8 * p->nt - 1) / (8 * p->nt);
-    const int ng_most = most / p->nwh > 1 ? most / p->nwh : 1;
+    p->nwh = (H + 7) / 8;
+    const int ng_most = p->cw / p->nwh;
     p->cb_bytes = tok * cb_stride(D_H);
     const int WS = merge_stride(D_H + R);
     const int tile = tok * q.row_bytes;
@@ -801,11 +795,13 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
     };
     for (int want = 3; want >= 2; --want)          // stages at least
         for (int ng = ng_most; ng >= 1; --ng)
-            for (int mul = 2; mul >= 1; --mul) {   // widened tiles per group
+            for (int mul = 3; mul >= 1; --mul) {   // widened tiles per group
                 const int ncb = ng * mul;
                 int nslot = 16;
                 while (nslot > 1 && nslot * p->stage_bytes + ncb * p->cb_bytes + fixed(nslot, ncb) > smem_limit) --nslot;
                 if (nslot < want) continue;
+                p->own_stages = p->st == 1 && nslot / ng * ng >= want;
+                if (p->own_stages) nslot = nslot / ng * ng;
                 if (ng > 1 && ((size_t)ng * H * (WS + 3) + 3) * 4 > (size_t)nslot * p->stage_bytes) continue;
                 p->ng = ng;
                 p->ncb = ncb;
@@ -821,9 +817,9 @@ template <int D_H, int R, int D_R>
 cudaError_t launch_t(QuantScanArgs& x, int sms, int smem_limit, cudaStream_t stream) {
     if (!make_plan<D_H, R, D_R>(&x.p, x.a.q, x.a.d.H, smem_limit)) return cudaErrorInvalidConfiguration;
     const int tok = tile_tokens(x.a.d.H, R);
-    auto kern = x.p.nt == 1 ? quant_scan_kernel<D_H, R, D_R, 1, 16> : quant_scan_kernel<D_H, R, D_R, 2, 16>;
+    auto kern = x.p.cw == 8 ? quant_scan_kernel<D_H, R, D_R, 8, 16> : quant_scan_kernel<D_H, R, D_R, 16, 16>;
     if constexpr (R == 32) {
-        if (tok == 8) kern = quant_scan_kernel<D_H, R, D_R, 2, 8>;
+        if (tok == 8) kern = quant_scan_kernel<D_H, R, D_R, 16, 8>;
     }
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, x.p.smem_bytes);
     if (e != cudaSuccess) return e;
