@@ -384,21 +384,34 @@ struct SharedPrefix {
     const int32_t* len;
 };
 
+static lrkv::PrefixPlan plan_prefix(const lrkv_dims* dims, int batch, int max_blocks, const DeviceInfo& di) {
+    return lrkv::prefix_plan(dims->H, dims->d_h, dims->r, dims->d_rope, batch, max_blocks, di.sms);
+}
+
 // Scan of the prefix (q~ is in p.d.qt) and the merge with the sequences' own partials, if any.
 static lrkv_status prefix_launch(lrkv::PrefixArgs& p, const lrkv_dims* dims, const lrkv_cache* cache,
-                                 const SharedPrefix& prefix, int suffix, int nsplit, void* ws, cudaStream_t st,
-                                 const char* what) {
-    p.sK = static_cast<const uint16_t*>(cache->sK);
-    p.sV = static_cast<const uint16_t*>(cache->sV);
-    p.zK = static_cast<const uint16_t*>(cache->zK);
-    p.zV = static_cast<const uint16_t*>(cache->zV);
+                                 const SharedPrefix& prefix, int suffix, const lrkv::PrefixPlan& plan, void* ws,
+                                 cudaStream_t st, const char* what) {
+    lrkv::PrefixMaps m;
+    const uint64_t rows = (uint64_t)cache->num_blocks * dims->block_size, HR = (uint64_t)dims->H * dims->r;
+    lrkv_status s;
+    if ((s = make_tmap(&m.sK, cache->sK, (uint64_t)dims->d_h + dims->d_rope, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                       "sK")) != LRKV_OK ||
+        (s = make_tmap(&m.sV, cache->sV, dims->d_h, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "sV")) != LRKV_OK ||
+        (s = make_tmap(&m.zK, cache->zK, HR, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "zK")) != LRKV_OK ||
+        (s = make_tmap(&m.zV, cache->zV, HR, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "zV")) != LRKV_OK)
+        return s;
     p.blocks = prefix.blocks;
     p.len = prefix.len;
     p.max_blocks = prefix.max_blocks;
     p.suffix = suffix;
-    p.nsplit = nsplit;
+    p.nsplit = plan.nsplit;
+    p.zw = plan.zw;
+    p.hb = plan.hb;
+    p.ns = plan.ns;
+    p.htiles = plan.htiles;
     lrkv::prefix_carve_workspace(&p, ws, dims->d_h, dims->r);
-    cudaError_t e = lrkv::launch_prefix_scan(p, dims->d_h, dims->r, dims->d_rope, st);
+    cudaError_t e = lrkv::launch_prefix_scan(m, p, dims->d_h, dims->r, dims->d_rope, st);
     if (e == cudaSuccess) e = lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st);
     return cuda_status(e, what);
 }
@@ -478,9 +491,10 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
     const int nvb = num_layers * batch;
     const int nranges = decode_ranges(dims, di.sms);
     const size_t scan_bytes = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, nvb, nranges);
-    const int psplits = prefix ? lrkv::prefix_splits(dims->H, dims->r, batch, prefix->max_blocks, di.sms) : 0;
+    lrkv::PrefixPlan pplan{};
+    if (prefix) pplan = plan_prefix(dims, batch, prefix->max_blocks, di);
     const size_t need =
-        scan_bytes + (prefix ? lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, psplits) : 0);
+        scan_bytes + (prefix ? lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, pplan.nsplit) : 0);
     if (!workspace || ((uintptr_t)workspace & 255u))
         return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
@@ -538,7 +552,7 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
         if (e != cudaSuccess) return cuda_status(e, "lrkv_decode_shared launch");
         lrkv::PrefixArgs p{};
         p.d = a;
-        return prefix_launch(p, dims, cache, *prefix, 1, psplits, static_cast<uint8_t*>(workspace) + scan_bytes, st,
+        return prefix_launch(p, dims, cache, *prefix, 1, pplan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
                              "lrkv_decode_shared launch");
     }
     return cuda_status(lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms,
@@ -603,9 +617,9 @@ size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, 
     if (check_dims(dims) != LRKV_OK || batch < 0 || max_prefix_blocks < 1) return 0;
     DeviceInfo di;
     if (device_info(&di) != LRKV_OK) return 0;
-    const int ns = lrkv::prefix_splits(dims->H, dims->r, batch, max_prefix_blocks, di.sms);
     return lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, decode_ranges(dims, di.sms)) +
-           lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, ns);
+           lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch,
+                                        plan_prefix(dims, batch, max_prefix_blocks, di).nsplit);
 }
 
 lrkv_status lrkv_decode_shared(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
@@ -636,8 +650,8 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
     if ((s = device_info(&di)) != LRKV_OK) return s;
     const int nranges = decode_ranges(dims, di.sms);
     const size_t scan_bytes = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, nranges);
-    const int ns = lrkv::prefix_splits(dims->H, dims->r, batch, max_prefix_blocks, di.sms);
-    const size_t need = scan_bytes + lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, ns);
+    const lrkv::PrefixPlan plan = plan_prefix(dims, batch, max_prefix_blocks, di);
+    const size_t need = scan_bytes + lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, plan.nsplit);
     if (!workspace || ((uintptr_t)workspace & 255u))
         return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
@@ -656,7 +670,7 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = lrkv::launch_decode_absorb(p.d, dims->d_h, dims->r, dims->d_rope, st);
     if (e != cudaSuccess) return cuda_status(e, "lrkv_prefix_partials launch");
-    return prefix_launch(p, dims, cache, prefix, 0, ns, static_cast<uint8_t*>(workspace) + scan_bytes, st,
+    return prefix_launch(p, dims, cache, prefix, 0, plan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
                          "lrkv_prefix_partials launch");
 }
 

@@ -5,8 +5,24 @@
 //     per (sequence b, head h):  s_t = (q_bh . s^K_t + q~_bh . z^K_{h,t}) * scale * log2 e
 //     m = max s_t,  l = sum 2^(s_t - m),  acc = sum 2^(s_t - m) [s^V_t | z^V_{h,t}]
 // and the combine merges its pieces with the partials of the sequences' own scan.
-// A block per (piece, head, sequence); a warp takes every eighth token with an online softmax of
-// its own, the warps' states are merged at the end.
+//
+// The scan is bound by the tensor cores or the memory, depending on the batch: per cached token and
+// head it does 4 B (d_h + r) flops on 4 (d_h / H + r) bytes.  A CTA has 128 query rows, hb heads x
+// ns sequences, and treats them as one attention problem of width d_h + zw, zw = hb r:
+//     S = [Q | diag(Q~)] . [s^K | z^K of the hb heads]^T,   O += P . [s^V | z^V of the hb heads]
+// where a row of diag(Q~) holds q~ in its own head's r columns and zeros elsewhere, and of a row's zw
+// latent sums only its own head's r are used.  That is hb times the latents' products needed, on
+// tensor cores that would otherwise wait: with a head per tile (no waste) the shared rows would be
+// read hb times as often, and the prefix's rows of a batch of 16 would fill an eighth of a tile.
+// zw = 128 for few sequences, 64 for more (prefix_plan).
+// Per 64-token page: S by tcgen05.mma (M = 128, N = 64, K = d_h + zw) from shared memory into one of
+// two TMEM buffers, P = 2^(S scale log2 e - m) in bf16 over the same columns, O by tcgen05.mma with
+// A = P from TMEM (N = d_h + zw).  Warp roles and the lazily raised maximum as in the prefill
+// (prefill_tc.cu): warp 0 key producer, 6 value producer (TMA, 128-byte swizzle), 1 issues S, 7 issues
+// P V, 2..5 one query row per thread.
+#include <type_traits>
+#include <utility>
+
 #include "lrkv_internal.cuh"
 #include "prefix.h"
 
@@ -14,7 +30,8 @@ namespace lrkv {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 256;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 __device__ __forceinline__ float bf(const uint16_t* p, size_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
 
@@ -22,67 +39,408 @@ __device__ __forceinline__ bool prefix_good(const PrefixArgs& a, int P) {
     return P >= 0 && P <= a.max_blocks * kBlockSize;
 }
 
-template <int D_H, int R, int D_R>
-__global__ void __launch_bounds__(kWarps * 32) prefix_scan_kernel(const PrefixArgs a) {
-    constexpr int D_K = D_H + D_R, W = D_H + R;
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Shared memory: Q [128][D_K + ZW] (64-column blocks of 16 KB), a ring of key stages [64 tokens][D_K
+// + ZW] and one of value stages [64][D_H + ZW] (blocks of 8 KB), barriers.  As many stages as fit.
+template <int D_H, int D_R, int ZW>
+struct PxLayout {
+    static constexpr int D_K = D_H + D_R;
+    static constexpr int NBK = (D_K + ZW) / 64, NBV = (D_H + ZW) / 64;  // 64-column blocks of a key / value row
+    static constexpr uint32_t Q_BYTES = NBK * 16384, K_BYTES = NBK * 8192, V_BYTES = NBV * 8192;
+    static constexpr uint32_t ROOM = 232448 - 1024 - 512 - Q_BYTES;
+    static constexpr int BOTH = ROOM / (K_BYTES + V_BYTES);
+    static constexpr int VST = BOTH > 4 ? 4 : BOTH;
+    static constexpr int KST = VST < 4 && ROOM - VST * (K_BYTES + V_BYTES) >= K_BYTES ? VST + 1 : VST;
+    static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
+    static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+    static_assert(VST >= 2 && SMEM <= 232448, "stages");
+    // TMEM columns: two S buffers, O
+    static constexpr uint32_t TM_S = 0, TM_O = 128;
+    static_assert(128 + D_H + ZW <= 512, "TMEM");
+};
+
+__device__ __forceinline__ uint64_t kdesc128(uint32_t a) { return sdesc(a, 16, 1024, 2); }
+__device__ __forceinline__ uint64_t mndesc128(uint32_t a) { return sdesc(a, 8192, 1024, 2); }
+
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, uint32_t* status) {
+    const bool ok = mbar_wait(bar, parity, status);
+    return __all_sync(0xffffffffu, ok);
+}
+
+constexpr int lcm2(int n) { return n % 2 ? 2 * n : n; }
+
+// f(j, U) for the tiles j0 + U < nt, U = 0, 1, .., stopping at the first failure: tile loops unrolled
+// over the ring's stages and the S buffers, so that every operand of every MMA is loop-invariant.
+template <class F, int... U>
+__device__ __forceinline__ bool tiles(F&& f, int j0, int nt, std::integer_sequence<int, U...>) {
+    return ((j0 + U < nt ? f(j0 + U, std::integral_constant<int, U>{}) : true) && ...);
+}
+
+template <int D_H, int D_R, int ZW>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_scan_kernel(const __grid_constant__ PrefixMaps m, const PrefixArgs a, const int R) {
+    using Lay = PxLayout<D_H, D_R, ZW>;
+    constexpr int D_K = Lay::D_K, NBK = Lay::NBK, NBV = Lay::NBV, KST = Lay::KST, VST = Lay::VST;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
+    const uint32_t S0 = smem_u32(smem);
     const DecodeArgs& d = a.d;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = d.H, W = D_H + R;
+    const int ht = blockIdx.x % a.htiles, stile = blockIdx.x / a.htiles, split = blockIdx.y;
+    const int h0 = ht * a.hb, b0 = stile * a.ns;
     const int P = prefix_good(a, a.len[0]) ? a.len[0] : 0;
-    const int per = (P + a.nsplit - 1) / a.nsplit;
-    const int t0 = split * per, t1 = min(P, t0 + per);
-    float qr[D_K / 32], o[D_H / 32];
-    const uint16_t* q = d.q + ((size_t)b * d.H + h) * D_K;
-#pragma unroll
-    for (int i = 0; i < D_K / 32; ++i) qr[i] = bf(q, i * 32 + lane);
-#pragma unroll
-    for (int i = 0; i < D_H / 32; ++i) o[i] = 0.f;
-    const float qt = lane < R ? d.qt[((size_t)b * d.H + h) * R + lane] : 0.f;
-    float oz = 0.f, m = -INFINITY, l = 0.f;
-    for (int t = t0 + warp; t < t1; t += kWarps) {
-        const int blk = a.blocks[t / kBlockSize];
-        if (blk < 0 || blk >= d.num_blocks) {
-            if (lane == 0) set_status(d.status, LRKV_DEV_BAD_BLOCK);
-            continue;
+    // this piece: pages [pg0, pg0 + nt)
+    const int np = (P + kBlockSize - 1) / kBlockSize;
+    const int pg0 = (int)((long long)np * split / a.nsplit);
+    const int nt = (int)((long long)np * (split + 1) / a.nsplit) - pg0;
+
+    // this thread's query row (softmax warps): TMEM lane = row = head x ns + sequence
+    const int qq = warp & 3;
+    const int row = qq * 32 + lane;
+    const int hl = row / a.ns, rb = b0 + row - hl * a.ns, rh = h0 + hl;
+    const bool live = rh < H && rb < d.B;
+    const size_t at = ((size_t)rb * H + rh) * a.nsplit + split;
+    if (nt == 0) {  // an empty piece: its sums are not read
+        if (warp >= 2 && warp < 6 && live) {
+            a.ml[at * 2] = -INFINITY;
+            a.ml[at * 2 + 1] = 0.f;
         }
-        const size_t row = (size_t)blk * kBlockSize + t % kBlockSize;
-        const size_t zrow = (row * d.H + h) * R + lane;
-        float s = lane < R ? qt * bf(a.zK, zrow) : 0.f;
-#pragma unroll
-        for (int i = 0; i < D_K / 32; ++i) s = fmaf(qr[i], bf(a.sK, row * D_K + i * 32 + lane), s);
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        s *= d.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float al = mn == -INFINITY ? 1.f : exp2f(m - mn), p = mn == -INFINITY ? 0.f : exp2f(s - mn);
-        m = mn;
-        l = l * al + p;
-#pragma unroll
-        for (int i = 0; i < D_H / 32; ++i) o[i] = fmaf(p, bf(a.sV, row * D_H + i * 32 + lane), o[i] * al);
-        if (lane < R) oz = fmaf(p, bf(a.zV, zrow), oz * al);
+        return;
     }
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][W];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < D_H / 32; ++i) so[warp][i * 32 + lane] = o[i];
-    if (lane < R) so[warp][D_H + lane] = oz;
-    __syncthreads();
-    float M = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    float ls = 0.f, v = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-        const float x = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - M);
-        ls = fmaf(x, sl[w], ls);
-        if (threadIdx.x < W) v = fmaf(x, so[w][threadIdx.x], v);
-    }
-    const size_t at = ((size_t)b * d.H + h) * a.nsplit + split;
-    if (threadIdx.x < W) a.acc[at * W + threadIdx.x] = v;
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+    uint64_t* q_ready = bars + 0;
+    uint64_t* p_full = bars + 1;
+    uint64_t* s_full = bars + 2;    // [2]
+    uint64_t* s_free = bars + 4;    // [2] P_j V_j done: buffer j % 2 may take S_{j+2}
+    // o_done[j % 2]: P_j V_j complete (waited for before a rescale only, which is why there are two: one
+    // cannot complete its next phase before the softmax has passed tile j + 2)
+    uint64_t* o_done = bars + 6;    // [2]
+    uint64_t* s_drain = bars + 8;   // all S MMAs of the CTA complete
+    uint64_t* pv_drain = bars + 9;
+    uint64_t* k_full = bars + 10;   // [4]
+    uint64_t* k_empty = bars + 14;
+    uint64_t* v_full = bars + 18;
+    uint64_t* v_empty = bars + 22;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+    volatile int* abort_flag = reinterpret_cast<int*>(bars + 27);
+    auto B = [&](uint64_t* p) { return smem_u32(p); };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
+
     if (threadIdx.x == 0) {
-        a.ml[at * 2] = M;
-        a.ml[at * 2 + 1] = ls;
+        mbar_init(B(q_ready), 128);
+        mbar_init(B(p_full), 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B(s_full + i), 1);
+            mbar_init(B(s_free + i), 1);
+            mbar_init(B(o_done + i), 1);
+        }
+        mbar_init(B(s_drain), 1);
+        mbar_init(B(pv_drain), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(B(k_full + i), 1);
+            mbar_init(B(k_empty + i), 1);
+            mbar_init(B(v_full + i), 1);
+            mbar_init(B(v_empty + i), 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0 || warp == 6) {
+        // ---------------------------------------------------------------- TMA producers
+        const bool keys = warp == 0;
+        const int oob_row = d.num_blocks * kBlockSize;  // whole box out of bounds: zeros
+        auto fetch = [&](int batch) {
+            const int i = batch * 32 + lane;
+            int r = oob_row;
+            if (i < nt) {
+                const int blk = a.blocks[pg0 + i];
+                if (blk >= 0 && blk < d.num_blocks)
+                    r = blk * kBlockSize;
+                else
+                    set_status(d.status, LRKV_DEV_BAD_BLOCK);
+            }
+            return r;
+        };
+        const int depth = keys ? KST : VST;
+        const uint32_t stage_bytes = keys ? Lay::K_BYTES : Lay::V_BYTES;
+        const int nblk = keys ? D_K / 64 : D_H / 64;
+        uint64_t* full = keys ? k_full : v_full;
+        uint64_t* empty = keys ? k_empty : v_empty;
+        const CUtensorMap* ms = keys ? &m.sK : &m.sV;
+        const CUtensorMap* mz = keys ? &m.zK : &m.zV;
+        const uint32_t ring = S0 + (keys ? Lay::OFF_K : Lay::OFF_V);
+        int cur = fetch(0), nxt = fetch(1);
+        int issued = 0, st = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int j = 0; j < nt; ++j) {
+            if (j > 0 && (j & 31) == 0) {
+                cur = nxt;
+                nxt = fetch((j >> 5) + 1);
+            }
+            const int prow = __shfl_sync(0xffffffffu, cur, j & 31);
+            if ((j >= depth && !wait_all(B(empty + st), phase, d.status)) || aborted()) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                uint32_t dst = ring + st * stage_bytes;
+                const uint32_t bar = B(full + st);
+                mbar_arrive_expect_tx(bar, stage_bytes);
+                for (int bk = 0; bk < nblk; ++bk, dst += 8192) tma_load_2d(dst, ms, 64 * bk, prow, bar);
+                for (int bk = 0; bk < ZW / 64; ++bk, dst += 8192) tma_load_2d(dst, mz, h0 * R + 64 * bk, prow, bar);
+            }
+            __syncwarp();
+            issued = j + 1;
+            if (++st == depth) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+        if (!ok) {
+            *abort_flag = 1;
+            // let this ring's copies still in flight land before the CTA exits
+            for (int k = max(0, issued - depth); k < issued; ++k) wait_all(B(full + k % depth), (k / depth) & 1, d.status);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- score MMAs
+        constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
+        const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K);
+        auto s_tile = [&](int j, auto UU) -> bool {
+            constexpr int U = decltype(UU)::value, st = U % KST, sb = U & 1;
+            if (aborted() || !wait_all(B(k_full + st), (j / KST) & 1, d.status) ||
+                (j >= 2 && !wait_all(B(s_free + sb), ((j >> 1) - 1) & 1, d.status)))
+                return false;
+            tc_fence_after();
+            constexpr uint64_t so = st * (Lay::K_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < NBK * 4; ++kk)
+                if (elect_one_sync())
+                    tc_mma_bf16(tmem + Lay::TM_S + sb * 64, dQ + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                dK + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_S, kk > 0);
+            if (elect_one_sync()) {
+                tc_commit(B(s_full + sb));
+                tc_commit(B(k_empty + st));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = wait_all(B(q_ready), 0, d.status);
+        tc_fence_after();
+        for (int j = 0; j < nt && ok; j += lcm2(KST))
+            ok = tiles(s_tile, j, nt, std::make_integer_sequence<int, lcm2(KST)>{});
+        if (!ok) *abort_flag = 1;
+        // every MMA this warp issued has finished before the CTA tears TMEM down
+        if (elect_one_sync()) tc_commit(B(s_drain));
+        __syncwarp();
+        wait_all(B(s_drain), 0, d.status);
+    } else if (warp == 7) {
+        // ---------------------------------------------------------------- P V MMAs
+        constexpr uint32_t id_PV = idesc_bf16_f32(128, D_H + ZW) | (1u << 16);  // B is MN-major
+        const uint64_t dV = mndesc128(S0 + Lay::OFF_V);
+        auto pv_tile = [&](int j, auto UU) -> bool {
+            constexpr int U = decltype(UU)::value, st = U % VST, sb = U & 1;
+            if (aborted() || !wait_all(B(p_full), j & 1, d.status) ||
+                !wait_all(B(v_full + st), (j / VST) & 1, d.status))
+                return false;
+            tc_fence_after();
+            constexpr uint64_t so = st * (Lay::V_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kBlockSize / 16; ++kk)
+                if (elect_one_sync())
+                    tc_mma_bf16_ts(tmem + Lay::TM_O, tmem + Lay::TM_S + sb * 64 + kk * 8, dV + so + (kk * 2048 >> 4),
+                                   id_PV, (j | kk) != 0);
+            if (elect_one_sync()) {
+                tc_commit(B(o_done + sb));
+                tc_commit(B(v_empty + st));
+                tc_commit(B(s_free + sb));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = true;
+        for (int j = 0; j < nt && ok; j += lcm2(VST))
+            ok = tiles(pv_tile, j, nt, std::make_integer_sequence<int, lcm2(VST)>{});
+        if (!ok) *abort_flag = 1;
+        if (elect_one_sync()) tc_commit(B(pv_drain));
+        __syncwarp();
+        wait_all(B(pv_drain), 0, d.status);
+    } else {
+        // ---------------------------------------------------------------- query rows: softmax, partials
+        const uint32_t tl = (uint32_t)(qq * 32) << 16;
+        {
+            // [Q | diag(Q~)] row, K-major with 128-byte swizzle: 16-byte chunk c of a 64-column block lies at c ^
+            // (row mod 8).  q~ is rounded to bf16, as in the prefill.
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const uint4* q = reinterpret_cast<const uint4*>(d.q + ((size_t)(live ? rb : 0) * H + (live ? rh : 0)) * D_K);
+            uint8_t* qrow = smem + row * 128;
+#pragma unroll 8
+            for (int c = 0; c < D_K / 8; ++c)
+                *reinterpret_cast<uint4*>(qrow + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = live ? q[c] : zero;
+            const float* qt = d.qt + ((size_t)(live ? rb : 0) * H + (live ? rh : 0)) * R;
+            for (int c = 0; c < ZW / 8; ++c) {
+                const int col = c * 8 - hl * R;
+                uint4 v = zero;
+                if (live && col >= 0 && col < R) {
+                    const float4 x = *reinterpret_cast<const float4*>(qt + col);
+                    const float4 y = *reinterpret_cast<const float4*>(qt + col + 4);
+                    v = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                                   pack_bf16x2(y.z, y.w));
+                }
+                *reinterpret_cast<uint4*>(qrow + (D_K / 64 + (c >> 3)) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(B(q_ready));
+        }
+        bool ok = true;
+        float mref = -INFINITY, l = 0.f;
+        int vst = 0;
+        uint32_t vphase = 0;
+        for (int j = 0; j < nt; ++j) {
+            if (!ok || aborted()) {
+                ok = false;
+                break;
+            }
+            // visible tokens of this page: none of a page with a bad id
+            const int blk = a.blocks[pg0 + j];
+            const int lim = blk >= 0 && blk < d.num_blocks ? P - (pg0 + j) * kBlockSize : 0;
+            ok = wait_all(B(s_full + (j & 1)), (j >> 1) & 1, d.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sb = tmem + tl + Lay::TM_S + (j & 1) * 64;
+            uint32_t sv[64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32_nowait(sb + c * 32, sv + c * 32);
+            tmem_wait_ld();
+            if (lim < kBlockSize) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
+                // rows of s^V, z^V behind the end may hold any bits: cleared before P V reads them
+                ok = wait_all(B(v_full + vst), vphase, d.status);
+                if (!ok) break;
+                const int vr = row & 63;
+                if (vr >= lim) {
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    for (int bk = row >> 6; bk < NBV; bk += 2) {
+                        uint4* r0 = reinterpret_cast<uint4*>(smem + Lay::OFF_V + vst * Lay::V_BYTES + bk * 8192 + vr * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) r0[i] = z;
+                    }
+                }
+            }
+            if (++vst == VST) {
+                vst = 0;
+                vphase ^= 1;
+            }
+            float m8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m8[i] = __uint_as_float(sv[i]);
+#pragma unroll
+            for (int e = 8; e < 64; ++e) m8[e & 7] = fmaxf(m8[e & 7], __uint_as_float(sv[e]));
+            float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            mx *= d.scale_log2;
+            const float mnew = fmaxf(mref, mx);
+            const bool raise = mnew > mref + kRescaleThreshold;  // also the first time a row sees a token
+            const float muse = raise ? mnew : mref;
+            const float alpha = raise ? (mref == -INFINITY ? 0.f : ex2_approx(mref - mnew)) : 1.f;
+            // p = 2^(s scale log2 e - m), 0 everywhere as long as the row has seen no token
+            const float nm = muse == -INFINITY ? -INFINITY : -muse;
+            float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t* v = sv + c * 32;
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = ex2_approx(fmaf(__uint_as_float(v[e]), d.scale_log2, nm));
+                    const float p1 = ex2_approx(fmaf(__uint_as_float(v[e + 1]), d.scale_log2, nm));
+                    r8[(e >> 1) & 7] += p0 + p1;
+                    pk[e / 2] = pack_bf16x2(p0, p1);
+                }
+                tmem_st_32x32b_x16(sb + c * 16, pk);
+            }
+            l = l * alpha + (((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7])));
+            mref = muse;
+            // O may only be rescaled once P_{j-1} V_{j-1} has finished accumulating into it
+            if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                ok = wait_all(B(o_done + ((j - 1) & 1)), ((j - 1) >> 1) & 1, d.status);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t v[32];
+#pragma unroll 1
+                for (int c = 0; c < (D_H + ZW) / 32; ++c) {
+                    tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                    tmem_st_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
+                }
+            }
+            tmem_wait_st();
+            fence_proxy_async_smem();  // cleared value rows (if any) before the tensor cores read them
+            tc_fence_before();
+            mbar_arrive(B(p_full));
+        }
+        // ---- partials, unnormalised
+        if (ok) ok = wait_all(B(o_done + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, d.status);
+        if (ok) {
+            tc_fence_after();
+            const bool nan = l != l;  // handed on as NaN values with a weight, not as an empty part
+            if (nan) {
+                l = 1.f;
+                if (!(fabsf(mref) < INFINITY)) mref = 0.f;
+            }
+            if (live) {
+                a.ml[at * 2] = mref;
+                a.ml[at * 2 + 1] = l;
+            }
+            float* dst = a.acc + at * W;
+#pragma unroll 1
+            for (int c = 0; c < D_H / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(dst + c * 32 + i * 4) =
+                            nan ? make_uint4(0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u)
+                                : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                }
+            }
+            // latent sums: 32 columns at a time, each row keeps its own head's
+#pragma unroll 1
+            for (int c = 0; c < ZW / 32; ++c) {
+                // (a warp's rows span heads hl of its first to its last lane)
+                const int first = (qq * 32) / a.ns * R, last = (qq * 32 + 31) / a.ns * R + R;
+                if (c * 32 + 32 <= first || c * 32 >= last) continue;
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + D_H + c * 32, v);
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int col = c * 32 + i * 4 - hl * R;
+                        if (col >= 0 && col < R)
+                            *reinterpret_cast<uint4*>(dst + D_H + col) =
+                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+            }
+        } else {
+            *abort_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
@@ -156,9 +514,38 @@ __global__ void __launch_bounds__(192) prefix_combine_kernel(const PrefixArgs a)
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-int prefix_splits(int H, int R, int B, int max_blocks, int sms) {
-    (void)H, (void)R, (void)B, (void)sms;
-    return max_blocks < 16 ? max_blocks : 16;
+// Which tile: the fewest tensor-core products, tiles x (d_k + d_h + 2 zw) (one of 64 columns covers
+// twice the sequences of one of 128 with half the heads).  How many pieces: a piece costs its pages
+// and about kPieceCost pages more (Q, pipeline fill, partials), and the pieces of all tiles run in
+// waves of one CTA per SM.
+PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, int sms) {
+    constexpr int kPieceCost = 7;
+    PrefixPlan best{};
+    long long best_cost = -1;
+    for (int zw = 128; zw >= 64; zw /= 2) {
+        PrefixPlan p{};
+        p.zw = zw;
+        p.hb = zw / R;
+        p.ns = 128 / p.hb;
+        p.htiles = (H + p.hb - 1) / p.hb;
+        p.stiles = (B + p.ns - 1) / p.ns;
+        const long long cost = (long long)p.htiles * p.stiles * (2 * D_H + D_R + 2 * zw);
+        if (best_cost < 0 || cost < best_cost) {
+            best = p;
+            best_cost = cost;
+        }
+    }
+    const long long ntiles = (long long)best.htiles * best.stiles;
+    long long least = -1;
+    for (int s = 1; s <= max_blocks && s <= 65535 && (s == 1 || ntiles * s <= 4LL * sms); ++s) {
+        const long long waves = (ntiles * s + sms - 1) / sms;
+        const long long t = waves * ((max_blocks + s - 1) / s + kPieceCost);
+        if (least < 0 || t < least) {
+            least = t;
+            best.nsplit = s;
+        }
+    }
+    return best;
 }
 
 size_t prefix_workspace_bytes(int H, int D_H, int R, int B, int nsplit) {
@@ -173,17 +560,24 @@ void prefix_carve_workspace(PrefixArgs* a, void* ws, int D_H, int R) {
                                       align256((size_t)a->d.B * a->d.H * a->nsplit * 2 * sizeof(float)));
 }
 
-cudaError_t launch_prefix_scan(const PrefixArgs& a, int D_H, int R, int D_R, cudaStream_t stream) {
-    const dim3 grid(a.nsplit, a.d.H, a.d.B);
-#define LRKV_PS(DH, RR)                                                                           \
-    if (D_H == DH && R == RR) {                                                                   \
-        if (D_R == 0)                                                                             \
-            prefix_scan_kernel<DH, RR, 0><<<grid, kWarps * 32, 0, stream>>>(a);                   \
-        else                                                                                      \
-            prefix_scan_kernel<DH, RR, 64><<<grid, kWarps * 32, 0, stream>>>(a);                  \
-        return cudaGetLastError();                                                                \
-    }
-    LRKV_PS(64, 8) LRKV_PS(64, 16) LRKV_PS(64, 32) LRKV_PS(128, 8) LRKV_PS(128, 16) LRKV_PS(128, 32)
+template <int D_H, int D_R, int ZW>
+static cudaError_t launch_scan_t(const PrefixMaps& maps, const PrefixArgs& a, int R, cudaStream_t stream) {
+    constexpr uint32_t smem = PxLayout<D_H, D_R, ZW>::SMEM;
+    auto kern = prefix_scan_kernel<D_H, D_R, ZW>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int stiles = (a.d.B + a.ns - 1) / a.ns;
+    kern<<<dim3(a.htiles * stiles, a.nsplit), kThreads, smem, stream>>>(maps, a, R);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_scan(const PrefixMaps& maps, const PrefixArgs& a, int D_H, int R, int D_R,
+                               cudaStream_t stream) {
+#define LRKV_PS(DH, DR)                                                               \
+    if (D_H == DH && D_R == DR)                                                       \
+        return a.zw == 128 ? launch_scan_t<DH, DR, 128>(maps, a, R, stream)           \
+                           : launch_scan_t<DH, DR, 64>(maps, a, R, stream);
+    LRKV_PS(64, 0) LRKV_PS(64, 64) LRKV_PS(128, 0) LRKV_PS(128, 64)
 #undef LRKV_PS
     return cudaErrorInvalidValue;
 }
