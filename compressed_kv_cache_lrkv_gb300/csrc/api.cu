@@ -547,8 +547,9 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
     if (prefix) {
         a.no_combine = 1;
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
-        cudaError_t e = lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms,
-                                            di.smem_optin, st);
+        cudaError_t e = lrkv::launch_decode_absorb(a, dims->d_h, dims->r, dims->d_rope, st);
+        if (e == cudaSuccess)
+            e = lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms, di.smem_optin, st);
         if (e != cudaSuccess) return cuda_status(e, "lrkv_decode_shared launch");
         lrkv::PrefixArgs p{};
         p.d = a;

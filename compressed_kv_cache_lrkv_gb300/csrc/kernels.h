@@ -56,7 +56,7 @@ struct DecodeArgs {
     int pmax;          // partial slots per head in the workspace (layers * B * nhg + nranges)
     float scale_log2;  // softmax scale * log2(e)
     unsigned long long wait_ns;  // limit of the split kernel's pipeline waits (a debugging aid may shorten it)
-    int no_combine;   // 1: stop after the scan (its partials are merged by the caller's own kernel)
+    int no_combine;   // 1: the scan alone (q~ is in qt or will be by the launch before; the caller merges)
     // Partials out (a token-range split of the sequences): when set, the combine writes each
     // (sequence, head)'s merged, unnormalised [acc_s | acc_z | m | l] ([B][H][D_H + R + 2],
     // m in the log2 domain) here instead of out, and no B^V is read.
@@ -107,7 +107,7 @@ cudaError_t launch_decode(const CUtensorMap& tK, const CUtensorMap& tV, const CU
                           const CUtensorMap& tZV, DecodeArgs a, int D_H, int R, int D_R, int sms, int smem_limit,
                           cudaStream_t stream);
 
-// The absorb kernel alone (q~ = q B^K into a.qt), and the combine alone.
+// q~ = q B^K into a.qt alone (one layer), and the combine alone.
 cudaError_t launch_decode_absorb(const DecodeArgs& a, int D_H, int R, int D_R, cudaStream_t stream);
 cudaError_t launch_decode_combine(const DecodeArgs& a, int D_H, int R, int sms, cudaStream_t stream);
 

@@ -30,22 +30,27 @@ namespace lrkv {
 
 namespace {
 
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr int kThreads = 256;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-
-__device__ __forceinline__ float bf(const uint16_t* p, size_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
 
 __device__ __forceinline__ bool prefix_good(const PrefixArgs& a, int P) {
     return P >= 0 && P <= a.max_blocks * kBlockSize;
 }
 
-// Shared memory: Q [128][D_K + ZW] (64-column blocks of 16 KB), a ring of key stages [64 tokens][D_K
-// + ZW] and one of value stages [64][D_H + ZW] (blocks of 8 KB), barriers.  As many stages as fit.
+// [Q | diag(Q~)] is the A operand of S: its first four 64-column blocks sit in TMEM (an MMA of N = 64
+// would read twice as many bytes of A from shared memory as of B, and shared memory is what bounds
+// it: 32 heads of r = 32 x 32 sequences, 32 K tokens, 33 us instead of 38), a fifth (positional key with zw =
+// 128) in shared memory.  Shared memory: that block (16 KB), a ring of key stages [64 tokens][D_K + ZW] and one
+// of value stages [64][D_H + ZW] (64-column blocks of 8 KB), barriers.  As many stages as fit.
 template <int D_H, int D_R, int ZW>
 struct PxLayout {
     static constexpr int D_K = D_H + D_R;
     static constexpr int NBK = (D_K + ZW) / 64, NBV = (D_H + ZW) / 64;  // 64-column blocks of a key / value row
-    static constexpr uint32_t Q_BYTES = NBK * 16384, K_BYTES = NBK * 8192, V_BYTES = NBV * 8192;
+    static constexpr int QBT = NBK < 4 ? NBK : 4, QBS = NBK - QBT;  // blocks of Q in TMEM, in shared memory
+    static constexpr uint32_t Q_BYTES = QBS * 16384, K_BYTES = NBK * 8192, V_BYTES = NBV * 8192;
     static constexpr uint32_t ROOM = 232448 - 1024 - 512 - Q_BYTES;
     static constexpr int BOTH = ROOM / (K_BYTES + V_BYTES);
     static constexpr int VST = BOTH > 4 ? 4 : BOTH;
@@ -53,9 +58,9 @@ struct PxLayout {
     static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
     static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
     static_assert(VST >= 2 && SMEM <= 232448, "stages");
-    // TMEM columns: two S buffers, O
-    static constexpr uint32_t TM_S = 0, TM_O = 128;
-    static_assert(128 + D_H + ZW <= 512, "TMEM");
+    // TMEM columns: two S buffers, O, Q (two bf16 a column)
+    static constexpr uint32_t TM_S = 0, TM_O = 128, TM_Q = TM_O + D_H + ZW;
+    static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
 };
 
 __device__ __forceinline__ uint64_t kdesc128(uint32_t a) { return sdesc(a, 16, 1024, 2); }
@@ -102,6 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = rh < H && rb < d.B;
     const size_t at = ((size_t)rb * H + rh) * a.nsplit + split;
     if (nt == 0) {  // an empty piece: its sums are not read
+        pdl_wait();  // (this grid's end stands for that of the launches before it)
         if (warp >= 2 && warp < 6 && live) {
             a.ml[at * 2] = -INFINITY;
             a.ml[at * 2 + 1] = 0.f;
@@ -111,7 +117,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
     uint64_t* q_ready = bars + 0;
-    uint64_t* p_full = bars + 1;
+    // p_full[j % 2]: P_j written.  Two, because S_{j+1} may be there before P_j: with one barrier the rows
+    // could write P_{j+1}, a softmax of some 0.5 us later, before warp 7 has looked at the phase of P_j.  P_{j+2}
+    // needs S_{j+2} and that needs P_j V_j.
+    uint64_t* p_full = bars + 28;   // [2]
     uint64_t* s_full = bars + 2;    // [2]
     uint64_t* s_free = bars + 4;    // [2] P_j V_j done: buffer j % 2 may take S_{j+2}
     // o_done[j % 2]: P_j V_j complete (waited for before a rescale only, which is why there are two: one
@@ -130,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(B(q_ready), 128);
-        mbar_init(B(p_full), 128);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(B(p_full + i), 128);
             mbar_init(B(s_full + i), 1);
             mbar_init(B(s_free + i), 1);
             mbar_init(B(o_done + i), 1);
@@ -222,10 +231,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             constexpr uint64_t so = st * (Lay::K_BYTES >> 4);
 #pragma unroll
-            for (int kk = 0; kk < NBK * 4; ++kk)
-                if (elect_one_sync())
-                    tc_mma_bf16(tmem + Lay::TM_S + sb * 64, dQ + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                                dK + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_S, kk > 0);
+            for (int kk = 0; kk < NBK * 4; ++kk) {
+                const uint64_t bd = dK + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
+                if (elect_one_sync()) {
+                    if (kk < Lay::QBT * 4)
+                        tc_mma_bf16_ts(tmem + Lay::TM_S + sb * 64, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
+                    else
+                        tc_mma_bf16(tmem + Lay::TM_S + sb * 64, dQ + ((kk & 3) * 32 >> 4), bd, id_S, 1);
+                }
+            }
             if (elect_one_sync()) {
                 tc_commit(B(s_full + sb));
                 tc_commit(B(k_empty + st));
@@ -248,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dV = mndesc128(S0 + Lay::OFF_V);
         auto pv_tile = [&](int j, auto UU) -> bool {
             constexpr int U = decltype(UU)::value, st = U % VST, sb = U & 1;
-            if (aborted() || !wait_all(B(p_full), j & 1, d.status) ||
+            if (aborted() || !wait_all(B(p_full + sb), (j >> 1) & 1, d.status) ||
                 !wait_all(B(v_full + st), (j / VST) & 1, d.status))
                 return false;
             tc_fence_after();
@@ -277,27 +291,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------------- query rows: softmax, partials
         const uint32_t tl = (uint32_t)(qq * 32) << 16;
         {
-            // [Q | diag(Q~)] row, K-major with 128-byte swizzle: 16-byte chunk c of a 64-column block lies at c ^
-            // (row mod 8).  q~ is rounded to bf16, as in the prefill.
+            // [Q | diag(Q~)] row, block by block of 64 columns: into TMEM (two columns a register), or K-major with
+            // 128-byte swizzle (16-byte chunk c at c ^ (row mod 8)).  q~ is rounded to bf16, as in the prefill.
             const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint4* q = reinterpret_cast<const uint4*>(d.q + ((size_t)(live ? rb : 0) * H + (live ? rh : 0)) * D_K);
-            uint8_t* qrow = smem + row * 128;
-#pragma unroll 8
-            for (int c = 0; c < D_K / 8; ++c)
-                *reinterpret_cast<uint4*>(qrow + (c >> 3) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = live ? q[c] : zero;
-            const float* qt = d.qt + ((size_t)(live ? rb : 0) * H + (live ? rh : 0)) * R;
-            for (int c = 0; c < ZW / 8; ++c) {
-                const int col = c * 8 - hl * R;
-                uint4 v = zero;
-                if (live && col >= 0 && col < R) {
-                    const float4 x = *reinterpret_cast<const float4*>(qt + col);
-                    const float4 y = *reinterpret_cast<const float4*>(qt + col + 4);
-                    v = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
-                                   pack_bf16x2(y.z, y.w));
+            const size_t qr = (size_t)(live ? rb : 0) * H + (live ? rh : 0);
+            const uint4* q = reinterpret_cast<const uint4*>(d.q + qr * D_K);
+            const float* qt = d.qt + qr * R;
+#pragma unroll
+            for (int bk = 0; bk < NBK; ++bk) {
+                if (bk == D_K / 64) pdl_wait();  // q~
+                uint32_t v[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint4 x = zero;
+                    if (bk < D_K / 64) {
+                        if (live) x = q[bk * 8 + c];
+                    } else {
+                        const int col = (bk - D_K / 64) * 64 + c * 8 - hl * R;
+                        if (live && col >= 0 && col < R) {
+                            const float4 y = *reinterpret_cast<const float4*>(qt + col);
+                            const float4 z = *reinterpret_cast<const float4*>(qt + col + 4);
+                            x = make_uint4(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w), pack_bf16x2(z.x, z.y),
+                                           pack_bf16x2(z.z, z.w));
+                        }
+                    }
+                    v[4 * c] = x.x;
+                    v[4 * c + 1] = x.y;
+                    v[4 * c + 2] = x.z;
+                    v[4 * c + 3] = x.w;
                 }
-                *reinterpret_cast<uint4*>(qrow + (D_K / 64 + (c >> 3)) * 16384 + (((c & 7) ^ (row & 7)) << 4)) = v;
+                if (bk < Lay::QBT) {
+                    tmem_st_32x32b_x32(tmem + tl + Lay::TM_Q + bk * 32, v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4*>(smem + row * 128 + ((c ^ (row & 7)) << 4)) =
+                            make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                }
             }
+            tmem_wait_st();
             fence_proxy_async_smem();
+            tc_fence_before();
             mbar_arrive(B(q_ready));
         }
         bool ok = true;
@@ -386,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             fence_proxy_async_smem();  // cleared value rows (if any) before the tensor cores read them
             tc_fence_before();
-            mbar_arrive(B(p_full));
+            mbar_arrive(B(p_full + (j & 1)));
         }
         // ---- partials, unnormalised
         if (ok) ok = wait_all(B(o_done + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, d.status);
@@ -436,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     }
+    pdl_trigger();  // the combine waits for this grid's end
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -444,16 +479,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// grid (H, B), a thread per column of the accumulator.
+// Merge of the prefix's pieces and the sequence's own partials: grid (H, B), block nsl slices x W / 4
+// column quads (nsl a power of two, at least D_H threads).  A slice merges every nsl-th partial, four
+// loads in flight; the slices are merged in shared memory, then B_h^V (copied there meanwhile).  (One
+// thread per column walking all partials took 27 us for 32 heads x 32 sequences x 20 partials; this
+// takes 6.)
 template <int D_H, int R>
-__global__ void __launch_bounds__(192) prefix_combine_kernel(const PrefixArgs a) {
-    constexpr int W = D_H + R;
+__global__ void __launch_bounds__(8 * (D_H + R) / 4) prefix_combine_kernel(const PrefixArgs a) {
+    constexpr int W = D_H + R, W4 = W / 4, NSL_MAX = 8, PPS = 4;
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int nsl = blockDim.x / W4;
     const DecodeArgs& d = a.d;
+    __shared__ float sm_m[NSL_MAX], sm_l[NSL_MAX];
+    __shared__ __align__(16) float sm_acc[NSL_MAX][W];
+    __shared__ __align__(16) uint16_t sm_bv[D_H * R];
     const int P = a.len[0], L = a.suffix ? d.seq_lens[b] : 0;
     const bool bad = !prefix_good(a, P) || L < 0 || L > d.max_pages * kBlockSize || (!d.part_out && P + L == 0);
     float* pdst = d.part_out ? d.part_out + ((size_t)b * d.H + h) * (W + 2) : nullptr;
     uint16_t* dst = d.out + ((size_t)b * d.H + h) * D_H;
+    if (!pdst && !bad) {
+        const uint16_t* bv = d.BV + (size_t)h * D_H * R;
+        for (int i = tid; i < D_H * R / 8; i += blockDim.x)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(sm_bv + i * 8)), "l"(bv + i * 8)
+                         : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    pdl_wait();  // the scans
     if (bad) {
         if (tid == 0 && h == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
         if (pdst) {
@@ -464,48 +515,109 @@ __global__ void __launch_bounds__(192) prefix_combine_kernel(const PrefixArgs a)
         return;
     }
     const size_t at = ((size_t)b * d.H + h) * a.nsplit;
-    const float* ml0 = a.ml + at * 2;
-    const float* ac0 = a.acc + at * W;
-    int np = 0;
-    const float *ml1 = nullptr, *ac1 = nullptr;
+    const float2* ml0 = reinterpret_cast<const float2*>(a.ml) + at;
+    const float4* ac0 = reinterpret_cast<const float4*>(a.acc + at * W);
+    const int n0 = P > 0 ? a.nsplit : 0;
+    int n = n0;
+    const float2* ml1 = ml0;
+    const float4* ac1 = ac0;
     if (L > 0) {
         const int2 fe = d.seg_table[b * d.nhg + h / (d.H / d.nhg)];
-        np = fe.y;
-        ml1 = d.part_ml + ((size_t)h * d.pmax + fe.x) * 2;
-        ac1 = d.part_acc + ((size_t)h * d.pmax + fe.x) * W;
+        n += fe.y;
+        ml1 = reinterpret_cast<const float2*>(d.part_ml) + (size_t)h * d.pmax + fe.x - n0;
+        ac1 = reinterpret_cast<const float4*>(d.part_acc + ((size_t)h * d.pmax + fe.x) * W) - (ptrdiff_t)n0 * W4;
     }
-    const int n0 = P > 0 ? a.nsplit : 0;
-    float M = -INFINITY;
-    for (int i = 0; i < n0; ++i) M = fmaxf(M, ml0[2 * i]);
-    for (int i = 0; i < np; ++i) M = fmaxf(M, ml1[2 * i]);
-    float l = 0.f, v = 0.f;
-    for (int i = 0; i < n0; ++i) {
-        const float w = ml0[2 * i] == -INFINITY ? 0.f : exp2f(ml0[2 * i] - M);
-        l = fmaf(w, ml0[2 * i + 1], l);
-        if (tid < W && w != 0.f) v = fmaf(w, ac0[(size_t)i * W + tid], v);
-    }
-    for (int i = 0; i < np; ++i) {
-        const float w = ml1[2 * i] == -INFINITY ? 0.f : exp2f(ml1[2 * i] - M);
-        l = fmaf(w, ml1[2 * i + 1], l);
-        if (tid < W && w != 0.f) v = fmaf(w, ac1[(size_t)i * W + tid], v);
-    }
-    if (pdst) {
-        if (tid < W) pdst[tid] = v;
-        if (tid == 0) {
-            pdst[W] = M;
-            pdst[W + 1] = l;
+    const int sl = tid / W4, c4 = tid - sl * W4;
+    float m = -INFINITY, l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = sl; p0 < n; p0 += nsl * PPS) {
+        float2 ml[PPS];
+        float4 x[PPS];
+#pragma unroll
+        for (int u = 0; u < PPS; ++u) {
+            const int p = p0 + u * nsl;
+            ml[u] = p < n ? (p < n0 ? ml0 : ml1)[p] : make_float2(-INFINITY, 0.f);
+            // (an empty piece's sums were not written; those of a part that has them are read whatever m is)
+            x[u] = p < n && ml[u].x != -INFINITY ? (p < n0 ? ac0 : ac1)[(size_t)p * W4 + c4]
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        return;
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < PPS; ++u) mn = fmaxf(mn, ml[u].x);
+        if (mn == -INFINITY) continue;
+        const float sc = m == -INFINITY ? 0.f : exp2f(m - mn);
+        l *= sc;
+        v.x *= sc;
+        v.y *= sc;
+        v.z *= sc;
+        v.w *= sc;
+#pragma unroll
+        for (int u = 0; u < PPS; ++u) {
+            const float w = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - mn);
+            l = fmaf(w, ml[u].y, l);
+            v.x = fmaf(w, x[u].x, v.x);
+            v.y = fmaf(w, x[u].y, v.y);
+            v.z = fmaf(w, x[u].z, v.z);
+            v.w = fmaf(w, x[u].w, v.w);
+        }
+        m = mn;
     }
-    __shared__ float sv[W];
-    if (tid < W) sv[tid] = v;
+    if (sl < nsl) {
+        *reinterpret_cast<float4*>(&sm_acc[sl][c4 * 4]) = v;
+        if (c4 == 0) {
+            sm_m[sl] = m;
+            sm_l[sl] = l;
+        }
+    }
+    __syncthreads();
+    if (tid < W4) {
+        float M = -INFINITY;
+        for (int i = 0; i < nsl; ++i) M = fmaxf(M, sm_m[i]);
+        float ls = 0.f;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < nsl; ++i) {
+            const float w = sm_m[i] == -INFINITY ? 0.f : exp2f(sm_m[i] - M);
+            const float4 x = *reinterpret_cast<const float4*>(&sm_acc[i][tid * 4]);
+            ls = fmaf(w, sm_l[i], ls);
+            t.x = fmaf(w, x.x, t.x);
+            t.y = fmaf(w, x.y, t.y);
+            t.z = fmaf(w, x.z, t.z);
+            t.w = fmaf(w, x.w, t.w);
+        }
+        if (pdst) {  // unnormalised
+            pdst[tid * 4] = t.x;
+            pdst[tid * 4 + 1] = t.y;
+            pdst[tid * 4 + 2] = t.z;
+            pdst[tid * 4 + 3] = t.w;
+            if (tid == 0) {
+                pdst[W] = M;
+                pdst[W + 1] = ls;
+            }
+        }
+        // (ls is 0 only where every page of the tokens was a bad one: zeros then)
+        const float inv = ls == 0.f ? 0.f : 1.f / ls;
+        *reinterpret_cast<float4*>(&sm_acc[0][tid * 4]) = make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
+    }
+    if (pdst) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (tid < D_H) {
-        float x = sv[tid];
-        const uint16_t* bv = d.BV + ((size_t)h * D_H + tid) * R;
+        float x = sm_acc[0][tid];
+        const uint4* bvr = reinterpret_cast<const uint4*>(sm_bv + tid * R);
+        const float* z = &sm_acc[0][D_H];
 #pragma unroll
-        for (int j = 0; j < R; ++j) x = fmaf(bf(bv, j), sv[D_H + j], x);
-        const __nv_bfloat16 ob = __float2bfloat16_rn(l > 0.f ? x / l : 0.f);
+        for (int i = 0; i < R / 8; ++i) {
+            const uint4 w = bvr[i];
+            x = fmaf(bf16lo(w.x), z[i * 8 + 0], x);
+            x = fmaf(bf16hi(w.x), z[i * 8 + 1], x);
+            x = fmaf(bf16lo(w.y), z[i * 8 + 2], x);
+            x = fmaf(bf16hi(w.y), z[i * 8 + 3], x);
+            x = fmaf(bf16lo(w.z), z[i * 8 + 4], x);
+            x = fmaf(bf16hi(w.z), z[i * 8 + 5], x);
+            x = fmaf(bf16lo(w.w), z[i * 8 + 6], x);
+            x = fmaf(bf16hi(w.w), z[i * 8 + 7], x);
+        }
+        const __nv_bfloat16 ob = __float2bfloat16_rn(x);
         dst[tid] = *reinterpret_cast<const uint16_t*>(&ob);
     }
 }
@@ -560,6 +672,24 @@ void prefix_carve_workspace(PrefixArgs* a, void* ws, int D_H, int R) {
                                       align256((size_t)a->d.B * a->d.H * a->nsplit * 2 * sizeof(float)));
 }
 
+// A launch that may start before the one before it on the stream has ended (programmatic dependent
+// launch): the kernels wait for it where they first read what it writes, and in every block.
+template <typename... Args>
+static cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int D_H, int D_R, int ZW>
 static cudaError_t launch_scan_t(const PrefixMaps& maps, const PrefixArgs& a, int R, cudaStream_t stream) {
     constexpr uint32_t smem = PxLayout<D_H, D_R, ZW>::SMEM;
@@ -567,8 +697,7 @@ static cudaError_t launch_scan_t(const PrefixMaps& maps, const PrefixArgs& a, in
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int stiles = (a.d.B + a.ns - 1) / a.ns;
-    kern<<<dim3(a.htiles * stiles, a.nsplit), kThreads, smem, stream>>>(maps, a, R);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(a.htiles * stiles, a.nsplit), kThreads, smem, stream, maps, a, R);
 }
 
 cudaError_t launch_prefix_scan(const PrefixMaps& maps, const PrefixArgs& a, int D_H, int R, int D_R,
@@ -585,8 +714,9 @@ cudaError_t launch_prefix_scan(const PrefixMaps& maps, const PrefixArgs& a, int 
 cudaError_t launch_prefix_combine(const PrefixArgs& a, int D_H, int R, cudaStream_t stream) {
 #define LRKV_PC(DH, RR)                                                               \
     if (D_H == DH && R == RR) {                                                       \
-        prefix_combine_kernel<DH, RR><<<dim3(a.d.H, a.d.B), 192, 0, stream>>>(a);     \
-        return cudaGetLastError();                                                    \
+        const int nsl = a.nsplit > 4 ? 8 : 4;                                         \
+        return launch_dependent(prefix_combine_kernel<DH, RR>, dim3(a.d.H, a.d.B),    \
+                                nsl * (DH + RR) / 4, 0, stream, a);                   \
     }
     LRKV_PC(64, 8) LRKV_PC(64, 16) LRKV_PC(64, 32) LRKV_PC(128, 8) LRKV_PC(128, 16) LRKV_PC(128, 32)
 #undef LRKV_PC
