@@ -388,8 +388,8 @@ static lrkv::PrefixPlan plan_prefix(const lrkv_dims* dims, int batch, int max_bl
     return lrkv::prefix_plan(dims->H, dims->d_h, dims->r, dims->d_rope, batch, max_blocks, di.sms);
 }
 
-// Scan of the prefix (q~ is in p.d.qt) and the merge with the sequences' own partials, if any.
-static lrkv_status prefix_launch(lrkv::PrefixArgs& p, const lrkv_dims* dims, const lrkv_cache* cache,
+// Scan of the prefix behind the launch that leaves q~ in p->d.qt; fills *p for the merge.
+static lrkv_status prefix_launch(lrkv::PrefixArgs* p, const lrkv_dims* dims, const lrkv_cache* cache,
                                  const SharedPrefix& prefix, int suffix, const lrkv::PrefixPlan& plan, void* ws,
                                  cudaStream_t st, const char* what) {
     lrkv::PrefixMaps m;
@@ -401,19 +401,17 @@ static lrkv_status prefix_launch(lrkv::PrefixArgs& p, const lrkv_dims* dims, con
         (s = make_tmap(&m.zK, cache->zK, HR, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "zK")) != LRKV_OK ||
         (s = make_tmap(&m.zV, cache->zV, HR, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "zV")) != LRKV_OK)
         return s;
-    p.blocks = prefix.blocks;
-    p.len = prefix.len;
-    p.max_blocks = prefix.max_blocks;
-    p.suffix = suffix;
-    p.nsplit = plan.nsplit;
-    p.zw = plan.zw;
-    p.hb = plan.hb;
-    p.ns = plan.ns;
-    p.htiles = plan.htiles;
-    lrkv::prefix_carve_workspace(&p, ws, dims->d_h, dims->r);
-    cudaError_t e = lrkv::launch_prefix_scan(m, p, dims->d_h, dims->r, dims->d_rope, st);
-    if (e == cudaSuccess) e = lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st);
-    return cuda_status(e, what);
+    p->blocks = prefix.blocks;
+    p->len = prefix.len;
+    p->max_blocks = prefix.max_blocks;
+    p->suffix = suffix;
+    p->nsplit = plan.nsplit;
+    p->zw = plan.zw;
+    p->hb = plan.hb;
+    p->ns = plan.ns;
+    p->htiles = plan.htiles;
+    lrkv::prefix_carve_workspace(p, ws, dims->d_h, dims->r);
+    return cuda_status(lrkv::launch_prefix_scan(m, *p, dims->d_h, dims->r, dims->d_rope, st), what);
 }
 
 static lrkv_status check_prefix(const lrkv_dims* dims, const SharedPrefix& p) {
@@ -547,14 +545,26 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
     if (prefix) {
         a.no_combine = 1;
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        what = "lrkv_decode_shared launch";
+        // Absorb, the prefix's scan, the sequences' own, the merge.  The second scan starts on SMs as the
+        // first leaves them; where nobody asks for a number of pieces it has one per 256 KB of the
+        // tables' capacity, as short own parts cut into one piece per SM cost more in start-up than they stream.
+        if (dims->num_splits == 0) {
+            const double cap = (double)batch * max_blocks_per_seq * (double)lrkv_cache_block_bytes(dims);
+            const double pieces = cap / (256 << 10);
+            a.nranges = pieces < 16 ? (nranges < 16 ? nranges : 16) : pieces < nranges ? (int)pieces : nranges;
+        }
         cudaError_t e = lrkv::launch_decode_absorb(a, dims->d_h, dims->r, dims->d_rope, st);
-        if (e == cudaSuccess)
-            e = lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms, di.smem_optin, st);
-        if (e != cudaSuccess) return cuda_status(e, "lrkv_decode_shared launch");
         lrkv::PrefixArgs p{};
         p.d = a;
-        return prefix_launch(p, dims, cache, *prefix, 1, pplan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
-                             "lrkv_decode_shared launch");
+        if (e == cudaSuccess &&
+            (s = prefix_launch(&p, dims, cache, *prefix, 1, pplan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
+                               what)) != LRKV_OK)
+            return s;
+        if (e == cudaSuccess)
+            e = lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms, di.smem_optin, st);
+        if (e == cudaSuccess) e = lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st);
+        return cuda_status(e, what);
     }
     return cuda_status(lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms,
                                            di.smem_optin,
@@ -671,8 +681,10 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = lrkv::launch_decode_absorb(p.d, dims->d_h, dims->r, dims->d_rope, st);
     if (e != cudaSuccess) return cuda_status(e, "lrkv_prefix_partials launch");
-    return prefix_launch(p, dims, cache, prefix, 0, plan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
-                         "lrkv_prefix_partials launch");
+    if ((s = prefix_launch(&p, dims, cache, prefix, 0, plan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
+                           "lrkv_prefix_partials launch")) != LRKV_OK)
+        return s;
+    return cuda_status(lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st), "lrkv_prefix_partials launch");
 }
 
 // ------------------------------------------------------------------ quantised cache

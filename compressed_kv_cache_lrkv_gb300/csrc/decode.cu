@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(256, 1)
             ctl->advance(a.seg_table);
         }
         if (!qt_ready) {
-            pdl_wait();  // q~ written by the absorb kernel
+            if (!a.no_combine) pdl_wait();  // q~ written by the absorb kernel (else it was there at the launch)
             qt_ready = true;
         }
 
@@ -621,6 +621,8 @@ __global__ void __launch_bounds__(256, 1)
             }
         }
     }
+    // This grid's end stands for that of the launch before it, too.
+    if (a.no_combine) pdl_wait();
     // The combine kernel may now be scheduled; it waits for this grid to finish.
     pdl_trigger();
     // After an expired wait, make sure no copy is still landing in shared memory

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 a.seg_table[vb] = make_int2(pslot, np);
             }
             if (!qt_ready) {
-                pdl_wait_grid();  // q~ written by the absorb kernel (no-op for an ordinary launch)
+                if (!a.no_combine) pdl_wait_grid();  // q~ written by the absorb kernel (no-op for an ordinary launch)
                 qt_ready = true;
             }
             float qt[R];
@@ -515,6 +515,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++segn;
         }
     }
+    if (a.no_combine) pdl_wait_grid();  // this grid's end stands for that of the launch before it, too
     pdl_trigger_grid();
     tc_fence_before();
     __syncthreads();

@@ -56,7 +56,9 @@ struct DecodeArgs {
     int pmax;          // partial slots per head in the workspace (layers * B * nhg + nranges)
     float scale_log2;  // softmax scale * log2(e)
     unsigned long long wait_ns;  // limit of the split kernel's pipeline waits (a debugging aid may shorten it)
-    int no_combine;   // 1: the scan alone (q~ is in qt or will be by the launch before; the caller merges)
+    // 1: the scan alone, as a dependent launch behind one that itself has waited for q~ (so the scan does
+    // not, and ends only after that launch); the caller merges the partials.
+    int no_combine;
     // Partials out (a token-range split of the sequences): when set, the combine writes each
     // (sequence, head)'s merged, unnormalised [acc_s | acc_z | m | l] ([B][H][D_H + R + 2],
     // m in the log2 domain) here instead of out, and no B^V is read.

@@ -299,7 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* qt = d.qt + qr * R;
 #pragma unroll
             for (int bk = 0; bk < NBK; ++bk) {
-                if (bk == D_K / 64) pdl_wait();  // q~
+                if (bk == D_K / 64) {
+                    pdl_wait();     // q~
+                    pdl_trigger();  // the scan of the sequences' own tokens may fill the SMs that this grid leaves
+                }
                 uint32_t v[32];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
@@ -470,7 +473,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort_flag = 1;
         }
     }
-    pdl_trigger();  // the combine waits for this grid's end
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -537,9 +539,7 @@ __global__ void __launch_bounds__(8 * (D_H + R) / 4) prefix_combine_kernel(const
         for (int u = 0; u < PPS; ++u) {
             const int p = p0 + u * nsl;
             ml[u] = p < n ? (p < n0 ? ml0 : ml1)[p] : make_float2(-INFINITY, 0.f);
-            // (an empty piece's sums were not written; those of a part that has them are read whatever m is)
-            x[u] = p < n && ml[u].x != -INFINITY ? (p < n0 ? ac0 : ac1)[(size_t)p * W4 + c4]
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[u] = p < n ? (p < n0 ? ac0 : ac1)[(size_t)p * W4 + c4] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float mn = m;
 #pragma unroll
@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(8 * (D_H + R) / 4) prefix_combine_kernel(const
         v.w *= sc;
 #pragma unroll
         for (int u = 0; u < PPS; ++u) {
-            const float w = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - mn);
+            if (ml[u].x == -INFINITY) continue;  // an empty piece: its sums were not written
+            const float w = exp2f(ml[u].x - mn);
             l = fmaf(w, ml[u].y, l);
             v.x = fmaf(w, x[u].x, v.x);
             v.y = fmaf(w, x[u].y, v.y);
@@ -626,6 +627,9 @@ __global__ void __launch_bounds__(8 * (D_H + R) / 4) prefix_combine_kernel(const
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+#ifndef PXS
+#define PXS 0
+#endif
 // Which tile: the fewest tensor-core products, tiles x (d_k + d_h + 2 zw) (one of 64 columns covers
 // twice the sequences of one of 128 with half the heads).  How many pieces: a piece costs its pages
 // and about kPieceCost pages more (Q, pipeline fill, partials), and the pieces of all tiles run in
@@ -648,6 +652,7 @@ PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, in
         }
     }
     const long long ntiles = (long long)best.htiles * best.stiles;
+    sms -= PXS;
     long long least = -1;
     for (int s = 1; s <= max_blocks && s <= 65535 && (s == 1 || ntiles * s <= 4LL * sms); ++s) {
         const long long waves = (ntiles * s + sms - 1) / sms;
