@@ -711,7 +711,7 @@ static lrkv_status quant_store(bool write, const lrkv_dims* dims, int32_t n_tok,
     if (s != LRKV_OK) return s;
     if ((s = check_cache(cache)) != LRKV_OK) return s;
     if ((s = check_quant_cache(qcache)) != LRKV_OK) return s;
-    if (n_tok < 0) return fail(LRKV_ERR_INVALID_ARG, "n_tok %d < 0", n_tok);
+    if (n_tok < 0 || n_tok > (1 << 30)) return fail(LRKV_ERR_INVALID_ARG, "n_tok %d outside [0, 2^30]", n_tok);
     if (n_tok == 0) return ok();
     if (!bf16_slots || !quant_slots) return fail(LRKV_ERR_INVALID_ARG, "bf16_slots or quant_slots is NULL");
     lrkv::QuantStoreArgs a{};
@@ -727,9 +727,11 @@ static lrkv_status quant_store(bool write, const lrkv_dims* dims, int32_t n_tok,
     a.bf_nslots = (long long)cache->num_blocks * dims->block_size;
     a.q_nslots = (long long)qcache->num_blocks * dims->block_size;
     a.q = lrkv::quant_layout(dims->d_h, dims->d_rope, dims->H, dims->r);
+    DeviceInfo di;
+    if ((s = device_info(&di)) != LRKV_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return write ? cuda_status(lrkv::launch_cache_quantize(a, st), "lrkv_cache_quantize launch")
-                 : cuda_status(lrkv::launch_cache_dequantize(a, st), "lrkv_cache_dequantize launch");
+    return write ? cuda_status(lrkv::launch_cache_quantize(a, di.sms, st), "lrkv_cache_quantize launch")
+                 : cuda_status(lrkv::launch_cache_dequantize(a, di.sms, st), "lrkv_cache_dequantize launch");
 }
 
 lrkv_status lrkv_cache_quantize(const lrkv_dims* dims, int32_t n_tok, const lrkv_cache* cache,

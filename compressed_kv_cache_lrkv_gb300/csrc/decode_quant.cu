@@ -32,6 +32,7 @@
 
 #include "decode_work.cuh"
 #include "lrkv_internal.cuh"
+#include "quant.cuh"
 #include "quant.h"
 
 namespace lrkv {
@@ -80,15 +81,6 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     return *static_cast<const uint8_t*>(__cvta_shared_to_generic(a));
-}
-// Values q_i 2^k of two bytes (b0, b1 of [b0, 0, b1, 0]) as bf16, s2 = (2^k, 2^k): with the low seven
-// bits in its mantissa bf16 holds 128 + u mod 128, from which 256 or, where the byte's top bit is
-// set, 128 is taken; both steps and the product are exact.
-__device__ __forceinline__ uint32_t bytes_bf16(uint32_t v, __nv_bfloat162 s2) {
-    const uint32_t lo = (v & 0x007f007fu) | 0x43004300u, hi = (v & 0x00800080u) ^ 0x43804380u;
-    const __nv_bfloat162 r = __hmul2(
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&lo), *reinterpret_cast<const __nv_bfloat162*>(&hi)), s2);
-    return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -337,10 +329,8 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                                              : "=r"(x[0]), "=r"(x[1])
                                              : "r"(ra + D_K + c * 8));
                                 const uint32_t sb = lds8(ra + ql.off_sc + D_K / kQuantBlock + (c >> 2));
-                                // the scale twice in bf16 (NaN for byte 255); zero for tokens behind the end
-                                // (their probabilities are 0, and 0 x NaN is not)
-                                uint32_t s2 = sb == 255 ? 0x7fc07fc0u : sb * 0x00800080u;
-                                s2 = row < nvalid ? s2 : 0u;
+                                // zero for tokens behind the end (their probabilities are 0, and 0 x NaN is not)
+                                const uint32_t s2 = row < nvalid ? scale_bf16x2(sb) : 0u;
                                 const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&s2);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)

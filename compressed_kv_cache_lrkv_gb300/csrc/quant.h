@@ -55,8 +55,8 @@ struct QuantStoreArgs {
     long long bf_nslots, q_nslots;
     QuantLayout q;
 };
-cudaError_t launch_cache_quantize(const QuantStoreArgs& a, cudaStream_t stream);
-cudaError_t launch_cache_dequantize(const QuantStoreArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_quantize(const QuantStoreArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_cache_dequantize(const QuantStoreArgs& a, int sms, cudaStream_t stream);
 
 // Decode over quantised rows.  `d` carries queries, factors, outputs, workspace and the work plan
 // as for the bf16 decode (its pools are unused); one layer, one head group.
