@@ -384,8 +384,17 @@ struct SharedPrefix {
     const int32_t* len;
 };
 
-static lrkv::PrefixPlan plan_prefix(const lrkv_dims* dims, int batch, int max_blocks, const DeviceInfo& di) {
-    return lrkv::prefix_plan(dims->H, dims->d_h, dims->r, dims->d_rope, batch, max_blocks, di.sms);
+// own_blocks: pages per sequence of the sequences' own tables (0: none).
+static lrkv::PrefixPlan plan_prefix(const lrkv_dims* dims, int batch, int max_blocks, int own_blocks,
+                                    const DeviceInfo& di) {
+    const double own = (double)batch * own_blocks * (double)lrkv_cache_block_bytes(dims);
+    return lrkv::prefix_plan(dims->H, dims->d_h, dims->r, dims->d_rope, batch, max_blocks, own, di.sms);
+}
+
+// Workspace of the prefix's partials, enough for any plan of these sizes.
+static size_t prefix_bytes(const lrkv_dims* dims, int batch, int max_blocks, const DeviceInfo& di) {
+    const int most = lrkv::prefix_most_splits(dims->H, dims->d_h, dims->r, dims->d_rope, batch, max_blocks, di.sms);
+    return lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, most);
 }
 
 // Scan of the prefix behind the launch that leaves q~ in p->d.qt; fills *p for the merge.
@@ -490,9 +499,9 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
     const int nranges = decode_ranges(dims, di.sms);
     const size_t scan_bytes = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, nvb, nranges);
     lrkv::PrefixPlan pplan{};
-    if (prefix) pplan = plan_prefix(dims, batch, prefix->max_blocks, di);
+    if (prefix) pplan = plan_prefix(dims, batch, prefix->max_blocks, max_blocks_per_seq, di);
     const size_t need =
-        scan_bytes + (prefix ? lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, pplan.nsplit) : 0);
+        scan_bytes + (prefix ? prefix_bytes(dims, batch, prefix->max_blocks, di) : 0);
     if (!workspace || ((uintptr_t)workspace & 255u))
         return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
@@ -546,12 +555,14 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
         a.no_combine = 1;
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
         what = "lrkv_decode_shared launch";
-        // Absorb, the prefix's scan, the sequences' own, the merge.  The second scan starts on SMs as the
-        // first leaves them; where nobody asks for a number of pieces it has one per 256 KB of the
-        // tables' capacity, as short own parts cut into one piece per SM cost more in start-up than they stream.
+        // Absorb, the prefix's scan, the sequences' own, the merge.  The second scan starts on the SMs that
+        // the first has left to it, or as it leaves them.  Where nobody asks for a number of pieces it
+        // has one per SM left to it, else one per 256 KB of the tables' capacity: short own parts cut into one piece
+        // per SM cost more in start-up than they stream.
         if (dims->num_splits == 0) {
+            const int idle = di.sms - pplan.htiles * pplan.stiles * pplan.nsplit;
             const double cap = (double)batch * max_blocks_per_seq * (double)lrkv_cache_block_bytes(dims);
-            const double pieces = cap / (256 << 10);
+            const double pieces = pplan.own_sms > 0 ? (idle > pplan.own_sms ? idle : pplan.own_sms) : cap / (256 << 10);
             a.nranges = pieces < 16 ? (nranges < 16 ? nranges : 16) : pieces < nranges ? (int)pieces : nranges;
         }
         cudaError_t e = lrkv::launch_decode_absorb(a, dims->d_h, dims->r, dims->d_rope, st);
@@ -563,7 +574,7 @@ static lrkv_status decode_impl(const lrkv_dims* dims, int32_t num_layers, const 
             return s;
         if (e == cudaSuccess)
             e = lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms, di.smem_optin, st);
-        if (e == cudaSuccess) e = lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st);
+        if (e == cudaSuccess) e = lrkv::launch_prefix_combine(p, dims->d_h, dims->r, di.sms, st);
         return cuda_status(e, what);
     }
     return cuda_status(lrkv::launch_decode(tK, tV, tZK, tZV, a, dims->d_h, dims->r, dims->d_rope, di.sms,
@@ -629,8 +640,7 @@ size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, 
     DeviceInfo di;
     if (device_info(&di) != LRKV_OK) return 0;
     return lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, decode_ranges(dims, di.sms)) +
-           lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch,
-                                        plan_prefix(dims, batch, max_prefix_blocks, di).nsplit);
+           prefix_bytes(dims, batch, max_prefix_blocks, di);
 }
 
 lrkv_status lrkv_decode_shared(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
@@ -661,8 +671,8 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
     if ((s = device_info(&di)) != LRKV_OK) return s;
     const int nranges = decode_ranges(dims, di.sms);
     const size_t scan_bytes = lrkv::decode_workspace_bytes(dims->H, dims->d_h, dims->r, batch, nranges);
-    const lrkv::PrefixPlan plan = plan_prefix(dims, batch, max_prefix_blocks, di);
-    const size_t need = scan_bytes + lrkv::prefix_workspace_bytes(dims->H, dims->d_h, dims->r, batch, plan.nsplit);
+    const lrkv::PrefixPlan plan = plan_prefix(dims, batch, max_prefix_blocks, 0, di);
+    const size_t need = scan_bytes + prefix_bytes(dims, batch, max_prefix_blocks, di);
     if (!workspace || ((uintptr_t)workspace & 255u))
         return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
@@ -684,7 +694,7 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
     if ((s = prefix_launch(&p, dims, cache, prefix, 0, plan, static_cast<uint8_t*>(workspace) + scan_bytes, st,
                            "lrkv_prefix_partials launch")) != LRKV_OK)
         return s;
-    return cuda_status(lrkv::launch_prefix_combine(p, dims->d_h, dims->r, st), "lrkv_prefix_partials launch");
+    return cuda_status(lrkv::launch_prefix_combine(p, dims->d_h, dims->r, di.sms, st), "lrkv_prefix_partials launch");
 }
 
 // ------------------------------------------------------------------ quantised cache

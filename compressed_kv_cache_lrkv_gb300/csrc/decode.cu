@@ -985,49 +985,73 @@ static cudaError_t launch_decode_t(const CUtensorMap& tK, const CUtensorMap& tV,
     return launch_combine<D_H, R>(a, nvb, sms, stream);
 }
 
-// q~ of eight sequences per block (grid (H, ceil(B / 8)), a warp per sequence, one layer): B_h^K is
-// read once for the eight instead of once per (head, sequence).  Lane = (slice of d, j) so that a
-// warp reads 32 consecutive floats of B_h^K per step.  (48 sequences of 128 heads: 10 -> 4 us.)
+// q~ of sixteen sequences and one head per block, on the warp-level tensor cores (sequences on M, the r
+// columns on N; bf16 products are exact and summed in fp32): B_h^K is read once for the sixteen instead
+// of once per (head, sequence).  Four warps split d, so that a warp's loads (B's fragments want pairs along d
+// of the row-major [d][r] and are gathered as single values) are all in flight together.
+// (128 heads x 48 sequences: 10 us with a block per head and sequence; with a warp per head over all of d 6.)
 template <int D_H, int R, int D_R>
-__global__ void __launch_bounds__(256) absorb_batch_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(128) absorb_batch_kernel(const DecodeArgs a) {
     pdl_wait();
     pdl_trigger();
-    constexpr int SL = 32 / R;  // slices of d
-    const int h = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.y * 8 + warp;
-    __shared__ __align__(16) float bk[D_H * R];
-    __shared__ __align__(16) float qs[8][D_H];
-    const uint4* src = reinterpret_cast<const uint4*>(a.BK + (size_t)h * D_H * R);
-    for (int i = threadIdx.x; i < D_H * R / 8; i += 256) {
-        const uint4 v = src[i];
-        float4* dst = reinterpret_cast<float4*>(bk + i * 8);
-        dst[0] = make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
-        dst[1] = make_float4(bf16lo(v.z), bf16hi(v.z), bf16lo(v.w), bf16hi(v.w));
+    constexpr int KS = D_H / 64;  // 16-wide k steps of a warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
+    const int h = blockIdx.x, b0 = blockIdx.y * 16;
+    __shared__ float part[3][16][R];
+    const uint16_t* bk = a.BK + (size_t)h * D_H * R;
+    auto qrow = [&](int b) {
+        return reinterpret_cast<const uint32_t*>(a.q + ((size_t)min(b, a.B - 1) * a.H + h) * (D_H + D_R));
+    };
+    const uint32_t *q0 = qrow(b0 + g), *q1 = qrow(b0 + g + 8);
+    uint32_t af[KS][4], bf[KS][R / 8][2];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const int k = warp * KS + i;
+        af[i][0] = q0[k * 8 + tq];
+        af[i][1] = q1[k * 8 + tq];
+        af[i][2] = q0[k * 8 + 4 + tq];
+        af[i][3] = q1[k * 8 + 4 + tq];
+#pragma unroll
+        for (int n = 0; n < R / 8; ++n) {
+            const uint16_t* c = bk + (k * 16 + 2 * tq) * R + n * 8 + g;
+            bf[i][n][0] = c[0] | ((uint32_t)c[R] << 16);
+            bf[i][n][1] = c[8 * R] | ((uint32_t)c[9 * R] << 16);
+        }
     }
-    if (b < a.B) {
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + ((size_t)b * a.H + h) * (D_H + D_R));
-        for (int i = lane; i < D_H / 2; i += 32) {
-            const uint32_t v = q[i];
-            *reinterpret_cast<float2*>(&qs[warp][2 * i]) = make_float2(bf16lo(v), bf16hi(v));
+    float acc[R / 8][4];
+#pragma unroll
+    for (int n = 0; n < R / 8; ++n) {
+        acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) mma_16816(acc[n], af[i], bf[i][n][0], bf[i][n][1]);
+        if (warp > 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[warp - 1][g + 8 * (e >> 1)][n * 8 + 2 * tq + (e & 1)] = acc[n][e];
         }
     }
     __syncthreads();
-    if (b >= a.B) return;
-    const int sl = lane / R;
-    float acc = 0.f;
-#pragma unroll 16
-    for (int i = 0; i < D_H / SL; ++i) acc = fmaf(qs[warp][i * SL + sl], bk[i * 32 + lane], acc);
+    if (warp > 0) return;
 #pragma unroll
-    for (int o = R; o < 32; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane < R) a.qt[((size_t)b * a.H + h) * R + lane] = acc;
+    for (int n = 0; n < R / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int b = b0 + g + 8 * e, j = n * 8 + 2 * tq;
+            float x = acc[n][2 * e], y = acc[n][2 * e + 1];
+#pragma unroll
+            for (int w = 0; w < 3; ++w) {
+                x += part[w][g + 8 * e][j];
+                y += part[w][g + 8 * e][j + 1];
+            }
+            if (b < a.B) *reinterpret_cast<float2*>(a.qt + ((size_t)b * a.H + h) * R + j) = make_float2(x, y);
+        }
 }
 
 cudaError_t launch_decode_absorb(const DecodeArgs& a, int D_H, int R, int D_R, cudaStream_t stream) {
-    const dim3 grid(a.H, (a.B + 7) / 8);
+    const dim3 grid(a.H, (a.B + 15) / 16);
 #define LRKV_ABS(DH, RR)                                                                                          \
     if (D_H == DH && R == RR)                                                                                     \
-        return D_R == 0 ? launch_pdl(absorb_batch_kernel<DH, RR, 0>, grid, dim3(256), 0, stream, a)               \
-                        : launch_pdl(absorb_batch_kernel<DH, RR, 64>, grid, dim3(256), 0, stream, a);
+        return D_R == 0 ? launch_pdl(absorb_batch_kernel<DH, RR, 0>, grid, dim3(128), 0, stream, a)               \
+                        : launch_pdl(absorb_batch_kernel<DH, RR, 64>, grid, dim3(128), 0, stream, a);
     LRKV_ABS(64, 8) LRKV_ABS(64, 16) LRKV_ABS(64, 32) LRKV_ABS(128, 8) LRKV_ABS(128, 16) LRKV_ABS(128, 32)
 #undef LRKV_ABS
     return cudaErrorInvalidValue;

@@ -19,7 +19,8 @@
 // two TMEM buffers, P = 2^(S scale log2 e - m) in bf16 over the same columns, O by tcgen05.mma with
 // A = P from TMEM (N = d_h + zw).  Warp roles and the lazily raised maximum as in the prefill
 // (prefill_tc.cu): warp 0 key producer, 6 value producer (TMA, 128-byte swizzle), 1 issues S, 7 issues
-// P V, 2..5 one query row per thread.
+// P V; 2..5 and 8..11 take the first and the second 32 tokens of a page for one query row per thread (one
+// warp per scheduler spent some 1000 cycles on a page's 64, twice what the MMAs need).
 #include <type_traits>
 #include <utility>
 
@@ -33,7 +34,11 @@ namespace {
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-constexpr int kThreads = 256;
+__device__ __forceinline__ void named_bar(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 __device__ __forceinline__ bool prefix_good(const PrefixArgs& a, int P) {
@@ -51,12 +56,12 @@ struct PxLayout {
     static constexpr int NBK = (D_K + ZW) / 64, NBV = (D_H + ZW) / 64;  // 64-column blocks of a key / value row
     static constexpr int QBT = NBK < 4 ? NBK : 4, QBS = NBK - QBT;  // blocks of Q in TMEM, in shared memory
     static constexpr uint32_t Q_BYTES = QBS * 16384, K_BYTES = NBK * 8192, V_BYTES = NBV * 8192;
-    static constexpr uint32_t ROOM = 232448 - 1024 - 512 - Q_BYTES;
+    static constexpr uint32_t ROOM = 232448 - 1024 - 1536 - Q_BYTES;
     static constexpr int BOTH = ROOM / (K_BYTES + V_BYTES);
     static constexpr int VST = BOTH > 4 ? 4 : BOTH;
     static constexpr int KST = VST < 4 && ROOM - VST * (K_BYTES + V_BYTES) >= K_BYTES ? VST + 1 : VST;
     static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
-    static constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+    static constexpr uint32_t OFF_MX = OFF_BAR + 512, SMEM = OFF_MX + 1024 + 1024;
     static_assert(VST >= 2 && SMEM <= 232448, "stages");
     // TMEM columns: two S buffers, O, Q (two bf16 a column)
     static constexpr uint32_t TM_S = 0, TM_O = 128, TM_Q = TM_O + D_H + ZW;
@@ -100,15 +105,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pg0 = (int)((long long)np * split / a.nsplit);
     const int nt = (int)((long long)np * (split + 1) / a.nsplit) - pg0;
 
-    // this thread's query row (softmax warps): TMEM lane = row = head x ns + sequence
-    const int qq = warp & 3;
+    // this thread's query row (softmax warps): TMEM lane = row = head x ns + sequence; and its half of a page
+    const int qq = warp & 3, half = warp >> 3;
     const int row = qq * 32 + lane;
     const int hl = row / a.ns, rb = b0 + row - hl * a.ns, rh = h0 + hl;
     const bool live = rh < H && rb < d.B;
     const size_t at = ((size_t)rb * H + rh) * a.nsplit + split;
     if (nt == 0) {  // an empty piece: its sums are not read
         pdl_wait();  // (this grid's end stands for that of the launches before it)
-        if (warp >= 2 && warp < 6 && live) {
+        if (warp >= 8 && live) {
             a.ml[at * 2] = -INFINITY;
             a.ml[at * 2 + 1] = 0.f;
         }
@@ -138,9 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
 
     if (threadIdx.x == 0) {
-        mbar_init(B(q_ready), 128);
+        mbar_init(B(q_ready), 256);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(B(p_full + i), 128);
+            mbar_init(B(p_full + i), 256);
             mbar_init(B(s_full + i), 1);
             mbar_init(B(s_free + i), 1);
             mbar_init(B(o_done + i), 1);
@@ -293,15 +298,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
             // [Q | diag(Q~)] row, block by block of 64 columns: into TMEM (two columns a register), or K-major with
             // 128-byte swizzle (16-byte chunk c at c ^ (row mod 8)).  q~ is rounded to bf16, as in the prefill.
+            // The two halves' threads of a row take every other block.
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const size_t qr = (size_t)(live ? rb : 0) * H + (live ? rh : 0);
             const uint4* q = reinterpret_cast<const uint4*>(d.q + qr * D_K);
             const float* qt = d.qt + qr * R;
+            bool waited = false;
 #pragma unroll
             for (int bk = 0; bk < NBK; ++bk) {
-                if (bk == D_K / 64) {
+                if ((bk & 1) != half) continue;
+                if (bk >= D_K / 64 && !waited) {
                     pdl_wait();     // q~
                     pdl_trigger();  // the scan of the sequences' own tokens may fill the SMs that this grid leaves
+                    waited = true;
                 }
                 uint32_t v[32];
 #pragma unroll
@@ -332,6 +341,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                 }
             }
+            // (a half without a block of q~ waits too: this grid's end stands for that of the launches before it, and
+            // the next launch must find q~ there)
+            if (!waited) {
+                pdl_wait();
+                pdl_trigger();
+            }
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
@@ -341,79 +356,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mref = -INFINITY, l = 0.f;
         int vst = 0;
         uint32_t vphase = 0;
+        // [row][page parity][half], later [row][half] sums: eight bytes that only the row's two threads touch
+        uint16_t* const mxs = reinterpret_cast<uint16_t*>(smem + Lay::OFF_MX) + row * 4;
+        // After an expired wait the loop goes on without work, so that the two halves still meet at their barrier.
         for (int j = 0; j < nt; ++j) {
-            if (!ok || aborted()) {
-                ok = false;
-                break;
-            }
             // visible tokens of this page: none of a page with a bad id
             const int blk = a.blocks[pg0 + j];
             const int lim = blk >= 0 && blk < d.num_blocks ? P - (pg0 + j) * kBlockSize : 0;
-            ok = wait_all(B(s_full + (j & 1)), (j >> 1) & 1, d.status);
-            if (!ok) break;
-            tc_fence_after();
+            ok = ok && !aborted() && wait_all(B(s_full + (j & 1)), (j >> 1) & 1, d.status);
             const uint32_t sb = tmem + tl + Lay::TM_S + (j & 1) * 64;
-            uint32_t sv[64];
+            uint32_t sv[32];
+            float mx = -INFINITY;
+            if (ok) {
+                tc_fence_after();
+                tmem_ld_32x32b_x32(sb + half * 32, sv);
+                if (lim < kBlockSize) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x32_nowait(sb + c * 32, sv + c * 32);
-            tmem_wait_ld();
-            if (lim < kBlockSize) {
+                    for (int e = 0; e < 32; ++e) sv[e] = half * 32 + e < lim ? sv[e] : 0xff800000u;
+                    // rows of s^V, z^V behind the end may hold any bits: cleared before P V reads them
+                    ok = wait_all(B(v_full + vst), vphase, d.status);
+                    const int vr = row & 63;
+                    if (ok && vr >= lim) {
+                        const uint4 z = make_uint4(0, 0, 0, 0);
+                        for (int bk = (row >> 6) + 2 * half; bk < NBV; bk += 4) {
+                            uint4* r0 =
+                                reinterpret_cast<uint4*>(smem + Lay::OFF_V + vst * Lay::V_BYTES + bk * 8192 + vr * 128);
 #pragma unroll
-                for (int e = 0; e < 64; ++e) sv[e] = e < lim ? sv[e] : 0xff800000u;
-                // rows of s^V, z^V behind the end may hold any bits: cleared before P V reads them
-                ok = wait_all(B(v_full + vst), vphase, d.status);
-                if (!ok) break;
-                const int vr = row & 63;
-                if (vr >= lim) {
-                    const uint4 z = make_uint4(0, 0, 0, 0);
-                    for (int bk = row >> 6; bk < NBV; bk += 2) {
-                        uint4* r0 = reinterpret_cast<uint4*>(smem + Lay::OFF_V + vst * Lay::V_BYTES + bk * 8192 + vr * 128);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) r0[i] = z;
+                            for (int i = 0; i < 8; ++i) r0[i] = z;
+                        }
                     }
                 }
+                float m4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[4 + i]));
+#pragma unroll
+                for (int e = 8; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * d.scale_log2;
             }
             if (++vst == VST) {
                 vst = 0;
                 vphase ^= 1;
             }
-            float m8[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m8[i] = __uint_as_float(sv[i]);
-#pragma unroll
-            for (int e = 8; e < 64; ++e) m8[e & 7] = fmaxf(m8[e & 7], __uint_as_float(sv[e]));
-            float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
-            mx *= d.scale_log2;
+            // The row's maximum over both halves, in bf16 (as the reference of the exponents it only has to be the
+            // same for both; the next write to this parity's slot comes after the next page's barrier).
+            mxs[(j & 1) * 2 + half] = (uint16_t)(__float_as_uint(mx) >> 16);
+            named_bar(1 + qq, 64);
+            const uint32_t both = *reinterpret_cast<const uint32_t*>(mxs + (j & 1) * 2);
+            mx = fmaxf(bf16lo(both), bf16hi(both));
+            if (!ok) continue;
             const float mnew = fmaxf(mref, mx);
             const bool raise = mnew > mref + kRescaleThreshold;  // also the first time a row sees a token
             const float muse = raise ? mnew : mref;
             const float alpha = raise ? (mref == -INFINITY ? 0.f : ex2_approx(mref - mnew)) : 1.f;
             // p = 2^(s scale log2 e - m), 0 everywhere as long as the row has seen no token
             const float nm = muse == -INFINITY ? -INFINITY : -muse;
-            float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            float r4[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const uint32_t* v = sv + c * 32;
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float p0 = ex2_approx(fmaf(__uint_as_float(v[e]), d.scale_log2, nm));
-                    const float p1 = ex2_approx(fmaf(__uint_as_float(v[e + 1]), d.scale_log2, nm));
-                    r8[(e >> 1) & 7] += p0 + p1;
-                    pk[e / 2] = pack_bf16x2(p0, p1);
-                }
-                tmem_st_32x32b_x16(sb + c * 16, pk);
+            for (int e = 0; e < 32; e += 2) {
+                const float p0 = ex2_approx(fmaf(__uint_as_float(sv[e]), d.scale_log2, nm));
+                const float p1 = ex2_approx(fmaf(__uint_as_float(sv[e + 1]), d.scale_log2, nm));
+                r4[(e >> 1) & 3] += p0 + p1;
+                pk[e / 2] = pack_bf16x2(p0, p1);
             }
-            l = l * alpha + (((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7])));
+            // (both halves have read their S before either writes P over it: the barrier above)
+            tmem_st_32x32b_x16(sb + half * 16, pk);
+            l = l * alpha + ((r4[0] + r4[1]) + (r4[2] + r4[3]));
             mref = muse;
             // O may only be rescaled once P_{j-1} V_{j-1} has finished accumulating into it
             if (j > 0 && __any_sync(0xffffffffu, raise)) {
                 ok = wait_all(B(o_done + ((j - 1) & 1)), ((j - 1) >> 1) & 1, d.status);
-                if (!ok) break;
+                if (!ok) continue;
                 tc_fence_after();
                 uint32_t v[32];
 #pragma unroll 1
-                for (int c = 0; c < (D_H + ZW) / 32; ++c) {
+                for (int c = half; c < (D_H + ZW) / 32; c += 2) {
                     tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
@@ -425,6 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(B(p_full + (j & 1)));
         }
+        // the row's sum over both halves
+        named_bar(1 + qq, 64);  // (the maxima have been read)
+        float* const ls = reinterpret_cast<float*>(smem + Lay::OFF_MX) + row * 2;
+        ls[half] = l;
+        named_bar(1 + qq, 64);
+        l += ls[half ^ 1];
         // ---- partials, unnormalised
         if (ok) ok = wait_all(B(o_done + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, d.status);
         if (ok) {
@@ -434,13 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = 1.f;
                 if (!(fabsf(mref) < INFINITY)) mref = 0.f;
             }
-            if (live) {
+            if (live && half == 0) {
                 a.ml[at * 2] = mref;
                 a.ml[at * 2 + 1] = l;
             }
             float* dst = a.acc + at * W;
 #pragma unroll 1
-            for (int c = 0; c < D_H / 32; ++c) {
+            for (int c = half; c < D_H / 32; c += 2) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
                 if (live) {
@@ -453,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // latent sums: 32 columns at a time, each row keeps its own head's
 #pragma unroll 1
-            for (int c = 0; c < ZW / 32; ++c) {
+            for (int c = half; c < ZW / 32; c += 2) {
                 // (a warp's rows span heads hl of its first to its last lane)
                 const int first = (qq * 32) / a.ns * R, last = (qq * 32 + 31) / a.ns * R + R;
                 if (c * 32 + 32 <= first || c * 32 >= last) continue;
@@ -481,145 +504,141 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Merge of the prefix's pieces and the sequence's own partials: grid (H, B), block nsl slices x W / 4
-// column quads (nsl a power of two, at least D_H threads).  A slice merges every nsl-th partial, four
-// loads in flight; the slices are merged in shared memory, then B_h^V (copied there meanwhile).  (One
-// thread per column walking all partials took 27 us for 32 heads x 32 sequences x 20 partials; this
-// takes 6.)
+// Merge of the prefix's pieces and the sequences' own partials: grid (H, ceil(B / blockDim.z)), block
+// (W / 4 column quads, slices, sequences).  A slice merges every blockDim.y-th partial of its sequence, PPS
+// loads in flight; the slices are merged in shared memory; then B_h^V, copied there meanwhile for all
+// sequences of the block.  The host takes as many slices as fill the GPU about once: each block is one chain of
+// dependent loads of some 5 us, so a second wave costs as much as the first.  (One thread per column walking
+// all partials: 27 us for 32 heads x 32 sequences x 20 partials; eight slices for every block: 10 us there, but 18
+// for 128 heads x 48 sequences x 5.)
 template <int D_H, int R>
-__global__ void __launch_bounds__(8 * (D_H + R) / 4) prefix_combine_kernel(const PrefixArgs a) {
-    constexpr int W = D_H + R, W4 = W / 4, NSL_MAX = 8, PPS = 4;
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    const int nsl = blockDim.x / W4;
+__global__ void __launch_bounds__(512) prefix_combine_kernel(const PrefixArgs a) {
+    constexpr int W = D_H + R, W4 = W / 4, ROWS_MAX = 512 / W4, PPS = 6;
     const DecodeArgs& d = a.d;
-    __shared__ float sm_m[NSL_MAX], sm_l[NSL_MAX];
-    __shared__ __align__(16) float sm_acc[NSL_MAX][W];
+    const int c4 = threadIdx.x, sl = threadIdx.y, nsl = blockDim.y;
+    const int h = blockIdx.x, b = blockIdx.y * blockDim.z + threadIdx.z;
+    const int tid = (threadIdx.z * nsl + sl) * W4 + c4, nthreads = W4 * nsl * blockDim.z;
+    __shared__ float sm_m[ROWS_MAX], sm_l[ROWS_MAX];
+    __shared__ __align__(16) float sm_acc[ROWS_MAX][W];
     __shared__ __align__(16) uint16_t sm_bv[D_H * R];
-    const int P = a.len[0], L = a.suffix ? d.seq_lens[b] : 0;
+    const bool have = b < d.B;
+    const int P = a.len[0], L = a.suffix && have ? d.seq_lens[b] : 0;
     const bool bad = !prefix_good(a, P) || L < 0 || L > d.max_pages * kBlockSize || (!d.part_out && P + L == 0);
-    float* pdst = d.part_out ? d.part_out + ((size_t)b * d.H + h) * (W + 2) : nullptr;
-    uint16_t* dst = d.out + ((size_t)b * d.H + h) * D_H;
-    if (!pdst && !bad) {
+    if (!d.part_out) {
         const uint16_t* bv = d.BV + (size_t)h * D_H * R;
-        for (int i = tid; i < D_H * R / 8; i += blockDim.x)
+        for (int i = tid; i < D_H * R / 8; i += nthreads)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(sm_bv + i * 8)), "l"(bv + i * 8)
                          : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     pdl_wait();  // the scans
-    if (bad) {
-        if (tid == 0 && h == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
-        if (pdst) {
-            for (int i = tid; i < W + 2; i += blockDim.x) pdst[i] = i == W ? -INFINITY : 0.f;
-        } else {
-            for (int i = tid; i < D_H; i += blockDim.x) dst[i] = 0;
-        }
-        return;
-    }
-    const size_t at = ((size_t)b * d.H + h) * a.nsplit;
-    const float2* ml0 = reinterpret_cast<const float2*>(a.ml) + at;
-    const float4* ac0 = reinterpret_cast<const float4*>(a.acc + at * W);
-    const int n0 = P > 0 ? a.nsplit : 0;
-    int n = n0;
-    const float2* ml1 = ml0;
-    const float4* ac1 = ac0;
-    if (L > 0) {
-        const int2 fe = d.seg_table[b * d.nhg + h / (d.H / d.nhg)];
-        n += fe.y;
-        ml1 = reinterpret_cast<const float2*>(d.part_ml) + (size_t)h * d.pmax + fe.x - n0;
-        ac1 = reinterpret_cast<const float4*>(d.part_acc + ((size_t)h * d.pmax + fe.x) * W) - (ptrdiff_t)n0 * W4;
-    }
-    const int sl = tid / W4, c4 = tid - sl * W4;
+    const int row0 = threadIdx.z * nsl;  // the sequence's rows of sm_acc
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = sl; p0 < n; p0 += nsl * PPS) {
-        float2 ml[PPS];
-        float4 x[PPS];
-#pragma unroll
-        for (int u = 0; u < PPS; ++u) {
-            const int p = p0 + u * nsl;
-            ml[u] = p < n ? (p < n0 ? ml0 : ml1)[p] : make_float2(-INFINITY, 0.f);
-            x[u] = p < n ? (p < n0 ? ac0 : ac1)[(size_t)p * W4 + c4] : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (have && !bad) {
+        const size_t at = ((size_t)b * d.H + h) * a.nsplit;
+        const float2* ml0 = reinterpret_cast<const float2*>(a.ml) + at;
+        const float4* ac0 = reinterpret_cast<const float4*>(a.acc + at * W);
+        const int n0 = P > 0 ? a.nsplit : 0;
+        int n = n0;
+        const float2* ml1 = ml0;
+        const float4* ac1 = ac0;
+        if (L > 0) {
+            const int2 fe = d.seg_table[b * d.nhg + h / (d.H / d.nhg)];
+            n += fe.y;
+            ml1 = reinterpret_cast<const float2*>(d.part_ml) + (size_t)h * d.pmax + fe.x - n0;
+            ac1 = reinterpret_cast<const float4*>(d.part_acc + ((size_t)h * d.pmax + fe.x) * W) - (ptrdiff_t)n0 * W4;
         }
-        float mn = m;
+        for (int p0 = sl; p0 < n; p0 += nsl * PPS) {
+            float2 ml[PPS];
+            float4 x[PPS];
 #pragma unroll
-        for (int u = 0; u < PPS; ++u) mn = fmaxf(mn, ml[u].x);
-        if (mn == -INFINITY) continue;
-        const float sc = m == -INFINITY ? 0.f : exp2f(m - mn);
-        l *= sc;
-        v.x *= sc;
-        v.y *= sc;
-        v.z *= sc;
-        v.w *= sc;
+            for (int u = 0; u < PPS; ++u) {
+                const int p = p0 + u * nsl;
+                ml[u] = p < n ? (p < n0 ? ml0 : ml1)[p] : make_float2(-INFINITY, 0.f);
+                x[u] = p < n ? (p < n0 ? ac0 : ac1)[(size_t)p * W4 + c4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mn = m;
 #pragma unroll
-        for (int u = 0; u < PPS; ++u) {
-            if (ml[u].x == -INFINITY) continue;  // an empty piece: its sums were not written
-            const float w = exp2f(ml[u].x - mn);
-            l = fmaf(w, ml[u].y, l);
-            v.x = fmaf(w, x[u].x, v.x);
-            v.y = fmaf(w, x[u].y, v.y);
-            v.z = fmaf(w, x[u].z, v.z);
-            v.w = fmaf(w, x[u].w, v.w);
+            for (int u = 0; u < PPS; ++u) mn = fmaxf(mn, ml[u].x);
+            if (mn == -INFINITY) continue;
+            const float sc = m == -INFINITY ? 0.f : exp2f(m - mn);
+            l *= sc;
+            v.x *= sc;
+            v.y *= sc;
+            v.z *= sc;
+            v.w *= sc;
+#pragma unroll
+            for (int u = 0; u < PPS; ++u) {
+                if (ml[u].x == -INFINITY) continue;  // an empty piece: its sums were not written
+                const float w = exp2f(ml[u].x - mn);
+                l = fmaf(w, ml[u].y, l);
+                v.x = fmaf(w, x[u].x, v.x);
+                v.y = fmaf(w, x[u].y, v.y);
+                v.z = fmaf(w, x[u].z, v.z);
+                v.w = fmaf(w, x[u].w, v.w);
+            }
+            m = mn;
         }
-        m = mn;
     }
-    if (sl < nsl) {
-        *reinterpret_cast<float4*>(&sm_acc[sl][c4 * 4]) = v;
-        if (c4 == 0) {
-            sm_m[sl] = m;
-            sm_l[sl] = l;
-        }
+    *reinterpret_cast<float4*>(&sm_acc[row0 + sl][c4 * 4]) = v;
+    if (c4 == 0) {
+        sm_m[row0 + sl] = m;
+        sm_l[row0 + sl] = l;
     }
     __syncthreads();
-    if (tid < W4) {
+    float* pdst = d.part_out ? d.part_out + ((size_t)b * d.H + h) * (W + 2) : nullptr;
+    if (sl == 0) {
         float M = -INFINITY;
-        for (int i = 0; i < nsl; ++i) M = fmaxf(M, sm_m[i]);
+        for (int i = 0; i < nsl; ++i) M = fmaxf(M, sm_m[row0 + i]);
         float ls = 0.f;
         float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = 0; i < nsl; ++i) {
-            const float w = sm_m[i] == -INFINITY ? 0.f : exp2f(sm_m[i] - M);
-            const float4 x = *reinterpret_cast<const float4*>(&sm_acc[i][tid * 4]);
-            ls = fmaf(w, sm_l[i], ls);
+            const float w = sm_m[row0 + i] == -INFINITY ? 0.f : exp2f(sm_m[row0 + i] - M);
+            const float4 x = *reinterpret_cast<const float4*>(&sm_acc[row0 + i][c4 * 4]);
+            ls = fmaf(w, sm_l[row0 + i], ls);
             t.x = fmaf(w, x.x, t.x);
             t.y = fmaf(w, x.y, t.y);
             t.z = fmaf(w, x.z, t.z);
             t.w = fmaf(w, x.w, t.w);
         }
-        if (pdst) {  // unnormalised
-            pdst[tid * 4] = t.x;
-            pdst[tid * 4 + 1] = t.y;
-            pdst[tid * 4 + 2] = t.z;
-            pdst[tid * 4 + 3] = t.w;
-            if (tid == 0) {
+        if (have && bad && h == 0 && c4 == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
+        if (have && pdst) {  // unnormalised (a bad length: the empty state)
+            pdst[c4 * 4] = t.x;
+            pdst[c4 * 4 + 1] = t.y;
+            pdst[c4 * 4 + 2] = t.z;
+            pdst[c4 * 4 + 3] = t.w;
+            if (c4 == 0) {
                 pdst[W] = M;
                 pdst[W + 1] = ls;
             }
         }
-        // (ls is 0 only where every page of the tokens was a bad one: zeros then)
+        // (the sum is 0 for a bad length, and where every page of the tokens was a bad one: zeros)
         const float inv = ls == 0.f ? 0.f : 1.f / ls;
-        *reinterpret_cast<float4*>(&sm_acc[0][tid * 4]) = make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
+        *reinterpret_cast<float4*>(&sm_acc[row0][c4 * 4]) = make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
     }
     if (pdst) return;
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    if (tid < D_H) {
-        float x = sm_acc[0][tid];
-        const uint4* bvr = reinterpret_cast<const uint4*>(sm_bv + tid * R);
-        const float* z = &sm_acc[0][D_H];
+    if (!have) return;
+    for (int i = sl * W4 + c4; i < D_H; i += nsl * W4) {
+        float x = sm_acc[row0][i];
+        const uint4* bvr = reinterpret_cast<const uint4*>(sm_bv + i * R);
+        const float* z = &sm_acc[row0][D_H];
 #pragma unroll
-        for (int i = 0; i < R / 8; ++i) {
-            const uint4 w = bvr[i];
-            x = fmaf(bf16lo(w.x), z[i * 8 + 0], x);
-            x = fmaf(bf16hi(w.x), z[i * 8 + 1], x);
-            x = fmaf(bf16lo(w.y), z[i * 8 + 2], x);
-            x = fmaf(bf16hi(w.y), z[i * 8 + 3], x);
-            x = fmaf(bf16lo(w.z), z[i * 8 + 4], x);
-            x = fmaf(bf16hi(w.z), z[i * 8 + 5], x);
-            x = fmaf(bf16lo(w.w), z[i * 8 + 6], x);
-            x = fmaf(bf16hi(w.w), z[i * 8 + 7], x);
+        for (int k = 0; k < R / 8; ++k) {
+            const uint4 w = bvr[k];
+            x = fmaf(bf16lo(w.x), z[k * 8 + 0], x);
+            x = fmaf(bf16hi(w.x), z[k * 8 + 1], x);
+            x = fmaf(bf16lo(w.y), z[k * 8 + 2], x);
+            x = fmaf(bf16hi(w.y), z[k * 8 + 3], x);
+            x = fmaf(bf16lo(w.z), z[k * 8 + 4], x);
+            x = fmaf(bf16hi(w.z), z[k * 8 + 5], x);
+            x = fmaf(bf16lo(w.w), z[k * 8 + 6], x);
+            x = fmaf(bf16hi(w.w), z[k * 8 + 7], x);
         }
         const __nv_bfloat16 ob = __float2bfloat16_rn(x);
-        dst[tid] = *reinterpret_cast<const uint16_t*>(&ob);
+        d.out[((size_t)b * d.H + h) * D_H + i] = *reinterpret_cast<const uint16_t*>(&ob);
     }
 }
 
@@ -627,15 +646,9 @@ __global__ void __launch_bounds__(8 * (D_H + R) / 4) prefix_combine_kernel(const
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-#ifndef PXS
-#define PXS 0
-#endif
-// Which tile: the fewest tensor-core products, tiles x (d_k + d_h + 2 zw) (one of 64 columns covers
-// twice the sequences of one of 128 with half the heads).  How many pieces: a piece costs its pages
-// and about kPieceCost pages more (Q, pipeline fill, partials), and the pieces of all tiles run in
-// waves of one CTA per SM.
-PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, int sms) {
-    constexpr int kPieceCost = 7;
+// Which tile: the fewest tensor-core products, tiles x (d_k + d_h + 2 zw) (one of 64 columns covers twice
+// the sequences of one of 128 with half the heads).
+static PrefixPlan prefix_tile(int H, int D_H, int R, int D_R, int B) {
     PrefixPlan best{};
     long long best_cost = -1;
     for (int zw = 128; zw >= 64; zw /= 2) {
@@ -651,16 +664,41 @@ PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, in
             best_cost = cost;
         }
     }
+    return best;
+}
+
+int prefix_most_splits(int H, int D_H, int R, int D_R, int B, int max_blocks, int sms) {
+    const PrefixPlan t = prefix_tile(H, D_H, R, D_R, B);
+    const long long n = 2LL * sms / ((long long)t.htiles * t.stiles);
+    return (int)(n < 1 ? 1 : n < max_blocks ? n : max_blocks);
+}
+
+// How many pieces, and whether some SMs are kept for the scan of the sequences' own tokens, by a model of
+// the two launches in us: a piece costs 6 (queries, pipeline fill, partials) and 0.9 a page of 512 columns,
+// the pieces of all tiles run in waves of one CTA per SM; the other scan costs 6, as much again for each
+// sequence that a CTA meets, and streams 35 bytes a ns on one SM.  Of the own tables' capacity half is
+// taken to be in use.  Measured: 32 heads x 16 sequences behind 8 K tokens 33 us one after the other, 25 side by
+// side; 128 x 48 behind 4 K 76 and 68.
+PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, double own_bytes, int sms) {
+    PrefixPlan best = prefix_tile(H, D_H, R, D_R, B);
     const long long ntiles = (long long)best.htiles * best.stiles;
-    sms -= PXS;
-    long long least = -1;
-    for (int s = 1; s <= max_blocks && s <= 65535 && (s == 1 || ntiles * s <= 4LL * sms); ++s) {
-        const long long waves = (ntiles * s + sms - 1) / sms;
-        const long long t = waves * ((max_blocks + s - 1) / s + kPieceCost);
-        if (least < 0 || t < least) {
-            least = t;
-            best.nsplit = s;
+    const double page = 0.9 * (2 * D_H + D_R + 2 * best.zw) / 512;
+    double least = -1;
+    for (int own = 0; own <= sms / 2; own += 8) {
+        const int n = sms - own, m = own ? own : sms;
+        const double t_own = own_bytes > 0 ? 6 + 6 * (1 + (double)B / m) + own_bytes / 2 / 35e3 / m : 0;
+        for (int s = 1; s <= max_blocks && (s == 1 || ntiles * s <= 2LL * n); ++s) {
+            const long long waves = (ntiles * s + n - 1) / n;
+            const double t_prefix = waves * (page * ((max_blocks + s - 1) / s) + 6);
+            const double hi = t_own > t_prefix ? t_own : t_prefix, lo = t_own + t_prefix - hi;
+            const double t = own ? hi + 0.1 * lo : t_own + t_prefix;
+            if (least < 0 || t < least) {
+                least = t;
+                best.nsplit = s;
+                best.own_sms = own;
+            }
         }
+        if (own_bytes <= 0) break;
     }
     return best;
 }
@@ -680,11 +718,11 @@ void prefix_carve_workspace(PrefixArgs* a, void* ws, int D_H, int R) {
 // A launch that may start before the one before it on the stream has ended (programmatic dependent
 // launch): the kernels wait for it where they first read what it writes, and in every block.
 template <typename... Args>
-static cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+static cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                     Args... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -702,7 +740,7 @@ static cudaError_t launch_scan_t(const PrefixMaps& maps, const PrefixArgs& a, in
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int stiles = (a.d.B + a.ns - 1) / a.ns;
-    return launch_dependent(kern, dim3(a.htiles * stiles, a.nsplit), kThreads, smem, stream, maps, a, R);
+    return launch_dependent(kern, dim3(a.htiles * stiles, a.nsplit), dim3(kThreads), smem, stream, maps, a, R);
 }
 
 cudaError_t launch_prefix_scan(const PrefixMaps& maps, const PrefixArgs& a, int D_H, int R, int D_R,
@@ -716,12 +754,16 @@ cudaError_t launch_prefix_scan(const PrefixMaps& maps, const PrefixArgs& a, int 
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefix_combine(const PrefixArgs& a, int D_H, int R, cudaStream_t stream) {
+cudaError_t launch_prefix_combine(const PrefixArgs& a, int D_H, int R, int sms, cudaStream_t stream) {
 #define LRKV_PC(DH, RR)                                                               \
     if (D_H == DH && R == RR) {                                                       \
-        const int nsl = a.nsplit > 4 ? 8 : 4;                                         \
-        return launch_dependent(prefix_combine_kernel<DH, RR>, dim3(a.d.H, a.d.B),    \
-                                nsl * (DH + RR) / 4, 0, stream, a);                   \
+        constexpr int W4 = (DH + RR) / 4;                                             \
+        int nsl = 1;                                                                  \
+        while (nsl < 8 && (long long)a.d.H * a.d.B * W4 * nsl * 2 <= sms * 1536LL && W4 * nsl * 2 <= 512) nsl *= 2;   \
+        int nseq = 1;                                                                 \
+        while (nseq < a.d.B && W4 * nsl * nseq * 2 <= 256) nseq *= 2;                 \
+        return launch_dependent(prefix_combine_kernel<DH, RR>, dim3(a.d.H, (a.d.B + nseq - 1) / nseq), \
+                                dim3(W4, nsl, nseq), 0, stream, a);                   \
     }
     LRKV_PC(64, 8) LRKV_PC(64, 16) LRKV_PC(64, 32) LRKV_PC(128, 8) LRKV_PC(128, 16) LRKV_PC(128, 32)
 #undef LRKV_PC

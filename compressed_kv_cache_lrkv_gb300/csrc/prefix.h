@@ -20,11 +20,14 @@ struct PrefixArgs {
 
 // How the scan cuts the work.  A CTA's 128 query rows are hb heads x ns sequences with hb r = zw
 // columns of latents (zw 64 or 128); tiles = ceil(H / hb) ceil(B / ns), each cut into nsplit pieces
-// of the prefix.
+// of the prefix; own_sms SMs are left to the scan of the sequences' own tokens (0: it runs after).
 struct PrefixPlan {
-    int zw, hb, ns, htiles, stiles, nsplit;
+    int zw, hb, ns, htiles, stiles, nsplit, own_sms;
 };
-PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, int sms);
+// own_bytes: cache bytes the sequences' own tokens may have (0: none are scanned).
+PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, double own_bytes, int sms);
+// Pieces at most of any plan for these sizes (prefix_plan never takes more than two waves of pieces).
+int prefix_most_splits(int H, int D_H, int R, int D_R, int B, int max_blocks, int sms);
 size_t prefix_workspace_bytes(int H, int D_H, int R, int B, int nsplit);
 void prefix_carve_workspace(PrefixArgs* a, void* ws, int D_H, int R);
 
@@ -37,6 +40,6 @@ cudaError_t launch_prefix_scan(const PrefixMaps& maps, const PrefixArgs& a, int 
                                cudaStream_t stream);
 // Log-sum-exp merge of the prefix's partials with the sequences' own; B^V and the bf16 output, or
 // merged partials where d.part_out is set.
-cudaError_t launch_prefix_combine(const PrefixArgs& a, int D_H, int R, cudaStream_t stream);
+cudaError_t launch_prefix_combine(const PrefixArgs& a, int D_H, int R, int sms, cudaStream_t stream);
 
 }  // namespace lrkv
