@@ -449,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar(1 + qq, 64);
         l += ls[half ^ 1];
         // ---- partials, unnormalised
+        const uint32_t rs = 16u * ((W / 4) | 1);  // row stride of their staging
         if (ok) ok = wait_all(B(o_done + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, d.status);
         if (ok) {
             tc_fence_after();
@@ -461,18 +462,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a.ml[at * 2] = mref;
                 a.ml[at * 2 + 1] = l;
             }
-            float* dst = a.acc + at * W;
+            // The row goes through shared memory (the rings are idle: every copy has landed and every MMA that reads
+            // them is done) and leaves in one bulk copy: stored straight from registers, a warp's 16-byte pieces of 32
+            // rows took 4 to 5 us.  Rows start an odd number of 16-byte units apart.
+            uint8_t* const srow = smem + row * rs;
+            const uint4 nan4 = make_uint4(0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u);
 #pragma unroll 1
             for (int c = half; c < D_H / 32; c += 2) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
-                if (live) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(dst + c * 32 + i * 4) =
-                            nan ? make_uint4(0x7fc00000u, 0x7fc00000u, 0x7fc00000u, 0x7fc00000u)
-                                : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(srow + c * 128 + i * 16) =
+                        nan ? nan4 : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
             // latent sums: 32 columns at a time, each row keeps its own head's
 #pragma unroll 1
@@ -482,18 +484,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c * 32 + 32 <= first || c * 32 >= last) continue;
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + D_H + c * 32, v);
-                if (live) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int col = c * 32 + i * 4 - hl * R;
-                        if (col >= 0 && col < R)
-                            *reinterpret_cast<uint4*>(dst + D_H + col) =
-                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int col = c * 32 + i * 4 - hl * R;
+                    if (col >= 0 && col < R)
+                        *reinterpret_cast<uint4*>(srow + (D_H + col) * 4) =
+                            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
             }
+            fence_proxy_async_smem();
         } else {
             *abort_flag = 1;
+        }
+        named_bar(1 + qq, 64);  // both halves of the rows are written
+        if (ok && half == 0) {
+            if (live) {
+                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.acc + at * W),
+                             "r"(S0 + row * rs), "r"(W * 4)
+                             : "memory");
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         }
     }
     tc_fence_before();
