@@ -15,9 +15,8 @@
 // tensor cores that would otherwise wait: with a head per tile (no waste) the shared rows would be
 // read hb times as often, and the prefix's rows of a batch of 16 would fill an eighth of a tile.
 // zw = 128 for few sequences, 64 for more (prefix_plan).
-// Per 64-token page: S by tcgen05.mma (M = 128, N = 64, K = d_h + zw) from shared memory into one of
-// two TMEM buffers, P = 2^(S scale log2 e - m) in bf16 over the same columns, O by tcgen05.mma with
-// A = P from TMEM (N = d_h + zw).  Warp roles and the lazily raised maximum as in the prefill
+// Per 64-token page: S by tcgen05.mma (M = 128, N = 64, K = d_h + zw), P = 2^(S scale log2 e - m) in bf16
+// into one of two TMEM buffers, O by tcgen05.mma with A = P from TMEM (N = d_h + zw).  Warp roles and the lazily raised maximum as in the prefill
 // (prefill_tc.cu): warp 0 key producer, 6 value producer (TMA, 128-byte swizzle), 1 issues S, 7 issues
 // P V; 2..5 and 8..11 take the first and the second 32 tokens of a page for one query row per thread (one
 // warp per scheduler spent some 1000 cycles on a page's 64, twice what the MMAs need).
@@ -63,8 +62,10 @@ struct PxLayout {
     static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
     static constexpr uint32_t OFF_MX = OFF_BAR + 512, SMEM = OFF_MX + 1024 + 1024;
     static_assert(VST >= 2 && SMEM <= 232448, "stages");
-    // TMEM columns: two S buffers, O, Q (two bf16 a column)
-    static constexpr uint32_t TM_S = 0, TM_O = 128, TM_Q = TM_O + D_H + ZW;
+    // TMEM columns: S, two P buffers, O, Q (two bf16 a column in P and Q).  The rows take S into registers
+    // at once, so the next page's S is computed while they work on this one's.  (With two S buffers and P written
+    // over S, S_{j+1} had to wait for P_{j-1} V_{j-1}: 1700 cycles a page instead of 1200.)
+    static constexpr uint32_t TM_S = 0, TM_P = 64, TM_O = 128, TM_Q = TM_O + D_H + ZW;
     static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
 };
 
@@ -122,15 +123,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
     uint64_t* q_ready = bars + 0;
+    uint64_t* s_full = bars + 1;    // S_j computed
+    uint64_t* s_read = bars + 2;    // and taken by all rows
     // p_full[j % 2]: P_j written.  Two, because S_{j+1} may be there before P_j: with one barrier the rows
     // could write P_{j+1}, a softmax of some 0.5 us later, before warp 7 has looked at the phase of P_j.  P_{j+2}
-    // needs S_{j+2} and that needs P_j V_j.
-    uint64_t* p_full = bars + 28;   // [2]
-    uint64_t* s_full = bars + 2;    // [2]
-    uint64_t* s_free = bars + 4;    // [2] P_j V_j done: buffer j % 2 may take S_{j+2}
-    // o_done[j % 2]: P_j V_j complete (waited for before a rescale only, which is why there are two: one
-    // cannot complete its next phase before the softmax has passed tile j + 2)
-    uint64_t* o_done = bars + 6;    // [2]
+    // needs P_j V_j.
+    uint64_t* p_full = bars + 4;    // [2]
+    uint64_t* o_done = bars + 6;    // [2] o_done[j % 2]: P_j V_j complete, P buffer j % 2 free
     uint64_t* s_drain = bars + 8;   // all S MMAs of the CTA complete
     uint64_t* pv_drain = bars + 9;
     uint64_t* k_full = bars + 10;   // [4]
@@ -144,10 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         mbar_init(B(q_ready), 256);
+        mbar_init(B(s_full), 1);
+        mbar_init(B(s_read), 256);
         for (int i = 0; i < 2; ++i) {
             mbar_init(B(p_full + i), 256);
-            mbar_init(B(s_full + i), 1);
-            mbar_init(B(s_free + i), 1);
             mbar_init(B(o_done + i), 1);
         }
         mbar_init(B(s_drain), 1);
@@ -229,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
         const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K);
         auto s_tile = [&](int j, auto UU) -> bool {
-            constexpr int U = decltype(UU)::value, st = U % KST, sb = U & 1;
+            constexpr int st = decltype(UU)::value % KST;
             if (aborted() || !wait_all(B(k_full + st), (j / KST) & 1, d.status) ||
-                (j >= 2 && !wait_all(B(s_free + sb), ((j >> 1) - 1) & 1, d.status)))
+                (j >= 1 && !wait_all(B(s_read), (j - 1) & 1, d.status)))
                 return false;
             tc_fence_after();
             constexpr uint64_t so = st * (Lay::K_BYTES >> 4);
@@ -240,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t bd = dK + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
                 if (elect_one_sync()) {
                     if (kk < Lay::QBT * 4)
-                        tc_mma_bf16_ts(tmem + Lay::TM_S + sb * 64, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
+                        tc_mma_bf16_ts(tmem + Lay::TM_S, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
                     else
-                        tc_mma_bf16(tmem + Lay::TM_S + sb * 64, dQ + ((kk & 3) * 32 >> 4), bd, id_S, 1);
+                        tc_mma_bf16(tmem + Lay::TM_S, dQ + ((kk & 3) * 32 >> 4), bd, id_S, 1);
                 }
             }
             if (elect_one_sync()) {
-                tc_commit(B(s_full + sb));
+                tc_commit(B(s_full));
                 tc_commit(B(k_empty + st));
             }
             __syncwarp();
@@ -254,8 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = wait_all(B(q_ready), 0, d.status);
         tc_fence_after();
-        for (int j = 0; j < nt && ok; j += lcm2(KST))
-            ok = tiles(s_tile, j, nt, std::make_integer_sequence<int, lcm2(KST)>{});
+        for (int j = 0; j < nt && ok; j += KST) ok = tiles(s_tile, j, nt, std::make_integer_sequence<int, KST>{});
         if (!ok) *abort_flag = 1;
         // every MMA this warp issued has finished before the CTA tears TMEM down
         if (elect_one_sync()) tc_commit(B(s_drain));
@@ -275,12 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kBlockSize / 16; ++kk)
                 if (elect_one_sync())
-                    tc_mma_bf16_ts(tmem + Lay::TM_O, tmem + Lay::TM_S + sb * 64 + kk * 8, dV + so + (kk * 2048 >> 4),
+                    tc_mma_bf16_ts(tmem + Lay::TM_O, tmem + Lay::TM_P + sb * 32 + kk * 8, dV + so + (kk * 2048 >> 4),
                                    id_PV, (j | kk) != 0);
             if (elect_one_sync()) {
                 tc_commit(B(o_done + sb));
                 tc_commit(B(v_empty + st));
-                tc_commit(B(s_free + sb));
             }
             __syncwarp();
             return true;
@@ -363,13 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // visible tokens of this page: none of a page with a bad id
             const int blk = a.blocks[pg0 + j];
             const int lim = blk >= 0 && blk < d.num_blocks ? P - (pg0 + j) * kBlockSize : 0;
-            ok = ok && !aborted() && wait_all(B(s_full + (j & 1)), (j >> 1) & 1, d.status);
-            const uint32_t sb = tmem + tl + Lay::TM_S + (j & 1) * 64;
+            ok = ok && !aborted() && wait_all(B(s_full), j & 1, d.status);
             uint32_t sv[32];
             float mx = -INFINITY;
             if (ok) {
                 tc_fence_after();
-                tmem_ld_32x32b_x32(sb + half * 32, sv);
+                tmem_ld_32x32b_x32(tmem + tl + Lay::TM_S + half * 32, sv);
+                tc_fence_before();
+                mbar_arrive(B(s_read));
                 if (lim < kBlockSize) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sv[e] = half * 32 + e < lim ? sv[e] : 0xff800000u;
@@ -419,8 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 r4[(e >> 1) & 3] += p0 + p1;
                 pk[e / 2] = pack_bf16x2(p0, p1);
             }
-            // (both halves have read their S before either writes P over it: the barrier above)
-            tmem_st_32x32b_x16(sb + half * 16, pk);
+            if (j >= 2) {  // P_{j-2} V_{j-2} has read this P buffer
+                ok = wait_all(B(o_done + (j & 1)), ((j - 2) >> 1) & 1, d.status);
+                if (!ok) continue;
+                tc_fence_after();
+            }
+            tmem_st_32x32b_x16(tmem + tl + Lay::TM_P + (j & 1) * 32 + half * 16, pk);
             l = l * alpha + ((r4[0] + r4[1]) + (r4[2] + r4[3]));
             mref = muse;
             // O may only be rescaled once P_{j-1} V_{j-1} has finished accumulating into it
@@ -685,19 +687,19 @@ int prefix_most_splits(int H, int D_H, int R, int D_R, int B, int max_blocks, in
 }
 
 // How many pieces, and whether some SMs are kept for the scan of the sequences' own tokens, by a model of
-// the two launches in us: a piece costs 6 (queries, pipeline fill, partials) and 0.9 a page of 512 columns,
+// the two launches in us: a piece costs 6 (queries, pipeline fill, partials) and 0.8 a page of 512 columns,
 // the pieces of all tiles run in waves of one CTA per SM; the other scan costs 6, as much again for each
-// sequence that a CTA meets, and streams 35 bytes a ns on one SM.  Of the own tables' capacity half is
+// sequence that a CTA meets, and streams 28 bytes a ns on one SM.  Of the own tables' capacity half is
 // taken to be in use.  Measured: 32 heads x 16 sequences behind 8 K tokens 33 us one after the other, 25 side by
 // side; 128 x 48 behind 4 K 76 and 68.
 PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, double own_bytes, int sms) {
     PrefixPlan best = prefix_tile(H, D_H, R, D_R, B);
     const long long ntiles = (long long)best.htiles * best.stiles;
-    const double page = 0.9 * (2 * D_H + D_R + 2 * best.zw) / 512;
+    const double page = 0.8 * (2 * D_H + D_R + 2 * best.zw) / 512;
     double least = -1;
     for (int own = 0; own <= sms / 2; own += 8) {
         const int n = sms - own, m = own ? own : sms;
-        const double t_own = own_bytes > 0 ? 6 + 6 * (1 + (double)B / m) + own_bytes / 2 / 35e3 / m : 0;
+        const double t_own = own_bytes > 0 ? 6 + 6 * (1 + (double)B / m) + own_bytes / 2 / 28e3 / m : 0;
         for (int s = 1; s <= max_blocks && (s == 1 || ntiles * s <= 2LL * n); ++s) {
             const long long waves = (ntiles * s + n - 1) / n;
             const double t_prefix = waves * (page * ((max_blocks + s - 1) / s) + 6);
