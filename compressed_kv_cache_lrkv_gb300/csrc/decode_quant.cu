@@ -170,7 +170,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
     constexpr int NZC = R > 16 ? R / 16 : 1;       // 16-byte chunks of a head's latents (r = 8: of two heads')
     constexpr int NCH = 8 * R / 16;                // chunks of a tile of 8 heads
     constexpr int TPP = kBlockSize / TOK;          // tiles per page
-    constexpr int kUnroll = CW == 8 ? 8 : 4;       // of the loops over chunks (96 registers: 4)
+    constexpr int kUnroll = CW == 8 ? 8 : 2;       // of the loops over chunks (96 registers: 4)
     using WorkQ = WorkT<TOK>;
     static_assert(sizeof(WorkQ) <= 96 && alignof(WorkQ) <= 16, "room for the plan in shared memory");
     static_assert(CW + 1 + kConverters <= kMaxWalkers, "walkers");
