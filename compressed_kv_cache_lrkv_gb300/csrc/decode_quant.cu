@@ -144,13 +144,91 @@ struct QuantScanArgs {
     QuantPlan p;
 };
 
-// One warp's walk over the CTA's segments.
+// One warp's walk over the CTA's segments, as SegWalk's (decode_work.cuh, one layer), but stepped by the whole
+// warp: the search for the sequence that a piece or range begins in takes 32 sequences at a time.  (One lane
+// searching took up to 4 us of a CTA's start with 24 sequences.)
 struct alignas(16) Walker {
-    SegWalk walk;
+    int item, gcur, gend, vstart, seg_start;
     int valid, vb, g0, g1, slot;
+
+    // The first sequence b whose running total (of n(b), from `total` at b = 0 on) exceeds x, and the total before it.
+    template <class W, class F>
+    __device__ __forceinline__ static void search(const W& w, int x, int lane, F n, int* b_out, int* before) {
+        int total = 0;
+        for (int b0 = 0;; b0 += 32) {
+            const int b = b0 + lane;
+            const int mine = b < w.B ? n(b) : 0;
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += t;
+            }
+            const uint32_t hit = __ballot_sync(0xffffffffu, total + sum > x);
+            if (hit || b0 + 32 >= w.B) {
+                // (without a hit x lies behind the last sequence, which a plan never asks for: its last lane is taken)
+                const int l = hit ? __ffs(hit) - 1 : min(31, w.B - 1 - b0);
+                *b_out = b0 + l;
+                *before = total + __shfl_sync(0xffffffffu, sum - mine, l);
+                return;
+            }
+            total += __shfl_sync(0xffffffffu, sum, 31);
+        }
+    }
+    __device__ __forceinline__ void start(int first_item) {
+        item = first_item;
+        gcur = gend = vstart = seg_start = vb = 0;
+    }
+    // Steps to the next segment (valid = 0: none left).  The whole warp calls it; lane 0 keeps the state.
     template <class W>
-    __device__ __forceinline__ void advance(const W& w) {
-        valid = walk.next(w, &vb, &g0, &g1, &slot);
+    __device__ __forceinline__ void advance(const W& w, int lane) {
+        __syncwarp();
+        Walker n = *this;
+        n.valid = 1;
+        if (w.pieces) {
+            if (n.item >= w.work_items()) {
+                n.valid = 0;
+            } else {
+                int b, base;
+                search(w, n.item, lane, [&](int i) { return w.npieces(i, w.chunk); }, &b, &base);
+                const unsigned gr = (unsigned)w.gran_b(b);
+                const unsigned np = (gr + w.chunk - 1) / (unsigned)w.chunk, i = (unsigned)(n.item - base);
+                const unsigned q = gr / np, r = gr - q * np;  // floor(i gr / np), i < np <= 2^16
+                n.vb = b;
+                n.g0 = (int)(i * q + (i * r) / np);
+                n.g1 = (int)((i + 1) * q + ((i + 1) * r) / np);
+                n.slot = n.item;
+                n.item += gridDim.x;
+            }
+        } else {
+            if (n.gcur >= n.gend) {
+                if (n.gend > 0) n.item += gridDim.x;  // the current range is done
+                if (n.item >= w.nranges) {
+                    n.valid = 0;
+                } else {
+                    n.gcur = w.range_start(n.item);
+                    n.gend = w.range_start(n.item + 1);
+                    search(w, n.gcur, lane, [&](int i) { return w.gran_b(i); }, &n.vb, &n.vstart);
+                }
+            } else {
+                // the range goes on in the next sequence that has tokens
+                do {
+                    ++n.vb;
+                } while (n.vb < w.B && w.gran_b(n.vb) == 0);
+            }
+            if (n.valid) {
+                const int gr = w.gran_b(n.vb), se = min(n.gend, n.vstart + gr);
+                n.g0 = n.gcur - n.vstart;
+                n.g1 = se - n.vstart;
+                n.slot = n.vb + n.item;
+                n.seg_start = n.gcur;
+                n.gcur = se;
+                if (se == n.vstart + gr) n.vstart = se;  // the next segment, if any, starts another sequence
+            }
+        }
+        __syncwarp();
+        if (lane == 0) *this = n;
+        __syncwarp();
     }
 };
 static_assert(sizeof(Walker) == 48, "walkers are an array in shared memory with the work plan behind it");
@@ -222,11 +300,8 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
     }
     __syncthreads();
     Walker& wk = walkers[warp];
-    if (lane == 0) {
-        wk.walk.start(blockIdx.x);
-        wk.advance(*work);
-    }
-    __syncwarp();
+    if (lane == 0) wk.start(blockIdx.x);
+    wk.advance(*work, lane);
 
     // All roles walk the same tiles in the same order.  Tile u (counted over the CTA) belongs to group
     // u mod ng and is widened into buffer u mod ncb (ncb a multiple of ng), each buffer by one converter.
@@ -245,7 +320,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                 // a sequence's first segment records where the combine finds its partials
                 const int gr = work->gran(b);
                 const int np = work->pieces ? work->npieces(b, work->chunk)
-                                            : work->range_of(wk.walk.seg_start + gr - 1) - (wk.slot - b) + 1;
+                                            : work->range_of(wk.seg_start + gr - 1) - (wk.slot - b) + 1;
                 a.seg_table[b] = make_int2(wk.slot, np);
             }
             // the ring's memory serves the group merge at the end of a segment
@@ -291,8 +366,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                 f = e;
             }
             ++segs;
-            if (lane == 0) wk.advance(*work);
-            __syncwarp();
+            wk.advance(*work, lane);
         }
         // After an expired wait, let the copies in flight land before the CTA exits.
         if (*abort_flag)
@@ -356,9 +430,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                 }
                 f = e;
             }
-            __syncwarp();
-            if (lane == 0) wk.advance(*work);
-            __syncwarp();
+            wk.advance(*work, lane);
         }
     } else {
         // ---------------------------------------------------------------- consumers
@@ -753,9 +825,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(merged));
             }
-            __syncwarp();
-            if (lane == 0) wk.advance(*work);
-            __syncwarp();
+            wk.advance(*work, lane);
         }
     }
     pdl_trigger();  // the combine waits for this grid's end
