@@ -344,6 +344,9 @@ def lrkv_decode_layers(dims: Dims, q, BK, BV, cache: LayeredCache, block_table, 
     _check(rc, "lrkv_decode_layers")
 
 
+_page_bytes: dict[tuple, int] = {}
+
+
 class QuantCache:
     """One layer's quantised rows: uint8 [num_blocks, 64, quant_row_bytes(dims)]."""
 
@@ -356,7 +359,12 @@ class QuantCache:
         return cls(torch.empty((num_blocks, 64, quant_row_bytes(dims)), dtype=torch.uint8, device=device))
 
     def struct(self, dims: Dims) -> QuantCacheStruct:
-        if self.rows.numel() != self.num_blocks * quant_block_bytes(dims):
+        # (the row's width by dims, so that a decode step need not ask the library for it)
+        key = (dims.H, dims.d_h, dims.r, dims.d_rope, dims.block_size)
+        page = _page_bytes.get(key)
+        if page is None:
+            page = _page_bytes[key] = quant_block_bytes(dims)
+        if self.rows.numel() != self.num_blocks * page:
             raise ValueError(f"quantised rows {tuple(self.rows.shape)}: expected [num_blocks, 64, "
                              f"{quant_row_bytes(dims)}] for these dims")
         return QuantCacheStruct(_ptr(self.rows), self.num_blocks)

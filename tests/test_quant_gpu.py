@@ -383,3 +383,90 @@ def test_append_quantise_decode_step():
     got = c.parts(1)[0][-1]
     assert (got - y[1, :d_h]).abs().max() <= y[1, :d_h].abs().max() * (2.0 ** -7 + 2.0 ** -7)
     c.verify()
+
+
+@pytest.mark.parametrize("H,d_h,r,lens", [(1, 64, 8, [1 + 7 * (i % 90) for i in range(300)]),
+                                          (8, 128, 16, [2000] * 3 + [1] * 170 + [900]),
+                                          (16, 64, 32, [33] * 1100)], ids=["one_head", "uneven", "1100_sequences"])
+def test_more_sequences_than_thread_blocks(H, d_h, r, lens):
+    c = Case(22, H, d_h, r, 0, lens)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify(seqs=[0, 1, 2, 31, 32, 33, 127, 128, 151, 152, 153, len(lens) - 2, len(lens) - 1])
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,ns", [(8, 64, 8, 64, 1), (112, 128, 32, 64, 3), (2, 128, 16, 0, 0)])
+def test_long_sequences_in_few_pieces(H, d_h, r, d_rope, ns):
+    """Many rounds of each ring of buffers in one segment."""
+    c = Case(23, H, d_h, r, d_rope, [12001], num_splits=ns)
+    c.run()
+    assert int(c.st.item()) == 0
+    first = c.out.clone()
+    c.verify()
+    for _ in range(3):
+        assert torch.equal(c.run(), first)
+
+
+def test_cleared_rows():
+    """Rows as in memory that was cleared stand for zeros: among others, as a whole sequence, as its start."""
+    c = Case(24, 9, 64, 16, 0, [100, 70, 300])
+    rows = c.qc.rows.view(-1, c.qc.rows.shape[2])
+    rows[c.slots[0][::3]] = 0
+    rows[c.slots[1]] = 0
+    rows[c.slots[2][:200]] = 0
+    c.run()
+    assert int(c.st.item()) == 0 and (c.out[1] == 0).all()
+    c.verify()
+
+
+def test_pages_listed_twice_and_shared():
+    """The same page twice in a sequence, and in two sequences."""
+    c = Case(25, 16, 128, 16, 0, [200, 190])
+    c.bt[0, 2] = c.bt[0, 0]
+    c.bt[1, :2] = c.bt[0, :2]
+    for i, n in enumerate(c.lens):
+        t = torch.arange(n, device="cuda")
+        c.slots[i] = c.bt[i][t // 64].long() * 64 + t % 64
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify()
+
+
+def test_a_nan_query_stays_in_its_head():
+    c = Case(26, 9, 64, 16, 0, [200, 40])
+    c.q[0, 3, 5] = float("nan")
+    c.run()
+    nan = torch.isnan(c.out)
+    assert nan[0, 3].all() and int(nan.sum()) == 64
+    keep = c.out.clone()
+    c.q[0, 3, 5] = 1.0
+    c.run()
+    keep[0, 3] = c.out[0, 3]
+    assert torch.equal(keep, c.out)
+    c.verify()
+
+
+def test_calls_on_two_streams():
+    """Two calls at once, each with a workspace of its own."""
+    cases = [Case(27, 32, 128, 32, 0, [3000, 700]), Case(28, 8, 64, 16, 0, [5000] * 4)]
+    want = [c.run().clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            c.run(stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert torch.equal(c.out, w) and int(c.st.item()) == 0
+
+
+def test_small_workspaces_are_refused():
+    c = Case(29, 8, 64, 16, 0, [100, 3])
+    need = b.decode_quant_workspace_bytes(c.dims, 2)
+    c.ws = c.ws[:need]
+    c.run()
+    c.verify()
+    c.ws = c.ws[:need - 1]
+    with pytest.raises(b.LrkvError, match="workspace") as e:
+        c.run()
+    assert e.value.status == 3

@@ -207,3 +207,95 @@ def test_runs_are_bitwise_repeatable():
     first = c.run().clone()
     for _ in range(5):
         assert torch.equal(c.run(), first)
+
+
+@pytest.mark.parametrize("H,d_h,r,P,B,own", [(128, 64, 16, 6000, 64, 3), (32, 128, 32, 32768, 32, 20),
+                                             (8, 128, 8, 20011, 40, 0)])
+def test_many_pages_a_piece_repeated(H, d_h, r, P, B, own):
+    """Many rounds of every buffer in one thread block, run after run: results may not depend on who came first."""
+    c = Case(11, H, d_h, r, 0, P, [own] * B)
+    first = c.run().clone()
+    for _ in range(30):
+        c.run()
+        assert torch.equal(c.out, first)
+    assert int(c.st.item()) == 0
+    c.verify(seqs=[0, B - 1])
+
+
+@pytest.mark.parametrize("H,d_h,r,P,lens", [(1, 64, 8, 90, [i % 5 for i in range(1000)]),
+                                            (3, 128, 16, 130, [1 + i % 70 for i in range(257)])])
+def test_many_sequences(H, d_h, r, P, lens):
+    c = Case(12, H, d_h, r, 0, P, lens)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify(seqs=[0, 1, 15, 16, 127, 128, 129, len(lens) - 1])
+
+
+@pytest.mark.parametrize("ns", [1, 3, 500])
+def test_split_counts(ns):
+    c = Case(13, 16, 128, 16, 0, 1500, [900, 0, 1, 40], num_splits=ns)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify(what=f"num_splits {ns}")
+
+
+def test_pages_listed_twice_and_shared():
+    """A page twice in the prefix, and again among a sequence's own."""
+    c = Case(14, 16, 128, 16, 0, 200, [100, 70])
+    c.blocks[2] = c.blocks[0]
+    c.bt[1, 0] = c.blocks[1]
+    c.pslots = c.at(c.blocks, 200)
+    c.slots[1] = c.at(c.bt[1], 70)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify()
+
+
+def test_a_nan_query_stays_in_its_head():
+    c = Case(15, 9, 64, 16, 0, 300, [20, 0, 3])
+    c.q[1, 4, 7] = float("nan")
+    c.run()
+    nan = torch.isnan(c.out)
+    assert nan[1, 4].all() and int(nan.sum()) == 64
+    keep = c.out.clone()
+    c.q[1, 4, 7] = 1.0
+    c.run()
+    keep[1, 4] = c.out[1, 4]
+    assert torch.equal(keep, c.out)
+    c.verify()
+
+
+def test_calls_on_two_streams():
+    cases = [Case(16, 32, 128, 16, 0, 4000, [50] * 16), Case(17, 8, 64, 16, 0, 900, [5] * 4)]
+    want = [c.run().clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            c.run(stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert torch.equal(c.out, w) and int(c.st.item()) == 0
+
+
+def test_partials_of_a_bad_prefix_length():
+    c = Case(18, 8, 64, 16, 0, 200, [1, 1])
+    parts = torch.full((2, 8, 64 + 16 + 2), float("nan"), device="cuda")
+    for bad in (-1, 257, 2 ** 31 - 1):
+        c.st.zero_()
+        c.pl.fill_(bad)
+        b.lrkv_prefix_partials(c.dims, c.q, c.BK, c.cache, c.blocks, c.pl, parts, c.ws, status=c.st)
+        assert int(c.st.item()) == BAD_SEQLEN
+        assert torch.isneginf(parts[..., -2]).all() and (parts[..., -1] == 0).all() and (parts[..., :-2] == 0).all()
+
+
+def test_small_workspaces_are_refused():
+    c = Case(19, 8, 64, 16, 0, 200, [100, 3])
+    need = b.decode_shared_workspace_bytes(c.dims, 2, int(c.blocks.shape[0]))
+    c.ws = c.ws[:need]
+    c.run()
+    c.verify()
+    c.ws = c.ws[:need - 1]
+    with pytest.raises(b.LrkvError, match="workspace") as e:
+        c.run()
+    assert e.value.status == 3
