@@ -44,16 +44,20 @@ __device__ __forceinline__ bool prefix_good(const PrefixArgs& a, int P) {
     return P >= 0 && P <= a.max_blocks * kBlockSize;
 }
 
-// [Q | diag(Q~)] is the A operand of S: its first four 64-column blocks sit in TMEM (an MMA of N = 64
-// would read twice as many bytes of A from shared memory as of B, and shared memory is what bounds
-// it: 32 heads of r = 32 x 32 sequences, 32 K tokens, 33 us instead of 38), a fifth (positional key with zw =
-// 128) in shared memory.  Shared memory: that block (16 KB), a ring of key stages [64 tokens][D_K + ZW] and one
-// of value stages [64][D_H + ZW] (64-column blocks of 8 KB), barriers.  As many stages as fit.
+// [Q | diag(Q~)] is the A operand of S, diag(Q~) as two matrices: q~ rounded to bf16, and what that rounding
+// left, rounded to bf16 (each a product with the same z^K).  With the first alone the output's relative error was
+// 0.0031, of which the output's own rounding is 0.0016; with both it is 0.0024.
+// As many of its 64-column blocks as fit sit in TMEM (an MMA of N = 64 would read twice as many bytes of
+// A from shared memory as of B, and shared memory is what bounds it: 32 heads of r = 32 x 32 sequences, 32 K tokens,
+// 33 us instead of 38), the rest (zw = 128 with d_h = 128) in shared memory.  Shared memory: those blocks (16 KB
+// each), a ring of key stages [64 tokens][D_K + ZW] and one of value stages [64][D_H + ZW] (64-column
+// blocks of 8 KB), barriers.  As many stages as fit.
 template <int D_H, int D_R, int ZW>
 struct PxLayout {
     static constexpr int D_K = D_H + D_R;
     static constexpr int NBK = (D_K + ZW) / 64, NBV = (D_H + ZW) / 64;  // 64-column blocks of a key / value row
-    static constexpr int QBT = NBK < 4 ? NBK : 4, QBS = NBK - QBT;  // blocks of Q in TMEM, in shared memory
+    static constexpr int NBQ = NBK + ZW / 64, QROOM = (384 - D_H - ZW) / 32;  // blocks of Q, and room in TMEM
+    static constexpr int QBT = NBQ < QROOM ? NBQ : QROOM, QBS = NBQ - QBT;  // in TMEM, in shared memory
     static constexpr uint32_t Q_BYTES = QBS * 16384, K_BYTES = NBK * 8192, V_BYTES = NBV * 8192;
     static constexpr uint32_t ROOM = 232448 - 1024 - 1536 - Q_BYTES;
     static constexpr int BOTH = ROOM / (K_BYTES + V_BYTES);
@@ -90,7 +94,7 @@ template <int D_H, int D_R, int ZW>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_scan_kernel(const __grid_constant__ PrefixMaps m, const PrefixArgs a, const int R) {
     using Lay = PxLayout<D_H, D_R, ZW>;
-    constexpr int D_K = Lay::D_K, NBK = Lay::NBK, NBV = Lay::NBV, KST = Lay::KST, VST = Lay::VST;
+    constexpr int D_K = Lay::D_K, NBK = Lay::NBK, NBQ = Lay::NBQ, NBV = Lay::NBV, KST = Lay::KST, VST = Lay::VST;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
@@ -235,13 +239,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             constexpr uint64_t so = st * (Lay::K_BYTES >> 4);
 #pragma unroll
-            for (int kk = 0; kk < NBK * 4; ++kk) {
-                const uint64_t bd = dK + so + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
+            for (int kk = 0; kk < NBQ * 4; ++kk) {
+                const int kb = kk >> 2 < NBK ? kk >> 2 : (kk >> 2) - ZW / 64;  // z^K's blocks twice
+                const uint64_t bd = dK + so + ((kb * 8192 + (kk & 3) * 32) >> 4);
                 if (elect_one_sync()) {
                     if (kk < Lay::QBT * 4)
                         tc_mma_bf16_ts(tmem + Lay::TM_S, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
                     else
-                        tc_mma_bf16(tmem + Lay::TM_S, dQ + ((kk & 3) * 32 >> 4), bd, id_S, 1);
+                        tc_mma_bf16(tmem + Lay::TM_S, dQ + ((((kk >> 2) - Lay::QBT) * 16384 + (kk & 3) * 32) >> 4), bd,
+                                    id_S, 1);
                 }
             }
             if (elect_one_sync()) {
@@ -294,15 +300,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tl = (uint32_t)(qq * 32) << 16;
         {
             // [Q | diag(Q~)] row, block by block of 64 columns: into TMEM (two columns a register), or K-major with
-            // 128-byte swizzle (16-byte chunk c at c ^ (row mod 8)).  q~ is rounded to bf16, as in the prefill.
-            // The two halves' threads of a row take every other block.
+            // 128-byte swizzle (16-byte chunk c at c ^ (row mod 8)).  The two halves' threads of a row take every
+            // other block.
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const size_t qr = (size_t)(live ? rb : 0) * H + (live ? rh : 0);
             const uint4* q = reinterpret_cast<const uint4*>(d.q + qr * D_K);
             const float* qt = d.qt + qr * R;
             bool waited = false;
 #pragma unroll
-            for (int bk = 0; bk < NBK; ++bk) {
+            for (int bk = 0; bk < NBQ; ++bk) {
                 if ((bk & 1) != half) continue;
                 if (bk >= D_K / 64 && !waited) {
                     pdl_wait();     // q~
@@ -316,12 +322,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (bk < D_K / 64) {
                         if (live) x = q[bk * 8 + c];
                     } else {
-                        const int col = (bk - D_K / 64) * 64 + c * 8 - hl * R;
+                        const int col = (bk - (bk < NBK ? D_K / 64 : NBK)) * 64 + c * 8 - hl * R;
                         if (live && col >= 0 && col < R) {
                             const float4 y = *reinterpret_cast<const float4*>(qt + col);
                             const float4 z = *reinterpret_cast<const float4*>(qt + col + 4);
                             x = make_uint4(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w), pack_bf16x2(z.x, z.y),
                                            pack_bf16x2(z.z, z.w));
+                            if (bk >= NBK)  // what the rounding left
+                                x = make_uint4(pack_bf16x2(y.x - bf16lo(x.x), y.y - bf16hi(x.x)),
+                                               pack_bf16x2(y.z - bf16lo(x.y), y.w - bf16hi(x.y)),
+                                               pack_bf16x2(z.x - bf16lo(x.z), z.y - bf16hi(x.z)),
+                                               pack_bf16x2(z.z - bf16lo(x.w), z.w - bf16hi(x.w)));
                         }
                     }
                     v[4 * c] = x.x;
@@ -334,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4*>(smem + row * 128 + ((c ^ (row & 7)) << 4)) =
+                        *reinterpret_cast<uint4*>(smem + (bk - Lay::QBT) * 16384 + row * 128 +
+                                                  ((c ^ (row & 7)) << 4)) =
                             make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
                 }
             }
@@ -395,19 +407,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vst = 0;
                 vphase ^= 1;
             }
-            // The row's maximum over both halves, in bf16 (as the reference of the exponents it only has to be the
-            // same for both; the next write to this parity's slot comes after the next page's barrier).
+            // The row's maximum over both halves, in bf16 (the next write to this parity's slot comes after the next
+            // page's barrier).
             mxs[(j & 1) * 2 + half] = (uint16_t)(__float_as_uint(mx) >> 16);
             named_bar(1 + qq, 64);
             const uint32_t both = *reinterpret_cast<const uint32_t*>(mxs + (j & 1) * 2);
-            mx = fmaxf(bf16lo(both), bf16hi(both));
+            const bool raise = fmaxf(bf16lo(both), bf16hi(both)) > mref + kRescaleThreshold;  // or the row's first token
+            float alpha = 1.f;
+            // Where it is raised, the reference is the exact maximum, so that the heaviest token's probability, 1, is not
+            // rounded (pieces of a page or two: the output's error 0.0018 instead of 0.0027).  Every thread follows
+            // the exchange, after an expired wait too: the halves' references, and so their barriers, stay the same.
+            if (__any_sync(0xffffffffu, raise)) {
+                float* const fx = reinterpret_cast<float*>(mxs);  // [half], over both parities' slots
+                named_bar(1 + qq, 64);
+                fx[half] = mx;
+                named_bar(1 + qq, 64);
+                const float mnew = fmaxf(mref, fmaxf(fx[0], fx[1]));
+                named_bar(1 + qq, 64);
+                if (raise) {
+                    alpha = mref == -INFINITY ? 0.f : ex2_approx(mref - mnew);
+                    mref = mnew;
+                }
+            }
             if (!ok) continue;
-            const float mnew = fmaxf(mref, mx);
-            const bool raise = mnew > mref + kRescaleThreshold;  // also the first time a row sees a token
-            const float muse = raise ? mnew : mref;
-            const float alpha = raise ? (mref == -INFINITY ? 0.f : ex2_approx(mref - mnew)) : 1.f;
             // p = 2^(s scale log2 e - m), 0 everywhere as long as the row has seen no token
-            const float nm = muse == -INFINITY ? -INFINITY : -muse;
+            const float nm = mref == -INFINITY ? -INFINITY : -mref;
             float r4[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t pk[16];
 #pragma unroll
@@ -424,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_32x32b_x16(tmem + tl + Lay::TM_P + (j & 1) * 32 + half * 16, pk);
             l = l * alpha + ((r4[0] + r4[1]) + (r4[2] + r4[3]));
-            mref = muse;
             // O may only be rescaled once P_{j-1} V_{j-1} has finished accumulating into it
             if (j > 0 && __any_sync(0xffffffffu, raise)) {
                 ok = wait_all(B(o_done + ((j - 1) & 1)), ((j - 1) >> 1) & 1, d.status);
@@ -659,8 +682,10 @@ __global__ void __launch_bounds__(512) prefix_combine_kernel(const PrefixArgs a)
 
 static size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Which tile: the fewest tensor-core products, tiles x (d_k + d_h + 2 zw) (one of 64 columns covers twice
-// the sequences of one of 128 with half the heads).
+// Which tile: the fewest columns to take, tiles x (d_k + d_h + 2 zw) (one of 64 columns covers twice the
+// sequences of one of 128 with half the heads).  128 heads of r = 16 x 48 sequences, positional key: 48 tiles of
+// 128 columns, 64 us; 64 of 64, 84 us.  (The second product with z^K does not count: the tensor cores wait for the
+// softmax, and 32 heads of r = 32 x 32 sequences take 55 us with it and 57 without.)
 static PrefixPlan prefix_tile(int H, int D_H, int R, int D_R, int B) {
     PrefixPlan best{};
     long long best_cost = -1;

@@ -70,7 +70,7 @@ class Case:
         out = self.out if out is None else out
         seqs = range(len(self.lens)) if seqs is None else seqs
         for i in seqs:
-            # probabilities and q~ are rounded to bf16 for the tensor cores
+            # probabilities are rounded to bf16 for the tensor cores; so is q~ for a sequence's own tokens
             want, bound = attend64(self.q[i].double(), self.BK.double(), self.BV.double(), self.parts(i), self.d_rope,
                                    eps_p=2.0 ** -8, eps_qt=2.0 ** -8)
             check(out[i], want, bound, f"{what} P={self.P} sequence {i} of {self.lens[i]}", rel_max)
@@ -141,6 +141,17 @@ def test_sharp_and_flat_logits():
     c.q[10:15] = 0
     c.run()
     c.verify(rel_max=1.0)  # (logits 20 times as large magnify q~'s rounding: the bound says by how much)
+
+
+def test_queries_keep_more_than_one_rounding():
+    """Two roundings to bf16 are left over a prefix, the probabilities' and the output's.  Rounding x = f 2^e, f
+    spread evenly over [1, 2), is off by up to 2^-8 2^e: 2^-8 / sqrt 3 * sqrt E[f^-2] = 0.0016 of x, root mean
+    square, and two of them 0.0023.  q~ rounded to bf16 as well would move logits of unit spread by as much again:
+    0.0028."""
+    for H, d_h, P in ((32, 128, 4096), (8, 64, 500)):
+        c = Case(20, H, d_h, 16, 0, P, [0, 0])
+        c.run()
+        c.verify(rel_max=2.5e-3)
 
 
 def test_prefix_partials_join_other_caches():
