@@ -8,8 +8,8 @@
 // value, and each value must first be widened.  All products are therefore fed to the tensor
 // cores (mma.sync m16n8k16), the latents' too, straight from the row bytes:
 //   - a byte u = q + 128 becomes fp16 by one byte permute (two values 1024 + u at a time, exact);
-//     the offset 1152 = 1024 + 128 leaves the sums again as -1152 sum q~ (in the K sums' start) and
-//     -1152 sum w (one product with a constant A per tile);
+//     the offset 1152 = 1024 + 128 leaves the sums again as -1152 sum q~ (in the latents' K sums'
+//     start; s^K's likewise or by a product with a constant A) and -1152 sum w (one such product per tile);
 //   - tokens are the M of the logits' product (A = 16 tokens x 16 features, B = features x 8
 //     heads) and the K of the values' (A = features x 16 tokens, B = 16 tokens x 8 heads), so both
 //     leave a thread the same two heads and the probabilities pass from one to the other by a
@@ -24,8 +24,17 @@
 //     by converter warps.
 // Warps of a CTA: consumers (8 heads each, ng groups taking 16-token tiles in turn), one
 // producer (bulk copies of whole rows, which lie contiguous within a page, into a ring of
-// stages), three converters; connected by mbarriers only, so they drift freely.  One CTA per
+// stages), one or three converters; connected by mbarriers only, so they drift freely.  One CTA per
 // SM; the work is cut as in the bf16 decode (decode_work.cuh).
+//
+// Measured: 24 sequences of 1 to 8,191 tokens, 32 heads of r = 16 and a positional key 45 us (the rows alone 18
+// at the memory's pace); 4 of 16 to 32 K, 32 heads of r = 32, 50 (36); 8 of 8,192, 128 heads of r = 16, 90 (44);
+// 16 of 2,048, 8 heads, 16 (2).  Bound by the consumers' instructions: a tile of 16 tokens x 8 heads takes a
+// warp some 480, a quarter of them byte permutes, and 2,600 cycles, and twice as many warps take twice as long
+// each; about a third of the issue slots are used, waits being for the half-rate integer pipe, for the tensor
+// cores' results and for instructions (the tile's straight code outruns the instruction cache: unrolled less,
+// 128 heads gain, 32 heads lose).  A call's start (plan, first copies: 5 to 7 us) and end (groups merged, combine:
+// 5 us) make up most of the short cases.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -40,11 +49,14 @@ namespace lrkv {
 namespace {
 
 // Consumer warps at most: 8 (12 warps with the converters and the producer, so that a thread may hold
-// 168 registers) for up to 64 heads, 16 (20 warps, 96 registers) for more.  Measured for 128 heads of
-// r = 16: two tiles of 8 heads per warp in 12 warps 107 us, one in 20 warps 97; for 32 heads of r = 32
-// 16 consumers are slower, as every tile in work holds a stage of the ring: 58 us with 8, 81 with 16.
-constexpr int kConverters = 3;
-constexpr int kMaxWalkers = 20;   // warps of a CTA at most
+// 168 registers) for up to 64 heads, 16 (18 warps, 112 registers) for more.  Measured for 128 heads of
+// r = 16: two tiles of 8 heads per warp in 12 warps 107 us, one with 16 consumers 97 at that time; for 32 heads
+// more consumers are slower: with 8, 12 and 16 the ragged batch takes 45, 48 and 56 us, the long context 50, 60
+// and 78 (every tile in work holds a stage of the ring as well).
+// Warps that widen s^V: a tile takes one some 0.7 us.  With 8 consumers a tile is due every 0.75 us or less (one
+// converter 54 us for the ragged batch, two 47, three 45), with 16 every 3 us, and the registers are worth more.
+__host__ __device__ constexpr int converters(int cw) { return cw == 8 ? 3 : 1; }
+constexpr int kMaxWalkers = 18;   // warps of a CTA at most
 constexpr float kLazy = 8.0f;     // maxima are raised when exceeded by this much (log2 units)
 
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -241,14 +253,19 @@ __host__ __device__ constexpr int merge_stride(int W) { return W % 16 == 0 ? W +
 __host__ __device__ constexpr int cb_stride(int D_H) { return D_H * 2 + 16; }
 
 template <int D_H, int R, int D_R, int CW, int TOK>
-__global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_kernel(const QuantScanArgs args) {
+__global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_kernel(const QuantScanArgs args) {
     constexpr int D_K = D_H + D_R, W = D_H + R, WS = merge_stride(W);
     constexpr int SB = cb_stride(D_H);
     constexpr int NKK = D_K / 16;
     constexpr int NZC = R > 16 ? R / 16 : 1;       // 16-byte chunks of a head's latents (r = 8: of two heads')
     constexpr int NCH = 8 * R / 16;                // chunks of a tile of 8 heads
     constexpr int TPP = kBlockSize / TOK;          // tiles per page
-    constexpr int kUnroll = CW == 8 ? 8 : 2;       // of the loops over chunks (96 registers: 4)
+    constexpr int kConverters = converters(CW);
+    constexpr int kUnroll = CW == 8 ? 8 : 2;       // of the loops over chunks (128 heads: 8 takes 104 us, 4 101, 2 90)
+    // The bytes' offset leaves s^K's products by their sums' start instead of by products with a constant A, and
+    // r <= 16 sums its values' products in two chains (ragged batch 47 -> 45 us).  With 16 consumers the shared
+    // memory costs a stage, and the registers more than they bring (128 heads 90 -> 98).
+    constexpr bool kSums = CW == 8;
     using WorkQ = WorkT<TOK>;
     static_assert(sizeof(WorkQ) <= 96 && alignof(WorkQ) <= 16, "room for the plan in shared memory");
     static_assert(CW + 1 + kConverters <= kMaxWalkers, "walkers");
@@ -274,7 +291,8 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
     int* meta = reinterpret_cast<int*>(merged + 2);
     volatile int* abort_flag = meta + nslot;
     int* slc = meta + ((nslot + 1 + 3) & ~3);
-    Walker* walkers = reinterpret_cast<Walker*>(slc + kSeqCache);
+    float* qsums = reinterpret_cast<float*>(slc + kSeqCache);  // [CW][D_K / 32][8]: -1152 x a block's sum of q
+    Walker* walkers = reinterpret_cast<Walker*>(qsums + (kSums ? CW * (D_K / kQuantBlock) * 8 : 0));
     WorkQ* work = reinterpret_cast<WorkQ*>(walkers + kMaxWalkers);
 
     if (threadIdx.x == 0) {
@@ -451,6 +469,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
         constexpr int NSE = R == 32 ? 2 : 1;         // scales of the two heads (r <= 16: one block for both)
         const int sk_off = g * RB + tq * 4;          // s^K bytes of token g
         const int cv_off = (TOK == 16 ? (lane & 7) + ((lane >> 4) << 3) : lane & 7) * SB + ((lane >> 3) & 1) * 16;
+        float* const qs = qsums + warp * (D_K / kQuantBlock) * 8;
         pdl_wait();  // q~ written by the absorb kernel
         int slot = 0, until = grp;  // until: tiles before this group's next
         int cb = grp;               // and its widened tile
@@ -502,9 +521,23 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     qb[kk][i] = pack_f16x2(bf16lo(qb[kk][i]) * inv, bf16hi(qb[kk][i]) * inv);
-            // The products take 1152 + q for q: the sums start from -1152 sum q~ (as rounded).  (Against
-            // a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of it, more than
-            // q~ has.)
+            // The products take 1152 + u for u: the sums start from -1152 sum q~, and -1152 sum q over each block
+            // (as rounded).  (Against a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of
+            // it, more than q and q~ have.  Taken off by products with a constant A, a block is a chain of four
+            // products instead of two.)
+#pragma unroll
+            for (int bl = 0; bl < (kSums ? D_K / kQuantBlock : 0); ++bl) {
+                float x = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&qb[2 * bl + (i >> 1)][i & 1]));
+                    x += y.x + y.y;
+                }
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                if (tq == 0) qs[bl * 8 + g] = -kByteOffset * x;
+            }
+            __syncwarp();
             float sum = 0.f;
 #pragma unroll
             for (int c = 0; c < NZC; ++c)
@@ -563,7 +596,7 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                                 vb[hf][e] = lds8(row0 + sc_off[e] + hf * g8 + ql.nb_z);
                             }
                         // --- shared logits [q | q^R] . [s^K | k^R], block by block of 32 features: 16 tokens x 8
-                        // heads; the offset leaves by a product with a constant A
+                        // heads
                         constexpr int NBK = D_K / kQuantBlock;
                         uint32_t sc0[2], sc1[2];  // scale bytes of the blocks
                         sc0[0] = lds32(row0 + g * RB + ql.off_sc);
@@ -581,15 +614,18 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                         }
 #pragma unroll
                         for (int bl = 0; bl < NBK; ++bl) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            float2 off = make_float2(0.f, 0.f);
+                            if (kSums) off = *reinterpret_cast<const float2*>(qs + bl * 8 + 2 * tq);
+                            float d[4] = {off.x, off.y, off.x, off.y};
 #pragma unroll
                             for (int kk = 2 * bl; kk < 2 * bl + 2; ++kk) {
                                 const uint32_t x0 = lds32(row0 + sk_off + kk * 16);
                                 const uint32_t x1 = lds32(row0 + sk_off + g8 + kk * 16);
                                 const uint32_t a0 = bytes_f16(x0, 0x4140), a1 = bytes_f16(x1, 0x4140),
                                                a2 = bytes_f16(x0, 0x4342), a3 = bytes_f16(x1, 0x4342);
-                                mma_16816_f16(d, kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
-                                              qb[kk][0], qb[kk][1]);
+                                if (!kSums)
+                                    mma_16816_f16(d, kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2,
+                                                  qb[kk][0], qb[kk][1]);
                                 mma_16816_f16(d, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
                             }
                             const float f0 = byte_scale(sc0[bl >> 2], bl & 3), f1 = byte_scale(sc1[bl >> 2], bl & 3);
@@ -700,10 +736,12 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                         // elements are pairs of features, row g of A takes the even one, row g + 8 the odd
                         // one.  The offset 1152 of the bytes' products is taken off tile by tile (so that the
                         // sums never grow with it).
+                        // (One accumulator would be a chain of all chunks' products; every other goes to a second one.)
+                        float tz[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int zc = 0; zc < NZC; ++zc)
-                            mma_16816_f16(oz[zc], kMinusOffset2, kMinusOffset2, kMinusOffset2, kMinusOffset2, wb0,
-                                          wb1);
+                            mma_16816_f16(NZC == 1 && kSums ? tz : oz[zc], kMinusOffset2, kMinusOffset2, kMinusOffset2,
+                                          kMinusOffset2, wb0, wb1);
 #pragma unroll kUnroll
                         for (int c2 = 0; c2 < NCH; c2 += 2) {
                             uint32_t x[4];
@@ -713,10 +751,14 @@ __global__ void __launch_bounds__((CW + 1 + kConverters) * 32, 1) quant_scan_ker
                                 const int ch = c2 + w;
                                 const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
                                 const int zc = R == 32 ? ch & 1 : 0;
-                                mma_16816_f16(oz[zc], bytes_f16(x[2 * w], 0x4240), bytes_f16(x[2 * w], 0x4341),
+                                mma_16816_f16(NZC == 1 && kSums && w ? tz : oz[zc], bytes_f16(x[2 * w], 0x4240), bytes_f16(x[2 * w], 0x4341),
                                               bytes_f16(x[2 * w + 1], 0x4240), bytes_f16(x[2 * w + 1], 0x4341),
                                               mine ? wb0 : 0u, mine ? wb1 : 0u);
                             }
+                        }
+                        if (NZC == 1 && kSums) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) oz[0][i] += tz[i];
                         }
                     }
                     if (ok && !have) ok = warp_wait(smem_u32(vfull + cb), cphase, abort_flag, a.status, a.wait_ns);
@@ -851,7 +893,7 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
     p->stage_bytes = p->st * tile;
     auto fixed = [&](int nslot, int ncb) {
         return (2 * nslot + 2 * ncb + 2) * 8 + ((nslot + 1 + 3) & ~3) * 4 + kSeqCache * 4 +
-               kMaxWalkers * (int)sizeof(Walker) + 96 + 128;
+               (p->cw == 8 ? p->cw * (D_H + D_R) : 0) + kMaxWalkers * (int)sizeof(Walker) + 96 + 128;
     };
     for (int want = 3; want >= 2; --want)          // stages at least
         for (int ng = ng_most; ng >= 1; --ng)
@@ -866,7 +908,7 @@ bool make_plan(QuantPlan* p, const QuantLayout& q, int H, int smem_limit) {
                 p->ng = ng;
                 p->ncb = ncb;
                 p->nslot = nslot;
-                p->threads = (p->nwh * ng + 1 + kConverters) * 32;
+                p->threads = (p->nwh * ng + 1 + converters(p->cw)) * 32;
                 p->smem_bytes = nslot * p->stage_bytes + ncb * p->cb_bytes + fixed(nslot, ncb);
                 return true;
             }
