@@ -957,8 +957,9 @@ static cudaError_t launch_decode_t(const CUtensorMap& tK, const CUtensorMap& tV,
     if (e != cudaSuccess) return e;
     const int nvb = a.layers * a.B;
     const int grid = a.nranges < sms ? a.nranges : sms;
-    // 128 heads of d_h = 128: the scan on the 5th-generation tensor cores (heads = the MMAs' M)
-    if constexpr (D_H == 128 && D_R == 0 && (R == 8 || R == 16)) {
+    // 128 heads of d_h = 128, r = 16: the scan on the 5th-generation tensor cores (heads = the MMAs' M).  (With
+    // r = 8 its extra shared memory and the six stages planned for a row of that size are above the limit.)
+    if constexpr (D_H == 128 && D_R == 0 && R == 16) {
         if (a.H == 128 && a.nhg == 1 && a.gpst == 1) {
             if (!a.qt_in && !a.no_combine) {
                 e = launch_pdl(decode_absorb_kernel<D_H, R, D_R>, dim3(a.H, nvb), dim3(256), 0, stream, a);

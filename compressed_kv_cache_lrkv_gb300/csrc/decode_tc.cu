@@ -549,8 +549,6 @@ cudaError_t launch_decode_tc_split(const CUtensorMap& tK, const CUtensorMap& tV,
     return cudaLaunchKernelEx(&cfg, k, tK, tV, a);
 }
 
-template cudaError_t launch_decode_tc_split<8>(const CUtensorMap&, const CUtensorMap&, const DecodeArgs&, int, int,
-                                               bool, cudaStream_t);
 template cudaError_t launch_decode_tc_split<16>(const CUtensorMap&, const CUtensorMap&, const DecodeArgs&, int, int,
                                                 bool, cudaStream_t);
 

@@ -470,3 +470,44 @@ def test_small_workspaces_are_refused():
     with pytest.raises(b.LrkvError, match="workspace") as e:
         c.run()
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("H,d_h,r,lens", [(32, 128, 16, [900, 30]), (128, 128, 16, [200] * 9), (8, 64, 8, [1, 600])])
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_back_to_back_share_a_workspace(H, d_h, r, lens, graph):
+    """Rows written and decoded with other queries, lengths and values, call behind call in one workspace."""
+    c = Case(30, H, d_h, r, 0, lens)
+    g = gen(31)
+    qs = [torch.randn(len(lens), H, d_h, generator=g, device="cuda").to(torch.bfloat16) for _ in range(6)]
+    sls = [(c.sl - 7 * i).clamp(min=1) for i in range(6)]
+    last = torch.stack([s[0] for s in c.slots]).int()
+    news = [bf16_cache(g, 1, H, d_h, r, 0) for _ in range(6)]
+    src = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(c.out) for _ in range(6)]
+
+    def call(i, out):
+        b.lrkv_cache_quantize(c.dims, news[i], src, c.qc, last, status=c.st)
+        b.lrkv_decode_quant(c.dims, qs[i], c.BK, c.BV, c.qc, c.bt, sls[i], out, c.ws, status=c.st)
+
+    want = []
+    for i in range(6):
+        call(i, outs[i])
+        torch.cuda.synchronize()
+        want.append(outs[i].clone())
+    if graph:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            for i in range(6):
+                call(i, outs[i])
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        if graph:
+            gr.replay()
+        else:
+            for i in range(6):
+                call(i, outs[i])
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    assert int(c.st.item()) == 0

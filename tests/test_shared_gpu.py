@@ -82,7 +82,7 @@ CASES = [
     (16, 128, 16, 0, 2000, list(range(0, 33))), (32, 128, 16, 0, 4100, [17] * 16), (32, 128, 32, 0, 777, [1] * 33),
     (20, 64, 16, 64, 200, [3] * 130), (40, 128, 8, 0, 500, [0] * 9), (128, 128, 16, 64, 640, [50, 0, 1]),
     (128, 64, 8, 0, 100, [10] * 20), (100, 128, 32, 0, 320, [7, 8]), (128, 128, 32, 0, 192, [66, 2]),
-    (2, 128, 16, 0, 9000, [1, 2, 3]),
+    (2, 128, 16, 0, 9000, [1, 2, 3]), (128, 128, 16, 0, 300, [66, 2, 0, 500]), (128, 128, 8, 0, 70, [1] * 17 + [300]),
 ]
 
 
@@ -105,6 +105,14 @@ def test_no_prefix():
     c.run()
     assert int(c.st.item()) == BAD_SEQLEN and (c.out[1] == 0).all()
     c.verify(seqs=[0])
+
+
+def test_decode_of_128_heads_with_r_8():
+    """The sequences' own scan by itself, lrkv_decode."""
+    c = Case(22, 128, 128, 8, 0, 0, [300, 9, 64])
+    b.lrkv_decode(c.dims, c.q, c.BK, c.BV, c.cache, c.bt, c.sl, c.out, c.ws, status=c.st)
+    assert int(c.st.item()) == 0
+    c.verify(what="decode")
 
 
 def test_table_longer_than_the_prefix():
@@ -310,3 +318,45 @@ def test_small_workspaces_are_refused():
     with pytest.raises(b.LrkvError, match="workspace") as e:
         c.run()
     assert e.value.status == 3
+
+
+@pytest.mark.parametrize("H,d_h,r,lens", [(32, 128, 16, [40] * 16), (128, 128, 8, [3, 200, 70]), (8, 64, 32, [0, 9])])
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_back_to_back_share_a_workspace(H, d_h, r, lens, graph):
+    """Calls with other queries, lengths and prefixes, one behind the other in one workspace: a launch of a call may
+    begin before the one in front of it has ended, and must still see what it left."""
+    c = Case(21, H, d_h, r, 0, 700, lens)
+    B = len(lens)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    qs = [torch.randn(B, H, d_h, generator=g, device="cuda").to(torch.bfloat16) for _ in range(6)]
+    sls = [(c.sl - i).clamp(min=0) for i in range(6)]
+    pls = [c.pl - 100 * i for i in range(6)]
+    outs = [torch.empty_like(c.out) for _ in range(6)]
+
+    def call(i, out):
+        b.lrkv_decode_shared(c.dims, qs[i], c.BK, c.BV, c.cache, c.blocks, pls[i], c.bt, sls[i], out, c.ws,
+                             status=c.st)
+
+    want = []
+    for i in range(6):
+        call(i, outs[i])
+        torch.cuda.synchronize()
+        want.append(outs[i].clone())
+    if graph:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            for i in range(6):
+                call(i, outs[i])
+    for _ in range(10):
+        for o in outs:
+            o.zero_()
+        if graph:
+            gr.replay()
+        else:
+            for i in range(6):
+                call(i, outs[i])
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    assert int(c.st.item()) == 0
