@@ -364,7 +364,7 @@ class QuantCache:
         page = _page_bytes.get(key)
         if page is None:
             page = _page_bytes[key] = quant_block_bytes(dims)
-        if self.rows.numel() != self.num_blocks * page:
+        if self.rows.numel() * self.rows.element_size() != self.num_blocks * page:
             raise ValueError(f"quantised rows {tuple(self.rows.shape)}: expected [num_blocks, 64, "
                              f"{quant_row_bytes(dims)}] for these dims")
         return QuantCacheStruct(_ptr(self.rows), self.num_blocks)

@@ -49,7 +49,7 @@ namespace lrkv {
 namespace {
 
 // Consumer warps at most: 8 (12 warps with the converters and the producer, so that a thread may hold
-// 168 registers) for up to 64 heads, 16 (18 warps, 112 registers) for more.  Measured for 128 heads of
+// 168 registers) for up to 64 heads, 16 (18 warps, 96 registers) for more.  Measured for 128 heads of
 // r = 16: two tiles of 8 heads per warp in 12 warps 107 us, one with 16 consumers 97 at that time; for 32 heads
 // more consumers are slower: with 8, 12 and 16 the ragged batch takes 45, 48 and 56 us, the long context 50, 60
 // and 78 (every tile in work holds a stage of the ring as well).

@@ -14,12 +14,16 @@
 // latent sums only its own head's r are used.  That is hb times the latents' products needed, on
 // tensor cores that would otherwise wait: with a head per tile (no waste) the shared rows would be
 // read hb times as often, and the prefix's rows of a batch of 16 would fill an eighth of a tile.
-// zw = 128 for few sequences, 64 for more (prefix_plan).
-// Per 64-token page: S by tcgen05.mma (M = 128, N = 64, K = d_h + zw), P = 2^(S scale log2 e - m) in bf16
-// into one of two TMEM buffers, O by tcgen05.mma with A = P from TMEM (N = d_h + zw).  Warp roles and the lazily raised maximum as in the prefill
-// (prefill_tc.cu): warp 0 key producer, 6 value producer (TMA, 128-byte swizzle), 1 issues S, 7 issues
-// P V; 2..5 and 8..11 take the first and the second 32 tokens of a page for one query row per thread (one
-// warp per scheduler spent some 1000 cycles on a page's 64, twice what the MMAs need).
+// zw = 128 for few sequences, 64 for more (prefix_tile).
+// Per 64-token page: S by tcgen05.mma (M = 128, N = 64, K = d_k + 2 zw), P = 2^(S scale log2 e - m) in bf16
+// into one of two TMEM buffers, O by tcgen05.mma with A = P from TMEM (N = d_h + zw).  Warp roles and the lazily
+// raised maximum as in the prefill (prefill_tc.cu): warp 0 key producer, 6 value producer (TMA, 128-byte swizzle),
+// 1 issues S, 7 issues P V; 2..5 and 8..11 take the first and the second 32 tokens of a page for one query row
+// per thread (one warp per scheduler spent some 1000 cycles on a page's 64, twice what the MMAs need).
+// Measured, the call as a whole: 32 heads of r = 16 x 16 sequences behind 8,192 tokens 25 us, 32 heads of r = 32 x
+// 32 sequences behind 32,768 55 us, 128 heads of r = 16 with the positional key x 48 behind 4,001 64 us.  A page
+// takes a CTA some 1,900 cycles, of which its products need 1,280 (d_h = zw = 128); the rest is the chain S, softmax,
+// P V of one tile, and a piece's start and end some 6 us.
 #include <type_traits>
 #include <utility>
 
@@ -716,7 +720,7 @@ int prefix_most_splits(int H, int D_H, int R, int D_R, int B, int max_blocks, in
 // the pieces of all tiles run in waves of one CTA per SM; the other scan costs 6, as much again for each
 // sequence that a CTA meets, and streams 28 bytes a ns on one SM.  Of the own tables' capacity half is
 // taken to be in use.  Measured: 32 heads x 16 sequences behind 8 K tokens 33 us one after the other, 25 side by
-// side; 128 x 48 behind 4 K 76 and 68.
+// side; 128 x 48 behind 4 K 76 and 66.
 PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, double own_bytes, int sms) {
     PrefixPlan best = prefix_tile(H, D_H, R, D_R, B);
     const long long ntiles = (long long)best.htiles * best.stiles;
