@@ -158,9 +158,7 @@ def make_mla_dims(H: int, d: int, d_head: int = 128, d_c: int = 512, d_rope: int
 
 
 def _ptr(t) -> int | None:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -407,9 +405,10 @@ def lrkv_cache_dequantize(dims: Dims, qcache: QuantCache, quant_slots, cache: Pa
 
 
 def _same_length(a, b) -> int:
-    if int(a.shape[0]) != int(b.shape[0]):
-        raise ValueError(f"slot arrays of {int(a.shape[0])} and {int(b.shape[0])} rows")
-    return int(a.shape[0])
+    n, m = a.shape[0], b.shape[0]
+    if n != m:
+        raise ValueError(f"slot arrays of {n} and {m} rows")
+    return n
 
 
 def lrkv_decode_quant(dims: Dims, q, BK, BV, qcache: QuantCache, block_table, seq_lens, out, workspace, status=None,
@@ -417,8 +416,8 @@ def lrkv_decode_quant(dims: Dims, q, BK, BV, qcache: QuantCache, block_table, se
     """lrkv_decode over quantised rows: q [B, H, d_h] -> out [B, H, d_h]."""
     qc = qcache.struct(dims)
     rc = load().lrkv_decode_quant(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(qc),
-                                  _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(q.shape[0]),
-                                  _ptr(out), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                  _ptr(block_table), block_table.shape[1], _ptr(seq_lens), q.shape[0],
+                                  _ptr(out), _ptr(workspace), workspace.nbytes,
                                   _ptr(status), _stream(stream))
     _check(rc, "lrkv_decode_quant")
 
@@ -428,9 +427,9 @@ def lrkv_decode_quant_partials(dims: Dims, q, BK, qcache: QuantCache, block_tabl
     """lrkv_decode_partials over quantised rows: -> partials [B, H, d_h + r + 2] fp32."""
     qc = qcache.struct(dims)
     rc = load().lrkv_decode_quant_partials(ctypes.byref(dims), _ptr(q), _ptr(BK), ctypes.byref(qc),
-                                           _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens),
-                                           int(q.shape[0]), _ptr(partials), _ptr(workspace),
-                                           int(workspace.numel() * workspace.element_size()), _ptr(status),
+                                           _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+                                           q.shape[0], _ptr(partials), _ptr(workspace),
+                                           workspace.nbytes, _ptr(status),
                                            _stream(stream))
     _check(rc, "lrkv_decode_quant_partials")
 
@@ -441,9 +440,9 @@ def lrkv_decode_shared(dims: Dims, q, BK, BV, cache: PagedCache, prefix_blocks, 
     tokens in block_table, seq_lens (0 allowed): q [B, H, d_h] -> out [B, H, d_h]."""
     c = cache.struct()
     rc = load().lrkv_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(c),
-                                   _ptr(prefix_blocks), int(prefix_blocks.shape[0]), _ptr(prefix_len),
-                                   _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), int(q.shape[0]),
-                                   _ptr(out), _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                   _ptr(prefix_blocks), prefix_blocks.shape[0], _ptr(prefix_len),
+                                   _ptr(block_table), block_table.shape[1], _ptr(seq_lens), q.shape[0],
+                                   _ptr(out), _ptr(workspace), workspace.nbytes,
                                    _ptr(status), _stream(stream))
     _check(rc, "lrkv_decode_shared")
 
@@ -453,8 +452,8 @@ def lrkv_prefix_partials(dims: Dims, q, BK, cache: PagedCache, prefix_blocks, pr
     """Decode partials of the whole batch over the shared prefix: -> partials [B, H, d_h + r + 2] fp32."""
     c = cache.struct()
     rc = load().lrkv_prefix_partials(ctypes.byref(dims), _ptr(q), _ptr(BK), ctypes.byref(c), _ptr(prefix_blocks),
-                                     int(prefix_blocks.shape[0]), _ptr(prefix_len), int(q.shape[0]), _ptr(partials),
-                                     _ptr(workspace), int(workspace.numel() * workspace.element_size()),
+                                     prefix_blocks.shape[0], _ptr(prefix_len), q.shape[0], _ptr(partials),
+                                     _ptr(workspace), workspace.nbytes,
                                      _ptr(status), _stream(stream))
     _check(rc, "lrkv_prefix_partials")
 
