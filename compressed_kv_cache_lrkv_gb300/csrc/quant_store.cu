@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(kMaxThreads) store_kernel(const QuantStoreArgs
 
 template <bool WRITE>
 cudaError_t launch_store(const QuantStoreArgs& a, int sms, cudaStream_t stream) {
-    const int nc = (total_chunks(a.q) + 31) & ~31;
-    const int threads = nc < kMaxThreads ? nc : kMaxThreads;
-    const int ny = (nc + threads - 1) / threads;
+    const int nc = total_chunks(a.q);
+    const int ny = (nc + kMaxThreads - 1) / kMaxThreads;
+    const int threads = ((nc + ny - 1) / ny + 31) & ~31;
     // some five waves of blocks: with 2048 threads per SM 203 us on the case above, with 16384 169.  (Rows are
     // counted up to n + 2 gridDim.x, below 2^31.)
     const int most = (int)((long long)sms * 8192 / (threads * ny)) + 1;

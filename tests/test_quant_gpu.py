@@ -76,7 +76,7 @@ def flat(cache, H, r):
 
 
 SHAPES = [(1, 64, 8, 0), (3, 64, 8, 64), (8, 64, 16, 0), (5, 128, 32, 0), (33, 128, 16, 64), (32, 128, 32, 0),
-          (128, 128, 16, 0)]
+          (128, 128, 16, 0), (128, 128, 32, 64), (7, 128, 8, 0)]
 
 
 @pytest.mark.parametrize("H,d_h,r,d_rope", SHAPES)
