@@ -511,3 +511,43 @@ def test_calls_back_to_back_share_a_workspace(H, d_h, r, lens, graph):
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
     assert int(c.st.item()) == 0
+
+
+def test_offsets_beyond_32_bits():
+    """The same rows in the last pages of pools of more than 2^31 elements and 2^32 bytes as in small ones: written,
+    read back, decoded, and as a shared prefix."""
+    H, d_h, r, n, big = 128, 64, 32, 150, 8300
+    g = gen(32)
+    dims = b.make_dims(H, d_h, r, H * d_h)
+    small = bf16_cache(g, 3, H, d_h, r, 0)
+    large = b.PagedCache.empty(big, H, d_h, r)
+    assert large.zK.numel() > 2 ** 31 and big * b.quant_block_bytes(dims) > 2 ** 32
+    for s, t in zip(small.tensors(), large.tensors()):
+        t[big - 3:] = s
+    q = torch.randn(1, H, d_h, generator=g, device="cuda").to(torch.bfloat16)
+    BK, BV = ((torch.randn(H, d_h, r, generator=g, device="cuda") * r ** -0.5).to(torch.bfloat16) for _ in range(2))
+    sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    own = torch.tensor([64], dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    results = []
+    for cache in (small, large):
+        nb = cache.num_blocks
+        pages = torch.arange(nb - 3, nb, device="cuda", dtype=torch.int32)
+        slots = torch.arange((nb - 3) * PAGE, (nb - 3) * PAGE + n, device="cuda", dtype=torch.int32)
+        qc = b.QuantCache.empty(dims, nb)
+        b.lrkv_cache_quantize(dims, cache, slots, qc, slots, status=st)
+        out = torch.empty(2, 1, H, d_h, dtype=torch.bfloat16, device="cuda")
+        ws = b.alloc_workspace(max(b.decode_quant_workspace_bytes(dims, 1), b.decode_shared_workspace_bytes(dims, 1, 2)))
+        b.lrkv_decode_quant(dims, q, BK, BV, qc, pages[None], sl, out[0], ws, status=st)
+        b.lrkv_decode_shared(dims, q, BK, BV, cache, pages[:2], torch.full_like(sl, 100), pages[None, 2:], own, out[1], ws,
+                             status=st)
+        for t in cache.tensors():
+            t[nb - 3:] = 0
+        b.lrkv_cache_dequantize(dims, qc, slots, cache, slots, status=st)
+        off, at, blocks, _ = layout(H, d_h, r, 0)  # (the row's padding is not written)
+        results.append([qc.rows[nb - 3:].view(-1, qc.rows.shape[2])[:n, :at + sum(blocks)].clone(), out] +
+                       [t[nb - 3:].clone() for t in cache.tensors()])
+        assert int(st.item()) == 0
+        del qc
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
