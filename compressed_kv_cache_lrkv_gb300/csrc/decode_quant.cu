@@ -30,11 +30,11 @@
 // Measured: 24 sequences of 1 to 8,191 tokens, 32 heads of r = 16 and a positional key 45 us (the rows alone 18
 // at the memory's pace); 4 of 16 to 32 K, 32 heads of r = 32, 50 (36); 8 of 8,192, 128 heads of r = 16, 90 (44);
 // 16 of 2,048, 8 heads, 16 (2).  Bound by the consumers' instructions: a tile of 16 tokens x 8 heads takes a
-// warp some 480, a quarter of them byte permutes, and 2,600 cycles, and twice as many warps take twice as long
-// each; about a third of the issue slots are used, waits being for the half-rate integer pipe, for the tensor
-// cores' results and for instructions (the tile's straight code outruns the instruction cache: unrolled less,
-// 128 heads gain, 32 heads lose).  A call's start (plan, first copies: 5 to 7 us) and end (groups merged, combine:
-// 5 us) make up most of the short cases.
+// warp some 500, a quarter of them byte permutes, and up to 2,900 cycles with the rows already there; with twice as
+// many warps each takes twice as long.  A third to a half of the issue slots are used; the waits are for the
+// half-rate integer pipe, the tensor cores' results, and instructions (unrolled less, 128 heads gain and 32 lose).
+// A call's start (plan, first copies: some 5 us) and end (groups merged, combine: 5 us) make up most of the short
+// cases.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -751,8 +751,9 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                                 const int ch = c2 + w;
                                 const bool mine = R == 8 ? (g >> 1) == ch : g == (R == 32 ? ch >> 1 : ch);
                                 const int zc = R == 32 ? ch & 1 : 0;
-                                mma_16816_f16(NZC == 1 && kSums && w ? tz : oz[zc], bytes_f16(x[2 * w], 0x4240), bytes_f16(x[2 * w], 0x4341),
-                                              bytes_f16(x[2 * w + 1], 0x4240), bytes_f16(x[2 * w + 1], 0x4341),
+                                mma_16816_f16(NZC == 1 && kSums && w ? tz : oz[zc], bytes_f16(x[2 * w], 0x4240),
+                                              bytes_f16(x[2 * w], 0x4341), bytes_f16(x[2 * w + 1], 0x4240),
+                                              bytes_f16(x[2 * w + 1], 0x4341),
                                               mine ? wb0 : 0u, mine ? wb1 : 0u);
                             }
                         }
