@@ -411,23 +411,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vst = 0;
                 vphase ^= 1;
             }
-            // The row's maximum over both halves, in bf16 (the next write to this parity's slot comes after the next
-            // page's barrier).
-            mxs[(j & 1) * 2 + half] = (uint16_t)(__float_as_uint(mx) >> 16);
+            // The row's maximum over both halves, exchanged in bf16 rounded up (a truncated one hides up to 1/128 of a
+            // positive maximum, from 2^14 on more than the log2 units that make p overflow).  (The next write to this
+            // parity's slot comes after the next page's barrier.)
+            mxs[(j & 1) * 2 + half] = (uint16_t)((__float_as_uint(mx) + (mx > 0.f ? 0xffffu : 0u)) >> 16);
             named_bar(1 + qq, 64);
             const uint32_t both = *reinterpret_cast<const uint32_t*>(mxs + (j & 1) * 2);
-            const bool raise = fmaxf(bf16lo(both), bf16hi(both)) > mref + kRescaleThreshold;  // or the row's first token
+            bool raise = fmaxf(bf16lo(both), bf16hi(both)) > mref + kRescaleThreshold;  // or the row's first token
             float alpha = 1.f;
-            // Where it is raised, the reference is the exact maximum, so that the heaviest token's probability, 1, is not
-            // rounded (pieces of a page or two: the output's error 0.0018 instead of 0.0027).  Every thread follows
-            // the exchange, after an expired wait too: the halves' references, and so their barriers, stay the same.
+            // Where it may have to be raised, the exact maxima decide, and become the reference, so that the heaviest
+            // token's probability, 1, is not rounded (pieces of a page or two: the output's error 0.0018 instead of
+            // 0.0027).  Every thread follows the exchange, after an expired wait too: the halves' references, and so
+            // their barriers, stay the same.
             if (__any_sync(0xffffffffu, raise)) {
                 float* const fx = reinterpret_cast<float*>(mxs);  // [half], over both parities' slots
                 named_bar(1 + qq, 64);
                 fx[half] = mx;
                 named_bar(1 + qq, 64);
-                const float mnew = fmaxf(mref, fmaxf(fx[0], fx[1]));
+                const float mnew = fmaxf(fx[0], fx[1]);
                 named_bar(1 + qq, 64);
+                raise = mnew > mref + kRescaleThreshold;
                 if (raise) {
                     alpha = mref == -INFINITY ? 0.f : ex2_approx(mref - mnew);
                     mref = mnew;

@@ -360,3 +360,41 @@ def test_calls_back_to_back_share_a_workspace(H, d_h, r, lens, graph):
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
     assert int(c.st.item()) == 0
+
+
+@pytest.mark.parametrize("start,step", [(0, 20), (0, 45), (0, 60), (10, 85), (0, 250), (250, -60), (0, 3)])
+@pytest.mark.parametrize("d_h", [64, 128])
+def test_large_logits_rise_from_page_to_page(start, step, d_h):
+    """Logits of 2^15 log2 units and more whose page maxima rise by less than 2^-7 of their size: every one has to be
+    compared in full, or probabilities overflow.
+
+    Queries of one sign and rows of whole numbers make every dot product exact, latents of the keys are zero, so a
+    logit is off only by the roundings of x = s * (scale log2 e): the factor's 2^-24 (which moves all logits of a row
+    by one factor, differences of at most 2^10 by 2^-14) and those of x - m and m, |m| < 2^17, 2^-8 each, for a piece
+    and once more in the merge: 4 * 2^-8 ln 2 of a probability, plus 2^-8 for its rounding to bf16."""
+    H, r, P = 8, 16, 1000
+    B = 2400  # 150 tiles of query rows: pieces of eight pages and more
+    c = Case(23, H, d_h, r, 0, P, [0] * B)
+    scale = 2.0 if d_h == 64 else 1.0
+    c.dims = b.make_dims(H, d_h, r, H * d_h, softmax_scale=scale)
+    sK = c.cache.sK.view(-1, d_h)
+    page = torch.arange(P, device="cuda") // 64
+    top = (start + step * page) % 256 if step > 0 else (start + step * page).clamp(min=0)
+    within = torch.randint(0, 4, (P,), generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    base = torch.full((P, d_h), 256.0 if d_h == 64 else 192.0, device="cuda")
+    base[:, 0] = (top - within * 4).clamp(min=0).float()
+    sK[c.pslots] = base.to(torch.bfloat16)
+    c.cache.zK.zero_()
+    c.q.fill_(1.0)
+    logits = sK[c.pslots].double().sum(1) * scale
+    assert logits.min() * 1.4427 > 2 ** 15 and logits.max() * 1.4427 < 2 ** 17
+    c.run()
+    assert int(c.st.item()) == 0
+    sV, zV = c.cache.sV.view(-1, d_h)[c.pslots].double(), c.cache.zV.view(-1, H, r)[c.pslots].double()
+    p = torch.softmax(logits, 0)
+    V = sV[:, None] + torch.einsum("thr,hdr->thd", zV, c.BV.double())
+    absV = sV.abs()[:, None] + torch.einsum("thr,hdr->thd", zV.abs(), c.BV.double().abs())
+    want = torch.einsum("t,thd->hd", p, V)
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 4 * 2.0 ** -8 * 0.694 + 2.0 ** -13) * torch.einsum("t,thd->hd", p, absV)
+    check(c.out[0], want, bound, f"page maxima from {start} by {step}", rel_max=1.0)
+    assert (c.out == c.out[0]).all()
