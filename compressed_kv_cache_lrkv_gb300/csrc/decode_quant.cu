@@ -27,8 +27,8 @@
 // stages), one or three converters; connected by mbarriers only, so they drift freely.  One CTA per
 // SM; the work is cut as in the bf16 decode (decode_work.cuh).
 //
-// Measured: 24 sequences of 1 to 8,191 tokens, 32 heads of r = 16 and a positional key 45 us (the rows alone 18
-// at the memory's pace); 4 of 16 to 32 K, 32 heads of r = 32, 50 (36); 8 of 8,192, 128 heads of r = 16, 90 (44);
+// Measured: 24 sequences of 1 to 8,191 tokens, 32 heads of r = 16 and a positional key 46 us (the rows alone 18
+// at the memory's pace); 4 of 16 to 32 K, 32 heads of r = 32, 50 (36); 8 of 8,192, 128 heads of r = 16, 91 (44);
 // 16 of 2,048, 8 heads, 16 (2).  Bound by the consumers' instructions: a tile of 16 tokens x 8 heads takes a
 // warp some 500, a quarter of them byte permutes, and up to 2,900 cycles with the rows already there; with twice as
 // many warps each takes twice as long.  A third to a half of the issue slots are used; the waits are for the
@@ -477,17 +477,18 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1, pslot = wk.slot;
             const int L = b < kSeqCache ? slc[b] : a.seq_lens[b];
-            // Queries and q~ as B fragments (features x heads, head h0 + g in this lane's column),
-            // fp16, both divided by the power of two that brings the head's largest magnitude into [1, 2).
+            // Queries and q~ as B fragments (features x heads, head h0 + g in this lane's column), fp16, each
+            // divided by a power of two of its own that brings the head's largest magnitude into [1, 2): with one for
+            // both the smaller, where it is below 2^-14 of the larger, would lose its bits.
             // This lane holds features 4 tq .. 4 tq + 3 of each chunk of 16 (the order of the A fragments).
             uint32_t qb[NKK][2];
             uint32_t qz[NZC][2];
             float ci[2];  // start of the latent logits' sums
-            float fz[2];  // the power of two times the softmax scale, for heads 2 tq, 2 tq + 1 of each tile
+            uint32_t pw = 0;  // exponents of the powers of q and q~, head 2 tq's and head 2 tq + 1's, a byte each
             const int h = h0 + g;
             const bool live = h < H;
             const uint16_t* q = a.q + ((size_t)b * H + (live ? h : 0)) * D_K + tq * 4;
-            float mx = 0.f;
+            float mq = 0.f, mv = 0.f;
 #pragma unroll
             for (int kk = 0; kk < NKK; ++kk) {
                 const uint2 x = *reinterpret_cast<const uint2*>(q + kk * 16);
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                 qb[kk][1] = live ? x.y : 0u;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qb[kk][i])), fabsf(bf16hi(qb[kk][i]))));
+                    mq = fmaxf(mq, fmaxf(fabsf(bf16lo(qb[kk][i])), fabsf(bf16hi(qb[kk][i]))));
             }
             const float* qt = a.qt + ((size_t)b * H + (live ? h : 0)) * R;
             float v[NZC][4];
@@ -509,18 +510,21 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                 v[c][2] = mine ? x.z : 0.f;
                 v[c][3] = mine ? x.w : 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[c][i]));
+                for (int i = 0; i < 4; ++i) mv = fmaxf(mv, fabsf(v[c][i]));
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const uint32_t ex = min(max(__float_as_uint(mx) >> 23, 1u), 253u);
-            const float inv = __uint_as_float((254u - ex) << 23);
-            const float fac = __uint_as_float(ex << 23);
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
+                mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+            }
+            const uint32_t exq = min(max(__float_as_uint(mq) >> 23, 1u), 253u);
+            const uint32_t exv = min(max(__float_as_uint(mv) >> 23, 1u), 253u);
+            const float invq = __uint_as_float((254u - exq) << 23), invv = __uint_as_float((254u - exv) << 23);
 #pragma unroll
             for (int kk = 0; kk < NKK; ++kk)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    qb[kk][i] = pack_f16x2(bf16lo(qb[kk][i]) * inv, bf16hi(qb[kk][i]) * inv);
+                    qb[kk][i] = pack_f16x2(bf16lo(qb[kk][i]) * invq, bf16hi(qb[kk][i]) * invq);
             // The products take 1152 + u for u: the sums start from -1152 sum q~, and -1152 sum q over each block
             // (as rounded).  (Against a typical sum the offset is some 160 times as large, so fp32 keeps 16 bits of
             // it, more than q and q~ have.  Taken off by products with a constant A, a block is a chain of four
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
             for (int c = 0; c < NZC; ++c)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    qz[c][i] = pack_f16x2(v[c][2 * i] * inv, v[c][2 * i + 1] * inv);
+                    qz[c][i] = pack_f16x2(v[c][2 * i] * invv, v[c][2 * i + 1] * invv);
                     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qz[c][i]));
                     sum += x.x + x.y;
                 }
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                fz[e] = __shfl_sync(0xffffffffu, fac, 8 * tq + 4 * e) * a.scale_log2;
+                pw |= __shfl_sync(0xffffffffu, exq | exv << 8, 8 * tq + 4 * e) << (16 * e);
                 ci[e] = -kByteOffset * __shfl_sync(0xffffffffu, sum, 8 * tq + 4 * e);
             }
             float o[D_H / 16][4], oz[NZC][4];
@@ -667,11 +671,21 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                                 // weight then becomes infinity - infinity
                                 kv[hf][e] = lg2_approx(__uint_as_float(vb[hf][e] << 23));
                             }
+                        // The powers times the softmax scale, formed tile by tile: 16 consumers have no registers for
+                        // four floats, and the compiler must not form them before the loop (128 heads 91 us, 98 where
+                        // it may, 102 with floats).
+                        if (!kSums) asm volatile("" : "+r"(pw));
+                        float fq[2], fz[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            fq[e] = byte_scale(pw, 2 * e) * a.scale_log2;
+                            fz[e] = byte_scale(pw, 2 * e + 1) * a.scale_log2;
+                        }
                         float over = -INFINITY;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int e = i & 1, es = e & (NSE - 1), hf = i >> 1;
-                            const float s = fmaf(cz[i], ks[hf][es], c[i]) * fz[e];
+                            const float s = fmaf(cz[i], ks[hf][es] * fz[e], c[i] * fq[e]);
                             const bool in = hf ? in1 : in0;
                             sv[i] = in ? s : -INFINITY;
                             sw[i] = in ? s + kv[hf][es] : -INFINITY;

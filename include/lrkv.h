@@ -350,8 +350,10 @@ size_t lrkv_decode_quant_workspace_bytes(const lrkv_dims* dims, int32_t batch);
  *   or a shared prefix in bf16 pools).
  *   Arguments, lengths, errors and status bits are those of lrkv_decode / lrkv_decode_partials with
  *   `qcache` in place of the pools; workspace of lrkv_decode_quant_workspace_bytes(dims, batch)
- *   bytes, 256-byte aligned.  The latents' products take q~ and the probabilities in fp16 (11
- *   significant bits, scaled by powers of two so that nothing overflows) and sum in fp32.
+ *   bytes, 256-byte aligned.  All sums are fp32.  The products take q and q~ in fp16, each head's q and each
+ *   head's q~ divided by a power of two of its own, that of its largest magnitude: 11 significant bits down to 2^-14
+ *   of the largest, half a step of 2^-25 of it below.  Probabilities enter the products with s^V in bf16 and those
+ *   with z^V in fp16 (times the tokens' scales, relative to the largest such weight).
  */
 lrkv_status lrkv_decode_quant(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
                               const lrkv_quant_cache* qcache, const int32_t* block_table, int32_t max_blocks_per_seq,

@@ -551,3 +551,25 @@ def test_offsets_beyond_32_bits():
         del qc
     for x, y in zip(*results):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope", [(8, 64, 8, 0), (9, 128, 16, 64), (32, 128, 32, 0), (72, 64, 16, 0),
+                                            (128, 128, 32, 64)])
+@pytest.mark.parametrize("shift", [14, 18, 24, 60, -14, -18, -24, -60])
+def test_factors_and_latents_of_any_ratio(H, d_h, r, d_rope, shift):
+    """B^K times 2^k with z^K times 2^-k is the same model: q~ is then 2^k times what it was, and nothing else
+    changes.  Powers of two round nothing, so not a bit of the output may change either."""
+    c = Case(33, H, d_h, r, d_rope, [300, 5, 2, 1])
+    want = c.run().clone()
+    c.verify(seqs=[0, 1])
+    off, at, blocks, _ = layout(H, d_h, r, d_rope)
+    first = at + blocks[0] + blocks[1]
+    for s in c.slots:
+        e = c.qc.rows.view(-1, c.qc.rows.shape[2])[s, first:first + blocks[2]].int() - shift
+        assert 1 <= int(e.min()) and int(e.max()) <= 254
+        c.qc.rows.view(-1, c.qc.rows.shape[2])[s, first:first + blocks[2]] = e.to(torch.uint8)
+    c.BK = (c.BK.float() * 2.0 ** shift).to(torch.bfloat16)
+    c.run()
+    assert int(c.st.item()) == 0
+    c.verify()
+    assert torch.equal(c.out, want)
