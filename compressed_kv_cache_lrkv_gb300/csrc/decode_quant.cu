@@ -28,7 +28,7 @@
 // SM; the work is cut as in the bf16 decode (decode_work.cuh).
 //
 // Measured: 24 sequences of 1 to 8,191 tokens, 32 heads of r = 16 and a positional key 46 us (the rows alone 18
-// at the memory's pace); 4 of 16 to 32 K, 32 heads of r = 32, 50 (36); 8 of 8,192, 128 heads of r = 16, 91 (44);
+// at the memory's pace); 4 of 16 to 32 K, 32 heads of r = 32, 50 (36); 8 of 8,192, 128 heads of r = 16, 86 (44);
 // 16 of 2,048, 8 heads, 16 (2).  Bound by the consumers' instructions: a tile of 16 tokens x 8 heads takes a
 // warp some 500, a quarter of them byte permutes, and up to 2,900 cycles with the rows already there; with twice as
 // many warps each takes twice as long.  A third to a half of the issue slots are used; the waits are for the
@@ -107,14 +107,24 @@ __device__ __forceinline__ float byte_scale(uint32_t x, int i) {
     return __uint_as_float(__byte_perm(x, 0u, 0x0444 | (i << 12)) >> 1);
 }
 
-// try_wait that may sleep in hardware for some microseconds before it reports failure: a waiting warp
-// then takes few issue slots from the others.
+// try_wait that may sleep in hardware for some microseconds before it reports failure: a waiting warp then takes few
+// issue slots from the others.
 __device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
         : "=r"(ok)
         : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+// The same without sleeping.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
@@ -125,14 +135,18 @@ __device__ __forceinline__ float lg2_approx(float x) {
     return y;
 }
 
-// Bounded wait of a whole warp; false (with the abort flag set) once it, or any other, gave up.
+// Bounded wait of a whole warp; false (with the abort flag set) once it, or any other, gave up.  One look, then
+// tries that sleep, unless the limit is a shortened one.  (Sleeping tries alone: 128 heads 87 us instead of 86, the
+// ragged batch 46.6 instead of 45.7.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
                                           uint64_t limit_ns) {
-    if (__all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    const bool sleep = limit_ns == kWaitLimitNs;
+    if (sleep && __all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-        if (__all_sync(0xffffffffu, mbar_try_sleep(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, sleep ? mbar_try_sleep(bar, parity) : mbar_test(bar, parity))) return true;
         if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) {
             set_status(status, LRKV_DEV_TIMEOUT);
             *abort_flag = 1;
@@ -327,10 +341,14 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
     // and so does every consumer unless each slot of the ring belongs to one group: nobody can then miss
     // a round of a barrier or take one for another.  Ring positions and phases are counted along (a
     // division by a run-time count costs as much as a chunk's product).
+    // A role whose wait has run out (ok false) walks on to its end without waiting, copying or arriving again; every
+    // other one then gives up at its next wait.
+    int issued = 0;  // stages the producer has filled
+    bool ok = true;
     if (warp == NCW) {
         // ---------------------------------------------------------------- producer
         const uint64_t pol = policy_evict_first();
-        int slot = 0, issued = 0, segs = 0;
+        int slot = 0, segs = 0;
         uint32_t phase = 1;  // parity of the round before this one of a slot's `empty`
         while (wk.valid) {
             const int b = wk.vb, g0 = wk.g0, g1 = wk.g1;
@@ -342,8 +360,8 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                 a.seg_table[b] = make_int2(wk.slot, np);
             }
             // the ring's memory serves the group merge at the end of a segment
-            bool ok = segs == 0 || p.ng == 1 ||
-                      warp_wait(smem_u32(merged), (segs - 1) & 1, abort_flag, a.status, a.wait_ns);
+            ok = ok && (segs == 0 || p.ng == 1 ||
+                        warp_wait(smem_u32(merged), (segs - 1) & 1, abort_flag, a.status, a.wait_ns));
             const int32_t* bt = a.block_table + (size_t)b * a.max_pages;
             const int last_page = (g1 - 1) / TPP;
             int page0 = g0 / TPP, ids = page0 + lane <= last_page ? bt[page0 + lane] : -1;
@@ -386,10 +404,6 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
             ++segs;
             wk.advance(*work, lane);
         }
-        // After an expired wait, let the copies in flight land before the CTA exits.
-        if (*abort_flag)
-            for (int i = max(0, issued - nslot); i < issued; ++i)
-                mbar_wait(smem_u32(full + i % nslot), (i / nslot) & 1, a.status);
     } else if (warp > NCW) {
         // ---------------------------------------------------------------- converters
         const int cv = warp - NCW - 1;
@@ -402,7 +416,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
             const int L = b < kSeqCache ? slc[b] : a.seq_lens[b];
             for (int f = g0; f < g1;) {
                 const int e = min(g1, (f | (ST - 1)) + 1);
-                bool ok = warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
+                ok = ok && warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
                 const int have = meta[slot];
                 uint32_t src = ring + slot * p.stage_bytes;
                 for (int t = f; t < e; ++t, src += TOK * RB) {
@@ -441,7 +455,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(empty + slot));
+                if (lane == 0 && ok) mbar_arrive(smem_u32(empty + slot));
                 if (++slot == nslot) {
                     slot = 0;
                     phase ^= 1;
@@ -580,7 +594,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                     ++f;
                     continue;
                 }
-                bool ok = warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
+                ok = ok && warp_wait(smem_u32(full + slot), phase, abort_flag, a.status, a.wait_ns);
                 const int have = meta[slot];
                 const uint32_t stage = ring + slot * p.stage_bytes;
 #pragma unroll 1
@@ -672,8 +686,8 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                                 kv[hf][e] = lg2_approx(__uint_as_float(vb[hf][e] << 23));
                             }
                         // The powers times the softmax scale, formed tile by tile: 16 consumers have no registers for
-                        // four floats, and the compiler must not form them before the loop (128 heads 91 us, 98 where
-                        // it may, 102 with floats).
+                        // four floats, and the compiler must not form them before the loop (128 heads 91 us at that
+                        // time, 98 where it may, 102 with floats).
                         if (!kSums) asm volatile("" : "+r"(pw));
                         float fq[2], fz[2];
 #pragma unroll
@@ -787,7 +801,7 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
                 }
                 until -= e1 - f;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(empty + slot));
+                if (lane == 0 && ok) mbar_arrive(smem_u32(empty + slot));
                 if (++slot == nslot) {
                     slot = 0;
                     phase ^= 1;
@@ -886,6 +900,12 @@ __global__ void __launch_bounds__((CW + 1 + converters(CW)) * 32, 1) quant_scan_
         }
     }
     pdl_trigger();  // the combine waits for this grid's end
+    // Whichever wait ran out, and however late: the copies in flight land (the full limit again) before the block
+    // gives up its shared memory.
+    __syncthreads();
+    if (warp == NCW && *abort_flag)
+        for (int i = max(0, issued - nslot); i < issued; ++i)
+            mbar_wait(smem_u32(full + i % nslot), (i / nslot) & 1, a.status);
 }
 
 // Tokens of a tile.

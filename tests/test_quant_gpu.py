@@ -573,3 +573,25 @@ def test_factors_and_latents_of_any_ratio(H, d_h, r, d_rope, shift):
     assert int(c.st.item()) == 0
     c.verify()
     assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,lens", [(32, 128, 32, 0, [20000, 9000]), (128, 128, 16, 64, [4000, 3000, 1]),
+                                                 (8, 64, 8, 0, [30000] + [50] * 200), (128, 128, 32, 0, [6000])])
+def test_expired_wait_reports_timeout_and_gpu_stays_usable(monkeypatch, H, d_h, r, d_rope, lens):
+    """With the debugging limit LRKV_DEBUG_WAIT_LIMIT_NS=0 the scan's waits give up as soon as something is not already
+    there.  The call ends, reports LRKV_DEV_TIMEOUT and nothing else, and the next one is right to the bit."""
+    c = Case(34, H, d_h, r, d_rope, lens)
+    want = c.run().clone()
+    c.verify(seqs=[0, len(lens) - 1])
+    monkeypatch.setenv("LRKV_DEBUG_WAIT_LIMIT_NS", "0")
+    seen = 0
+    for _ in range(5):
+        c.run()
+        seen |= int(c.st.item())
+    assert seen == b.DEV_TIMEOUT
+    monkeypatch.delenv("LRKV_DEBUG_WAIT_LIMIT_NS")
+    c.st.zero_()
+    c.out.fill_(float("nan"))
+    c.run()
+    assert int(c.st.item()) == 0
+    assert torch.equal(c.out, want)
