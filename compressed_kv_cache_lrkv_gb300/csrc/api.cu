@@ -58,7 +58,7 @@ lrkv_status check_dims(const lrkv_dims* dm) {
     return LRKV_OK;
 }
 
-// Limit of the decode split kernel's pipeline waits: about 2 s, unless the environment
+// Limit of the pipeline waits of the decode's scans (bf16, 8-bit, shared prefix): about 2 s, unless the environment
 // variable LRKV_DEBUG_WAIT_LIMIT_NS sets another (a debugging aid: with a short limit a wait
 // that is merely slow gives up and the call reports LRKV_DEV_TIMEOUT, which lets a test see
 // the expiry path run to its end on a healthy GPU).
@@ -686,6 +686,7 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
     p.d.H = dims->H;
     p.d.layers = 1;
     p.d.num_blocks = cache->num_blocks;
+    p.d.wait_ns = decode_wait_limit_ns();
     p.d.scale_log2 = logit_scale(dims) * 1.4426950408889634f;
     lrkv::decode_carve_workspace(&p.d, workspace, dims->H, dims->d_h, dims->r, batch, nranges);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

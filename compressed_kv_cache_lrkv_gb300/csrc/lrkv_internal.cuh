@@ -87,6 +87,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_
     }
 }
 
+// A look at the barrier that does not wait at all (try_wait may, for as long as the hardware likes).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // mbar_wait with a caller-chosen limit.  The timer is read every 256 tries at the full limit;
 // below it, after every failed try, so that a limit of 0 gives up at the first wait that
 // does not succeed within the timer's tick.

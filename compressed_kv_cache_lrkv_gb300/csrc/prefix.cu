@@ -80,9 +80,24 @@ struct PxLayout {
 __device__ __forceinline__ uint64_t kdesc128(uint32_t a) { return sdesc(a, 16, 1024, 2); }
 __device__ __forceinline__ uint64_t mndesc128(uint32_t a) { return sdesc(a, 8192, 1024, 2); }
 
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, uint32_t* status) {
-    const bool ok = mbar_wait(bar, parity, status);
+// Wait of a role, with the call's limit (a shortened one is not napped through), and one for what the block has in
+// flight, with the full limit.
+__device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const DecodeArgs& d) {
+    bool ok = mbar_test(bar, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        const bool nap = d.wait_ns == kWaitLimitNs;
+        for (uint32_t it = 1; !(ok = nap ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)); ++it)
+            if (((it & 255u) == 0 || !nap) && globaltimer_ns() - t0 > d.wait_ns) {
+                set_status(d.status, LRKV_DEV_TIMEOUT);
+                break;
+            }
+    }
     return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* status) {
+    mbar_wait(bar, parity, status);
+    __syncwarp();
 }
 
 constexpr int lcm2(int n) { return n % 2 ? 2 * n : n; }
@@ -174,9 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
+    const bool keys = warp == 0;  // (of the two producers)
+    int issued = 0;               // stages a producer has filled
     if (warp == 0 || warp == 6) {
         // ---------------------------------------------------------------- TMA producers
-        const bool keys = warp == 0;
         const int oob_row = d.num_blocks * kBlockSize;  // whole box out of bounds: zeros
         auto fetch = [&](int batch) {
             const int i = batch * 32 + lane;
@@ -199,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const CUtensorMap* mz = keys ? &m.zK : &m.zV;
         const uint32_t ring = S0 + (keys ? Lay::OFF_K : Lay::OFF_V);
         int cur = fetch(0), nxt = fetch(1);
-        int issued = 0, st = 0;
+        int st = 0;
         uint32_t phase = 1;
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
@@ -208,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nxt = fetch((j >> 5) + 1);
             }
             const int prow = __shfl_sync(0xffffffffu, cur, j & 31);
-            if ((j >= depth && !wait_all(B(empty + st), phase, d.status)) || aborted()) {
+            if ((j >= depth && !wait_role(B(empty + st), phase, d)) || aborted()) {
                 ok = false;
                 break;
             }
@@ -226,19 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 phase ^= 1;
             }
         }
-        if (!ok) {
-            *abort_flag = 1;
-            // let this ring's copies still in flight land before the CTA exits
-            for (int k = max(0, issued - depth); k < issued; ++k) wait_all(B(full + k % depth), (k / depth) & 1, d.status);
-        }
+        if (!ok) *abort_flag = 1;
     } else if (warp == 1) {
         // ---------------------------------------------------------------- score MMAs
         constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
         const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K);
         auto s_tile = [&](int j, auto UU) -> bool {
             constexpr int st = decltype(UU)::value % KST;
-            if (aborted() || !wait_all(B(k_full + st), (j / KST) & 1, d.status) ||
-                (j >= 1 && !wait_all(B(s_read), (j - 1) & 1, d.status)))
+            if (aborted() || !wait_role(B(k_full + st), (j / KST) & 1, d) ||
+                (j >= 1 && !wait_role(B(s_read), (j - 1) & 1, d)))
                 return false;
             tc_fence_after();
             constexpr uint64_t so = st * (Lay::K_BYTES >> 4);
@@ -261,22 +273,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return true;
         };
-        bool ok = wait_all(B(q_ready), 0, d.status);
+        bool ok = wait_role(B(q_ready), 0, d);
         tc_fence_after();
         for (int j = 0; j < nt && ok; j += KST) ok = tiles(s_tile, j, nt, std::make_integer_sequence<int, KST>{});
         if (!ok) *abort_flag = 1;
         // every MMA this warp issued has finished before the CTA tears TMEM down
         if (elect_one_sync()) tc_commit(B(s_drain));
         __syncwarp();
-        wait_all(B(s_drain), 0, d.status);
+        drain(B(s_drain), 0, d.status);
     } else if (warp == 7) {
         // ---------------------------------------------------------------- P V MMAs
         constexpr uint32_t id_PV = idesc_bf16_f32(128, D_H + ZW) | (1u << 16);  // B is MN-major
         const uint64_t dV = mndesc128(S0 + Lay::OFF_V);
         auto pv_tile = [&](int j, auto UU) -> bool {
             constexpr int U = decltype(UU)::value, st = U % VST, sb = U & 1;
-            if (aborted() || !wait_all(B(p_full + sb), (j >> 1) & 1, d.status) ||
-                !wait_all(B(v_full + st), (j / VST) & 1, d.status))
+            if (aborted() || !wait_role(B(p_full + sb), (j >> 1) & 1, d) ||
+                !wait_role(B(v_full + st), (j / VST) & 1, d))
                 return false;
             tc_fence_after();
             constexpr uint64_t so = st * (Lay::V_BYTES >> 4);
@@ -298,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) *abort_flag = 1;
         if (elect_one_sync()) tc_commit(B(pv_drain));
         __syncwarp();
-        wait_all(B(pv_drain), 0, d.status);
+        drain(B(pv_drain), 0, d.status);
     } else {
         // ---------------------------------------------------------------- query rows: softmax, partials
         const uint32_t tl = (uint32_t)(qq * 32) << 16;
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // visible tokens of this page: none of a page with a bad id
             const int blk = a.blocks[pg0 + j];
             const int lim = blk >= 0 && blk < d.num_blocks ? P - (pg0 + j) * kBlockSize : 0;
-            ok = ok && !aborted() && wait_all(B(s_full), j & 1, d.status);
+            ok = ok && !aborted() && wait_role(B(s_full), j & 1, d);
             uint32_t sv[32];
             float mx = -INFINITY;
             if (ok) {
@@ -388,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) sv[e] = half * 32 + e < lim ? sv[e] : 0xff800000u;
                     // rows of s^V, z^V behind the end may hold any bits: cleared before P V reads them
-                    ok = wait_all(B(v_full + vst), vphase, d.status);
+                    ok = wait_role(B(v_full + vst), vphase, d);
                     const int vr = row & 63;
                     if (ok && vr >= lim) {
                         const uint4 z = make_uint4(0, 0, 0, 0);
@@ -449,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pk[e / 2] = pack_bf16x2(p0, p1);
             }
             if (j >= 2) {  // P_{j-2} V_{j-2} has read this P buffer
-                ok = wait_all(B(o_done + (j & 1)), ((j - 2) >> 1) & 1, d.status);
+                ok = wait_role(B(o_done + (j & 1)), ((j - 2) >> 1) & 1, d);
                 if (!ok) continue;
                 tc_fence_after();
             }
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l = l * alpha + ((r4[0] + r4[1]) + (r4[2] + r4[3]));
             // O may only be rescaled once P_{j-1} V_{j-1} has finished accumulating into it
             if (j > 0 && __any_sync(0xffffffffu, raise)) {
-                ok = wait_all(B(o_done + ((j - 1) & 1)), ((j - 1) >> 1) & 1, d.status);
+                ok = wait_role(B(o_done + ((j - 1) & 1)), ((j - 1) >> 1) & 1, d);
                 if (!ok) continue;
                 tc_fence_after();
                 uint32_t v[32];
@@ -474,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(B(p_full + (j & 1)));
         }
+        tmem_wait_st();  // (a wait that ran out may have left stores to TMEM behind)
         // the row's sum over both halves
         named_bar(1 + qq, 64);  // (the maxima have been read)
         float* const ls = reinterpret_cast<float*>(smem + Lay::OFF_MX) + row * 2;
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += ls[half ^ 1];
         // ---- partials, unnormalised
         const uint32_t rs = 16u * ((W / 4) | 1);  // row stride of their staging
-        if (ok) ok = wait_all(B(o_done + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, d.status);
+        if (ok) ok = wait_role(B(o_done + ((nt - 1) & 1)), ((nt - 1) >> 1) & 1, d);
         if (ok) {
             tc_fence_after();
             const bool nan = l != l;  // handed on as NaN values with a weight, not as an empty part
@@ -541,6 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // Whichever wait ran out, and however late: the copies in flight land before the block gives up its shared memory.
+    if ((warp == 0 || warp == 6) && *abort_flag) {
+        const int depth = keys ? KST : VST;
+        for (int k = max(0, issued - depth); k < issued; ++k)
+            drain(B((keys ? k_full : v_full) + k % depth), (k / depth) & 1, d.status);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

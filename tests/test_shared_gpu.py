@@ -398,3 +398,36 @@ def test_large_logits_rise_from_page_to_page(start, step, d_h):
     bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 4 * 2.0 ** -8 * 0.694 + 2.0 ** -13) * torch.einsum("t,thd->hd", p, absV)
     check(c.out[0], want, bound, f"page maxima from {start} by {step}", rel_max=1.0)
     assert (c.out == c.out[0]).all()
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,P,B,partials", [(32, 128, 16, 0, 20000, 16, False), (128, 128, 16, 64, 9000, 16, True),
+                                                        (8, 64, 8, 0, 40000, 64, True), (32, 128, 32, 0, 65, 3, True)])
+def test_expired_wait_reports_timeout_and_gpu_stays_usable(monkeypatch, H, d_h, r, d_rope, P, B, partials):
+    """With the debugging limit LRKV_DEBUG_WAIT_LIMIT_NS=0 the scans' waits give up as soon as something is not already
+    there.  The call ends, reports LRKV_DEV_TIMEOUT and nothing else, and the next one is right to the bit."""
+    c = Case(24, H, d_h, r, d_rope, P, [70] * B)
+    out = torch.empty(B, H, d_h + r + 2, device="cuda") if partials else c.out
+
+    def call():
+        if partials:
+            b.lrkv_prefix_partials(c.dims, c.q, c.BK, c.cache, c.blocks, c.pl, out, c.ws, status=c.st)
+        else:
+            c.run()
+
+    call()
+    want = out.clone()
+    if not partials:
+        c.verify(seqs=[0, B - 1])
+    assert int(c.st.item()) == 0 and torch.isfinite(want).all()
+    monkeypatch.setenv("LRKV_DEBUG_WAIT_LIMIT_NS", "0")
+    seen = 0
+    for _ in range(5):
+        call()
+        seen |= int(c.st.item())
+    assert seen == b.DEV_TIMEOUT
+    monkeypatch.delenv("LRKV_DEBUG_WAIT_LIMIT_NS")
+    c.st.zero_()
+    out.fill_(float("nan"))
+    call()
+    assert int(c.st.item()) == 0
+    assert torch.equal(out, want)
