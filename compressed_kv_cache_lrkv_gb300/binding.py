@@ -361,8 +361,10 @@ class QuantCache:
         key = (dims.H, dims.d_h, dims.r, dims.d_rope, dims.block_size)
         page = _page_bytes.get(key)
         if page is None:
-            page = _page_bytes[key] = quant_block_bytes(dims)
-        if self.rows.numel() * self.rows.element_size() != self.num_blocks * page:
+            page = quant_block_bytes(dims)
+            if page:  # (0: dims that the call will refuse, perhaps for what is not in the key)
+                _page_bytes[key] = page
+        if page and self.rows.numel() * self.rows.element_size() != self.num_blocks * page:
             raise ValueError(f"quantised rows {tuple(self.rows.shape)}: expected [num_blocks, 64, "
                              f"{quant_row_bytes(dims)}] for these dims")
         return QuantCacheStruct(_ptr(self.rows), self.num_blocks)

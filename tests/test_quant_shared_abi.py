@@ -106,3 +106,19 @@ def test_binding_checks_row_width_and_slot_counts():
         b.QuantCache(rows).struct(GOOD)
     with pytest.raises(ValueError):
         b._same_length(torch.zeros(3), torch.zeros(4))
+
+
+def test_refused_dims_leave_nothing_behind():
+    """Dims that the library refuses are reported as its refusal, and good dims of the same heads and widths are taken
+    afterwards."""
+    torch = pytest.importorskip("torch")
+    good = b.make_dims(24, 64, 16, 1536)
+    rows = torch.zeros(2, 64, b.quant_row_bytes(good), dtype=torch.uint8)
+    x = torch.zeros(64, dtype=torch.uint8)
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    for bad, status in ((b.make_dims(24, 64, 16, 12), 2), (b.make_dims(24, 64, 16, 1536, softmax_scale=float("nan")), 1),
+                        (b.make_dims(24, 64, 16, 1536, num_splits=-1), 1)):
+        with pytest.raises(b.LrkvError) as e:
+            b.lrkv_decode_quant(bad, x, x, x, b.QuantCache(rows), i, i[0], x, x, stream=0)
+        assert e.value.status == status
+    assert b.QuantCache(rows).struct(good).num_blocks == 2
