@@ -364,10 +364,12 @@ class QuantCache:
             page = quant_block_bytes(dims)
             if page:  # (0: dims that the call will refuse, perhaps for what is not in the key)
                 _page_bytes[key] = page
-        if page and self.rows.numel() * self.rows.element_size() != self.num_blocks * page:
-            raise ValueError(f"quantised rows {tuple(self.rows.shape)}: expected [num_blocks, 64, "
-                             f"{quant_row_bytes(dims)}] for these dims")
-        return QuantCacheStruct(_ptr(self.rows), self.num_blocks)
+        rows = self.rows
+        if page and (rows.numel() != self.num_blocks * page or rows.dtype is not torch.uint8 or
+                     not rows.is_contiguous()):
+            raise ValueError(f"quantised rows {tuple(rows.shape)} of {rows.dtype}, strides {rows.stride()}: expected "
+                             f"contiguous uint8 [num_blocks, 64, {quant_row_bytes(dims)}] for these dims")
+        return QuantCacheStruct(_ptr(rows), self.num_blocks)
 
 
 def quant_row_bytes(dims: Dims) -> int:

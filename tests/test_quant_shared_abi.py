@@ -122,3 +122,19 @@ def test_refused_dims_leave_nothing_behind():
             b.lrkv_decode_quant(bad, x, x, x, b.QuantCache(rows), i, i[0], x, x, stream=0)
         assert e.value.status == status
     assert b.QuantCache(rows).struct(good).num_blocks == 2
+
+
+def test_binding_refuses_rows_that_are_not_whole_bytes_in_order():
+    """Rows are addressed as [num_blocks, 64, row bytes] from the first one on: views of the right size that lie
+    otherwise, and other types, are refused; a slice of whole pages is not."""
+    torch = pytest.importorskip("torch")
+    rb = b.quant_row_bytes(GOOD)
+    rows = torch.zeros(4, 64, 2 * rb, dtype=torch.uint8)
+    for bad in (rows[:, :, :rb], torch.zeros(8, 64, rb, dtype=torch.uint8)[::2],
+                torch.zeros(64, 2, rb, dtype=torch.uint8).transpose(0, 1),
+                torch.zeros(2, 64, rb // 2, dtype=torch.bfloat16), torch.zeros(2, 64, rb, dtype=torch.int8)):
+        with pytest.raises(ValueError, match="contiguous uint8"):
+            b.QuantCache(bad).struct(GOOD)
+    whole = torch.zeros(8, 64, rb, dtype=torch.uint8)
+    assert b.QuantCache(whole[2:5]).struct(GOOD).num_blocks == 3
+    assert b.QuantCache(whole[2:5].view(3, -1)).struct(GOOD).num_blocks == 3
