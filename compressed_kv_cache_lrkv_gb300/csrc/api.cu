@@ -410,6 +410,8 @@ static lrkv_status prefix_launch(lrkv::PrefixArgs* p, const lrkv_dims* dims, con
         (s = make_tmap(&m.zK, cache->zK, HR, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "zK")) != LRKV_OK ||
         (s = make_tmap(&m.zV, cache->zV, HR, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "zV")) != LRKV_OK)
         return s;
+    p->sK = static_cast<const uint16_t*>(cache->sK);
+    p->zK = static_cast<const uint16_t*>(cache->zK);
     p->blocks = prefix.blocks;
     p->len = prefix.len;
     p->max_blocks = prefix.max_blocks;

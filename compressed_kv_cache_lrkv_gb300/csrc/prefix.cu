@@ -21,7 +21,7 @@
 // 1 issues S, 7 issues P V; 2..5 and 8..11 take the first and the second 32 tokens of a page for one query row
 // per thread (one warp per scheduler spent some 1000 cycles on a page's 64, twice what the MMAs need).
 // Measured, the call as a whole: 32 heads of r = 16 x 16 sequences behind 8,192 tokens 25 us, 32 heads of r = 32 x
-// 32 sequences behind 32,768 55 us, 128 heads of r = 16 with the positional key x 48 behind 4,001 64 us.  A page
+// 32 sequences behind 32,768 56 us, 128 heads of r = 16 with the positional key x 48 behind 4,001 65 us.  A page
 // takes a CTA some 1,900 cycles, of which its products need 1,280 (d_h = zw = 128); the rest is the chain S, softmax,
 // P V of one tile, and a piece's start and end some 6 us.
 #include <type_traits>
@@ -98,6 +98,37 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const D
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* status) {
     mbar_wait(bar, parity, status);
     __syncwarp();
+}
+
+// max(a, b), NaN where either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// n (a multiple of 8) products of bf16 a with bf16 b, or of fp32 a, summed in fp32.
+__device__ __forceinline__ float dot8(const uint16_t* a, const uint16_t* b, int n) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(a + i), y = *reinterpret_cast<const uint4*>(b + i);
+        s = fmaf(bf16lo(x.x), bf16lo(y.x), fmaf(bf16hi(x.x), bf16hi(y.x), s));
+        s = fmaf(bf16lo(x.y), bf16lo(y.y), fmaf(bf16hi(x.y), bf16hi(y.y), s));
+        s = fmaf(bf16lo(x.z), bf16lo(y.z), fmaf(bf16hi(x.z), bf16hi(y.z), s));
+        s = fmaf(bf16lo(x.w), bf16lo(y.w), fmaf(bf16hi(x.w), bf16hi(y.w), s));
+    }
+    return s;
+}
+__device__ __forceinline__ float dot8(const float* a, const uint16_t* b, int n) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(a + i);
+        const uint2 y = *reinterpret_cast<const uint2*>(b + i);
+        s = fmaf(x.x, bf16lo(y.x), fmaf(x.y, bf16hi(y.x), fmaf(x.z, bf16lo(y.y), fmaf(x.w, bf16hi(y.y), s))));
+    }
+    return s;
 }
 
 constexpr int lcm2(int n) { return n % 2 ? 2 * n : n; }
@@ -414,10 +445,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float m4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[4 + i]));
+                for (int i = 0; i < 4; ++i) m4[i] = max_nan(__uint_as_float(sv[i]), __uint_as_float(sv[4 + i]));
 #pragma unroll
-                for (int e = 8; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sv[e]));
-                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * d.scale_log2;
+                for (int e = 8; e < 32; ++e) m4[e & 3] = max_nan(m4[e & 3], __uint_as_float(sv[e]));
+                mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+                // diag(Q~)'s zeros times another head's NaN or infinity are NaN (and so is what rounding an infinite
+                // product left): such logits are formed again from the row's own head alone.  (The look for
+                // them, in the maximum's own instructions and a vote, costs 1%: 55.2 us -> 56.0 for 32,768 tokens.)
+                if (__any_sync(0xffffffffu, mx != mx)) {
+                    uint32_t nans = 0;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) nans |= (__uint_as_float(sv[e]) != __uint_as_float(sv[e])) << e;
+                    const size_t qr = (size_t)rb * H + rh;
+                    for (uint32_t todo = live ? nans : 0u; todo != 0; todo &= todo - 1) {
+                        const int e = __ffs(todo) - 1;
+                        const size_t t = (size_t)blk * kBlockSize + half * 32 + e;
+                        const float x = dot8(d.q + qr * D_K, a.sK + t * D_K, D_K) +
+                                        dot8(d.qt + qr * R, a.zK + (t * H + rh) * R, R);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sv[i] = i == e ? __float_as_uint(x) : sv[i];
+                    }
+                    __syncwarp();
+                    mx = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sv[e]));
+                }
+                mx *= d.scale_log2;
             }
             if (++vst == VST) {
                 vst = 0;

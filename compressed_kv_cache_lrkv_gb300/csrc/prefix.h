@@ -9,6 +9,7 @@ struct PrefixArgs {
     // Queries, q~, factors, output (or partials out) and, where the sequences have tokens of their
     // own, their lengths and the workspace their scan leaves its partials in.
     DecodeArgs d;
+    const uint16_t *sK, *zK;            // the pools that the tensor maps show (logits formed again, prefix.cu)
     const int32_t* blocks;              // [max_blocks] pages of the prefix
     const int32_t* len;                 // [1] tokens of the prefix
     int max_blocks;

@@ -387,7 +387,7 @@ size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, 
  *   outside its range, or no token at all, sets LRKV_DEV_BAD_SEQLEN and writes zeros (a bad
  *   prefix_len: for all sequences).  A page id of the prefix outside [0, num_blocks) sets
  *   LRKV_DEV_BAD_BLOCK and its tokens are left out.  Rows behind the prefix's last token may hold
- *   any bits.  A NaN or infinity among the prefix's rows may reach all heads of the batch.  The
+ *   any bits.  A NaN or infinity in a head's latents stays in that head, as in lrkv_decode.  The
  *   prefix's products take the probabilities in bf16 and q~ in two bf16 pieces and sum in fp32.
  * lrkv_prefix_partials -- the prefix's part alone, as lrkv_decode_partials returns it (for
  *   lrkv_decode_merge with the partials of other caches); prefix_len 0 gives empty partials.

@@ -431,3 +431,42 @@ def test_expired_wait_reports_timeout_and_gpu_stays_usable(monkeypatch, H, d_h, 
     call()
     assert int(c.st.item()) == 0
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,P,B", [(8, 64, 8, 0, 300, 3), (32, 128, 16, 0, 700, 16), (20, 128, 32, 64, 200, 5),
+                                               (128, 64, 16, 0, 130, 40), (128, 128, 8, 64, 1000, 2)])
+def test_nan_and_infinity_in_a_head_stay_in_it(H, d_h, r, d_rope, P, B):
+    """Latents of one head that are not finite, of keys and of values: all other heads are as without them.  An
+    infinity among a key's latents moves its token's logit to the infinity of q~'s sign: with the minus sign the token
+    has no weight, with the plus sign the head's output is NaN."""
+    c = Case(25, H, d_h, r, d_rope, P, [5] * B)
+    zK, zV = c.cache.zK.view(-1, H, r), c.cache.zV.view(-1, H, r)
+
+    def verify(i, heads, what):
+        want, bound = attend64(c.q[i].double(), c.BK.double(), c.BV.double(), c.parts(i), d_rope)
+        check(c.out[i][heads], want[heads], bound[heads], what)
+
+    heads = torch.arange(H, device="cuda")
+    for value, pool, tok in ((float("nan"), zK, 0), (float("inf"), zK, P - 1), (float("-inf"), zK, P // 2),
+                             (float("nan"), zV, P // 3), (float("inf"), zV, P - 2)):
+        h, t = (7 * tok) % H, c.pslots[tok]
+        keep = pool[t, h, 1].clone()
+        pool[t, h, 1] = value
+        c.run()
+        assert int(c.st.item()) == 0
+        for i in (0, B // 2, B - 1):
+            verify(i, heads != h, f"heads beside one with {value}")
+        if value != value:
+            assert torch.isnan(c.out[:, h]).all()
+        elif pool is zV:
+            assert not torch.isfinite(c.out[:, h]).any()
+        else:
+            qt = torch.einsum("bd,d->b", c.q[:, h, :d_h].double(), c.BK[h, :, 1].double())
+            plus = qt * value > 0
+            assert torch.isnan(c.out[plus, h]).all()
+            slots = c.pslots
+            c.pslots = torch.cat([slots[:tok], slots[tok + 1:]])  # (the reference without that token)
+            for i in torch.nonzero(~plus).flatten().tolist():
+                verify(i, heads == h, "a head without one token")
+            c.pslots = slots
+        pool[t, h, 1] = keep
