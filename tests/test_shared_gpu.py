@@ -470,3 +470,20 @@ def test_nan_and_infinity_in_a_head_stay_in_it(H, d_h, r, d_rope, P, B):
                 verify(i, heads == h, "a head without one token")
             c.pslots = slots
         pool[t, h, 1] = keep
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,P,factor", [(16, 128, 16, 0, 1500, 20), (32, 128, 8, 0, 3000, 8),
+                                                    (8, 64, 32, 64, 700, 20), (128, 64, 16, 0, 5000, 30)])
+def test_sharp_logits_over_a_prefix_alone(H, d_h, r, d_rope, P, factor):
+    """Without tokens of the sequences' own q~ enters in two bf16 pieces: two roundings to half a step of 2^-8, 2^-16
+    left, so large queries move no logit much.  The outputs' roundings are 0.0016 of them, root mean square; the
+    probabilities', where a few tokens have all the weight, at most 2^-8 each: sqrt(0.0016^2 + 0.0039^2) = 0.0042.
+    (Logits 20% off take up 6 to 14 times the elementwise bound, and 2% off leave a relative error of up to 0.007.)"""
+    c = Case(26, H, d_h, r, d_rope, P, [0] * 3)
+    c.q *= factor
+    c.run()
+    assert int(c.st.item()) == 0
+    for i in range(3):
+        want, bound = attend64(c.q[i].double(), c.BK.double(), c.BV.double(), c.parts(i), d_rope, eps_p=2.0 ** -8,
+                               eps_qt=2.0 ** -16)
+        check(c.out[i], want, bound, f"queries times {factor}, sequence {i}", rel_max=4.3e-3)
