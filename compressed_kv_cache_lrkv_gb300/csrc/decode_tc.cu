@@ -136,20 +136,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const Work wk = *plan;
     const uint32_t tmem = *tmem_slot;
 
+    int issued = 0;  // stages the producer has filled (ring position and phase)
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
         SegWalk walk;
         walk.start(blockIdx.x);
         int vb = 0, sg0 = 0, sg1 = 0, pslot = 0;
-        int g = 0;  // stages issued so far (ring position and phase)
         bool ok = true;
         while (ok && walk.next(wk, &vb, &sg0, &sg1, &pslot)) {
             const int l = vb / a.B, bb = vb - l * a.B;
             const int pg0 = sg0 >> 3;
             const int32_t* bt_row = a.block_table + (size_t)bb * a.max_pages;
             int batch = -1, pid = -1;
-            for (int gi = sg0; gi < sg1; ++gi, ++g) {
+            for (int gi = sg0; gi < sg1; ++gi, ++issued) {
                 const int pi = (gi >> 3) - pg0;  // page of the segment; lane i holds page 32 batch + i
                 if ((pi >> 5) != batch) {
                     batch = pi >> 5;
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     pid = pp < a.max_pages ? bt_row[pp] : -1;
                 }
                 const int blk = __shfl_sync(0xffffffffu, pid, pi & 31);
-                const int s = g % nslot;
-                if (g >= nslot && !tc_wait(smem_u32(&empty[s]), ((g / nslot) - 1) & 1, a)) {
+                const int s = issued % nslot;
+                if (issued >= nslot && !tc_wait(smem_u32(&empty[s]), ((issued / nslot) - 1) & 1, a)) {
                     ok = false;
                     break;
                 }
@@ -187,12 +187,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
             }
         }
-        if (!ok) {
-            *abort_flag = 1;
-            // let the copies still in flight land before the CTA exits (always the full limit)
-            if (lane == 0)
-                for (int k = max(0, g - nslot); k < g; ++k) mbar_wait(smem_u32(&full[k % nslot]), (k / nslot) & 1, a.status);
-        }
+        if (!ok) *abort_flag = 1;
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
         constexpr uint32_t id_S = idesc_bf16_f32(128, 16);
@@ -204,7 +199,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         while (ok && walk.next(wk, &vb, &sg0, &sg1, &pslot)) {
             const int nst = sg1 - sg0;
-            ok = !aborted() && tc_wait(smem_u32(q_ready), segn & 1, a);  // this segment's Q in TMEM
+            // this segment's Q in TMEM (never there at once, so a limit of 0 is sure to run out here, with copies in
+            // flight; the stages' waits are left as they are: looking first costs this kernel 0.4%)
+            ok = !aborted() && __all_sync(0xffffffffu, mbar_look_wait(smem_u32(q_ready), segn & 1, a.status, a.wait_ns));
             for (int k = 0; ok && k <= nst; ++k) {
                 if (k < nst) {
                     // S_k = Q . [s^K of the stage | 8 zero rows]^T into buffer (g + k) % 2.  That buffer's
@@ -253,7 +250,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // every MMA this warp issued has finished before TMEM is released
         if (elect_one_sync()) tc_commit(smem_u32(drain));
         __syncwarp();
-        tc_wait(smem_u32(drain), 0, a);
+        mbar_wait(smem_u32(drain), 0, a.status);
+        __syncwarp();
     } else {
         // ------------------------------------------------------------------ softmax: two threads per head
         // Warps 2-9: quarter q = warp % 4 of the TMEM lanes (head 32 q + lane), token half th = 0
@@ -520,6 +518,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // Whichever wait ran out, and however late: the copies in flight land (always the full limit) before the block
+    // gives up its shared memory.
+    if (warp == 0 && lane == 0 && *abort_flag)
+        for (int k = max(0, issued - nslot); k < issued; ++k)
+            mbar_wait(smem_u32(&full[k % nslot]), (k / nslot) & 1, a.status);
     if (warp == 1) tmem_dealloc(tmem, TC_COLS);
 }
 

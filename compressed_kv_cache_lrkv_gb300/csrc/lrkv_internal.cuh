@@ -114,6 +114,21 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uin
     }
 }
 
+// mbar_wait_for that looks first, and at a shortened limit only looks: try_wait may itself wait longer than the limit
+// and then find the phase complete.
+__device__ __forceinline__ bool mbar_look_wait(uint32_t bar, uint32_t parity, uint32_t* status, uint64_t limit_ns) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    const bool nap = limit_ns == kWaitLimitNs;
+    for (uint32_t it = 1;; ++it) {
+        if (nap ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
+        if (((it & 255u) == 0 || !nap) && globaltimer_ns() - t0 > limit_ns) {
+            set_status(status, LRKV_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(

@@ -80,19 +80,9 @@ struct PxLayout {
 __device__ __forceinline__ uint64_t kdesc128(uint32_t a) { return sdesc(a, 16, 1024, 2); }
 __device__ __forceinline__ uint64_t mndesc128(uint32_t a) { return sdesc(a, 8192, 1024, 2); }
 
-// Wait of a role, with the call's limit (a shortened one is not napped through), and one for what the block has in
-// flight, with the full limit.
+// Wait of a role, with the call's limit, and one for what the block has in flight, with the full limit.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const DecodeArgs& d) {
-    bool ok = mbar_test(bar, parity);
-    if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        const bool nap = d.wait_ns == kWaitLimitNs;
-        for (uint32_t it = 1; !(ok = nap ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)); ++it)
-            if (((it & 255u) == 0 || !nap) && globaltimer_ns() - t0 > d.wait_ns) {
-                set_status(d.status, LRKV_DEV_TIMEOUT);
-                break;
-            }
-    }
+    const bool ok = mbar_look_wait(bar, parity, d.status, d.wait_ns);
     return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* status) {

@@ -487,3 +487,32 @@ def test_sharp_logits_over_a_prefix_alone(H, d_h, r, d_rope, P, factor):
         want, bound = attend64(c.q[i].double(), c.BK.double(), c.BV.double(), c.parts(i), d_rope, eps_p=2.0 ** -8,
                                eps_qt=2.0 ** -16)
         check(c.out[i], want, bound, f"queries times {factor}, sequence {i}", rel_max=4.3e-3)
+
+
+@pytest.mark.parametrize("P,lens", [(0, [9000, 7000, 1]), (700, [3000] * 6)])
+def test_expired_wait_of_128_heads(monkeypatch, P, lens):
+    """The same for the tensor-core scan of 128 heads, by itself (lrkv_decode) and as the sequences' own scan."""
+    c = Case(27, 128, 128, 16, 0, P, lens)
+
+    def call():
+        if P:
+            c.run()
+        else:
+            b.lrkv_decode(c.dims, c.q, c.BK, c.BV, c.cache, c.bt, c.sl, c.out, c.ws, status=c.st)
+
+    call()
+    assert int(c.st.item()) == 0
+    want = c.out.clone()
+    c.verify(seqs=[0, len(lens) - 1])
+    monkeypatch.setenv("LRKV_DEBUG_WAIT_LIMIT_NS", "0")
+    seen = 0
+    for _ in range(5):
+        call()
+        seen |= int(c.st.item())
+    assert seen == b.DEV_TIMEOUT
+    monkeypatch.delenv("LRKV_DEBUG_WAIT_LIMIT_NS")
+    c.st.zero_()
+    c.out.fill_(float("nan"))
+    call()
+    assert int(c.st.item()) == 0
+    assert torch.equal(c.out, want)
