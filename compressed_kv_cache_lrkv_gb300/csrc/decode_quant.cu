@@ -52,7 +52,9 @@ namespace {
 // 168 registers) for up to 64 heads, 16 (18 warps, 96 registers) for more.  Measured for 128 heads of
 // r = 16: two tiles of 8 heads per warp in 12 warps 107 us, one with 16 consumers 97 at that time; for 32 heads
 // more consumers are slower: with 8, 12 and 16 the ragged batch takes 45, 48 and 56 us, the long context 50, 60
-// and 78 (every tile in work holds a stage of the ring as well).
+// and 78 (every tile in work holds a stage of the ring as well).  Whole groups of warps take the tiles, so a head count
+// that leaves warps over costs about as much as the next one that does not; 8 x 8,192 tokens of r = 16: 8 heads 23 us,
+// 16 25, 24 and 32 30, 40 to 64 44 to 46, 72 71, 96 75, 112 80, 128 86.
 // Warps that widen s^V: a tile takes one some 0.7 us.  With 8 consumers a tile is due every 0.75 us or less (one
 // converter 54 us for the ragged batch, two 47, three 45), with 16 every 3 us, and the registers are worth more.
 __host__ __device__ constexpr int converters(int cw) { return cw == 8 ? 3 : 1; }

@@ -55,7 +55,7 @@ struct DecodeArgs {
     int gpst;          // 8-token granules per pipeline stage (1 or 2)
     int pmax;          // partial slots per head in the workspace (layers * B * nhg + nranges)
     float scale_log2;  // softmax scale * log2(e)
-    unsigned long long wait_ns;  // limit of the split kernel's pipeline waits (a debugging aid may shorten it)
+    unsigned long long wait_ns;  // limit of the scans' pipeline waits (a debugging aid may shorten it)
     // 1: the scan alone, as a dependent launch behind one that itself has waited for q~ (so the scan does
     // not, and ends only after that launch); the caller merges the partials.
     int no_combine;

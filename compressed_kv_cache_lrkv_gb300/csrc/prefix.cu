@@ -785,7 +785,10 @@ int prefix_most_splits(int H, int D_H, int R, int D_R, int B, int max_blocks, in
 // the pieces of all tiles run in waves of one CTA per SM; the other scan costs 6, as much again for each
 // sequence that a CTA meets, and streams 28 bytes a ns on one SM.  Of the own tables' capacity half is
 // taken to be in use.  Measured: 32 heads x 16 sequences behind 8 K tokens 33 us one after the other, 25 side by
-// side; 128 x 48 behind 4 K 76 and 66.
+// side; 128 x 48 behind 4 K 76 and 66.  The lengths are on the device, so the plan knows the tables' widths alone: the
+// first case with own tables of 8 and 16 pages a sequence 25 us, of 32 and more (planned one after the other) 33; with
+// 128, 256, 512 and 2,048 pages listed for the prefix's 128 25, 25, 28 and 47.  The search takes the host 0.3 to 3 us
+// for short prefixes or many tiles, some 10 for one tile of 512 pages.
 PrefixPlan prefix_plan(int H, int D_H, int R, int D_R, int B, int max_blocks, double own_bytes, int sms) {
     PrefixPlan best = prefix_tile(H, D_H, R, D_R, B);
     const long long ntiles = (long long)best.htiles * best.stiles;

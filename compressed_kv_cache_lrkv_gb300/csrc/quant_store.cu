@@ -17,8 +17,9 @@
 // bytes of four blocks leave in one word.
 // 65,536 rows of 2,304 values in random order, there and back: 164 us, 5.6 TB/s (of 6.8 measured for a copy);
 // with eight values a thread 179 us (a third more instructions per value); with streaming loads 171 us, streaming
-// stores too 183; with registers for full occupancy 183; two rows in flight 188, a warp per row 204.  1,000
-// rows of 1,344 values: 5.1 us for both calls, 16 rows (a decode step's) 3.9; with a warp per row 11.6.
+// stores too 183; with registers for full occupancy 183; two rows in flight 188, a warp per row 204.  In a
+// graph 1,000 rows of 1,344 values take 5.3 us there and back, 16 rows (a decode step's) 3.9, with a warp per row 11.6;
+// called one after the other from the host both take 14, the calls themselves.
 #include "lrkv_internal.cuh"
 #include "quant.cuh"
 #include "quant.h"

@@ -389,6 +389,8 @@ size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, 
  *   LRKV_DEV_BAD_BLOCK and its tokens are left out.  Rows behind the prefix's last token may hold
  *   any bits.  A NaN or infinity in a head's latents stays in that head, as in lrkv_decode.  The
  *   prefix's products take the probabilities in bf16 and q~ in two bf16 pieces and sum in fp32.
+ *   The work is planned from the tables' widths (the lengths are on the device): max_prefix_blocks and
+ *   max_blocks_per_seq well above what is in use are allowed, but cost time.
  * lrkv_prefix_partials -- the prefix's part alone, as lrkv_decode_partials returns it (for
  *   lrkv_decode_merge with the partials of other caches); prefix_len 0 gives empty partials.
  */
