@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
                 // diag(Q~)'s zeros times another head's NaN or infinity are NaN (and so is what rounding an infinite
                 // product left): such logits are formed again from the row's own head alone.  (The look for
-                // them, in the maximum's own instructions and a vote, costs 1%: 55.2 us -> 56.0 for 32,768 tokens.)
+                // them, in the maximum's own instructions and a vote, costs 1%: 55.2 us -> 56.0 for 32,768 tokens;
+                // a page with one such token takes 5 us more, one full of them 150.)
                 if (__any_sync(0xffffffffu, mx != mx)) {
                     uint32_t nans = 0;
 #pragma unroll

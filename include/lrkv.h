@@ -387,7 +387,8 @@ size_t lrkv_decode_shared_workspace_bytes(const lrkv_dims* dims, int32_t batch, 
  *   outside its range, or no token at all, sets LRKV_DEV_BAD_SEQLEN and writes zeros (a bad
  *   prefix_len: for all sequences).  A page id of the prefix outside [0, num_blocks) sets
  *   LRKV_DEV_BAD_BLOCK and its tokens are left out.  Rows behind the prefix's last token may hold
- *   any bits.  A NaN or infinity in a head's latents stays in that head, as in lrkv_decode.  The
+ *   any bits.  A NaN or infinity in a head's latents stays in that head, as in lrkv_decode (a page
+ *   that holds one takes longer).  The
  *   prefix's products take the probabilities in bf16 and q~ in two bf16 pieces and sum in fp32.
  *   The work is planned from the tables' widths (the lengths are on the device): max_prefix_blocks and
  *   max_blocks_per_seq well above what is in use are allowed, but cost time.
