@@ -18,6 +18,7 @@ LRKV_OK = 0
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "workspace too small", 4: "CUDA error",
                 5: "device bounds", 6: "timeout"}
 DEV_BAD_BLOCK, DEV_BAD_SEQLEN, DEV_BAD_SLOT, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_NO_PAGES, DEV_BAD_INDEX = 0x10, 0x20
 
 EXPORTED = ["lrkv_abi_version", "lrkv_status_string", "lrkv_last_error", "lrkv_cache_block_bytes", "lrkv_append",
             "lrkv_decode_workspace_bytes", "lrkv_decode", "lrkv_decode_fused", "lrkv_decode_static_ws",
@@ -28,7 +29,10 @@ EXPORTED = ["lrkv_abi_version", "lrkv_status_string", "lrkv_last_error", "lrkv_c
             "lrkv_train_backward", "lrkv_quant_row_bytes", "lrkv_quant_block_bytes", "lrkv_cache_quantize",
             "lrkv_cache_dequantize", "lrkv_decode_quant_workspace_bytes", "lrkv_decode_quant",
             "lrkv_decode_quant_partials", "lrkv_decode_shared_workspace_bytes", "lrkv_decode_shared",
-            "lrkv_prefix_partials"]
+            "lrkv_prefix_partials", "lrkv_decode_tree_workspace_bytes", "lrkv_decode_tree", "lrkv_rope_make_plan",
+            "lrkv_rope", "lrkv_pages_reserve", "lrkv_pages_fork", "lrkv_pages_free", "lrkv_pages_copy",
+            "lrkv_cache_compact"]
+MAX_TREE = 64  # LRKV_MAX_TREE
 STATIC_WS_BYTES = 16 << 20  # LRKV_STATIC_WS_BYTES
 
 
@@ -62,6 +66,27 @@ class Cache(ctypes.Structure):
 
 class QuantCacheStruct(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("d_rot", "layout", "scaling", "reserved")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "original_len", "low", "high", "magnitude")]
+
+
+class RopePlan(ctypes.Structure):
+    """Speeds of a rotation (lrkv_rope_plan), made by rope_plan."""
+    _fields_ = [("d_rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turn", ctypes.c_uint64 * 128)]
+
+
+class RowsStruct(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("num_rows", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("index", ctypes.c_void_p)]
+
+
+class PoolsStruct(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p * 4), ("row_bytes", ctypes.c_int64 * 4), ("layer_bytes", ctypes.c_int64 * 4),
+                ("num_pools", ctypes.c_int32), ("num_layers", ctypes.c_int32), ("num_blocks", ctypes.c_int32)]
 
 
 _lib = None
@@ -143,6 +168,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                        vp]
     lib.lrkv_prefix_partials.restype = ctypes.c_int
     lib.lrkv_prefix_partials.argtypes = [P(Dims), vp, vp, P(Cache), vp, i32, vp, i32, vp, vp, sz, vp, vp]
+    lib.lrkv_decode_tree_workspace_bytes.restype = sz
+    lib.lrkv_decode_tree_workspace_bytes.argtypes = [P(Dims), i32, i32]
+    lib.lrkv_rope_make_plan.argtypes = [P(RopeSpec), P(RopePlan)]
+    lib.lrkv_decode_tree.argtypes = [P(Dims), vp, vp, vp, P(Cache), vp, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp, vp]
+    lib.lrkv_rope.argtypes = [P(RopePlan), i32, i32, i32, i32, i32, P(RowsStruct), P(RowsStruct), vp, i32, vp, vp]
+    lib.lrkv_pages_reserve.argtypes = [i32, vp, vp, i32, vp, vp, i32, vp, vp]
+    lib.lrkv_pages_fork.argtypes = [P(PoolsStruct), vp, vp, i32, vp, i32, vp, vp, i32, vp, vp]
+    lib.lrkv_pages_free.argtypes = [i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp]
+    lib.lrkv_pages_copy.argtypes = [P(PoolsStruct), vp, P(PoolsStruct), vp, i32, vp, vp]
+    lib.lrkv_cache_compact.argtypes = [P(PoolsStruct), vp, i32, vp, i32, vp, vp, i32, vp, vp, vp]
+    for f in (lib.lrkv_rope_make_plan, lib.lrkv_decode_tree, lib.lrkv_rope, lib.lrkv_pages_reserve,
+              lib.lrkv_pages_fork, lib.lrkv_pages_free, lib.lrkv_pages_copy, lib.lrkv_cache_compact):
+        f.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -460,6 +498,151 @@ def lrkv_prefix_partials(dims: Dims, q, BK, cache: PagedCache, prefix_blocks, pr
                                      _ptr(workspace), workspace.nbytes,
                                      _ptr(status), _stream(stream))
     _check(rc, "lrkv_prefix_partials")
+
+
+def decode_tree_workspace_bytes(dims: Dims, batch: int, T: int) -> int:
+    return int(load().lrkv_decode_tree_workspace_bytes(ctypes.byref(dims), batch, T))
+
+
+def lrkv_decode_tree(dims: Dims, q, BK, BV, cache: PagedCache, block_table, seq_lens, tree_mask, tree_lens, out,
+                     workspace, status=None, stream=None):
+    """Drafted tokens over the cache: q [B, T, H, d_h + d_rope] -> out [B, T, H, d_h]; tree_mask [B, T] int64 bit sets
+    of the drafted tokens seen (None: a chain), tree_lens [B] int32 drafted tokens of each sequence (None: T)."""
+    c = cache.struct()
+    B, T = q.shape[0], q.shape[1]
+    if tree_mask is not None and (tree_mask.element_size() != 8 or tuple(tree_mask.shape) != (B, T)):
+        raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype}: expected 64-bit words [{B}, {T}]")
+    rc = load().lrkv_decode_tree(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(c), _ptr(block_table),
+                                 block_table.shape[1], _ptr(seq_lens), _ptr(tree_mask), _ptr(tree_lens), B, T,
+                                 _ptr(out), _ptr(workspace), workspace.nbytes, _ptr(status), _stream(stream))
+    _check(rc, "lrkv_decode_tree")
+
+
+_ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "parts": 2}
+_ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def rope_plan(d_rot: int, layout: str = "interleaved", base: float = 10000.0, scaling: str = "none",
+              factor: float = 1.0, original_len: float = 0.0, low: float = 1.0, high: float = 32.0,
+              magnitude: float = 1.0) -> RopePlan:
+    """Speeds of a rotation of d_rot values per head (lrkv_rope_make_plan); made once, kept by the caller."""
+    spec = RopeSpec(d_rot, _ROPE_LAYOUTS[layout], _ROPE_SCALINGS[scaling], 0, base, factor, original_len, low, high,
+                    magnitude)
+    plan = RopePlan()
+    _check(load().lrkv_rope_make_plan(ctypes.byref(spec), ctypes.byref(plan)), "lrkv_rope_make_plan")
+    return plan
+
+
+def _rows(t, index) -> RowsStruct:
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"rows {tuple(t.shape)}, strides {t.stride()}: expected [rows, heads, width], last stride 1")
+    return RowsStruct(_ptr(t), t.shape[0], t.stride(0), t.stride(1), _ptr(index))
+
+
+def lrkv_rope(plan: RopePlan, x, y, positions, begin: int = 0, x_rows=None, y_rows=None, transpose: bool = False,
+              status=None, stream=None):
+    """y = x with values [begin, begin + plan.d_rot) of every head rotated at positions [n] (int32): x, y
+    [rows, heads, width] of bf16 or fp32 (y is x: in place); x_rows, y_rows [n] int32 pick rows."""
+    n = positions.shape[0]
+    for index in (x_rows, y_rows):
+        if index is not None and index.shape[0] != n:
+            raise ValueError(f"{index.shape[0]} row indices for {n} positions")
+    if x.dtype is not y.dtype or x.dtype not in _ROPE_TYPES or x.shape[1:] != y.shape[1:]:
+        raise ValueError(f"x {tuple(x.shape)} of {x.dtype}, y {tuple(y.shape)} of {y.dtype}: expected equal heads and "
+                         "widths in bfloat16 or float32")
+    xs, ys = _rows(x, x_rows), _rows(y, y_rows)
+    rc = load().lrkv_rope(ctypes.byref(plan), _ROPE_TYPES[x.dtype], n, x.shape[1], x.shape[2], begin,
+                          ctypes.byref(xs), ctypes.byref(ys), _ptr(positions), int(transpose), _ptr(status),
+                          _stream(stream))
+    _check(rc, "lrkv_rope")
+
+
+class Pools:
+    """Pools whose rows move together (lrkv_pools): made once from a cache and kept (it keeps the tensors)."""
+
+    def __init__(self, tensors):
+        """tensors: [layers, num_blocks, 64, ...] each, a layer contiguous."""
+        self.tensors = tuple(tensors)
+        s = self.c = PoolsStruct()
+        first = self.tensors[0]
+        s.num_pools, s.num_layers, s.num_blocks = len(self.tensors), first.shape[0], first.shape[1]
+        if not 1 <= len(self.tensors) <= 4:
+            raise ValueError(f"{len(self.tensors)} pools (1 to 4)")
+        for i, t in enumerate(self.tensors):
+            if t.dim() < 4 or t.shape[:3] != (first.shape[0], first.shape[1], 64) or not t[0].is_contiguous():
+                raise ValueError(f"pool {tuple(t.shape)}, strides {t.stride()}: expected [layers, num_blocks, 64, ...], "
+                                 "each layer contiguous, alike in all pools")
+            s.base[i] = _ptr(t)
+            s.row_bytes[i] = t[0, 0, 0].numel() * t.element_size()
+            s.layer_bytes[i] = t.stride(0) * t.element_size()
+
+    @classmethod
+    def of(cls, cache):
+        """Of a PagedCache, a LayeredCache, a QuantCache, or a pool tensor [num_blocks, 64, ...]."""
+        if isinstance(cache, LayeredCache):
+            return cls(cache.tensors())
+        if isinstance(cache, PagedCache):
+            return cls(t.unsqueeze(0) for t in cache.tensors())
+        return cls([(cache.rows if isinstance(cache, QuantCache) else cache).unsqueeze(0)])
+
+
+def _page_table(refs, block_table, seq_lens):
+    for t in (refs, block_table, seq_lens):
+        if t.dtype is not torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{tuple(t.shape)} of {t.dtype}: refs, block table and lengths are contiguous int32")
+    if block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"block table of {block_table.shape[0]} sequences, {seq_lens.shape[0]} lengths")
+    return block_table.shape[0]
+
+
+def lrkv_pages_reserve(refs, block_table, seq_lens, new_tokens, status=None, stream=None):
+    """Pages for new_tokens [B] more tokens of every sequence, from the pages with count 0 in refs [num_blocks]."""
+    B = _page_table(refs, block_table, seq_lens)
+    _same_length(seq_lens, new_tokens)
+    rc = load().lrkv_pages_reserve(refs.shape[0], _ptr(refs), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+                                   _ptr(new_tokens), B, _ptr(status), _stream(stream))
+    _check(rc, "lrkv_pages_reserve")
+
+
+def lrkv_pages_fork(pools: Pools, refs, block_table, seq_lens, parents, children, status=None, stream=None):
+    """Sequences children [n] become copies of sequences parents [n], sharing their full pages."""
+    B = _page_table(refs, block_table, seq_lens)
+    if refs.shape[0] != pools.c.num_blocks:
+        raise ValueError(f"{refs.shape[0]} counts for {pools.c.num_blocks} pages")
+    rc = load().lrkv_pages_fork(ctypes.byref(pools.c), _ptr(refs), _ptr(block_table), block_table.shape[1],
+                                _ptr(seq_lens), B, _ptr(parents), _ptr(children), _same_length(parents, children),
+                                _ptr(status), _stream(stream))
+    _check(rc, "lrkv_pages_fork")
+
+
+def lrkv_pages_free(refs, block_table, seq_lens, seqs, keep_lens=None, status=None, stream=None):
+    """Sequences seqs [n] give back their pages behind keep_lens [B] tokens (None: all)."""
+    B = _page_table(refs, block_table, seq_lens)
+    if keep_lens is not None:
+        _same_length(seq_lens, keep_lens)
+    rc = load().lrkv_pages_free(refs.shape[0], _ptr(refs), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+                                _ptr(seqs), seqs.shape[0], _ptr(keep_lens), _ptr(status), _stream(stream))
+    _check(rc, "lrkv_pages_free")
+
+
+def lrkv_pages_copy(src: Pools, src_pages, dst: Pools, dst_pages, status=None, stream=None):
+    """Pages src_pages [n] of src -> pages dst_pages [n] of dst, in all pools and layers."""
+    rc = load().lrkv_pages_copy(ctypes.byref(src.c), _ptr(src_pages), ctypes.byref(dst.c), _ptr(dst_pages),
+                                _same_length(src_pages, dst_pages), _ptr(status), _stream(stream))
+    _check(rc, "lrkv_pages_copy")
+
+
+def lrkv_cache_compact(pools: Pools, block_table, seq_lens, path, path_lens, new_lens=None, status=None, stream=None):
+    """Rows seq_lens[b] + path[b, i] -> seq_lens[b] + i, i < path_lens[b]; new_lens = seq_lens + path_lens (None: in
+    place)."""
+    B = _page_table(path, block_table, seq_lens)
+    _same_length(seq_lens, path)
+    _same_length(seq_lens, path_lens)
+    rc = load().lrkv_cache_compact(ctypes.byref(pools.c), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+                                   _ptr(path), _ptr(path_lens), path.shape[1], _ptr(new_lens), _ptr(status),
+                                   _stream(stream))
+    _check(rc, "lrkv_cache_compact")
 
 
 def lrkv_prefill(dims: Dims, q, BK, BV, cache: PagedCache, block_table, q_start, out, workspace=None, status=None,

@@ -11,11 +11,13 @@
 
 #include "lrkv_internal.cuh"
 
+#include "draft.h"
 #include "kernels.h"
 #include "mla.h"
 #include "prefix.h"
 #include "quant.h"
 #include "train.h"
+#include "tree.h"
 
 namespace {
 
@@ -840,6 +842,305 @@ lrkv_status lrkv_decode_quant_partials(const lrkv_dims* dims, const void* q, con
     if (!partials) return fail(LRKV_ERR_INVALID_ARG, "partials is NULL");
     return decode_quant_impl(dims, q, BK, nullptr, qcache, block_table, max_blocks_per_seq, seq_lens, batch, nullptr,
                              partials, workspace, workspace_bytes, status_dev, stream);
+}
+
+// ------------------------------------------------------------------ drafted tokens
+static lrkv_status check_tree(const lrkv_dims* dims, int32_t batch, int32_t T) {
+    lrkv_status s = check_dims(dims);
+    if (s != LRKV_OK) return s;
+    if (T < 1 || T > LRKV_MAX_TREE) return fail(LRKV_ERR_UNSUPPORTED, "T %d (supported: 1..%d)", T, LRKV_MAX_TREE);
+    if (batch < 0 || (long long)batch * T > 65535)
+        return fail(LRKV_ERR_INVALID_ARG, "batch %d x T %d (0..65535 queries)", batch, T);
+    return LRKV_OK;
+}
+
+size_t lrkv_decode_tree_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t T) {
+    if (check_tree(dims, batch, T) != LRKV_OK) return 0;
+    DeviceInfo di;
+    if (device_info(&di) != LRKV_OK) return 0;
+    return lrkv::tree_workspace_bytes(dims->H, dims->d_h, dims->r, dims->d_rope, batch, T, di.sms);
+}
+
+lrkv_status lrkv_decode_tree(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                             const lrkv_cache* cache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                             const int32_t* seq_lens, const uint64_t* tree_mask, const int32_t* tree_lens,
+                             int32_t batch, int32_t T, void* out, void* workspace, size_t workspace_bytes,
+                             uint32_t* status_dev, void* stream) {
+    lrkv_status s = check_tree(dims, batch, T);
+    if (s != LRKV_OK) return s;
+    if ((s = check_cache(cache)) != LRKV_OK) return s;
+    if (batch == 0) return ok();
+    if (max_blocks_per_seq < 1 || (long long)max_blocks_per_seq * dims->block_size > (1LL << 30))
+        return fail(LRKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", max_blocks_per_seq);
+    LRKV_REQUIRE_PTR(q);
+    LRKV_REQUIRE_PTR(BK);
+    LRKV_REQUIRE_PTR(BV);
+    LRKV_REQUIRE_PTR(out);
+    if (!block_table || !seq_lens) return fail(LRKV_ERR_INVALID_ARG, "block_table or seq_lens is NULL");
+    if (((uintptr_t)tree_mask & 7u) != 0) return fail(LRKV_ERR_INVALID_ARG, "tree_mask not 8-byte aligned");
+    DeviceInfo di;
+    if ((s = device_info(&di)) != LRKV_OK) return s;
+    lrkv::TreeArgs a{};
+    a.d.q = static_cast<const uint16_t*>(q);
+    a.d.BK = static_cast<const uint16_t*>(BK);
+    a.d.BV = static_cast<const uint16_t*>(BV);
+    a.d.out = static_cast<uint16_t*>(out);
+    a.d.status = status_dev;
+    a.d.B = batch * T;  // (the absorb's: every drafted token is a query of its own)
+    a.d.H = dims->H;
+    a.d.layers = 1;
+    a.d.block_table = block_table;
+    a.d.seq_lens = seq_lens;
+    a.d.max_pages = max_blocks_per_seq;
+    a.d.num_blocks = cache->num_blocks;
+    a.d.wait_ns = decode_wait_limit_ns();
+    a.d.scale_log2 = logit_scale(dims) * 1.4426950408889634f;
+    a.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+    a.tree_lens = tree_lens;
+    a.batch = batch;
+    a.T = T;
+    a.sK = static_cast<const uint16_t*>(cache->sK);
+    a.sV = static_cast<const uint16_t*>(cache->sV);
+    a.zK = static_cast<const uint16_t*>(cache->zK);
+    a.zV = static_cast<const uint16_t*>(cache->zV);
+    const size_t need = lrkv::tree_workspace_bytes(dims->H, dims->d_h, dims->r, dims->d_rope, batch, T, di.sms);
+    if (!workspace || ((uintptr_t)workspace & 255u))
+        return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(LRKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    return cuda_status(lrkv::launch_tree(a, dims->d_h, dims->r, dims->d_rope, workspace, di.sms,
+                                         static_cast<cudaStream_t>(stream)),
+                       "lrkv_decode_tree launch");
+}
+
+// ------------------------------------------------------------------ rotary positions
+lrkv_status lrkv_rope_make_plan(const lrkv_rope_spec* spec, lrkv_rope_plan* plan) {
+    if (!spec || !plan) return fail(LRKV_ERR_INVALID_ARG, "spec or plan is NULL");
+    if (spec->d_rot < 8 || spec->d_rot > 256 || spec->d_rot % 8 != 0)
+        return fail(LRKV_ERR_UNSUPPORTED, "d_rot %d (supported: multiples of 8, 8..256)", spec->d_rot);
+    if (spec->layout != LRKV_ROPE_INTERLEAVED && spec->layout != LRKV_ROPE_HALF)
+        return fail(LRKV_ERR_INVALID_ARG, "layout %d", spec->layout);
+    if (spec->scaling < LRKV_ROPE_NONE || spec->scaling > LRKV_ROPE_PARTS)
+        return fail(LRKV_ERR_INVALID_ARG, "scaling %d", spec->scaling);
+    const double base = spec->base == 0.0 ? 10000.0 : spec->base;
+    if (!(base > 1.0) || std::isinf(base)) return fail(LRKV_ERR_INVALID_ARG, "base %g (0 for 10000, else > 1)", base);
+    if (spec->scaling != LRKV_ROPE_NONE && (!(spec->factor >= 1.0) || std::isinf(spec->factor)))
+        return fail(LRKV_ERR_INVALID_ARG, "factor %g (at least 1)", spec->factor);
+    if (spec->scaling == LRKV_ROPE_PARTS &&
+        (!(spec->original_len > 0.0) || std::isinf(spec->original_len) || !(spec->low >= 0.0) ||
+         !(spec->high > spec->low) || std::isinf(spec->high)))
+        return fail(LRKV_ERR_INVALID_ARG, "original_len %g, low %g, high %g (original_len > 0, 0 <= low < high)",
+                    spec->original_len, spec->low, spec->high);
+    const double mag = spec->magnitude == 0.0 ? 1.0 : spec->magnitude;
+    if (!std::isfinite((float)mag)) return fail(LRKV_ERR_INVALID_ARG, "magnitude %g", mag);
+    // (long double: a speed is multiplied by positions up to 2^31, so double's 53 bits would show)
+    const long double two_pi = 6.283185307179586476925286766559L;
+    *plan = lrkv_rope_plan{};
+    plan->d_rot = spec->d_rot;
+    plan->layout = spec->layout;
+    plan->magnitude = (float)mag;
+    for (int i = 0; i < spec->d_rot / 2; ++i) {
+        long double f = std::pow((long double)base, -2.0L * i / spec->d_rot);
+        if (spec->scaling == LRKV_ROPE_LINEAR) {
+            f /= spec->factor;
+        } else if (spec->scaling == LRKV_ROPE_PARTS) {
+            long double g = (spec->original_len * f / two_pi - spec->low) / (spec->high - spec->low);
+            g = g < 0.0L ? 0.0L : g > 1.0L ? 1.0L : g;
+            f = g * f + (1.0L - g) * f / spec->factor;
+        }
+        plan->turn[i] = (uint64_t)std::nearbyint(f / two_pi * 18446744073709551616.0L);  // f <= 1: below 2^62
+    }
+    return ok();
+}
+
+lrkv_status lrkv_rope(const lrkv_rope_plan* plan, int32_t dtype, int32_t n, int32_t heads, int32_t width,
+                      int32_t begin, const lrkv_rows* x, const lrkv_rows* y, const int32_t* positions,
+                      int32_t transpose, uint32_t* status_dev, void* stream) {
+    if (!plan || !x || !y) return fail(LRKV_ERR_INVALID_ARG, "plan, x or y is NULL");
+    if (plan->d_rot < 8 || plan->d_rot > 256 || plan->d_rot % 8 != 0 || plan->layout < 0 || plan->layout > 1)
+        return fail(LRKV_ERR_INVALID_ARG, "plan not made by lrkv_rope_make_plan");
+    if (dtype != LRKV_BF16 && dtype != LRKV_FP32) return fail(LRKV_ERR_UNSUPPORTED, "dtype %d", dtype);
+    if (transpose != 0 && transpose != 1) return fail(LRKV_ERR_INVALID_ARG, "transpose %d (0 or 1)", transpose);
+    if (n < 0) return fail(LRKV_ERR_INVALID_ARG, "n %d < 0", n);
+    if (heads < 1 || heads > 65535) return fail(LRKV_ERR_INVALID_ARG, "heads %d (1..65535)", heads);
+    if (width % 8 != 0 || begin % 8 != 0 || begin < 0 || width > 1024 || begin > width - plan->d_rot)
+        return fail(LRKV_ERR_UNSUPPORTED,
+                    "width %d, begin %d, d_rot %d (multiples of 8, begin + d_rot <= width <= 1024)", width, begin,
+                    plan->d_rot);
+    if (n == 0) return ok();
+    const lrkv_rows* both[2] = {x, y};
+    for (int k = 0; k < 2; ++k) {
+        const lrkv_rows* t = both[k];
+        const char* name = k ? "y" : "x";
+        if (!t->base || !aligned16(t->base))
+            return fail(LRKV_ERR_INVALID_ARG, "%s is NULL or not 16-byte aligned", name);
+        if (t->row_stride < 0 || t->head_stride < 0 || t->row_stride % 8 != 0 || t->head_stride % 8 != 0 ||
+            t->row_stride > (1LL << 40) || t->head_stride > (1LL << 40))
+            return fail(LRKV_ERR_INVALID_ARG, "strides %lld, %lld of %s (multiples of 8, 0..2^40)",
+                        (long long)t->row_stride, (long long)t->head_stride, name);
+        if (t->num_rows < 1 || (!t->index && t->num_rows < n))
+            return fail(LRKV_ERR_INVALID_ARG, "%s has %lld rows for %d items", name, (long long)t->num_rows, n);
+    }
+    // y's rows and heads lie apart: heads within a row, or rows within a head
+    const long long rs = y->row_stride, hs = y->head_stride, rows = y->num_rows;
+    const bool by_row = (heads == 1 || hs >= width) && (rows == 1 || rs >= (heads - 1) * hs + width);
+    const bool by_head = (rows == 1 || rs >= width) && (heads == 1 || (double)hs >= (double)(rows - 1) * rs + width);
+    if (!by_row && !by_head)
+        return fail(LRKV_ERR_INVALID_ARG, "y's rows and heads overlap (strides %lld, %lld, width %d)", rs, hs, width);
+    if (!positions) return fail(LRKV_ERR_INVALID_ARG, "positions is NULL");
+    DeviceInfo di;
+    const lrkv_status s = device_info(&di);
+    if (s != LRKV_OK) return s;
+    lrkv::RopeArgs a{};
+    a.plan = *plan;
+    a.x = x->base;
+    a.y = y->base;
+    a.x_index = x->index;
+    a.y_index = y->index;
+    a.positions = positions;
+    a.x_rows = x->num_rows;
+    a.y_rows = y->num_rows;
+    a.x_row = x->row_stride;
+    a.x_head = x->head_stride;
+    a.y_row = y->row_stride;
+    a.y_head = y->head_stride;
+    a.status = status_dev;
+    a.n = n;
+    a.heads = heads;
+    a.width = width;
+    a.begin = begin;
+    a.transpose = transpose;
+    a.in_place = x->base == y->base && x->index == y->index && x->row_stride == y->row_stride &&
+                 x->head_stride == y->head_stride;
+    return cuda_status(lrkv::launch_rope(a, dtype == LRKV_FP32, di.sms, static_cast<cudaStream_t>(stream)),
+                       "lrkv_rope launch");
+}
+
+// ------------------------------------------------------------------ pages
+static lrkv_status check_pools(const lrkv_pools* p, lrkv::PoolArgs* a) {
+    if (!p) return fail(LRKV_ERR_INVALID_ARG, "pools is NULL");
+    if (p->num_pools < 1 || p->num_pools > LRKV_MAX_POOLS)
+        return fail(LRKV_ERR_INVALID_ARG, "num_pools %d (1..%d)", p->num_pools, LRKV_MAX_POOLS);
+    if (p->num_layers < 1 || p->num_layers > 65535)
+        return fail(LRKV_ERR_INVALID_ARG, "num_layers %d (1..65535)", p->num_layers);
+    if (p->num_blocks < 1 || p->num_blocks > (1 << 24))
+        return fail(LRKV_ERR_INVALID_ARG, "num_blocks %d outside [1, 2^24]", p->num_blocks);
+    *a = lrkv::PoolArgs{};
+    a->pools = p->num_pools;
+    a->layers = p->num_layers;
+    a->num_blocks = p->num_blocks;
+    for (int i = 0; i < p->num_pools; ++i) {
+        if (!p->base[i] || !aligned16(p->base[i]))
+            return fail(LRKV_ERR_INVALID_ARG, "pool %d is NULL or not 16-byte aligned", i);
+        if (p->row_bytes[i] < 16 || p->row_bytes[i] % 16 != 0 || p->row_bytes[i] > (1 << 16))
+            return fail(LRKV_ERR_INVALID_ARG, "row of %lld bytes in pool %d (multiples of 16, 16..65536)",
+                        (long long)p->row_bytes[i], i);
+        if (p->num_layers > 1 && (p->layer_bytes[i] % 16 != 0 ||
+                                  p->layer_bytes[i] < (int64_t)p->num_blocks * 64 * p->row_bytes[i]))
+            return fail(LRKV_ERR_INVALID_ARG, "layers of pool %d are %lld bytes apart (a multiple of 16, at least %lld)", i,
+                        (long long)p->layer_bytes[i], (long long)p->num_blocks * 64 * p->row_bytes[i]);
+        a->base[i] = static_cast<uint4*>(p->base[i]);
+        a->layer[i] = p->num_layers > 1 ? p->layer_bytes[i] / 16 : 0;
+        a->u[i] = (int)(p->row_bytes[i] / 16);
+        a->units += a->u[i];
+    }
+    return LRKV_OK;
+}
+
+static lrkv_status check_table(const void* table, int32_t max_blocks, const void* lens, int32_t batch) {
+    if (batch < 0 || batch > LRKV_MAX_PAGE_BATCH)
+        return fail(LRKV_ERR_INVALID_ARG, "batch %d (0..%d)", batch, LRKV_MAX_PAGE_BATCH);
+    if (max_blocks < 1 || (long long)max_blocks * 64 > (1LL << 30))
+        return fail(LRKV_ERR_INVALID_ARG, "max_blocks_per_seq %d", max_blocks);
+    if (batch > 0 && (!table || !lens)) return fail(LRKV_ERR_INVALID_ARG, "block_table or seq_lens is NULL");
+    return LRKV_OK;
+}
+
+static lrkv_status check_refs(const int32_t* refs, int32_t num_blocks) {
+    if (num_blocks < 1 || num_blocks > (1 << 24))
+        return fail(LRKV_ERR_INVALID_ARG, "num_blocks %d outside [1, 2^24]", num_blocks);
+    LRKV_REQUIRE_PTR(refs);
+    return LRKV_OK;
+}
+
+lrkv_status lrkv_pages_reserve(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* new_tokens, int32_t batch,
+                               uint32_t* status_dev, void* stream) {
+    lrkv_status s = check_refs(refs, num_blocks);
+    if (s != LRKV_OK || (s = check_table(block_table, max_blocks_per_seq, seq_lens, batch)) != LRKV_OK) return s;
+    if (batch == 0) return ok();
+    if (!new_tokens) return fail(LRKV_ERR_INVALID_ARG, "new_tokens is NULL");
+    const lrkv::PageArgs a{refs, block_table, const_cast<int32_t*>(seq_lens), nullptr, new_tokens, status_dev, num_blocks,
+                           max_blocks_per_seq, batch, batch};
+    return cuda_status(lrkv::launch_pages_reserve(a, static_cast<cudaStream_t>(stream)), "lrkv_pages_reserve launch");
+}
+
+lrkv_status lrkv_pages_fork(const lrkv_pools* pools, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
+                            int32_t* seq_lens, int32_t batch, const int32_t* parents, const int32_t* children,
+                            int32_t n, uint32_t* status_dev, void* stream) {
+    lrkv::PoolArgs p;
+    lrkv_status s = check_pools(pools, &p);
+    if (s != LRKV_OK || (s = check_refs(refs, pools->num_blocks)) != LRKV_OK ||
+        (s = check_table(block_table, max_blocks_per_seq, seq_lens, batch)) != LRKV_OK)
+        return s;
+    if (n < 0 || n > LRKV_MAX_PAGE_BATCH) return fail(LRKV_ERR_INVALID_ARG, "n %d (0..%d)", n, LRKV_MAX_PAGE_BATCH);
+    if (n == 0) return ok();
+    if (batch == 0) return fail(LRKV_ERR_INVALID_ARG, "batch 0");
+    if (!parents || !children) return fail(LRKV_ERR_INVALID_ARG, "parents or children is NULL");
+    const lrkv::PageArgs a{refs, block_table, seq_lens, parents, children, status_dev, pools->num_blocks,
+                           max_blocks_per_seq, batch, n};
+    return cuda_status(lrkv::launch_pages_fork(p, a, static_cast<cudaStream_t>(stream)), "lrkv_pages_fork launch");
+}
+
+lrkv_status lrkv_pages_free(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
+                            int32_t* seq_lens, int32_t batch, const int32_t* seqs, int32_t n,
+                            const int32_t* keep_lens, uint32_t* status_dev, void* stream) {
+    lrkv_status s = check_refs(refs, num_blocks);
+    if (s != LRKV_OK || (s = check_table(block_table, max_blocks_per_seq, seq_lens, batch)) != LRKV_OK) return s;
+    if (n < 0 || n > LRKV_MAX_PAGE_BATCH) return fail(LRKV_ERR_INVALID_ARG, "n %d (0..%d)", n, LRKV_MAX_PAGE_BATCH);
+    if (n == 0) return ok();
+    if (batch == 0) return fail(LRKV_ERR_INVALID_ARG, "batch 0");
+    if (!seqs) return fail(LRKV_ERR_INVALID_ARG, "seqs is NULL");
+    const lrkv::PageArgs a{refs, block_table, seq_lens, seqs, keep_lens, status_dev, num_blocks, max_blocks_per_seq,
+                           batch, n};
+    return cuda_status(lrkv::launch_pages_free(a, static_cast<cudaStream_t>(stream)), "lrkv_pages_free launch");
+}
+
+lrkv_status lrkv_pages_copy(const lrkv_pools* src, const int32_t* src_pages, const lrkv_pools* dst,
+                            const int32_t* dst_pages, int32_t n, uint32_t* status_dev, void* stream) {
+    lrkv::PoolArgs f, t;
+    lrkv_status s = check_pools(src, &f);
+    if (s != LRKV_OK || (s = check_pools(dst, &t)) != LRKV_OK) return s;
+    bool same = f.pools == t.pools && f.layers == t.layers;
+    for (int i = 0; same && i < f.pools; ++i) same = f.u[i] == t.u[i];
+    if (!same) return fail(LRKV_ERR_INVALID_ARG, "src and dst differ in pools, layers or row widths");
+    if (n < 0 || n > (1 << 20)) return fail(LRKV_ERR_INVALID_ARG, "n %d (0..2^20)", n);
+    if (n == 0) return ok();
+    if (!src_pages || !dst_pages) return fail(LRKV_ERR_INVALID_ARG, "src_pages or dst_pages is NULL");
+    return cuda_status(lrkv::launch_pages_copy(f, t, src_pages, dst_pages, n, status_dev,
+                                               static_cast<cudaStream_t>(stream)),
+                       "lrkv_pages_copy launch");
+}
+
+lrkv_status lrkv_cache_compact(const lrkv_pools* pools, const int32_t* block_table, int32_t max_blocks_per_seq,
+                               int32_t* seq_lens, int32_t batch, const int32_t* path, const int32_t* path_lens,
+                               int32_t max_path, int32_t* new_lens, uint32_t* status_dev, void* stream) {
+    lrkv::CompactArgs a{};
+    lrkv_status s = check_pools(pools, &a.p);
+    if (s != LRKV_OK || (s = check_table(block_table, max_blocks_per_seq, seq_lens, batch)) != LRKV_OK) return s;
+    if (max_path < 1 || max_path > 1024) return fail(LRKV_ERR_INVALID_ARG, "max_path %d (1..1024)", max_path);
+    if (batch == 0) return ok();
+    if (!path || !path_lens) return fail(LRKV_ERR_INVALID_ARG, "path or path_lens is NULL");
+    a.table = block_table;
+    a.path = path;
+    a.path_lens = path_lens;
+    a.lens = seq_lens;
+    a.new_lens = new_lens ? new_lens : seq_lens;
+    a.status = status_dev;
+    a.max_pages = max_blocks_per_seq;
+    a.batch = batch;
+    a.max_path = max_path;
+    return cuda_status(lrkv::launch_cache_compact(a, static_cast<cudaStream_t>(stream)), "lrkv_cache_compact launch");
 }
 
 size_t lrkv_prefill_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t Tq) {

@@ -79,6 +79,9 @@ typedef enum lrkv_status {
                                     sequence's output rows are written as zeros */
 #define LRKV_DEV_BAD_SLOT 0x4u   /* slot_mapping entry >= num_blocks * block_size (row skipped) */
 #define LRKV_DEV_TIMEOUT 0x8u    /* a pipeline wait in a kernel gave up after its time limit (about 2 s) */
+#define LRKV_DEV_NO_PAGES 0x10u  /* a sequence asked for more pages than are free and got none */
+#define LRKV_DEV_BAD_INDEX 0x20u /* an index of a sequence or drafted token is out of range, out of order or listed
+                                    twice, or a page with reference count 0 was given back */
 
 /* Model dimensions (frame "LRKV constrains differences between heads"). */
 typedef struct lrkv_dims {
@@ -404,6 +407,189 @@ lrkv_status lrkv_prefix_partials(const lrkv_dims* dims, const void* q, const voi
                                  const int32_t* prefix_blocks, int32_t max_prefix_blocks, const int32_t* prefix_len,
                                  int32_t batch, float* partials, void* workspace, size_t workspace_bytes,
                                  uint32_t* status_dev, void* stream);
+
+/* ======================================================================
+ * Drafted tokens: a step that verifies up to 64 drafted tokens per sequence.
+ *
+ * The drafted tokens' rows are appended behind the sequence's own (lrkv_append, slots seq_lens[b] ..
+ * seq_lens[b] + tree_lens[b] - 1), attended to by lrkv_decode_tree, and the accepted ones moved
+ * together by lrkv_cache_compact; lrkv_pages_reserve and lrkv_pages_free take and give back pages.
+ * ====================================================================== */
+#define LRKV_MAX_TREE 64
+
+/* Workspace bytes of lrkv_decode_tree for `batch` sequences of up to T drafted tokens, on the CURRENT device;
+ * 0 for unsupported sizes. */
+size_t lrkv_decode_tree_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t T);
+
+/*
+ * lrkv_decode_tree -- Eqs. (6)-(7) for several queries per sequence: drafted token i of sequence b
+ *   attends to the seq_lens[b] cached tokens and to those drafted tokens j whose bit is set in
+ *   tree_mask[b][i] (usually its ancestors and itself; any set is allowed):
+ *     out_{i,h} = softmax attention of q_{i,h} over these tokens, as in lrkv_decode.
+ *   A query that sees no token at all gets zeros.
+ *   q          [batch][T][H][d_h + d_rope]  (q^R rotated at the token's depth, e.g. by lrkv_rope)
+ *   seq_lens   [batch] int32 (device), the tokens before the drafted ones; 0 is allowed
+ *   tree_mask  [batch][T] uint64 (device), bit j: drafted token j is seen; bits at and behind
+ *              tree_lens[b] are ignored.  NULL: a chain (token i sees j <= i)
+ *   tree_lens  [batch] int32 (device) drafted tokens, 0..T; rows i >= tree_lens[b] of out are left as they
+ *              were.  NULL: T for every sequence
+ *   out        [batch][T][H][d_h]
+ *   1 <= T <= LRKV_MAX_TREE.  A length or count outside its range (seq_lens[b] + tree_lens[b] beyond the
+ *   table included) sets LRKV_DEV_BAD_SEQLEN and writes zeros to all T rows of that sequence; the tokens
+ *   of a bad page id are left out (LRKV_DEV_BAD_BLOCK).  What a query does not see cannot reach its
+ *   result, whatever bits it holds (NaN and infinities included), and neither can another head's latents.
+ *   Probabilities enter the products with the values in bf16, q~ in two bf16 pieces; sums are fp32.
+ *   Everything else as for lrkv_decode (num_splits is not used); workspace of
+ *   lrkv_decode_tree_workspace_bytes(dims, batch, T) bytes, 256-byte aligned; batch x T at most 65535.
+ */
+lrkv_status lrkv_decode_tree(const lrkv_dims* dims, const void* q, const void* BK, const void* BV,
+                             const lrkv_cache* cache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                             const int32_t* seq_lens, const uint64_t* tree_mask, const int32_t* tree_lens,
+                             int32_t batch, int32_t T, void* out, void* workspace, size_t workspace_bytes,
+                             uint32_t* status_dev, void* stream);
+
+/* ======================================================================
+ * Rotary positions of rows: queries before a decode or prefill, cached positional keys that move.
+ *
+ * Pair i of a head's rotated part (d_rot values) turns by position x f_i and is multiplied by
+ * `magnitude`; f_i = base^(-2i / d_rot), scaled for contexts longer than the base was made for:
+ *   LRKV_ROPE_NONE    as it is (with LRKV_ROPE_INTERLEAVED the rotation that lrkv_append applies)
+ *   LRKV_ROPE_LINEAR  f_i / factor
+ *   LRKV_ROPE_PARTS   g f_i + (1 - g) f_i / factor, g = (original_len f_i / 2 pi - low) / (high - low)
+ *                     clamped to [0, 1]: pairs that turn more than `high` times over original_len
+ *                     positions stay, those that turn less than `low` times are interpolated
+ * ====================================================================== */
+enum { LRKV_ROPE_INTERLEAVED = 0, /* pairs (2i, 2i + 1) */ LRKV_ROPE_HALF = 1 /* pairs (i, i + d_rot / 2) */ };
+enum { LRKV_ROPE_NONE = 0, LRKV_ROPE_LINEAR = 1, LRKV_ROPE_PARTS = 2 };
+enum { LRKV_BF16 = 0, LRKV_FP32 = 1 };
+
+typedef struct lrkv_rope_spec {
+    int32_t d_rot;       /* rotated values of a head: a multiple of 8, 8..256 */
+    int32_t layout;      /* LRKV_ROPE_INTERLEAVED or LRKV_ROPE_HALF */
+    int32_t scaling;     /* LRKV_ROPE_NONE, _LINEAR or _PARTS */
+    int32_t reserved;    /* 0 */
+    double base;         /* > 1; 0 means 10000 */
+    double factor;       /* >= 1 (LINEAR, PARTS) */
+    double original_len; /* > 0 (PARTS) */
+    double low, high;    /* 0 <= low < high (PARTS) */
+    double magnitude;    /* of the rotated values; 0 means 1 */
+} lrkv_rope_spec;
+
+/* A spec's speeds as fractions of a turn (x 2^64), filled in by lrkv_rope_make_plan; host memory, plain data. */
+typedef struct lrkv_rope_plan {
+    int32_t d_rot, layout;
+    float magnitude;
+    int32_t reserved;
+    uint64_t turn[128];
+} lrkv_rope_plan;
+
+/* Host only; no device is touched. */
+lrkv_status lrkv_rope_make_plan(const lrkv_rope_spec* spec, lrkv_rope_plan* plan);
+
+/* Rows of heads: element (row, head, i) at base + row * row_stride + head * head_stride + i (strides in elements). */
+typedef struct lrkv_rows {
+    void* base;           /* device, 16-byte aligned */
+    int64_t num_rows;     /* rows that exist; indices are checked against it */
+    int64_t row_stride, head_stride; /* multiples of 8, >= 0 */
+    const int32_t* index; /* [n] (device): row of the call's i-th item; negative skips it.  NULL: row i */
+} lrkv_rows;
+
+/*
+ * lrkv_rope -- y_i = x_i with values [begin, begin + d_rot) of every head rotated at positions[i], i < n;
+ *   the head's other values (of `width`) are copied, or not touched where x and y are the same rows.
+ *   transpose = 1 applies the transposed rotation (angle -f_i x position, the same magnitude): the
+ *   gradient with respect to x, and the way back where the magnitude is 1.
+ *   positions   [n] int32 (device), any value (negative ones turn back: keys that move by a distance)
+ *   dtype       LRKV_BF16 or LRKV_FP32, of x and y; the angle is exact modulo a turn to 2^-32 of it for any
+ *               position, sine and cosine fp32, the products fp32 and rounded once
+ *   width, begin  multiples of 8, begin + d_rot <= width <= 1024;  1 <= heads <= 65535
+ *   x and y may be the same rows (equal struct contents: in place); otherwise no row may be read for one
+ *   item and written for another.  Rows written by a call must differ from one another, and y's strides
+ *   must keep its rows and heads apart.  An index at or beyond num_rows sets LRKV_DEV_BAD_SLOT and
+ *   skips the item.  n == 0 is a no-op.
+ */
+lrkv_status lrkv_rope(const lrkv_rope_plan* plan, int32_t dtype, int32_t n, int32_t heads, int32_t width,
+                      int32_t begin, const lrkv_rows* x, const lrkv_rows* y, const int32_t* positions,
+                      int32_t transpose, uint32_t* status_dev, void* stream);
+
+/* ======================================================================
+ * Pages: taken, shared, copied and given back on the device, in order of the stream.
+ *
+ * refs [num_blocks] int32 (device, caller-owned, zeroed at first) counts for each page the table entries
+ * that name it.  A page with count 0 is free.  A sequence's pages are the leading entries >= 0 of its row
+ * of the block table; the entries behind them are -1.  Free pages are taken lowest first, by the
+ * sequences in the order of the call, so the outcome does not depend on timing.  Counts may be raised
+ * by the caller to keep pages (a shared prefix).  Calls on the same refs or tables must not overlap.
+ * ====================================================================== */
+#define LRKV_MAX_POOLS 4
+#define LRKV_MAX_PAGE_BATCH 8192
+
+/* Pools whose rows move together: the four of an lrkv_cache, the rows of an lrkv_quant_cache, the rows of a latent
+ * cache, in one or several layers.  Token row t of layer l is row_bytes[p] bytes at base[p] + l layer_bytes[p] +
+ * t row_bytes[p]. */
+typedef struct lrkv_pools {
+    void* base[LRKV_MAX_POOLS];          /* 16-byte aligned */
+    int64_t row_bytes[LRKV_MAX_POOLS];   /* multiples of 16 */
+    int64_t layer_bytes[LRKV_MAX_POOLS]; /* multiples of 16, >= num_blocks x 64 rows; not used with one layer */
+    int32_t num_pools, num_layers, num_blocks;
+} lrkv_pools;
+
+/*
+ * lrkv_pages_reserve -- pages for seq_lens[b] + new_tokens[b] tokens of every sequence: the empty entries below
+ *   ceil((seq_lens[b] + new_tokens[b]) / 64) of its row are filled.  A sequence for whose pages too few are
+ *   left gets none (LRKV_DEV_NO_PAGES) and the next one is tried; one that asks for more than its row
+ *   holds, or a negative length or count, gets none (LRKV_DEV_BAD_SEQLEN).
+ */
+lrkv_status lrkv_pages_reserve(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* new_tokens, int32_t batch,
+                               uint32_t* status_dev, void* stream);
+
+/*
+ * lrkv_pages_fork -- sequence children[i] becomes a copy of sequence parents[i], i < n: what it held before is given
+ *   back, its row names the parent's full pages (counts raised), and the rows of the parent's last, partly
+ *   filled page are copied to a page of its own, in all pools and layers; seq_lens[child] = seq_lens[parent].
+ *   Pages that the parent holds behind its length are not passed on.
+ *   Where no page is left for a partly filled one, the child is left empty with length 0 (LRKV_DEV_NO_PAGES).
+ *   An index out of range, a child listed twice or also listed as a parent sets LRKV_DEV_BAD_INDEX and
+ *   that fork is left out; a parent's length outside its row LRKV_DEV_BAD_SEQLEN; a bad page id in the
+ *   part of its row that is passed on LRKV_DEV_BAD_BLOCK (either leaves the fork out).
+ */
+lrkv_status lrkv_pages_fork(const lrkv_pools* pools, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
+                            int32_t* seq_lens, int32_t batch, const int32_t* parents, const int32_t* children,
+                            int32_t n, uint32_t* status_dev, void* stream);
+
+/*
+ * lrkv_pages_free -- sequences seqs[i], i < n, give back their pages behind the first ceil(keep_lens[seqs[i]] / 64)
+ *   (keep_lens [batch], or NULL: all of them): entries become -1, counts go down, and seq_lens becomes
+ *   min(seq_lens, keep_lens) (0).  A sequence listed twice gives its pages back once.  A page with count 0
+ *   keeps it and sets LRKV_DEV_BAD_INDEX, as does a sequence out of range; a negative keep length sets
+ *   LRKV_DEV_BAD_SEQLEN and leaves that sequence alone.
+ */
+lrkv_status lrkv_pages_free(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
+                            int32_t* seq_lens, int32_t batch, const int32_t* seqs, int32_t n,
+                            const int32_t* keep_lens, uint32_t* status_dev, void* stream);
+
+/*
+ * lrkv_pages_copy -- page src_pages[i] of src to page dst_pages[i] of dst, i < n, in all pools and layers (both
+ *   described alike: pools, layers, row widths).  Pages written must differ from one another and from all
+ *   pages read.  A negative id skips the page, one at or beyond num_blocks sets LRKV_DEV_BAD_BLOCK.
+ */
+lrkv_status lrkv_pages_copy(const lrkv_pools* src, const int32_t* src_pages, const lrkv_pools* dst,
+                            const int32_t* dst_pages, int32_t n, uint32_t* status_dev, void* stream);
+
+/*
+ * lrkv_cache_compact -- keep the accepted ones of the tokens behind a sequence's length: row seq_lens[b] + path[b][i]
+ *   moves to row seq_lens[b] + i, i < path_lens[b], in all pools and layers, and
+ *   new_lens[b] = seq_lens[b] + path_lens[b]  (new_lens == NULL or == seq_lens: in place).
+ *   path      [batch][max_path] int32 (device), strictly increasing and >= 0;  1 <= max_path <= 1024
+ *   path_lens [batch] int32 (device), 0..max_path
+ *   A path that is out of order, out of range or longer than max_path sets LRKV_DEV_BAD_INDEX, rows beyond
+ *   the table or a negative length LRKV_DEV_BAD_SEQLEN, a bad page id LRKV_DEV_BAD_BLOCK; that sequence's
+ *   rows stay as they are and new_lens[b] = seq_lens[b].
+ */
+lrkv_status lrkv_cache_compact(const lrkv_pools* pools, const int32_t* block_table, int32_t max_blocks_per_seq,
+                               int32_t* seq_lens, int32_t batch, const int32_t* path, const int32_t* path_lens,
+                               int32_t max_path, int32_t* new_lens, uint32_t* status_dev, void* stream);
 
 /* Workspace bytes lrkv_prefill needs (0 today; kept so callers size it). */
 size_t lrkv_prefill_workspace_bytes(const lrkv_dims* dims, int32_t batch, int32_t Tq);
