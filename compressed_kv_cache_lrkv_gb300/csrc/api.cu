@@ -908,8 +908,18 @@ lrkv_status lrkv_decode_tree(const lrkv_dims* dims, const void* q, const void* B
         return fail(LRKV_ERR_INVALID_ARG, "workspace NULL or not 256-byte aligned");
     if (workspace_bytes < need)
         return fail(LRKV_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", workspace_bytes, need);
-    return cuda_status(lrkv::launch_tree(a, dims->d_h, dims->r, dims->d_rope, workspace, di.sms,
-                                         static_cast<cudaStream_t>(stream)),
+    lrkv::tree_carve_workspace(&a, workspace, dims->d_h, dims->r, dims->d_rope, di.sms);
+    lrkv::TreeMaps mp;
+    const uint64_t dh = (uint64_t)dims->d_h, dk = dh + (uint64_t)dims->d_rope, HR = (uint64_t)dims->H * dims->r;
+    const uint64_t rows = (uint64_t)cache->num_blocks * dims->block_size;
+    const uint32_t zbox = a.zw == 32 ? 32 : 64;
+    const CUtensorMapSwizzle zswz = a.zw == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if ((s = make_tmap(&mp.sK, cache->sK, dk, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "sK")) != LRKV_OK ||
+        (s = make_tmap(&mp.sV, cache->sV, dh, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "sV")) != LRKV_OK ||
+        (s = make_tmap(&mp.zK, cache->zK, HR, rows, zbox, 64, zswz, "zK")) != LRKV_OK ||
+        (s = make_tmap(&mp.zV, cache->zV, HR, rows, zbox, 64, zswz, "zV")) != LRKV_OK)
+        return s;
+    return cuda_status(lrkv::launch_tree(mp, a, dims->d_h, dims->r, dims->d_rope, static_cast<cudaStream_t>(stream)),
                        "lrkv_decode_tree launch");
 }
 

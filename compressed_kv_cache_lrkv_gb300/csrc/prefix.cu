@@ -29,17 +29,11 @@
 
 #include "lrkv_internal.cuh"
 #include "prefix.h"
+#include "tile_attn.cuh"
 
 namespace lrkv {
 
 namespace {
-
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-__device__ __forceinline__ void named_bar(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
@@ -76,50 +70,6 @@ struct PxLayout {
     static constexpr uint32_t TM_S = 0, TM_P = 64, TM_O = 128, TM_Q = TM_O + D_H + ZW;
     static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
 };
-
-__device__ __forceinline__ uint64_t kdesc128(uint32_t a) { return sdesc(a, 16, 1024, 2); }
-__device__ __forceinline__ uint64_t mndesc128(uint32_t a) { return sdesc(a, 8192, 1024, 2); }
-
-// Wait of a role, with the call's limit, and one for what the block has in flight, with the full limit.
-__device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const DecodeArgs& d) {
-    const bool ok = mbar_look_wait(bar, parity, d.status, d.wait_ns);
-    return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* status) {
-    mbar_wait(bar, parity, status);
-    __syncwarp();
-}
-
-// max(a, b), NaN where either is one.
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-    return y;
-}
-
-// n (a multiple of 8) products of bf16 a with bf16 b, or of fp32 a, summed in fp32.
-__device__ __forceinline__ float dot8(const uint16_t* a, const uint16_t* b, int n) {
-    float s = 0.f;
-#pragma unroll 1
-    for (int i = 0; i < n; i += 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(a + i), y = *reinterpret_cast<const uint4*>(b + i);
-        s = fmaf(bf16lo(x.x), bf16lo(y.x), fmaf(bf16hi(x.x), bf16hi(y.x), s));
-        s = fmaf(bf16lo(x.y), bf16lo(y.y), fmaf(bf16hi(x.y), bf16hi(y.y), s));
-        s = fmaf(bf16lo(x.z), bf16lo(y.z), fmaf(bf16hi(x.z), bf16hi(y.z), s));
-        s = fmaf(bf16lo(x.w), bf16lo(y.w), fmaf(bf16hi(x.w), bf16hi(y.w), s));
-    }
-    return s;
-}
-__device__ __forceinline__ float dot8(const float* a, const uint16_t* b, int n) {
-    float s = 0.f;
-#pragma unroll 1
-    for (int i = 0; i < n; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(a + i);
-        const uint2 y = *reinterpret_cast<const uint2*>(b + i);
-        s = fmaf(x.x, bf16lo(y.x), fmaf(x.y, bf16hi(y.x), fmaf(x.z, bf16lo(y.y), fmaf(x.w, bf16hi(y.y), s))));
-    }
-    return s;
-}
 
 constexpr int lcm2(int n) { return n % 2 ? 2 * n : n; }
 
@@ -824,24 +774,6 @@ void prefix_carve_workspace(PrefixArgs* a, void* ws, int D_H, int R) {
     a->ml = static_cast<float*>(ws);
     a->acc = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                       align256((size_t)a->d.B * a->d.H * a->nsplit * 2 * sizeof(float)));
-}
-
-// A launch that may start before the one before it on the stream has ended (programmatic dependent
-// launch): the kernels wait for it where they first read what it writes, and in every block.
-template <typename... Args>
-static cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                                    Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int D_H, int D_R, int ZW>

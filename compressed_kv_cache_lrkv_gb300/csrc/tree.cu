@@ -2,96 +2,847 @@
 // tokens and the drafted ones of its mask.
 //     s_t = ([q | q^R] . [s^K_t | k^R_t] + (q B_h^K) . z^K_{h,t}) scale,  p = softmax over what is seen,
 //     out = sum p_t s^V_t + B_h^V sum p_t z^V_{h,t}
+//
+// The cached rows are the same for all heads and drafted tokens, so 128 query rows, hb heads x ns tokens of one
+// sequence, are one attention tile of width d_h + zw, zw = hb r (as in prefix.cu, there over sequences):
+//     S = [Q | diag(Q~)] . [s^K | z^K of the hb heads]^T,   O += P . [s^V | z^V of the hb heads]
+// on tcgen05, M = 128, 64 tokens (a page) at a time.
 #include "lrkv_internal.cuh"
+#include "tile_attn.cuh"
 #include "tree.h"
 
 namespace lrkv {
 
 namespace {
 
-// One block per (head, query), four warps that take every fourth token, a lane's share of the features each.
-__global__ void __launch_bounds__(128) tree_kernel(const TreeArgs a, const int D_H, const int R, const int D_R) {
+constexpr int kThreads = 384;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.
+constexpr int kStartPages = 4;
+
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ uint64_t kdesc64(uint32_t a) { return sdesc(a, 16, 512, 4); }
+__device__ __forceinline__ uint64_t mndesc64(uint32_t a) { return sdesc(a, 16, 512, 4); }
+
+// [Q | diag(Q~)] is the A operand of S, diag(Q~) as two bf16 pieces (q~ rounded, and what that left). As many of
+// its 64-column blocks as fit sit in TMEM, the rest in shared memory, beside rings of key stages
+// [64 tokens][D_K + ZW] and value stages [64][D_H + ZW].
+// TMEM columns: two S buffers of 64 columns (P, two bf16 a column, is written over the first half of its own S), O, Q.
+template <int D_H, int D_R, int ZW>
+struct TrLayout {
+    static constexpr int D_K = D_H + D_R;
+    static constexpr int ZBLK = ZW == 32 ? 1 : ZW / 64;                 // blocks of latents in a stage
+    static constexpr uint32_t ZBLK_BYTES = ZW == 32 ? 4096 : 8192;
+    static constexpr uint32_t K_BYTES = D_K / 64 * 8192 + ZBLK * ZBLK_BYTES, V_BYTES = D_H / 64 * 8192 + ZBLK * ZBLK_BYTES;
+    static constexpr int NBQ = (D_K + 2 * ZW) / 64, QROOM = (384 - D_H - ZW) / 32;
+    static constexpr int QBT = NBQ < QROOM ? NBQ : QROOM, QBS = NBQ - QBT;  // blocks in TMEM, in shared memory
+    static constexpr uint32_t Q_BYTES = QBS * 16384;
+    static constexpr uint32_t ROOM = 232448 - 1024 - 4096 - Q_BYTES;
+    static constexpr int BOTH = ROOM / (K_BYTES + V_BYTES);
+    static constexpr int VST = BOTH > 6 ? 6 : BOTH;
+    static constexpr int KST = VST < 6 && ROOM - VST * (K_BYTES + V_BYTES) >= K_BYTES ? VST + 1 : VST;
+    static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
+    static constexpr uint32_t OFF_ROW = OFF_BAR + 512;  // 128 references, then 2 x 128 (sum, reference)
+    static constexpr uint32_t SMEM = OFF_ROW + 512 + 2048 + 1024;
+    static_assert(VST >= 2 && SMEM <= 232448, "stages");
+    static constexpr uint32_t TM_S = 0, TM_O = 128, TM_Q = TM_O + D_H + ZW;
+    static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
+};
+
+// Lengths of sequence b: tokens before the drafted ones, drafted tokens, pages (0: nothing to do, or a bad length).
+struct Seq {
+    int L, n, pages;
+    bool bad;
+};
+__device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b) {
+    Seq s;
+    s.L = a.d.seq_lens[b];
+    s.n = a.tree_lens ? a.tree_lens[b] : a.T;
+    s.bad = s.L < 0 || s.n < 0 || s.n > a.T || (long long)s.L + s.n > (long long)a.d.max_pages * kBlockSize;
+    if (s.bad) s.L = s.n = 0;
+    s.pages = s.n > 0 ? (s.L + s.n + kBlockSize - 1) / kBlockSize : 0;
+    return s;
+}
+// Tiles of a sequence with n drafted tokens, and its units of work.
+__device__ __forceinline__ int tiles_of(const TreeArgs& a, int n) { return (n + a.ns - 1) / a.ns * a.htiles; }
+__device__ __forceinline__ long long units_of(const TreeArgs& a, const Seq& s) {
+    return s.pages ? (long long)tiles_of(a, s.n) * (s.pages + kStartPages) : 0;
+}
+
+// The work: the tiles of all sequences one after the other, a tile's pages and then kStartPages empty units, cut into
+// `ranges` equal ranges, one per CTA.  A piece is what a range holds of a tile's pages; piece (range, tile) leaves
+// its partials at slot range + tile number, which is different for all pieces and consecutive for a tile's.
+struct Work {
+    long long total;
+    int ranges;  // (no range is empty, so a tile's pieces are in consecutive ones)
+    __device__ __forceinline__ Work(long long units, int ctas)
+        : total(units), ranges(units < ctas ? (units > 0 ? (int)units : 1) : ctas) {}
+    __device__ __forceinline__ long long start(int c) const { return c < ranges ? total * c / ranges : total; }
+    __device__ __forceinline__ int range_of(long long u) const { return (int)(((u + 1) * ranges - 1) / total); }
+};
+
+// Walks the pieces of one range.
+struct Walk {
+    long long hi, u, seg;  // end of the range, the next unit to look at, first unit of tile t
+    int b, t;              // sequence, and tile of it
+    Seq s;
+    // the piece
+    int p0, nt;  // pages [p0, p0 + nt) of the sequence
+
+    __device__ __forceinline__ void begin(const TreeArgs& a, long long lo, long long hi_, int b0, long long base) {
+        hi = hi_;
+        u = lo;
+        b = b0;
+        s = b < a.batch ? seq_of(a, b) : Seq{0, 0, 0, false};
+        t = s.pages ? (int)((lo - base) / (s.pages + kStartPages)) : 0;
+        seg = base + (long long)t * (s.pages + kStartPages);
+    }
+    __device__ __forceinline__ bool next(const TreeArgs& a) {
+        while (u < hi && b < a.batch) {
+            const long long end = seg + s.pages + kStartPages;
+            if (s.pages == 0 || t >= tiles_of(a, s.n)) {
+                if (++b < a.batch) s = seq_of(a, b);
+                t = 0;
+                continue;
+            }
+            const int from = (int)(u - seg), to = (int)((hi < end ? hi : end) - seg);
+            p0 = from;
+            nt = (to < s.pages ? to : s.pages) - from;
+            if (nt > 0) return true;
+            step();
+        }
+        return false;
+    }
+    __device__ __forceinline__ void step() {  // behind the tile of the present piece
+        seg += s.pages + kStartPages;
+        u = seg;
+        ++t;
+    }
+};
+
+template <int D_H, int D_R, int ZW>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_scan_kernel(const __grid_constant__ TreeMaps m, const __grid_constant__ TreeArgs a, const int R) {
+    using Lay = TrLayout<D_H, D_R, ZW>;
+    constexpr int D_K = Lay::D_K, NBQ = Lay::NBQ, KST = Lay::KST, VST = Lay::VST;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
+    const uint32_t S0 = smem_u32(smem);
     const DecodeArgs& d = a.d;
-    const int h = blockIdx.x, b = blockIdx.y / a.T, i = blockIdx.y - b * a.T;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int D_K = D_H + D_R, W = D_H + R;
-    __shared__ float q[192], qt[32], sm[4], sl[4], acc_s[4][160], o[160];
-    const int L = d.seq_lens[b], n = a.tree_lens ? a.tree_lens[b] : a.T;
-    const size_t row = ((size_t)b * a.T + i) * d.H + h;
-    uint16_t* out = d.out + row * D_H;
-    if (L < 0 || n < 0 || n > a.T || (long long)L + n > (long long)d.max_pages * kBlockSize) {
-        if (threadIdx.x == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
-        for (int c = threadIdx.x; c < D_H; c += 128) out[c] = 0;
-        return;
-    }
-    if (i >= n) return;
-    for (int c = threadIdx.x; c < D_K; c += 128) q[c] = __uint_as_float((uint32_t)d.q[row * D_K + c] << 16);
-    __syncthreads();
-    if (threadIdx.x < R) {
-        float s = 0.f;
-        for (int c = 0; c < D_H; ++c)
-            s = fmaf(q[c], __uint_as_float((uint32_t)d.BK[((size_t)h * D_H + c) * R + threadIdx.x] << 16), s);
-        qt[threadIdx.x] = s;
-    }
-    __syncthreads();
-    const unsigned long long mask = a.mask ? a.mask[(size_t)b * a.T + i] : ~0ull >> (63 - i);
-    float m = -INFINITY, l = 0.f, acc[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int t = warp; t < L + n; t += 4) {
-        if (t >= L && !(mask >> (t - L) & 1)) continue;
-        const int page = d.block_table[(size_t)b * d.max_pages + t / kBlockSize];
-        if (page < 0 || page >= d.num_blocks) {
-            if (lane == 0) set_status(d.status, LRKV_DEV_BAD_BLOCK);
-            continue;
+    const int H = d.H, W = D_H + R;
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
+    uint64_t* q_ready = bars + 0;   // Q of a piece written, O of the piece before it read
+    uint64_t* s_full = bars + 1;    // [2] S_g computed (g: pages of this CTA, counted through; buffer g % 2)
+    uint64_t* p_full = bars + 3;    // [2] P_g written
+    uint64_t* o_done = bars + 5;    // [2] P_g V_g complete
+    uint64_t* mma_drain = bars + 7;
+    uint64_t* k_full = bars + 8;    // [6]
+    uint64_t* k_empty = bars + 14;
+    uint64_t* v_full = bars + 20;
+    uint64_t* v_empty = bars + 26;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
+    volatile int* abort_flag = reinterpret_cast<int*>(bars + 33);
+    unsigned long long* poison = reinterpret_cast<unsigned long long*>(bars + 34);  // [2], by the piece's parity
+    long long* plan = reinterpret_cast<long long*>(bars + 36);                      // total, first sequence, its base
+    auto B = [&](uint64_t* p) { return smem_u32(p); };
+    auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
+
+    if (threadIdx.x == 32) {
+        mbar_init(B(q_ready), 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(B(s_full + i), 1);
+            mbar_init(B(p_full + i), 128);
+            mbar_init(B(o_done + i), 1);
+            poison[i] = 0;
         }
-        const size_t slot = (size_t)page * kBlockSize + t % kBlockSize;
-        auto val = [](uint16_t x) { return __uint_as_float((uint32_t)x << 16); };
-        float s = 0.f;
-        for (int c = lane; c < D_K; c += 32) s = fmaf(q[c], val(a.sK[slot * D_K + c]), s);
-        if (lane < R) s = fmaf(qt[lane], val(a.zK[(slot * d.H + h) * R + lane]), s);
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= d.scale_log2;
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - mn), p = exp2f(s - mn);
-        m = mn;
-        l = l * f + p;
-        for (int e = 0; e < 5; ++e) {
-            const int c = e * 32 + lane;
-            if (c >= W) break;
-            const float v = val(c < D_H ? a.sV[slot * D_H + c] : a.zV[(slot * d.H + h) * R + c - D_H]);
-            acc[e] = fmaf(p, v, acc[e] * f);
+        mbar_init(B(mma_drain), 1);
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(B(k_full + i), 1);
+            mbar_init(B(k_empty + i), 1);
+            mbar_init(B(v_full + i), 1);
+            mbar_init(B(v_empty + i), 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        // the units of all sequences, and the sequence that holds this range's first
+        long long total = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+            long long v = b0 + lane < a.batch ? units_of(a, seq_of(a, b0 + lane)) : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            total += v;
+        }
+        const Work w(total, a.ctas);
+        const long long lo = w.start(blockIdx.x);
+        long long base = 0;
+        int first = a.batch;
+        for (int b0 = 0; b0 < a.batch && first == a.batch; b0 += 32) {
+            const long long v = b0 + lane < a.batch ? units_of(a, seq_of(a, b0 + lane)) : 0;
+            long long incl = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            const unsigned holds = __ballot_sync(0xffffffffu, base + incl > lo);
+            if (holds) {
+                const int l = __ffs(holds) - 1;
+                first = b0 + l;
+                base += __shfl_sync(0xffffffffu, incl - v, l);
+            } else {
+                base += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+        if (lane == 0) {
+            plan[0] = total;
+            plan[1] = first;
+            plan[2] = base;
         }
     }
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-    for (int e = 0; e < 5; ++e)
-        if (e * 32 + lane < W) acc_s[warp][e * 32 + lane] = acc[e];
+    __syncwarp();
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
     __syncthreads();
-    const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float ls = 0.f, w[4];
-    for (int k = 0; k < 4; ++k) {
-        w[k] = sm[k] == -INFINITY ? 0.f : exp2f(sm[k] - M);
-        ls = fmaf(w[k], sl[k], ls);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Work work(plan[0], a.ctas);
+    Walk w;
+    w.begin(a, work.start(blockIdx.x), work.start(blockIdx.x + 1), (int)plan[1], plan[2]);
+
+    const bool keys = warp == 0;  // (of the two producers)
+    int issued = 0;               // stages a producer has filled
+    if (warp == 0 || warp == 6) {
+        // ---------------------------------------------------------------- TMA producers
+        const int oob_row = d.num_blocks * kBlockSize;  // whole box out of bounds: zeros
+        const int depth = keys ? KST : VST;
+        const uint32_t stage_bytes = keys ? Lay::K_BYTES : Lay::V_BYTES;
+        const int nblk = keys ? D_K / 64 : D_H / 64;
+        uint64_t* full = keys ? k_full : v_full;
+        uint64_t* empty = keys ? k_empty : v_empty;
+        const CUtensorMap* ms = keys ? &m.sK : &m.sV;
+        const CUtensorMap* mz = keys ? &m.zK : &m.zV;
+        const uint32_t ring = S0 + (keys ? Lay::OFF_K : Lay::OFF_V);
+        if (lane == 0) {
+            prefetch_tmap(ms);
+            prefetch_tmap(mz);
+        }
+        int st = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (; ok && w.next(a); w.step()) {
+            const int32_t* pages = d.block_table + (size_t)w.b * d.max_pages + w.p0;
+            const int x0 = w.t / ((w.s.n + a.ns - 1) / a.ns) * ZW;
+            auto fetch = [&](int i) {
+                int r = oob_row;
+                if (i < w.nt) {
+                    const int blk = pages[i];
+                    if (blk >= 0 && blk < d.num_blocks)
+                        r = blk * kBlockSize;
+                    else
+                        set_status(d.status, LRKV_DEV_BAD_BLOCK);
+                }
+                return r;
+            };
+            int cur = fetch(lane), nxt = fetch(32 + lane);
+            for (int j = 0; j < w.nt; ++j) {
+                if (j > 0 && (j & 31) == 0) {
+                    cur = nxt;
+                    nxt = fetch(j + 32 + lane);
+                }
+                const int prow = __shfl_sync(0xffffffffu, cur, j & 31);
+                if ((issued >= depth && !wait_role(B(empty + st), phase, d)) || aborted()) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    uint32_t dst = ring + st * stage_bytes;
+                    const uint32_t bar = B(full + st);
+                    mbar_arrive_expect_tx(bar, stage_bytes);
+                    for (int bk = 0; bk < nblk; ++bk, dst += 8192) tma_load_2d(dst, ms, 64 * bk, prow, bar);
+                    for (int bk = 0; bk < Lay::ZBLK; ++bk, dst += Lay::ZBLK_BYTES)
+                        tma_load_2d(dst, mz, x0 + 64 * bk, prow, bar);
+                }
+                __syncwarp();
+                ++issued;
+                if (++st == depth) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMAs
+        // One warp issues all of them, so they run in this order: S_0 S_1 | P_0 V_0, S_2 | P_1 V_1, S_3 | ...  S_{g+2}
+        // overwrites the buffer that P_g V_g has read; while the rows work on S_g, P_{g-1} V_{g-1} and S_{g+1} run.
+        constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
+        constexpr uint32_t id_PV = idesc_bf16_f32(128, ZW == 32 ? D_H : D_H + ZW) | (1u << 16);  // B is MN-major
+        constexpr uint32_t id_PZ = idesc_bf16_f32(128, 32) | (1u << 16);
+        const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K), dKz = kdesc64(S0 + Lay::OFF_K + D_K / 64 * 8192);
+        const uint64_t dV = mndesc128(S0 + Lay::OFF_V), dVz = mndesc64(S0 + Lay::OFF_V + D_H / 64 * 8192);
+        int kst = 0, vst = 0;
+        uint32_t kphase = 0, vphase = 0, qphase = 0;
+        int gs = 0, gp = 0;  // pages whose S, whose P V has been issued
+        auto s_tile = [&]() -> bool {
+            if (aborted() || !wait_role(B(k_full + kst), kphase, d)) return false;
+            tc_fence_after();
+            const uint64_t so = (uint64_t)(kst * (Lay::K_BYTES >> 4));
+            const uint32_t ts = tmem + Lay::TM_S + (gs & 1) * 64;
+#pragma unroll
+            for (int kk = 0; kk < NBQ * 4; ++kk) {
+                // 16 columns of Q; q's against s^K, both pieces of q~ against the same z^K
+                const int col = kk * 16, z = (col - D_K) % ZW;
+                uint64_t bd;
+                if (col < D_K)
+                    bd = dK + so + ((col / 64 * 8192 + col % 64 * 2) >> 4);
+                else if (ZW == 32)
+                    bd = dKz + so + (z * 2 >> 4);
+                else
+                    bd = dK + so + (((D_K + z) / 64 * 8192 + z % 64 * 2) >> 4);
+                if (elect_one_sync()) {
+                    if (kk < Lay::QBT * 4)
+                        tc_mma_bf16_ts(ts, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
+                    else
+                        tc_mma_bf16(ts, dQ + ((((kk >> 2) - Lay::QBT) * 16384 + (kk & 3) * 32) >> 4), bd, id_S, 1);
+                }
+            }
+            if (elect_one_sync()) {
+                tc_commit(B(s_full + (gs & 1)));
+                tc_commit(B(k_empty + kst));
+            }
+            __syncwarp();
+            ++gs;
+            if (++kst == KST) {
+                kst = 0;
+                kphase ^= 1;
+            }
+            return true;
+        };
+        auto pv_tile = [&](bool first) -> bool {
+            if (aborted() || !wait_role(B(p_full + (gp & 1)), (gp >> 1) & 1, d) || !wait_role(B(v_full + vst), vphase, d))
+                return false;
+            tc_fence_after();
+            const uint64_t so = (uint64_t)(vst * (Lay::V_BYTES >> 4));
+            const uint32_t tp = tmem + Lay::TM_S + (gp & 1) * 64;
+#pragma unroll
+            for (int kk = 0; kk < kBlockSize / 16; ++kk)
+                if (elect_one_sync()) {
+                    tc_mma_bf16_ts(tmem + Lay::TM_O, tp + kk * 8, dV + so + (kk * 2048 >> 4), id_PV, !first || kk > 0);
+                    if (ZW == 32)
+                        tc_mma_bf16_ts(tmem + Lay::TM_O + D_H, tp + kk * 8, dVz + so + (kk * 1024 >> 4), id_PZ,
+                                       !first || kk > 0);
+                }
+            if (elect_one_sync()) {
+                tc_commit(B(o_done + (gp & 1)));
+                tc_commit(B(v_empty + vst));
+            }
+            __syncwarp();
+            ++gp;
+            if (++vst == VST) {
+                vst = 0;
+                vphase ^= 1;
+            }
+            return true;
+        };
+        bool ok = true;
+        for (; ok && w.next(a); w.step()) {
+            ok = wait_role(B(q_ready), qphase, d);
+            qphase ^= 1;
+            tc_fence_after();
+            ok = ok && s_tile() && (w.nt < 2 || s_tile());
+            for (int j = 0; ok && j < w.nt; ++j) ok = pv_tile(j == 0) && (j + 2 >= w.nt || s_tile());
+        }
+        if (!ok) *abort_flag = 1;
+        // every MMA this warp issued has finished before the CTA tears TMEM down
+        if (elect_one_sync()) tc_commit(B(mma_drain));
+        __syncwarp();
+        drain(B(mma_drain), 0, d.status);
+    } else if (warp != 7) {
+        // ---------------------------------------------------------------- query rows: softmax, partials
+        // Two groups of four warps, a query row per thread in each; group g % 2 takes page g.  The reference maximum
+        // goes from page to page, so a group decides on it once the other has for the page before; the exponentials of
+        // two pages run side by side.
+        const int qq = warp & 3, half = warp >> 3;  // TMEM lanes 32 qq ..
+        const int row = qq * 32 + lane;
+        const uint32_t tl = (uint32_t)(qq * 32) << 16;
+        const int hl = row / a.ns, il = row - hl * a.ns;
+        volatile float* const refs = reinterpret_cast<float*>(smem + Lay::OFF_ROW);
+        float2* const sums = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
+        bool ok = true, waited = false;
+        int g = 0, piece = 0;
+        bool have = w.next(a);
+        while (have) {
+            const int b = w.b, L = w.s.L, n = w.s.n, st_b = (n + a.ns - 1) / a.ns;
+            const int h = w.t / st_b * a.hb + hl, i = w.t % st_b * a.ns + il;
+            const bool live = h < H && i < n;
+            const size_t qr = live ? ((size_t)b * a.T + i) * H + h : 0;
+            const int slot = blockIdx.x + b * a.tmax + w.t;
+            const int p0 = w.p0, nt = w.nt;
+            // the drafted tokens that the row sees
+            unsigned long long tree = ~0ull >> (64 - n);  // (n >= 1)
+            if (live) tree &= a.mask ? a.mask[(size_t)b * a.T + i] : ~0ull >> (63 - i);
+            if (p0 == 0 && warp == 2 && lane == 0) {
+                const int last = work.range_of(w.seg + w.s.pages - 1);
+                a.seg_table[b * a.tmax + w.t] = make_int2(slot, last - (int)blockIdx.x + 1);
+            }
+            w.step();
+            have = w.next(a);  // (from here on the walk shows the next piece)
+            {
+                // [Q | diag(Q~)] row, block by block of 64 columns: into TMEM (two columns a register), or K-major with
+                // 128-byte swizzle (16-byte chunk c at c ^ (row mod 8)).  The groups take every other block.
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                const uint4* q = reinterpret_cast<const uint4*>(d.q + qr * D_K);
+                const float* qt = d.qt + qr * R;
+#pragma unroll
+                for (int bk = 0; bk < NBQ; ++bk) {
+                    if ((bk & 1) != half) continue;
+                    if (bk >= D_K / 64 && !waited) {
+                        pdl_wait();  // q~
+                        waited = true;
+                    }
+                    uint32_t v[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 x = zero;
+                        const int gc = bk * 64 + c * 8;
+                        if (gc < D_K) {
+                            if (live) x = q[bk * 8 + c];
+                        } else {
+                            const bool rest = gc - D_K >= ZW;
+                            const int col = gc - D_K - (rest ? ZW : 0) - hl * R;
+                            if (live && col >= 0 && col < R) {
+                                const float4 y = *reinterpret_cast<const float4*>(qt + col);
+                                const float4 z = *reinterpret_cast<const float4*>(qt + col + 4);
+                                x = make_uint4(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w), pack_bf16x2(z.x, z.y),
+                                               pack_bf16x2(z.z, z.w));
+                                if (rest)  // what the rounding left
+                                    x = make_uint4(pack_bf16x2(y.x - bf16lo(x.x), y.y - bf16hi(x.x)),
+                                                   pack_bf16x2(y.z - bf16lo(x.y), y.w - bf16hi(x.y)),
+                                                   pack_bf16x2(z.x - bf16lo(x.z), z.y - bf16hi(x.z)),
+                                                   pack_bf16x2(z.z - bf16lo(x.w), z.w - bf16hi(x.w)));
+                            }
+                        }
+                        v[4 * c] = x.x;
+                        v[4 * c + 1] = x.y;
+                        v[4 * c + 2] = x.z;
+                        v[4 * c + 3] = x.w;
+                    }
+                    if (bk < Lay::QBT) {
+                        tmem_st_32x32b_x32(tmem + tl + Lay::TM_Q + bk * 32, v);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            *reinterpret_cast<uint4*>(smem + (bk - Lay::QBT) * 16384 + row * 128 +
+                                                      ((c ^ (row & 7)) << 4)) =
+                                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                    }
+                }
+                if (!waited) pdl_wait();  // (this grid's end stands for that of the launches before it)
+                waited = true;
+                tmem_wait_st();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(B(q_ready));
+            }
+            float mref = -INFINITY, l = 0.f;  // the reference that this group knows, and its sum relative to that
+            // After an expired wait the loop goes on without work, so that the groups still meet at their barriers.
+            for (int j = 0; j < nt; ++j, ++g) {
+                if ((g & 1) != half) continue;
+                const int base = (p0 + j) * kBlockSize;
+                const int blk = d.block_table[(size_t)b * d.max_pages + p0 + j];
+                const bool good = blk >= 0 && blk < d.num_blocks;
+                const bool inner = good && base + kBlockSize <= L;  // every row sees every token
+                ok = ok && !aborted() && wait_role(B(s_full + half), (g >> 1) & 1, d);
+                uint32_t sv[64];
+                float mx = -INFINITY;
+                if (ok) {
+                    if (j == 0 && row == 0) poison[(piece + 1) & 1] = 0;  // (every row is done with the piece before)
+                    tc_fence_after();
+                    tmem_ld_32x32b_x32_nowait(tmem + tl + Lay::TM_S + half * 64, sv);
+                    tmem_ld_32x32b_x32_nowait(tmem + tl + Lay::TM_S + half * 64 + 32, sv + 32);
+                    tmem_wait_ld();
+                    if (!inner) {
+                        const int c = L - base;  // tokens of the page before the drafted ones
+                        unsigned long long seen = c >= 0 ? (c < 64 ? tree << c : 0) | (c < 64 ? (1ull << c) - 1 : ~0ull)
+                                                         : (c > -64 ? tree >> -c : 0);
+                        if (!good) seen = 0;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) sv[e] = seen >> e & 1 ? sv[e] : 0xff800000u;
+                        // Values that not every row sees, or none: cleared where they could spoil a product with a
+                        // probability of 0.  Rows behind the end wholly; of a drafted token what is not finite,
+                        // which is noted and added at the end to the rows that do see it.
+                        ok = wait_role(B(v_full + g % VST), (g / VST) & 1, d);
+                        const int vr = row & 63, t = base + vr - L;
+                        if (ok && t >= 0) {
+                            uint8_t* const v0 = smem + Lay::OFF_V + g % VST * Lay::V_BYTES;
+                            bool found = false;
+                            auto clean = [&](uint4* p) {
+                                if (t >= n) {
+                                    *p = make_uint4(0, 0, 0, 0);
+                                    return;
+                                }
+                                uint32_t x[4] = {p->x, p->y, p->z, p->w};
+                                bool hit = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const bool lo = (x[e] & 0x7f80u) == 0x7f80u, hi = (x[e] & 0x7f800000u) == 0x7f800000u;
+                                    hit |= lo | hi;
+                                    x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+                                }
+                                if (hit) *p = make_uint4(x[0], x[1], x[2], x[3]);
+                                found |= hit;
+                            };
+                            for (int bk = row >> 6; bk < D_H / 64 + (ZW == 32 ? 0 : Lay::ZBLK); bk += 2)
+                                for (int c8 = 0; c8 < 8; ++c8)
+                                    clean(reinterpret_cast<uint4*>(v0 + bk * 8192 + vr * 128) + c8);
+                            if (ZW == 32)
+                                for (int c8 = row >> 6; c8 < 4; c8 += 2)
+                                    clean(reinterpret_cast<uint4*>(v0 + D_H / 64 * 8192 + vr * 64) + c8);
+                            if (found) atomicOr(poison + (piece & 1), 1ull << t);
+                        }
+                        __syncwarp();
+                    }
+                    float m4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m4[e] = max_nan(__uint_as_float(sv[e]), __uint_as_float(sv[4 + e]));
+#pragma unroll
+                    for (int e = 8; e < 64; ++e) m4[e & 3] = max_nan(m4[e & 3], __uint_as_float(sv[e]));
+                    mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+                    // diag(Q~)'s zeros times another head's NaN or infinity are NaN (and so is what rounding an
+                    // infinite product left): such logits are formed again from the row's own head alone.
+                    if (__any_sync(0xffffffffu, mx != mx)) {
+                        unsigned long long nans = 0;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            nans |= (unsigned long long)(__uint_as_float(sv[e]) != __uint_as_float(sv[e])) << e;
+                        for (unsigned long long todo = live ? nans : 0ull; todo != 0; todo &= todo - 1) {
+                            const int e = __ffsll(todo) - 1;
+                            const size_t t = (size_t)blk * kBlockSize + e;
+                            const float x = dot8(d.q + qr * D_K, a.sK + t * D_K, D_K) +
+                                            dot8(d.qt + qr * R, a.zK + (t * H + h) * R, R);
+#pragma unroll
+                            for (int k = 0; k < 64; ++k) sv[k] = k == e ? __float_as_uint(x) : sv[k];
+                        }
+                        __syncwarp();
+                        mx = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(sv[e]));
+                    }
+                    mx *= d.scale_log2;
+                }
+                if (g > 0) named_bar(1 + qq + 4 * half, 64);  // the other group has decided for the page before
+                const float before = j > 0 ? refs[row] : -INFINITY;
+                const bool raise = mx > before + kRescaleThreshold;  // or the row's first token
+                const float now = raise ? mx : before;
+                refs[row] = now;
+                if (j + 1 < nt || have) named_arrive(1 + qq + 4 * (half ^ 1), 64);
+                if (!ok) continue;
+                const float alpha = raise && before != -INFINITY ? ex2_approx(before - now) : 1.f;
+                if (mref != now) {
+                    l = mref == -INFINITY ? 0.f : l * ex2_approx(mref - now);
+                    mref = now;
+                }
+                // p = 2^(s scale log2 e - m), 0 everywhere as long as the row has seen no token
+                const float nm = now == -INFINITY ? -INFINITY : -now;
+                float r4[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 64; e += 2) {
+                    const float x0 = ex2_approx(fmaf(__uint_as_float(sv[e]), d.scale_log2, nm));
+                    const float x1 = ex2_approx(fmaf(__uint_as_float(sv[e + 1]), d.scale_log2, nm));
+                    r4[(e >> 1) & 3] += x0 + x1;
+                    pk[e / 2] = pack_bf16x2(x0, x1);
+                }
+                tmem_st_32x32b_x32(tmem + tl + Lay::TM_S + half * 64, pk);
+                l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
+                // O may only be rescaled once P_{g-1} V_{g-1} has finished accumulating into it
+                if (j > 0 && __any_sync(0xffffffffu, raise)) {
+                    ok = wait_role(B(o_done + (half ^ 1)), ((g - 1) >> 1) & 1, d);
+                    if (ok) {
+                        tc_fence_after();
+                        uint32_t v[32];
+#pragma unroll 1
+                        for (int c = 0; c < (D_H + ZW) / 32; ++c) {
+                            tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                            tmem_st_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                if (!ok) continue;
+                if (!inner) fence_proxy_async_smem();  // cleared values before the tensor cores read them
+                tc_fence_before();
+                mbar_arrive(B(p_full + half));
+            }
+            // the row's sum over both groups' pages
+            sums[half * 128 + row] = make_float2(l, mref);
+            named_bar(9 + qq, 64);
+            const float2 other = sums[(half ^ 1) * 128 + row];
+            const float M = fmaxf(mref, other.y);
+            float ls = (mref == -INFINITY ? 0.f : l * ex2_approx(mref - M)) +
+                       (other.y == -INFINITY ? 0.f : other.x * ex2_approx(other.y - M));
+            // ---- partials, unnormalised: [column quad][row], so that a warp's stores are consecutive
+            if (ok) ok = wait_role(B(o_done + ((g - 1) & 1)), ((g - 1) >> 1) & 1, d);
+            if (ok) {
+                tc_fence_after();
+                const bool nan = ls != ls;  // handed on as NaN values with a weight, not as an empty part
+                const float mo = nan && !(fabsf(M) < INFINITY) ? 0.f : M;
+                if (half == 0) a.ml[(size_t)slot * 128 + row] = make_float2(mo, nan ? 1.f : ls);
+                float4* const dst = a.acc + (size_t)slot * (W / 4) * 128 + row;
+                const unsigned long long spoilt = live ? poison[piece & 1] & tree : 0ull;
+                const float bad = __uint_as_float(0x7fc00000u);
+                auto put = [&](const uint32_t* v, int c) {  // columns c .. c + 3 of [s^V | z^V of the row's head]
+                    float4 x = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
+                                           __uint_as_float(v[3]));
+                    if (nan) x = make_float4(bad, bad, bad, bad);
+                    for (unsigned long long todo = spoilt; todo != 0; todo &= todo - 1) {
+                        const int t = L + __ffsll(todo) - 1;
+                        const size_t at = (size_t)d.block_table[(size_t)b * d.max_pages + t / kBlockSize] * kBlockSize +
+                                          t % kBlockSize;
+                        const uint2 y = *reinterpret_cast<const uint2*>(c < D_H ? a.sV + at * D_H + c
+                                                                                : a.zV + (at * H + h) * R + c - D_H);
+                        auto add = [](float& z, float e) { z += fabsf(e) < INFINITY ? 0.f : e; };
+                        add(x.x, bf16lo(y.x));
+                        add(x.y, bf16hi(y.x));
+                        add(x.z, bf16lo(y.y));
+                        add(x.w, bf16hi(y.y));
+                    }
+                    dst[(size_t)(c / 4) * 128] = x;
+                };
+#pragma unroll 1
+                for (int c = half; c < D_H / 32; c += 2) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + c * 32, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) put(v + 4 * e, c * 32 + e * 4);
+                }
+                // latent sums: 32 columns at a time, each row keeps its own head's
+#pragma unroll 1
+                for (int c = half; c < ZW / 32; c += 2) {
+                    // (a warp's rows span heads hl of its first to its last lane)
+                    const int first = (qq * 32) / a.ns * R, last = (qq * 32 + 31) / a.ns * R + R;
+                    if (c * 32 + 32 <= first || c * 32 >= last) continue;
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tmem + tl + Lay::TM_O + D_H + c * 32, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int col = c * 32 + e * 4 - hl * R;
+                        if (col >= 0 && col < R) put(v + 4 * e, D_H + col);
+                    }
+                }
+                tc_fence_before();
+            } else {
+                *abort_flag = 1;
+            }
+            ++piece;
+        }
+        if (!waited) pdl_wait();  // (a range without work)
     }
-    for (int c = threadIdx.x; c < W; c += 128) {
-        float x = 0.f;
-        for (int k = 0; k < 4; ++k) x += w[k] == 0.f ? 0.f : w[k] * acc_s[k][c];
-        o[c] = ls == 0.f ? 0.f : x / ls;
-    }
+    tc_fence_before();
     __syncthreads();
-    for (int c = threadIdx.x; c < D_H; c += 128) {
-        float x = o[c];
-        for (int k = 0; k < R; ++k)
-            x = fmaf(o[D_H + k], __uint_as_float((uint32_t)d.BV[((size_t)h * D_H + c) * R + k] << 16), x);
-        const __nv_bfloat16 y = __float2bfloat16_rn(x);
-        out[c] = *reinterpret_cast<const uint16_t*>(&y);
+    // Whichever wait ran out, and however late: the copies in flight land before the block gives up its shared memory.
+    if ((warp == 0 || warp == 6) && *abort_flag) {
+        const int depth = keys ? KST : VST;
+        for (int k = max(0, issued - depth); k < issued; ++k)
+            drain(B((keys ? k_full : v_full) + k % depth), (k / depth) & 1, d.status);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
 }
 
+// Merge of a tile's pieces, B_h^V, division by the sum: grid (4 groups of 32 rows, tiles, sequences), block (32, 8).
+// A lane is a row while the pieces are read (consecutive rows' quads lie side by side), columns of the output after.
+template <int D_H, int R>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int W = D_H + R, W4 = W / 4, QPW = (W4 + 7) / 8, DPL = D_H / 32;
+    const DecodeArgs& d = a.d;
+    const int lane = threadIdx.x, warp = threadIdx.y, b = blockIdx.z, t = blockIdx.y;
+    __shared__ float tile[32][W + 1];
+    pdl_wait();  // the scan (in every block: this grid's end stands for that of the launches before it)
+    const Seq s = seq_of(a, b);
+    if (s.bad) {  // zeros in all T rows: the tiles of a full sequence share them
+        if (t == 0 && blockIdx.x == 0 && lane == 0 && warp == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
+        const size_t n = (size_t)a.T * d.H * D_H / 8, step = (size_t)gridDim.x * gridDim.y * 256;
+        uint4* out = reinterpret_cast<uint4*>(d.out + (size_t)b * a.T * d.H * D_H);
+        for (size_t i = (size_t)(t * gridDim.x + blockIdx.x) * 256 + warp * 32 + lane; i < n; i += step)
+            out[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    if (t >= tiles_of(a, s.n)) return;
+    const int st_b = (s.n + a.ns - 1) / a.ns;
+    const int row0 = blockIdx.x * 32, row = row0 + lane;
+    auto head = [&](int r) { return t / st_b * a.hb + r / a.ns; };
+    auto token = [&](int r) { return t % st_b * a.ns + r % a.ns; };
+    if (head(row0) >= d.H || (a.ns >= 32 && token(row0) >= s.n)) return;
+    const int2 fe = a.seg_table[b * a.tmax + t];
+    float M = -INFINITY;
+    for (int k = 0; k < fe.y; ++k) M = fmaxf(M, a.ml[(size_t)(fe.x + k) * 128 + row].x);
+    float ls = 0.f;
+    float4 x[QPW];
+#pragma unroll
+    for (int e = 0; e < QPW; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < fe.y; ++k) {
+        const float2 ml = a.ml[(size_t)(fe.x + k) * 128 + row];
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        ls = fmaf(w, ml.y, ls);
+        const float4* src = a.acc + (size_t)(fe.x + k) * W4 * 128 + row;
+#pragma unroll
+        for (int e = 0; e < QPW; ++e) {
+            const int c = e * 8 + warp;
+            if (c >= W4) break;
+            const float4 y = src[(size_t)c * 128];
+            if (w == 0.f) continue;
+            x[e].x = fmaf(w, y.x, x[e].x);
+            x[e].y = fmaf(w, y.y, x[e].y);
+            x[e].z = fmaf(w, y.z, x[e].z);
+            x[e].w = fmaf(w, y.w, x[e].w);
+        }
+    }
+    // (the sum is 0 where the row sees no token: zeros)
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+#pragma unroll
+    for (int e = 0; e < QPW; ++e) {
+        const int c = (e * 8 + warp) * 4;
+        if (c >= W) break;
+        tile[lane][c] = x[e].x * inv;
+        tile[lane][c + 1] = x[e].y * inv;
+        tile[lane][c + 2] = x[e].z * inv;
+        tile[lane][c + 3] = x[e].w * inv;
+    }
+    __syncthreads();
+    // four rows of one head per warp (ns is a multiple of 4), DPL output columns per lane
+    const int r0 = warp * 4, h = head(row0 + r0);
+    if (h >= d.H) return;
+    const uint16_t* bv = d.BV + ((size_t)h * D_H + lane * DPL) * R;
+    float y[4][DPL];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) y[r][e] = tile[r0 + r][lane * DPL + e];
+#pragma unroll
+    for (int k = 0; k < R; k += 8) {
+        uint4 f[DPL];
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) f[e] = *reinterpret_cast<const uint4*>(bv + e * R + k);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = tile[r0 + r][D_H + k + i];
+#pragma unroll
+            for (int e = 0; e < DPL; ++e) {
+                y[r][e] = fmaf(bf16lo(f[e].x), z[0], fmaf(bf16hi(f[e].x), z[1], y[r][e]));
+                y[r][e] = fmaf(bf16lo(f[e].y), z[2], fmaf(bf16hi(f[e].y), z[3], y[r][e]));
+                y[r][e] = fmaf(bf16lo(f[e].z), z[4], fmaf(bf16hi(f[e].z), z[5], y[r][e]));
+                y[r][e] = fmaf(bf16lo(f[e].w), z[6], fmaf(bf16hi(f[e].w), z[7], y[r][e]));
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = token(row0 + r0 + r);
+        if (i >= s.n) continue;
+        uint16_t* out = d.out + (((size_t)b * a.T + i) * d.H + h) * D_H + lane * DPL;
+        if (DPL == 4)
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(y[r][0], y[r][1]), pack_bf16x2(y[r][2], y[r][3]));
+        else
+            *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(y[r][0], y[r][1]);
+    }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
 }  // namespace
 
-size_t tree_workspace_bytes(int, int, int, int, int, int, int) { return 256; }
+// Which tile: the fewest columns of products, tiles x (d_k + d_h + 3 zw).
+TreePlan tree_plan(int H, int D_H, int R, int D_R, int T) {
+    TreePlan best{};
+    long long least = -1;
+    for (int zw = 32; zw <= 128; zw *= 2) {
+        TreePlan p{};
+        p.zw = zw;
+        p.hb = zw / R;
+        p.ns = 128 / p.hb;
+        p.htiles = (H + p.hb - 1) / p.hb;
+        p.stiles = (T + p.ns - 1) / p.ns;
+        if (p.ns > 64) continue;
+        const long long cost = (long long)p.htiles * p.stiles * (2 * D_H + D_R + 3 * zw);
+        if (least < 0 || cost < least) {
+            best = p;
+            least = cost;
+        }
+    }
+    return best;
+}
 
-cudaError_t launch_tree(TreeArgs a, int D_H, int R, int D_R, void*, int, cudaStream_t stream) {
-    tree_kernel<<<dim3(a.d.H, a.batch * a.T), 128, 0, stream>>>(a, D_H, R, D_R);
-    return cudaGetLastError();
+static size_t tree_slots(int batch, const TreePlan& p, int sms) {
+    return (size_t)sms + (size_t)batch * p.htiles * p.stiles;
+}
+
+size_t tree_workspace_bytes(int H, int D_H, int R, int D_R, int batch, int T, int sms) {
+    const TreePlan p = tree_plan(H, D_H, R, D_R, T);
+    const size_t slots = tree_slots(batch, p, sms);
+    return align256((size_t)batch * T * H * R * sizeof(float)) +
+           align256((size_t)batch * p.htiles * p.stiles * sizeof(int2)) + align256(slots * 128 * sizeof(float2)) +
+           slots * 128 * (D_H + R) * sizeof(float) + 256;
+}
+
+void tree_carve_workspace(TreeArgs* a, void* ws, int D_H, int R, int D_R, int sms) {
+    const TreePlan p = tree_plan(a->d.H, D_H, R, D_R, a->T);
+    a->zw = p.zw;
+    a->hb = p.hb;
+    a->ns = p.ns;
+    a->htiles = p.htiles;
+    a->tmax = p.htiles * p.stiles;
+    a->ctas = sms;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    a->d.qt = reinterpret_cast<float*>(at);
+    at += align256((size_t)a->batch * a->T * a->d.H * R * sizeof(float));
+    a->seg_table = reinterpret_cast<int2*>(at);
+    at += align256((size_t)a->batch * a->tmax * sizeof(int2));
+    a->ml = reinterpret_cast<float2*>(at);
+    at += align256(tree_slots(a->batch, p, sms) * 128 * sizeof(float2));
+    a->acc = reinterpret_cast<float4*>(at);
+}
+
+template <int D_H, int D_R, int ZW>
+static cudaError_t launch_scan_t(const TreeMaps& maps, const TreeArgs& a, int R, cudaStream_t stream) {
+    constexpr uint32_t smem = TrLayout<D_H, D_R, ZW>::SMEM;
+    auto kern = tree_scan_kernel<D_H, D_R, ZW>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(a.ctas), dim3(kThreads), smem, stream, maps, a, R);
+}
+
+cudaError_t launch_tree(const TreeMaps& maps, const TreeArgs& a, int D_H, int R, int D_R, cudaStream_t stream) {
+    cudaError_t e = launch_decode_absorb(a.d, D_H, R, D_R, stream);
+    if (e != cudaSuccess) return e;
+    e = cudaErrorInvalidValue;
+#define LRKV_TS(DH, DR)                                                        \
+    if (D_H == DH && D_R == DR)                                                \
+        e = a.zw == 128  ? launch_scan_t<DH, DR, 128>(maps, a, R, stream)      \
+            : a.zw == 64 ? launch_scan_t<DH, DR, 64>(maps, a, R, stream)       \
+                         : launch_scan_t<DH, DR, 32>(maps, a, R, stream);
+    LRKV_TS(64, 0) LRKV_TS(64, 64) LRKV_TS(128, 0) LRKV_TS(128, 64)
+#undef LRKV_TS
+    if (e != cudaSuccess) return e;
+#define LRKV_TC(DH, RR)                                                                                          \
+    if (D_H == DH && R == RR)                                                                                    \
+        return launch_dependent(tree_combine_kernel<DH, RR>, dim3(4, a.tmax, a.batch), dim3(32, 8), 0, stream, a);
+    LRKV_TC(64, 8) LRKV_TC(64, 16) LRKV_TC(64, 32) LRKV_TC(128, 8) LRKV_TC(128, 16) LRKV_TC(128, 32)
+#undef LRKV_TC
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace lrkv
