@@ -24,6 +24,20 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const D
     const bool ok = mbar_look_wait(bar, parity, d.status, d.wait_ns);
     return __all_sync(0xffffffffu, ok);
 }
+// wait_role for a role that one thread plays: a look first, the stop flag only while it has to wait.
+__device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const DecodeArgs& d, volatile int* stop) {
+    if (mbar_test(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    const bool nap = d.wait_ns == kWaitLimitNs;
+    for (uint32_t it = 1;; ++it) {
+        if (nap ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
+        if (*stop) return false;
+        if (((it & 255u) == 0 || !nap) && globaltimer_ns() - t0 > d.wait_ns) {
+            set_status(d.status, LRKV_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* status) {
     mbar_wait(bar, parity, status);
     __syncwarp();

@@ -29,14 +29,16 @@ __device__ __forceinline__ uint64_t mndesc64(uint32_t a) { return sdesc(a, 16, 5
 // [Q | diag(Q~)] is the A operand of S, diag(Q~) as two bf16 pieces (q~ rounded, and what that left). As many of
 // its 64-column blocks as fit sit in TMEM, the rest in shared memory, beside rings of key stages
 // [64 tokens][D_K + ZW] and value stages [64][D_H + ZW].
-// TMEM columns: two S buffers of 64 columns (P, two bf16 a column, is written over the first half of its own S), O, Q.
+// TMEM columns: NSB S buffers of 64 columns (P, two bf16 a column, is written over the first half of its own S), O, Q.
+// Three S buffers where Q fits beside them, so that a group of rows finds its next page computed when it is done with one.
 template <int D_H, int D_R, int ZW>
 struct TrLayout {
     static constexpr int D_K = D_H + D_R;
     static constexpr int ZBLK = ZW == 32 ? 1 : ZW / 64;                 // blocks of latents in a stage
     static constexpr uint32_t ZBLK_BYTES = ZW == 32 ? 4096 : 8192;
     static constexpr uint32_t K_BYTES = D_K / 64 * 8192 + ZBLK * ZBLK_BYTES, V_BYTES = D_H / 64 * 8192 + ZBLK * ZBLK_BYTES;
-    static constexpr int NBQ = (D_K + 2 * ZW) / 64, QROOM = (384 - D_H - ZW) / 32;
+    static constexpr int NBQ = (D_K + 2 * ZW) / 64;
+    static constexpr int NSB = (512 - 192 - D_H - ZW) / 32 >= NBQ ? 3 : 2, QROOM = (512 - 64 * NSB - D_H - ZW) / 32;
     static constexpr int QBT = NBQ < QROOM ? NBQ : QROOM, QBS = NBQ - QBT;  // blocks in TMEM, in shared memory
     static constexpr uint32_t Q_BYTES = QBS * 16384;
     static constexpr uint32_t ROOM = 232448 - 1024 - 4096 - Q_BYTES;
@@ -47,7 +49,7 @@ struct TrLayout {
     static constexpr uint32_t OFF_ROW = OFF_BAR + 512;  // 128 references, then 2 x 128 (sum, reference)
     static constexpr uint32_t SMEM = OFF_ROW + 512 + 2048 + 1024;
     static_assert(VST >= 2 && SMEM <= 232448, "stages");
-    static constexpr uint32_t TM_S = 0, TM_O = 128, TM_Q = TM_O + D_H + ZW;
+    static constexpr uint32_t TM_S = 0, TM_O = 64 * NSB, TM_Q = TM_O + D_H + ZW;
     static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
 };
 
@@ -126,7 +128,7 @@ template <int D_H, int D_R, int ZW>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_scan_kernel(const __grid_constant__ TreeMaps m, const __grid_constant__ TreeArgs a, const int R) {
     using Lay = TrLayout<D_H, D_R, ZW>;
-    constexpr int D_K = Lay::D_K, NBQ = Lay::NBQ, KST = Lay::KST, VST = Lay::VST;
+    constexpr int D_K = Lay::D_K, NBQ = Lay::NBQ, NSB = Lay::NSB, KST = Lay::KST, VST = Lay::VST;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
@@ -137,29 +139,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
     uint64_t* q_ready = bars + 0;   // Q of a piece written, O of the piece before it read
-    uint64_t* s_full = bars + 1;    // [2] S_g computed (g: pages of this CTA, counted through; buffer g % 2)
-    uint64_t* p_full = bars + 3;    // [2] P_g written
-    uint64_t* o_done = bars + 5;    // [2] P_g V_g complete
-    uint64_t* mma_drain = bars + 7;
-    uint64_t* k_full = bars + 8;    // [6]
-    uint64_t* k_empty = bars + 14;
-    uint64_t* v_full = bars + 20;
-    uint64_t* v_empty = bars + 26;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
-    volatile int* abort_flag = reinterpret_cast<int*>(bars + 33);
-    unsigned long long* poison = reinterpret_cast<unsigned long long*>(bars + 34);  // [2], by the piece's parity
-    long long* plan = reinterpret_cast<long long*>(bars + 36);                      // total, first sequence, its base
+    uint64_t* s_full = bars + 1;    // [3] S_g computed (g: pages of this CTA, counted through; buffer g % NSB)
+    uint64_t* p_full = bars + 4;    // [3] P_g written
+    uint64_t* o_done = bars + 7;    // [3] P_g V_g complete
+    uint64_t* mma_drain = bars + 10;
+    uint64_t* k_full = bars + 11;   // [6]
+    uint64_t* k_empty = bars + 17;
+    uint64_t* v_full = bars + 23;
+    uint64_t* v_empty = bars + 29;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 35);
+    volatile int* abort_flag = reinterpret_cast<int*>(bars + 36);
+    unsigned long long* poison = reinterpret_cast<unsigned long long*>(bars + 37);  // [2], by the piece's parity
+    long long* plan = reinterpret_cast<long long*>(bars + 39);                      // total, first sequence, its base
     auto B = [&](uint64_t* p) { return smem_u32(p); };
     auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
 
     if (threadIdx.x == 32) {
         mbar_init(B(q_ready), 256);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(B(s_full + i), 1);
             mbar_init(B(p_full + i), 128);
             mbar_init(B(o_done + i), 1);
-            poison[i] = 0;
         }
+        poison[0] = poison[1] = 0;
         mbar_init(B(mma_drain), 1);
         for (int i = 0; i < 6; ++i) {
             mbar_init(B(k_full + i), 1);
@@ -280,89 +282,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) *abort_flag = 1;
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMAs
-        // One warp issues all of them, so they run in this order: S_0 S_1 | P_0 V_0, S_2 | P_1 V_1, S_3 | ...  S_{g+2}
-        // overwrites the buffer that P_g V_g has read; while the rows work on S_g, P_{g-1} V_{g-1} and S_{g+1} run.
+        // One thread issues all of them, so they run in this order: S_0 .. S_{NSB-1} | P_0 V_0, S_NSB | P_1 V_1, ..: S_{g+NSB}
+        // overwrites the buffer that P_g V_g has read; while the rows work on S_g, the products of its neighbours run.
+        // (With a vote of the warp at every wait and MMA the issue took 1,970 cycles a page of 12 + 8 MMAs, of which the
+        // tensor cores need 704; from one thread 1,390.)
         constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
         constexpr uint32_t id_PV = idesc_bf16_f32(128, ZW == 32 ? D_H : D_H + ZW) | (1u << 16);  // B is MN-major
         constexpr uint32_t id_PZ = idesc_bf16_f32(128, 32) | (1u << 16);
-        const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K), dKz = kdesc64(S0 + Lay::OFF_K + D_K / 64 * 8192);
-        const uint64_t dV = mndesc128(S0 + Lay::OFF_V), dVz = mndesc64(S0 + Lay::OFF_V + D_H / 64 * 8192);
-        int kst = 0, vst = 0;
-        uint32_t kphase = 0, vphase = 0, qphase = 0;
-        int gs = 0, gp = 0;  // pages whose S, whose P V has been issued
-        auto s_tile = [&]() -> bool {
-            if (aborted() || !wait_role(B(k_full + kst), kphase, d)) return false;
-            tc_fence_after();
-            const uint64_t so = (uint64_t)(kst * (Lay::K_BYTES >> 4));
-            const uint32_t ts = tmem + Lay::TM_S + (gs & 1) * 64;
+        if (elect_one_sync()) {
+            const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K);
+            const uint64_t dKz = kdesc64(S0 + Lay::OFF_K + D_K / 64 * 8192);
+            const uint64_t dV = mndesc128(S0 + Lay::OFF_V), dVz = mndesc64(S0 + Lay::OFF_V + D_H / 64 * 8192);
+            int kst = 0, vst = 0, sb = 0, pb = 0;  // stages and S buffers in turn
+            uint32_t kphase = 0, vphase = 0, qphase = 0, pphase = 0;
+            auto s_tile = [&]() -> bool {
+                if (!wait_one(B(k_full + kst), kphase, d, abort_flag)) return false;
+                tc_fence_after();
+                const uint64_t so = (uint64_t)(kst * (Lay::K_BYTES >> 4));
+                const uint32_t ts = tmem + Lay::TM_S + sb * 64;
 #pragma unroll
-            for (int kk = 0; kk < NBQ * 4; ++kk) {
-                // 16 columns of Q; q's against s^K, both pieces of q~ against the same z^K
-                const int col = kk * 16, z = (col - D_K) % ZW;
-                uint64_t bd;
-                if (col < D_K)
-                    bd = dK + so + ((col / 64 * 8192 + col % 64 * 2) >> 4);
-                else if (ZW == 32)
-                    bd = dKz + so + (z * 2 >> 4);
-                else
-                    bd = dK + so + (((D_K + z) / 64 * 8192 + z % 64 * 2) >> 4);
-                if (elect_one_sync()) {
+                for (int kk = 0; kk < NBQ * 4; ++kk) {
+                    // 16 columns of Q; q's against s^K, both pieces of q~ against the same z^K
+                    const int col = kk * 16, z = (col - D_K) % ZW;
+                    uint64_t bd;
+                    if (col < D_K)
+                        bd = dK + so + ((col / 64 * 8192 + col % 64 * 2) >> 4);
+                    else if (ZW == 32)
+                        bd = dKz + so + (z * 2 >> 4);
+                    else
+                        bd = dK + so + (((D_K + z) / 64 * 8192 + z % 64 * 2) >> 4);
                     if (kk < Lay::QBT * 4)
                         tc_mma_bf16_ts(ts, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
                     else
                         tc_mma_bf16(ts, dQ + ((((kk >> 2) - Lay::QBT) * 16384 + (kk & 3) * 32) >> 4), bd, id_S, 1);
                 }
-            }
-            if (elect_one_sync()) {
-                tc_commit(B(s_full + (gs & 1)));
+                tc_commit(B(s_full + sb));
                 tc_commit(B(k_empty + kst));
-            }
-            __syncwarp();
-            ++gs;
-            if (++kst == KST) {
-                kst = 0;
-                kphase ^= 1;
-            }
-            return true;
-        };
-        auto pv_tile = [&](bool first) -> bool {
-            if (aborted() || !wait_role(B(p_full + (gp & 1)), (gp >> 1) & 1, d) || !wait_role(B(v_full + vst), vphase, d))
-                return false;
-            tc_fence_after();
-            const uint64_t so = (uint64_t)(vst * (Lay::V_BYTES >> 4));
-            const uint32_t tp = tmem + Lay::TM_S + (gp & 1) * 64;
+                if (++sb == NSB) sb = 0;
+                if (++kst == KST) {
+                    kst = 0;
+                    kphase ^= 1;
+                }
+                return true;
+            };
+            auto pv_tile = [&](bool first) -> bool {
+                if (!wait_one(B(v_full + vst), vphase, d, abort_flag) || !wait_one(B(p_full + pb), pphase, d, abort_flag))
+                    return false;
+                tc_fence_after();
+                const uint64_t so = (uint64_t)(vst * (Lay::V_BYTES >> 4));
+                const uint32_t tp = tmem + Lay::TM_S + pb * 64;
 #pragma unroll
-            for (int kk = 0; kk < kBlockSize / 16; ++kk)
-                if (elect_one_sync()) {
+                for (int kk = 0; kk < kBlockSize / 16; ++kk)
                     tc_mma_bf16_ts(tmem + Lay::TM_O, tp + kk * 8, dV + so + (kk * 2048 >> 4), id_PV, !first || kk > 0);
-                    if (ZW == 32)
+                if (ZW == 32) {
+#pragma unroll
+                    for (int kk = 0; kk < kBlockSize / 16; ++kk)
                         tc_mma_bf16_ts(tmem + Lay::TM_O + D_H, tp + kk * 8, dVz + so + (kk * 1024 >> 4), id_PZ,
                                        !first || kk > 0);
                 }
-            if (elect_one_sync()) {
-                tc_commit(B(o_done + (gp & 1)));
+                tc_commit(B(o_done + pb));
                 tc_commit(B(v_empty + vst));
+                if (++pb == NSB) {
+                    pb = 0;
+                    pphase ^= 1;
+                }
+                if (++vst == VST) {
+                    vst = 0;
+                    vphase ^= 1;
+                }
+                return true;
+            };
+            bool ok = true;
+            for (; ok && w.next(a); w.step()) {
+                ok = wait_one(B(q_ready), qphase, d, abort_flag);
+                qphase ^= 1;
+                tc_fence_after();
+                for (int j = 0; ok && j < NSB && j < w.nt; ++j) ok = s_tile();
+                for (int j = 0; ok && j < w.nt; ++j) ok = pv_tile(j == 0) && (j + NSB >= w.nt || s_tile());
             }
-            __syncwarp();
-            ++gp;
-            if (++vst == VST) {
-                vst = 0;
-                vphase ^= 1;
-            }
-            return true;
-        };
-        bool ok = true;
-        for (; ok && w.next(a); w.step()) {
-            ok = wait_role(B(q_ready), qphase, d);
-            qphase ^= 1;
-            tc_fence_after();
-            ok = ok && s_tile() && (w.nt < 2 || s_tile());
-            for (int j = 0; ok && j < w.nt; ++j) ok = pv_tile(j == 0) && (j + 2 >= w.nt || s_tile());
+            if (!ok) *abort_flag = 1;
+            tc_commit(B(mma_drain));
         }
-        if (!ok) *abort_flag = 1;
-        // every MMA this warp issued has finished before the CTA tears TMEM down
-        if (elect_one_sync()) tc_commit(B(mma_drain));
         __syncwarp();
+        // every MMA this warp issued has finished before the CTA tears TMEM down
         drain(B(mma_drain), 0, d.status);
     } else if (warp != 7) {
         // ---------------------------------------------------------------- query rows: softmax, partials
@@ -376,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile float* const refs = reinterpret_cast<float*>(smem + Lay::OFF_ROW);
         float2* const sums = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
         bool ok = true, waited = false;
-        int g = 0, piece = 0;
+        int g = 0, sb = 0, piece = 0;  // pages so far, its S buffer, pieces so far
+        uint32_t sphase = 0;
         bool have = w.next(a);
         while (have) {
             const int b = w.b, L = w.s.L, n = w.s.n, st_b = (n + a.ns - 1) / a.ns;
@@ -453,20 +456,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float mref = -INFINITY, l = 0.f;  // the reference that this group knows, and its sum relative to that
             // After an expired wait the loop goes on without work, so that the groups still meet at their barriers.
-            for (int j = 0; j < nt; ++j, ++g) {
+            auto turn = [&]() {
+                ++g;
+                if (++sb == NSB) {
+                    sb = 0;
+                    sphase ^= 1;
+                }
+            };
+            for (int j = 0; j < nt; ++j, turn()) {
                 if ((g & 1) != half) continue;
+                const uint32_t tS = tmem + tl + Lay::TM_S + sb * 64;
                 const int base = (p0 + j) * kBlockSize;
                 const int blk = d.block_table[(size_t)b * d.max_pages + p0 + j];
                 const bool good = blk >= 0 && blk < d.num_blocks;
                 const bool inner = good && base + kBlockSize <= L;  // every row sees every token
-                ok = ok && !aborted() && wait_role(B(s_full + half), (g >> 1) & 1, d);
+                ok = ok && !aborted() && wait_role(B(s_full + sb), sphase, d);
                 uint32_t sv[64];
                 float mx = -INFINITY;
                 if (ok) {
                     if (j == 0 && row == 0) poison[(piece + 1) & 1] = 0;  // (every row is done with the piece before)
                     tc_fence_after();
-                    tmem_ld_32x32b_x32_nowait(tmem + tl + Lay::TM_S + half * 64, sv);
-                    tmem_ld_32x32b_x32_nowait(tmem + tl + Lay::TM_S + half * 64 + 32, sv + 32);
+                    tmem_ld_32x32b_x32_nowait(tS, sv);
+                    tmem_ld_32x32b_x32_nowait(tS + 32, sv + 32);
                     tmem_wait_ld();
                     if (!inner) {
                         const int c = L - base;  // tokens of the page before the drafted ones
@@ -560,11 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r4[(e >> 1) & 3] += x0 + x1;
                     pk[e / 2] = pack_bf16x2(x0, x1);
                 }
-                tmem_st_32x32b_x32(tmem + tl + Lay::TM_S + half * 64, pk);
+                tmem_st_32x32b_x32(tS, pk);
                 l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
                 // O may only be rescaled once P_{g-1} V_{g-1} has finished accumulating into it
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
-                    ok = wait_role(B(o_done + (half ^ 1)), ((g - 1) >> 1) & 1, d);
+                    ok = wait_role(B(o_done + (sb > 0 ? sb - 1 : NSB - 1)), sb > 0 ? sphase : sphase ^ 1, d);
                     if (ok) {
                         tc_fence_after();
                         uint32_t v[32];
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) continue;
                 if (!inner) fence_proxy_async_smem();  // cleared values before the tensor cores read them
                 tc_fence_before();
-                mbar_arrive(B(p_full + half));
+                mbar_arrive(B(p_full + sb));
             }
             // the row's sum over both groups' pages
             sums[half * 128 + row] = make_float2(l, mref);
@@ -591,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float ls = (mref == -INFINITY ? 0.f : l * ex2_approx(mref - M)) +
                        (other.y == -INFINITY ? 0.f : other.x * ex2_approx(other.y - M));
             // ---- partials, unnormalised: [column quad][row], so that a warp's stores are consecutive
-            if (ok) ok = wait_role(B(o_done + ((g - 1) & 1)), ((g - 1) >> 1) & 1, d);
+            if (ok) ok = wait_role(B(o_done + (sb > 0 ? sb - 1 : NSB - 1)), sb > 0 ? sphase : sphase ^ 1, d);
             if (ok) {
                 tc_fence_after();
                 const bool nan = ls != ls;  // handed on as NaN values with a weight, not as an empty part
