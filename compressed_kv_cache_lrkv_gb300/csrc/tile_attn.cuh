@@ -19,6 +19,31 @@ __device__ __forceinline__ void named_bar(int id, int threads) {
 __device__ __forceinline__ uint64_t kdesc128(uint32_t a) { return sdesc(a, 16, 1024, 2); }
 __device__ __forceinline__ uint64_t mndesc128(uint32_t a) { return sdesc(a, 8192, 1024, 2); }
 
+// Shared-memory descriptors in two halves, the upper one (strides, swizzle) a constant: MMAs whose TMEM addresses and
+// upper halves are constants leave their thread one operand to bring into a uniform register.
+constexpr uint32_t desc_upper(uint32_t sbo, uint32_t layout) { return (sbo >> 4) | (1u << 14) | (layout << 29); }
+__device__ __forceinline__ uint32_t desc_lower(uint32_t smem_addr, uint32_t lbo) {
+    return ((smem_addr >> 4) & 0x3FFFu) | ((lbo >> 4) & 0x3FFFu) << 16;
+}
+// D (TMEM) (+)= A (TMEM, or shared memory) . B (shared memory), bf16, fp32 sums.
+template <uint32_t B_UPPER>
+__device__ __forceinline__ void mma_ts_h(uint32_t d, uint32_t a, uint32_t b_lower, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lower), "n"(B_UPPER), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+template <uint32_t A_UPPER, uint32_t B_UPPER>
+__device__ __forceinline__ void mma_ss_h(uint32_t d, uint32_t a_lower, uint32_t b_lower, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lower), "n"(A_UPPER), "r"(b_lower), "n"(B_UPPER), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // Wait of a role, with the call's limit, and one for what the block has in flight, with the full limit.
 __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const DecodeArgs& d) {
     const bool ok = mbar_look_wait(bar, parity, d.status, d.wait_ns);

@@ -18,13 +18,11 @@ namespace {
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.
-constexpr int kStartPages = 4;
+constexpr int kStartPages = 8;
 
 __device__ __forceinline__ void named_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ uint64_t kdesc64(uint32_t a) { return sdesc(a, 16, 512, 4); }
-__device__ __forceinline__ uint64_t mndesc64(uint32_t a) { return sdesc(a, 16, 512, 4); }
 
 // [Q | diag(Q~)] is the A operand of S, diag(Q~) as two bf16 pieces (q~ rounded, and what that left). As many of
 // its 64-column blocks as fit sit in TMEM, the rest in shared memory, beside rings of key stages
@@ -48,7 +46,7 @@ struct TrLayout {
     static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
     static constexpr uint32_t OFF_ROW = OFF_BAR + 512;  // 128 references, then 2 x 128 (sum, reference)
     static constexpr uint32_t SMEM = OFF_ROW + 512 + 2048 + 1024;
-    static_assert(VST >= 2 && SMEM <= 232448, "stages");
+    static_assert(VST >= 2 && KST >= NSB && SMEM <= 232448, "stages");
     static constexpr uint32_t TM_S = 0, TM_O = 64 * NSB, TM_Q = TM_O + D_H + ZW;
     static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
 };
@@ -67,57 +65,64 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int b) {
     s.pages = s.n > 0 ? (s.L + s.n + kBlockSize - 1) / kBlockSize : 0;
     return s;
 }
-// Tiles of a sequence with n drafted tokens, and its units of work.
+// Tiles of a sequence with n drafted tokens (tile t: token group t % st, head group t / st, st = ceil(n / ns)), taken
+// `gang` at a time, and the sequence's units of work.
 __device__ __forceinline__ int tiles_of(const TreeArgs& a, int n) { return (n + a.ns - 1) / a.ns * a.htiles; }
+__device__ __forceinline__ int groups_of(const TreeArgs& a, int n) { return (tiles_of(a, n) + a.gang - 1) / a.gang; }
 __device__ __forceinline__ long long units_of(const TreeArgs& a, const Seq& s) {
-    return s.pages ? (long long)tiles_of(a, s.n) * (s.pages + kStartPages) : 0;
+    return s.pages ? (long long)groups_of(a, s.n) * (s.pages + kStartPages) : 0;
 }
 
-// The work: the tiles of all sequences one after the other, a tile's pages and then kStartPages empty units, cut into
-// `ranges` equal ranges, one per CTA.  A piece is what a range holds of a tile's pages; piece (range, tile) leaves
-// its partials at slot range + tile number, which is different for all pieces and consecutive for a tile's.
+// The work: groups of `gang` tiles, the groups of all sequences one after the other, a group's pages and then
+// kStartPages empty units, cut into equal ranges, one for each gang of CTAs, of which each takes a tile of the group.
+// So the CTAs that read one page's shared rows and the neighbouring latents of its tokens do it at about the same time:
+// with a range of its own for each CTA, a call over 600 MB of cache read 1,520 MB.  A piece is what a range holds of a
+// group's pages; piece (range, group) of member i leaves its partials at slot (range + group number) gang + i, which
+// is different for all pieces, and `gang` apart for a tile's.
 struct Work {
     long long total;
     int ranges;  // (no range is empty, so a tile's pieces are in consecutive ones)
-    __device__ __forceinline__ Work(long long units, int ctas)
-        : total(units), ranges(units < ctas ? (units > 0 ? (int)units : 1) : ctas) {}
+    __device__ __forceinline__ Work(long long units, int gangs)
+        : total(units), ranges(units < gangs ? (units > 0 ? (int)units : 1) : gangs) {}
     __device__ __forceinline__ long long start(int c) const { return c < ranges ? total * c / ranges : total; }
     __device__ __forceinline__ int range_of(long long u) const { return (int)(((u + 1) * ranges - 1) / total); }
 };
 
-// Walks the pieces of one range.
+// Walks a member's pieces of one range.
 struct Walk {
-    long long hi, u, seg;  // end of the range, the next unit to look at, first unit of tile t
-    int b, t;              // sequence, and tile of it
+    long long hi, u, seg;  // end of the range, the next unit to look at, first unit of group t
+    int b, t, member;      // sequence, group of its tiles, which of them
     Seq s;
-    // the piece
-    int p0, nt;  // pages [p0, p0 + nt) of the sequence
+    // the piece: pages [p0, p0 + nt) of the sequence
+    int p0, nt;
 
-    __device__ __forceinline__ void begin(const TreeArgs& a, long long lo, long long hi_, int b0, long long base) {
+    __device__ __forceinline__ void begin(const TreeArgs& a, long long lo, long long hi_, int b0, long long base, int i) {
         hi = hi_;
         u = lo;
         b = b0;
+        member = i;
         s = b < a.batch ? seq_of(a, b) : Seq{0, 0, 0, false};
         t = s.pages ? (int)((lo - base) / (s.pages + kStartPages)) : 0;
         seg = base + (long long)t * (s.pages + kStartPages);
     }
+    __device__ __forceinline__ int tile(const TreeArgs& a) const { return t * a.gang + member; }
     __device__ __forceinline__ bool next(const TreeArgs& a) {
         while (u < hi && b < a.batch) {
-            const long long end = seg + s.pages + kStartPages;
-            if (s.pages == 0 || t >= tiles_of(a, s.n)) {
+            if (s.pages == 0 || t >= groups_of(a, s.n)) {
                 if (++b < a.batch) s = seq_of(a, b);
                 t = 0;
                 continue;
             }
-            const int from = (int)(u - seg), to = (int)((hi < end ? hi : end) - seg);
-            p0 = from;
-            nt = (to < s.pages ? to : s.pages) - from;
-            if (nt > 0) return true;
+            const long long end = seg + s.pages + kStartPages;
+            const int to = (int)((hi < end ? hi : end) - seg);
+            p0 = (int)(u - seg);
+            nt = (to < s.pages ? to : s.pages) - p0;
+            if (nt > 0 && tile(a) < tiles_of(a, s.n)) return true;
             step();
         }
         return false;
     }
-    __device__ __forceinline__ void step() {  // behind the tile of the present piece
+    __device__ __forceinline__ void step() {  // behind the group of the present piece
         seg += s.pages + kStartPages;
         u = seg;
         ++t;
@@ -139,35 +144,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
     uint64_t* q_ready = bars + 0;   // Q of a piece written, O of the piece before it read
-    uint64_t* s_full = bars + 1;    // [3] S_g computed (g: pages of this CTA, counted through; buffer g % NSB)
-    uint64_t* p_full = bars + 4;    // [3] P_g written
-    uint64_t* o_done = bars + 7;    // [3] P_g V_g complete
-    uint64_t* mma_drain = bars + 10;
-    uint64_t* k_full = bars + 11;   // [6]
-    uint64_t* k_empty = bars + 17;
-    uint64_t* v_full = bars + 23;
-    uint64_t* v_empty = bars + 29;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 35);
-    volatile int* abort_flag = reinterpret_cast<int*>(bars + 36);
-    unsigned long long* poison = reinterpret_cast<unsigned long long*>(bars + 37);  // [2], by the piece's parity
-    long long* plan = reinterpret_cast<long long*>(bars + 39);                      // total, first sequence, its base
+    uint64_t* p_full = bars + 1;    // [3] P_g written (g: pages of this CTA, counted through; buffer g % NSB)
+    uint64_t* mma_drain = bars + 4;
+    uint64_t* k_full = bars + 5;    // [6] keys of page g there (stage g % KST)
+    uint64_t* s_done = bars + 11;   // S_g computed: the rows may read it, the stage is free
+    uint64_t* v_full = bars + 17;   // values of page g there (stage g % VST)
+    uint64_t* o_done = bars + 23;   // P_g V_g added to O, the stage is free
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 29);
+    volatile int* abort_flag = reinterpret_cast<int*>(bars + 30);
+    unsigned long long* poison = reinterpret_cast<unsigned long long*>(bars + 31);  // [2], by the piece's parity
+    long long* plan = reinterpret_cast<long long*>(bars + 33);                      // total, first sequence, its base
     auto B = [&](uint64_t* p) { return smem_u32(p); };
     auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
 
     if (threadIdx.x == 32) {
         mbar_init(B(q_ready), 256);
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(B(s_full + i), 1);
-            mbar_init(B(p_full + i), 128);
-            mbar_init(B(o_done + i), 1);
-        }
+        for (int i = 0; i < 3; ++i) mbar_init(B(p_full + i), 128);
         poison[0] = poison[1] = 0;
         mbar_init(B(mma_drain), 1);
         for (int i = 0; i < 6; ++i) {
             mbar_init(B(k_full + i), 1);
-            mbar_init(B(k_empty + i), 1);
+            mbar_init(B(s_done + i), 1);
             mbar_init(B(v_full + i), 1);
-            mbar_init(B(v_empty + i), 1);
+            mbar_init(B(o_done + i), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -181,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
             total += v;
         }
-        const Work w(total, a.ctas);
-        const long long lo = w.start(blockIdx.x);
+        const Work w(total, a.gangs);
+        const long long lo = w.start(blockIdx.x / a.gang);
         long long base = 0;
         int first = a.batch;
         for (int b0 = 0; b0 < a.batch && first == a.batch; b0 += 32) {
@@ -214,9 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Work work(plan[0], a.ctas);
+    const Work work(plan[0], a.gangs);
+    const int gang = blockIdx.x / a.gang, member = blockIdx.x - gang * a.gang;
     Walk w;
-    w.begin(a, work.start(blockIdx.x), work.start(blockIdx.x + 1), (int)plan[1], plan[2]);
+    w.begin(a, work.start(gang), work.start(gang + 1), (int)plan[1], plan[2], member);
 
     const bool keys = warp == 0;  // (of the two producers)
     int issued = 0;               // stages a producer has filled
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t stage_bytes = keys ? Lay::K_BYTES : Lay::V_BYTES;
         const int nblk = keys ? D_K / 64 : D_H / 64;
         uint64_t* full = keys ? k_full : v_full;
-        uint64_t* empty = keys ? k_empty : v_empty;
+        uint64_t* empty = keys ? s_done : o_done;
         const CUtensorMap* ms = keys ? &m.sK : &m.sV;
         const CUtensorMap* mz = keys ? &m.zK : &m.zV;
         const uint32_t ring = S0 + (keys ? Lay::OFF_K : Lay::OFF_V);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (; ok && w.next(a); w.step()) {
             const int32_t* pages = d.block_table + (size_t)w.b * d.max_pages + w.p0;
-            const int x0 = w.t / ((w.s.n + a.ns - 1) / a.ns) * ZW;
+            const int x0 = w.tile(a) / ((w.s.n + a.ns - 1) / a.ns) * ZW;
             auto fetch = [&](int i) {
                 int r = oob_row;
                 if (i < w.nt) {
@@ -290,34 +290,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_PV = idesc_bf16_f32(128, ZW == 32 ? D_H : D_H + ZW) | (1u << 16);  // B is MN-major
         constexpr uint32_t id_PZ = idesc_bf16_f32(128, 32) | (1u << 16);
         if (elect_one_sync()) {
-            const uint64_t dQ = kdesc128(S0), dK = kdesc128(S0 + Lay::OFF_K);
-            const uint64_t dKz = kdesc64(S0 + Lay::OFF_K + D_K / 64 * 8192);
-            const uint64_t dV = mndesc128(S0 + Lay::OFF_V), dVz = mndesc64(S0 + Lay::OFF_V + D_H / 64 * 8192);
+            constexpr uint32_t U128 = desc_upper(1024, 2), U64 = desc_upper(512, 4);
+            const uint32_t dQ = desc_lower(S0, 16), dK = desc_lower(S0 + Lay::OFF_K, 16);
+            const uint32_t dV = desc_lower(S0 + Lay::OFF_V, 8192), dVz = desc_lower(S0 + Lay::OFF_V + D_H / 64 * 8192, 16);
             int kst = 0, vst = 0, sb = 0, pb = 0;  // stages and S buffers in turn
             uint32_t kphase = 0, vphase = 0, qphase = 0, pphase = 0;
             auto s_tile = [&]() -> bool {
                 if (!wait_one(B(k_full + kst), kphase, d, abort_flag)) return false;
                 tc_fence_after();
-                const uint64_t so = (uint64_t)(kst * (Lay::K_BYTES >> 4));
-                const uint32_t ts = tmem + Lay::TM_S + sb * 64;
+                const uint32_t bs = dK + kst * (Lay::K_BYTES >> 4), ts = Lay::TM_S + sb * 64;
 #pragma unroll
                 for (int kk = 0; kk < NBQ * 4; ++kk) {
                     // 16 columns of Q; q's against s^K, both pieces of q~ against the same z^K
                     const int col = kk * 16, z = (col - D_K) % ZW;
-                    uint64_t bd;
-                    if (col < D_K)
-                        bd = dK + so + ((col / 64 * 8192 + col % 64 * 2) >> 4);
-                    else if (ZW == 32)
-                        bd = dKz + so + (z * 2 >> 4);
+                    const uint32_t at = col < D_K ? col / 64 * 8192 + col % 64 * 2
+                                        : ZW == 32 ? D_K / 64 * 8192 + z * 2
+                                                   : (D_K + z) / 64 * 8192 + z % 64 * 2;
+                    if (kk >= Lay::QBT * 4)
+                        mma_ss_h<U128, U128>(ts, dQ + ((((kk >> 2) - Lay::QBT) * 16384 + (kk & 3) * 32) >> 4),
+                                             bs + (at >> 4), id_S, 1);
+                    else if (ZW == 32 && col >= D_K)
+                        mma_ts_h<U64>(ts, Lay::TM_Q + kk * 8, bs + (at >> 4), id_S, kk > 0);
                     else
-                        bd = dK + so + (((D_K + z) / 64 * 8192 + z % 64 * 2) >> 4);
-                    if (kk < Lay::QBT * 4)
-                        tc_mma_bf16_ts(ts, tmem + Lay::TM_Q + kk * 8, bd, id_S, kk > 0);
-                    else
-                        tc_mma_bf16(ts, dQ + ((((kk >> 2) - Lay::QBT) * 16384 + (kk & 3) * 32) >> 4), bd, id_S, 1);
+                        mma_ts_h<U128>(ts, Lay::TM_Q + kk * 8, bs + (at >> 4), id_S, kk > 0);
                 }
-                tc_commit(B(s_full + sb));
-                tc_commit(B(k_empty + kst));
+                tc_commit(B(s_done + kst));
                 if (++sb == NSB) sb = 0;
                 if (++kst == KST) {
                     kst = 0;
@@ -329,19 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait_one(B(v_full + vst), vphase, d, abort_flag) || !wait_one(B(p_full + pb), pphase, d, abort_flag))
                     return false;
                 tc_fence_after();
-                const uint64_t so = (uint64_t)(vst * (Lay::V_BYTES >> 4));
-                const uint32_t tp = tmem + Lay::TM_S + pb * 64;
+                const uint32_t so = vst * (Lay::V_BYTES >> 4), tp = Lay::TM_S + pb * 64;
 #pragma unroll
                 for (int kk = 0; kk < kBlockSize / 16; ++kk)
-                    tc_mma_bf16_ts(tmem + Lay::TM_O, tp + kk * 8, dV + so + (kk * 2048 >> 4), id_PV, !first || kk > 0);
+                    mma_ts_h<U128>(Lay::TM_O, tp + kk * 8, dV + so + (kk * 2048 >> 4), id_PV, !first || kk > 0);
                 if (ZW == 32) {
 #pragma unroll
                     for (int kk = 0; kk < kBlockSize / 16; ++kk)
-                        tc_mma_bf16_ts(tmem + Lay::TM_O + D_H, tp + kk * 8, dVz + so + (kk * 1024 >> 4), id_PZ,
-                                       !first || kk > 0);
+                        mma_ts_h<U64>(Lay::TM_O + D_H, tp + kk * 8, dVz + so + (kk * 1024 >> 4), id_PZ, !first || kk > 0);
                 }
-                tc_commit(B(o_done + pb));
-                tc_commit(B(v_empty + vst));
+                tc_commit(B(o_done + vst));
                 if (++pb == NSB) {
                     pb = 0;
                     pphase ^= 1;
@@ -352,7 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return true;
             };
-            bool ok = true;
+            // (all 512 columns are this block's, so they begin at column 0 and the addresses above are constants)
+            bool ok = tmem == 0;
+            if (!ok) set_status(d.status, LRKV_DEV_TIMEOUT);
             for (; ok && w.next(a); w.step()) {
                 ok = wait_one(B(q_ready), qphase, d, abort_flag);
                 qphase ^= 1;
@@ -378,22 +374,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile float* const refs = reinterpret_cast<float*>(smem + Lay::OFF_ROW);
         float2* const sums = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
         bool ok = true, waited = false;
-        int g = 0, sb = 0, piece = 0;  // pages so far, its S buffer, pieces so far
-        uint32_t sphase = 0;
+        int g = 0, sb = 0, kst = 0, vst = 0, piece = 0;  // pages so far, its S buffer and stages, pieces so far
+        uint32_t kphase = 0, vphase = 0;
         bool have = w.next(a);
         while (have) {
             const int b = w.b, L = w.s.L, n = w.s.n, st_b = (n + a.ns - 1) / a.ns;
-            const int h = w.t / st_b * a.hb + hl, i = w.t % st_b * a.ns + il;
+            const int tile = w.tile(a), h = tile / st_b * a.hb + hl, i = tile % st_b * a.ns + il;
             const bool live = h < H && i < n;
             const size_t qr = live ? ((size_t)b * a.T + i) * H + h : 0;
-            const int slot = blockIdx.x + b * a.tmax + w.t;
+            const int slot = (gang + b * a.gmax + w.t) * a.gang + member;
             const int p0 = w.p0, nt = w.nt;
             // the drafted tokens that the row sees
             unsigned long long tree = ~0ull >> (64 - n);  // (n >= 1)
             if (live) tree &= a.mask ? a.mask[(size_t)b * a.T + i] : ~0ull >> (63 - i);
             if (p0 == 0 && warp == 2 && lane == 0) {
                 const int last = work.range_of(w.seg + w.s.pages - 1);
-                a.seg_table[b * a.tmax + w.t] = make_int2(slot, last - (int)blockIdx.x + 1);
+                a.seg_table[b * a.tmax + tile] = make_int2(slot, last - gang + 1);
             }
             w.step();
             have = w.next(a);  // (from here on the walk shows the next piece)
@@ -458,19 +454,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             // After an expired wait the loop goes on without work, so that the groups still meet at their barriers.
             auto turn = [&]() {
                 ++g;
-                if (++sb == NSB) {
-                    sb = 0;
-                    sphase ^= 1;
+                if (++sb == NSB) sb = 0;
+                if (++kst == KST) {
+                    kst = 0;
+                    kphase ^= 1;
+                }
+                if (++vst == VST) {
+                    vst = 0;
+                    vphase ^= 1;
                 }
             };
+            auto wait_before = [&]() {  // until the page before has been added to O
+                return wait_role(B(o_done + (vst > 0 ? vst - 1 : VST - 1)), vst > 0 ? vphase : vphase ^ 1, d);
+            };
+            // page ids of 32 pages at a time, the next ones on their way (a load per page, some 700 cycles late, was
+            // half of a page's time)
+            const int32_t* const pages = d.block_table + (size_t)b * d.max_pages + p0;
+            auto fetch = [&](int k) { return k < nt ? pages[k] : -1; };
+            int ids = fetch(lane), ids_next = fetch(32 + lane);
             for (int j = 0; j < nt; ++j, turn()) {
+                if (j > 0 && (j & 31) == 0) {
+                    ids = ids_next;
+                    ids_next = fetch(j + 32 + lane);
+                }
                 if ((g & 1) != half) continue;
                 const uint32_t tS = tmem + tl + Lay::TM_S + sb * 64;
                 const int base = (p0 + j) * kBlockSize;
-                const int blk = d.block_table[(size_t)b * d.max_pages + p0 + j];
+                const int blk = __shfl_sync(0xffffffffu, ids, j & 31);
                 const bool good = blk >= 0 && blk < d.num_blocks;
                 const bool inner = good && base + kBlockSize <= L;  // every row sees every token
-                ok = ok && !aborted() && wait_role(B(s_full + sb), sphase, d);
+                ok = ok && !aborted() && wait_role(B(s_done + kst), kphase, d);
                 uint32_t sv[64];
                 float mx = -INFINITY;
                 if (ok) {
@@ -489,10 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // Values that not every row sees, or none: cleared where they could spoil a product with a
                         // probability of 0.  Rows behind the end wholly; of a drafted token what is not finite,
                         // which is noted and added at the end to the rows that do see it.
-                        ok = wait_role(B(v_full + g % VST), (g / VST) & 1, d);
+                        ok = wait_role(B(v_full + vst), vphase, d);
                         const int vr = row & 63, t = base + vr - L;
                         if (ok && t >= 0) {
-                            uint8_t* const v0 = smem + Lay::OFF_V + g % VST * Lay::V_BYTES;
+                            uint8_t* const v0 = smem + Lay::OFF_V + vst * Lay::V_BYTES;
                             bool found = false;
                             auto clean = [&](uint4* p) {
                                 if (t >= n) {
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
                 // O may only be rescaled once P_{g-1} V_{g-1} has finished accumulating into it
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
-                    ok = wait_role(B(o_done + (sb > 0 ? sb - 1 : NSB - 1)), sb > 0 ? sphase : sphase ^ 1, d);
+                    ok = wait_before();
                     if (ok) {
                         tc_fence_after();
                         uint32_t v[32];
@@ -602,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float ls = (mref == -INFINITY ? 0.f : l * ex2_approx(mref - M)) +
                        (other.y == -INFINITY ? 0.f : other.x * ex2_approx(other.y - M));
             // ---- partials, unnormalised: [column quad][row], so that a warp's stores are consecutive
-            if (ok) ok = wait_role(B(o_done + (sb > 0 ? sb - 1 : NSB - 1)), sb > 0 ? sphase : sphase ^ 1, d);
+            if (ok) ok = wait_before();
             if (ok) {
                 tc_fence_after();
                 const bool nan = ls != ls;  // handed on as NaN values with a weight, not as an empty part
@@ -698,16 +711,16 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
     if (head(row0) >= d.H || (a.ns >= 32 && token(row0) >= s.n)) return;
     const int2 fe = a.seg_table[b * a.tmax + t];
     float M = -INFINITY;
-    for (int k = 0; k < fe.y; ++k) M = fmaxf(M, a.ml[(size_t)(fe.x + k) * 128 + row].x);
+    for (int k = 0; k < fe.y; ++k) M = fmaxf(M, a.ml[(size_t)(fe.x + k * a.gang) * 128 + row].x);
     float ls = 0.f;
     float4 x[QPW];
 #pragma unroll
     for (int e = 0; e < QPW; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < fe.y; ++k) {
-        const float2 ml = a.ml[(size_t)(fe.x + k) * 128 + row];
+        const float2 ml = a.ml[(size_t)(fe.x + k * a.gang) * 128 + row];
         const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
         ls = fmaf(w, ml.y, ls);
-        const float4* src = a.acc + (size_t)(fe.x + k) * W4 * 128 + row;
+        const float4* src = a.acc + (size_t)(fe.x + k * a.gang) * W4 * 128 + row;
 #pragma unroll
         for (int e = 0; e < QPW; ++e) {
             const int c = e * 8 + warp;
@@ -797,34 +810,60 @@ TreePlan tree_plan(int H, int D_H, int R, int D_R, int T) {
     return best;
 }
 
-static size_t tree_slots(int batch, const TreePlan& p, int sms) {
-    return (size_t)sms + (size_t)batch * p.htiles * p.stiles;
+// CTAs of a gang: as many as leave the fewest SMs and the fewest members without a tile, up to 16, more rather than
+// fewer.
+static int tree_gang(int tiles, int sms) {
+    int best = 1;
+    double most = 0;
+    for (int q = 1; q <= 16 && q <= tiles && q <= sms; ++q) {
+        const double use = (double)(sms / q * q) / sms * tiles / ((tiles + q - 1) / q * q);
+        if (use >= most - 0.02) {
+            best = q;
+            most = use > most ? use : most;
+        }
+    }
+    return best;
+}
+
+struct TreeSizes {
+    int gang, gangs, gmax;  // CTAs of a gang, gangs, groups of tiles of a sequence
+    size_t qt, seg, ml, acc;
+};
+static TreeSizes tree_sizes(int H, int D_H, int R, int batch, int T, const TreePlan& p, int sms) {
+    TreeSizes z{};
+    const int tiles = p.htiles * p.stiles;
+    z.gang = tree_gang(tiles, sms);
+    z.gangs = sms / z.gang;
+    z.gmax = (tiles + z.gang - 1) / z.gang;
+    const size_t slots = ((size_t)z.gangs + (size_t)batch * z.gmax) * z.gang;
+    z.qt = align256((size_t)batch * T * H * R * sizeof(float));
+    z.seg = align256((size_t)batch * tiles * sizeof(int2));
+    z.ml = align256(slots * 128 * sizeof(float2));
+    z.acc = align256(slots * 128 * (D_H + R) * sizeof(float));
+    return z;
 }
 
 size_t tree_workspace_bytes(int H, int D_H, int R, int D_R, int batch, int T, int sms) {
-    const TreePlan p = tree_plan(H, D_H, R, D_R, T);
-    const size_t slots = tree_slots(batch, p, sms);
-    return align256((size_t)batch * T * H * R * sizeof(float)) +
-           align256((size_t)batch * p.htiles * p.stiles * sizeof(int2)) + align256(slots * 128 * sizeof(float2)) +
-           slots * 128 * (D_H + R) * sizeof(float) + 256;
+    const TreeSizes z = tree_sizes(H, D_H, R, batch, T, tree_plan(H, D_H, R, D_R, T), sms);
+    return z.qt + z.seg + z.ml + z.acc + 256;  // (never 0)
 }
 
 void tree_carve_workspace(TreeArgs* a, void* ws, int D_H, int R, int D_R, int sms) {
     const TreePlan p = tree_plan(a->d.H, D_H, R, D_R, a->T);
+    const TreeSizes z = tree_sizes(a->d.H, D_H, R, a->batch, a->T, p, sms);
     a->zw = p.zw;
     a->hb = p.hb;
     a->ns = p.ns;
     a->htiles = p.htiles;
     a->tmax = p.htiles * p.stiles;
-    a->ctas = sms;
+    a->gang = z.gang;
+    a->gangs = z.gangs;
+    a->gmax = z.gmax;
     uint8_t* at = static_cast<uint8_t*>(ws);
     a->d.qt = reinterpret_cast<float*>(at);
-    at += align256((size_t)a->batch * a->T * a->d.H * R * sizeof(float));
-    a->seg_table = reinterpret_cast<int2*>(at);
-    at += align256((size_t)a->batch * a->tmax * sizeof(int2));
-    a->ml = reinterpret_cast<float2*>(at);
-    at += align256(tree_slots(a->batch, p, sms) * 128 * sizeof(float2));
-    a->acc = reinterpret_cast<float4*>(at);
+    a->seg_table = reinterpret_cast<int2*>(at += z.qt);
+    a->ml = reinterpret_cast<float2*>(at += z.seg);
+    a->acc = reinterpret_cast<float4*>(at += z.ml);
 }
 
 template <int D_H, int D_R, int ZW>
@@ -833,7 +872,7 @@ static cudaError_t launch_scan_t(const TreeMaps& maps, const TreeArgs& a, int R,
     auto kern = tree_scan_kernel<D_H, D_R, ZW>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(a.ctas), dim3(kThreads), smem, stream, maps, a, R);
+    return launch_dependent(kern, dim3(a.gang * a.gangs), dim3(kThreads), smem, stream, maps, a, R);
 }
 
 cudaError_t launch_tree(const TreeMaps& maps, const TreeArgs& a, int D_H, int R, int D_R, cudaStream_t stream) {

@@ -14,7 +14,7 @@ struct TreeArgs {
     const int32_t* tree_lens;           // [batch], or null: T
     int batch, T;
     int zw, hb, ns, htiles, tmax;  // the tile (below); tmax: tiles of a sequence with T drafted tokens
-    int ctas;                      // of the scan
+    int gang, gangs, gmax;         // CTAs that take neighbouring tiles together, gangs, groups of a sequence's tiles
     int2* seg_table;               // [batch * tmax] first partial and their number
     float2* ml;                    // [slot][128] running max (log2 domain) and sum
     float4* acc;                   // [slot][(D_H + R) / 4][128]
