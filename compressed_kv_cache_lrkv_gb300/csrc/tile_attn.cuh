@@ -49,11 +49,12 @@ __device__ __forceinline__ bool wait_role(uint32_t bar, uint32_t parity, const D
     const bool ok = mbar_look_wait(bar, parity, d.status, d.wait_ns);
     return __all_sync(0xffffffffu, ok);
 }
-// wait_role for a role that one thread plays: a look first, the stop flag only while it has to wait.
+// wait_role for a role that one thread plays: the stop flag and the timer only while it has to wait.
 __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const DecodeArgs& d, volatile int* stop) {
     if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
     const bool nap = d.wait_ns == kWaitLimitNs;
+    if (nap && (mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (nap ? mbar_try_wait(bar, parity) : mbar_test(bar, parity)) return true;
         if (*stop) return false;
@@ -63,9 +64,53 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, const De
         }
     }
 }
+// The same for the 32 threads of a warp together.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const DecodeArgs& d, volatile int* stop) {
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_one(bar, parity, d, stop));
+}
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* status) {
     mbar_wait(bar, parity, status);
     __syncwarp();
+}
+
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t* v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Pairs of fp32 values in one register pair, and what works on both at once.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// max(a, b, c), NaN where one of them is one.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
 }
 
 // max(a, b), NaN where either is one.

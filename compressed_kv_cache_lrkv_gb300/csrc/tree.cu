@@ -155,11 +155,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     unsigned long long* poison = reinterpret_cast<unsigned long long*>(bars + 31);  // [2], by the piece's parity
     long long* plan = reinterpret_cast<long long*>(bars + 33);                      // total, first sequence, its base
     auto B = [&](uint64_t* p) { return smem_u32(p); };
+    // (one arrival a warp: those of 32 lanes on one barrier take their turns)
+    auto arrive = [&](uint64_t* p) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B(p));
+    };
     auto aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
 
     if (threadIdx.x == 32) {
-        mbar_init(B(q_ready), 256);
-        for (int i = 0; i < 3; ++i) mbar_init(B(p_full + i), 128);
+        mbar_init(B(q_ready), 8);
+        for (int i = 0; i < 3; ++i) mbar_init(B(p_full + i), 4);
         poison[0] = poison[1] = 0;
         mbar_init(B(mma_drain), 1);
         for (int i = 0; i < 6; ++i) {
@@ -444,11 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!waited) pdl_wait();  // (this grid's end stands for that of the launches before it)
+                if (piece == 0) pdl_trigger();  // the merge may be set up: its blocks wait for this grid's end
                 waited = true;
                 tmem_wait_st();
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(B(q_ready));
+                arrive(q_ready);
             }
             float mref = -INFINITY, l = 0.f;  // the reference that this group knows, and its sum relative to that
             // After an expired wait the loop goes on without work, so that the groups still meet at their barriers.
@@ -465,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto wait_before = [&]() {  // until the page before has been added to O
-                return wait_role(B(o_done + (vst > 0 ? vst - 1 : VST - 1)), vst > 0 ? vphase : vphase ^ 1, d);
+                return wait_warp(B(o_done + (vst > 0 ? vst - 1 : VST - 1)), vst > 0 ? vphase : vphase ^ 1, d, abort_flag);
             };
             // page ids of 32 pages at a time, the next ones on their way (a load per page, some 700 cycles late, was
             // half of a page's time)
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int blk = __shfl_sync(0xffffffffu, ids, j & 31);
                 const bool good = blk >= 0 && blk < d.num_blocks;
                 const bool inner = good && base + kBlockSize <= L;  // every row sees every token
-                ok = ok && !aborted() && wait_role(B(s_done + kst), kphase, d);
+                ok = ok && wait_warp(B(s_done + kst), kphase, d, abort_flag);
                 uint32_t sv[64];
                 float mx = -INFINITY;
                 if (ok) {
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // Values that not every row sees, or none: cleared where they could spoil a product with a
                         // probability of 0.  Rows behind the end wholly; of a drafted token what is not finite,
                         // which is noted and added at the end to the rows that do see it.
-                        ok = wait_role(B(v_full + vst), vphase, d);
+                        ok = wait_warp(B(v_full + vst), vphase, d, abort_flag);
                         const int vr = row & 63, t = base + vr - L;
                         if (ok && t >= 0) {
                             uint8_t* const v0 = smem + Lay::OFF_V + vst * Lay::V_BYTES;
@@ -535,10 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float m4[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m4[e] = max_nan(__uint_as_float(sv[e]), __uint_as_float(sv[4 + e]));
+                    for (int e = 0; e < 4; ++e)
+                        m4[e] = max3_nan(__uint_as_float(sv[e]), __uint_as_float(sv[4 + e]), __uint_as_float(sv[8 + e]));
 #pragma unroll
-                    for (int e = 8; e < 64; ++e) m4[e & 3] = max_nan(m4[e & 3], __uint_as_float(sv[e]));
-                    mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+                    for (int e = 12; e < 60; e += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            m4[k] = max3_nan(m4[k], __uint_as_float(sv[e + k]), __uint_as_float(sv[e + 4 + k]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m4[k] = max_nan(m4[k], __uint_as_float(sv[60 + k]));
+                    mx = max_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3]);
                     // diag(Q~)'s zeros times another head's NaN or infinity are NaN (and so is what rounding an
                     // infinite product left): such logits are formed again from the row's own head alone.
                     if (__any_sync(0xffffffffu, mx != mx)) {
@@ -575,17 +587,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // p = 2^(s scale log2 e - m), 0 everywhere as long as the row has seen no token
                 const float nm = now == -INFINITY ? -INFINITY : -now;
-                float r4[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t nm2 = pair(__float_as_uint(nm), __float_as_uint(nm));
+                const uint64_t sc2 = pair(__float_as_uint(d.scale_log2), __float_as_uint(d.scale_log2));
+                uint64_t l2[2] = {0, 0};
                 uint32_t pk[32];
 #pragma unroll
                 for (int e = 0; e < 64; e += 2) {
-                    const float x0 = ex2_approx(fmaf(__uint_as_float(sv[e]), d.scale_log2, nm));
-                    const float x1 = ex2_approx(fmaf(__uint_as_float(sv[e + 1]), d.scale_log2, nm));
-                    r4[(e >> 1) & 3] += x0 + x1;
+                    float x0, x1;
+                    unpair(fma2(pair(sv[e], sv[e + 1]), sc2, nm2), x0, x1);
+                    x0 = ex2_approx(x0);
+                    x1 = ex2_approx(x1);
+                    l2[e / 2 & 1] = add2(l2[e / 2 & 1], pair(__float_as_uint(x0), __float_as_uint(x1)));
                     pk[e / 2] = pack_bf16x2(x0, x1);
                 }
                 tmem_st_32x32b_x32(tS, pk);
-                l += (r4[0] + r4[1]) + (r4[2] + r4[3]);
+                {
+                    float x0, x1;
+                    unpair(add2(l2[0], l2[1]), x0, x1);
+                    l += x0 + x1;
+                }
                 // O may only be rescaled once P_{g-1} V_{g-1} has finished accumulating into it
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
                     ok = wait_before();
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) continue;
                 if (!inner) fence_proxy_async_smem();  // cleared values before the tensor cores read them
                 tc_fence_before();
-                mbar_arrive(B(p_full + sb));
+                arrive(p_full + sb);
             }
             // the row's sum over both groups' pages
             sums[half * 128 + row] = make_float2(l, mref);
@@ -685,16 +705,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Merge of a tile's pieces, B_h^V, division by the sum: grid (4 groups of 32 rows, tiles, sequences), block (32, 8).
-// A lane is a row while the pieces are read (consecutive rows' quads lie side by side), columns of the output after.
-template <int D_H, int R>
+// Merge of a tile's pieces, B_h^V, division by the sum: grid (4 groups of 32 rows x D_H / DC groups of DC output columns,
+// tiles, sequences), block (32, 8).  A lane is a row while the pieces are read (consecutive rows' quads lie side by
+// side), output columns after.  Where there are few tiles a block takes few columns (and reads the latents' sums again) and
+// has the loads of four pieces in flight; many tiles are of one or two pieces each, and more blocks fit with one.
+template <int D_H, int R, int DC>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
-    constexpr int W = D_H + R, W4 = W / 4, QPW = (W4 + 7) / 8, DPL = D_H / 32;
+    constexpr int W4 = (D_H + R) / 4, C4 = (DC + R) / 4, QPW = (C4 + 7) / 8, DPL = DC / 32, kPieces = DC == 32 ? 4 : 1;
     const DecodeArgs& d = a.d;
     const int lane = threadIdx.x, warp = threadIdx.y, b = blockIdx.z, t = blockIdx.y;
-    __shared__ float tile[32][W + 1];
+    const int row0 = (blockIdx.x & 3) * 32, row = row0 + lane, d0 = (blockIdx.x >> 2) * DC;
+    __shared__ float tile[32][DC + R + 1];
+    const Seq s = seq_of(a, b);  // (the caller's, not of a launch before this one)
+    const int st_b = max(1, (s.n + a.ns - 1) / a.ns), h0 = t / st_b * a.hb, i0 = t % st_b * a.ns;
+    // four rows of one head per warp (ns is a multiple of 4), DPL output columns per lane
+    const int r0 = warp * 4, h = h0 + (row0 + r0) / a.ns;
+    const bool mine = !s.bad && t < tiles_of(a, s.n) && h < d.H;
+    uint4 f[DPL][R / 8];
+    if (mine) {
+        const uint16_t* bv = d.BV + ((size_t)h * D_H + d0 + lane * DPL) * R;
+#pragma unroll
+        for (int e = 0; e < DPL; ++e)
+#pragma unroll
+            for (int k = 0; k < R / 8; ++k) f[e][k] = *reinterpret_cast<const uint4*>(bv + e * R + k * 8);
+    }
     pdl_wait();  // the scan (in every block: this grid's end stands for that of the launches before it)
-    const Seq s = seq_of(a, b);
     if (s.bad) {  // zeros in all T rows: the tiles of a full sequence share them
         if (t == 0 && blockIdx.x == 0 && lane == 0 && warp == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
         const size_t n = (size_t)a.T * d.H * D_H / 8, step = (size_t)gridDim.x * gridDim.y * 256;
@@ -703,34 +738,55 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
             out[i] = make_uint4(0, 0, 0, 0);
         return;
     }
-    if (t >= tiles_of(a, s.n)) return;
-    const int st_b = (s.n + a.ns - 1) / a.ns;
-    const int row0 = blockIdx.x * 32, row = row0 + lane;
-    auto head = [&](int r) { return t / st_b * a.hb + r / a.ns; };
-    auto token = [&](int r) { return t % st_b * a.ns + r % a.ns; };
-    if (head(row0) >= d.H || (a.ns >= 32 && token(row0) >= s.n)) return;
+    if (t >= tiles_of(a, s.n) || h0 + row0 / a.ns >= d.H || (a.ns >= 32 && i0 + row0 % a.ns >= s.n)) return;
+    const bool live = h0 + row / a.ns < d.H && i0 + row % a.ns < s.n;
     const int2 fe = a.seg_table[b * a.tmax + t];
-    float M = -INFINITY;
-    for (int k = 0; k < fe.y; ++k) M = fmaxf(M, a.ml[(size_t)(fe.x + k * a.gang) * 128 + row].x);
-    float ls = 0.f;
+    float M = -INFINITY, ls = 0.f;
     float4 x[QPW];
 #pragma unroll
     for (int e = 0; e < QPW; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < fe.y; ++k) {
-        const float2 ml = a.ml[(size_t)(fe.x + k * a.gang) * 128 + row];
-        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-        ls = fmaf(w, ml.y, ls);
-        const float4* src = a.acc + (size_t)(fe.x + k * a.gang) * W4 * 128 + row;
+    const float2* const ml0 = a.ml + (size_t)fe.x * 128 + row;
+    const float4* const acc0 = a.acc + (size_t)fe.x * W4 * 128 + row;
+    for (int k0 = 0; live && k0 < fe.y; k0 += kPieces) {
+        float2 ml[kPieces];
+        float4 y[kPieces][QPW];
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const bool there = k0 + k < fe.y;
+            ml[k] = there ? ml0[(size_t)(k0 + k) * a.gang * 128] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < QPW; ++e) {
+                const int c = e * 8 + warp, at = c < DC / 4 ? d0 / 4 + c : D_H / 4 + c - DC / 4;
+                y[k][e] = there && c < C4 ? acc0[((size_t)(k0 + k) * a.gang * W4 + at) * 128]
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) mn = fmaxf(mn, ml[k].x);
+        if (mn == -INFINITY) continue;
+        const float sc = M == -INFINITY ? 0.f : exp2f(M - mn);
+        M = mn;
+        ls *= sc;
 #pragma unroll
         for (int e = 0; e < QPW; ++e) {
-            const int c = e * 8 + warp;
-            if (c >= W4) break;
-            const float4 y = src[(size_t)c * 128];
-            if (w == 0.f) continue;
-            x[e].x = fmaf(w, y.x, x[e].x);
-            x[e].y = fmaf(w, y.y, x[e].y);
-            x[e].z = fmaf(w, y.z, x[e].z);
-            x[e].w = fmaf(w, y.w, x[e].w);
+            x[e].x *= sc;
+            x[e].y *= sc;
+            x[e].z *= sc;
+            x[e].w *= sc;
+        }
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            if (ml[k].x == -INFINITY) continue;  // a piece of which the row sees nothing
+            const float w = exp2f(ml[k].x - mn);
+            ls = fmaf(w, ml[k].y, ls);
+#pragma unroll
+            for (int e = 0; e < QPW; ++e) {
+                x[e].x = fmaf(w, y[k][e].x, x[e].x);
+                x[e].y = fmaf(w, y[k][e].y, x[e].y);
+                x[e].z = fmaf(w, y[k][e].z, x[e].z);
+                x[e].w = fmaf(w, y[k][e].w, x[e].w);
+            }
         }
     }
     // (the sum is 0 where the row sees no token: zeros)
@@ -738,50 +794,43 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
 #pragma unroll
     for (int e = 0; e < QPW; ++e) {
         const int c = (e * 8 + warp) * 4;
-        if (c >= W) break;
+        if (c >= DC + R) break;
         tile[lane][c] = x[e].x * inv;
         tile[lane][c + 1] = x[e].y * inv;
         tile[lane][c + 2] = x[e].z * inv;
         tile[lane][c + 3] = x[e].w * inv;
     }
     __syncthreads();
-    // four rows of one head per warp (ns is a multiple of 4), DPL output columns per lane
-    const int r0 = warp * 4, h = head(row0 + r0);
-    if (h >= d.H) return;
-    const uint16_t* bv = d.BV + ((size_t)h * D_H + lane * DPL) * R;
-    float y[4][DPL];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int e = 0; e < DPL; ++e) y[r][e] = tile[r0 + r][lane * DPL + e];
-#pragma unroll
-    for (int k = 0; k < R; k += 8) {
-        uint4 f[DPL];
-#pragma unroll
-        for (int e = 0; e < DPL; ++e) f[e] = *reinterpret_cast<const uint4*>(bv + e * R + k);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            float z[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = tile[r0 + r][D_H + k + i];
-#pragma unroll
-            for (int e = 0; e < DPL; ++e) {
-                y[r][e] = fmaf(bf16lo(f[e].x), z[0], fmaf(bf16hi(f[e].x), z[1], y[r][e]));
-                y[r][e] = fmaf(bf16lo(f[e].y), z[2], fmaf(bf16hi(f[e].y), z[3], y[r][e]));
-                y[r][e] = fmaf(bf16lo(f[e].z), z[4], fmaf(bf16hi(f[e].z), z[5], y[r][e]));
-                y[r][e] = fmaf(bf16lo(f[e].w), z[6], fmaf(bf16hi(f[e].w), z[7], y[r][e]));
-            }
-        }
-    }
+    if (!mine) return;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int i = token(row0 + r0 + r);
+        const int i = i0 + (row0 + r0 + r) % a.ns;
         if (i >= s.n) continue;
-        uint16_t* out = d.out + (((size_t)b * a.T + i) * d.H + h) * D_H + lane * DPL;
-        if (DPL == 4)
-            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(y[r][0], y[r][1]), pack_bf16x2(y[r][2], y[r][3]));
-        else
-            *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(y[r][0], y[r][1]);
+        float y[DPL];
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) y[e] = tile[r0 + r][lane * DPL + e];
+#pragma unroll
+        for (int k = 0; k < R / 8; ++k) {
+            float z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = tile[r0 + r][DC + k * 8 + j];
+#pragma unroll
+            for (int e = 0; e < DPL; ++e) {
+                y[e] = fmaf(bf16lo(f[e][k].x), z[0], fmaf(bf16hi(f[e][k].x), z[1], y[e]));
+                y[e] = fmaf(bf16lo(f[e][k].y), z[2], fmaf(bf16hi(f[e][k].y), z[3], y[e]));
+                y[e] = fmaf(bf16lo(f[e][k].z), z[4], fmaf(bf16hi(f[e][k].z), z[5], y[e]));
+                y[e] = fmaf(bf16lo(f[e][k].w), z[6], fmaf(bf16hi(f[e][k].w), z[7], y[e]));
+            }
+        }
+        uint16_t* out = d.out + (((size_t)b * a.T + i) * d.H + h) * D_H + d0 + lane * DPL;
+        if (DPL == 4) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[DPL - 2], y[DPL - 1]));
+        } else if (DPL == 2) {
+            *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(y[0], y[DPL - 1]);
+        } else {
+            const __nv_bfloat16 o = __float2bfloat16_rn(y[0]);
+            *out = *reinterpret_cast<const uint16_t*>(&o);
+        }
     }
 }
 
@@ -887,9 +936,13 @@ cudaError_t launch_tree(const TreeMaps& maps, const TreeArgs& a, int D_H, int R,
     LRKV_TS(64, 0) LRKV_TS(64, 64) LRKV_TS(128, 0) LRKV_TS(128, 64)
 #undef LRKV_TS
     if (e != cudaSuccess) return e;
-#define LRKV_TC(DH, RR)                                                                                          \
-    if (D_H == DH && R == RR)                                                                                    \
-        return launch_dependent(tree_combine_kernel<DH, RR>, dim3(4, a.tmax, a.batch), dim3(32, 8), 0, stream, a);
+    const bool few = (long long)a.tmax * a.batch * 4 <= 4 * a.gang * a.gangs;  // blocks for fewer than four an SM
+#define LRKV_TC(DH, RR)                                                                                             \
+    if (D_H == DH && R == RR)                                                                                       \
+        return few ? launch_dependent(tree_combine_kernel<DH, RR, 32>, dim3(4 * (DH / 32), a.tmax, a.batch),        \
+                                      dim3(32, 8), 0, stream, a)                                                    \
+                   : launch_dependent(tree_combine_kernel<DH, RR, DH>, dim3(4, a.tmax, a.batch), dim3(32, 8), 0,    \
+                                      stream, a);
     LRKV_TC(64, 8) LRKV_TC(64, 16) LRKV_TC(64, 32) LRKV_TC(128, 8) LRKV_TC(128, 16) LRKV_TC(128, 32)
 #undef LRKV_TC
     return cudaErrorInvalidValue;
