@@ -534,27 +534,24 @@ def rope_plan(d_rot: int, layout: str = "interleaved", base: float = 10000.0, sc
     return plan
 
 
-def _rows(t, index) -> RowsStruct:
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"rows {tuple(t.shape)}, strides {t.stride()}: expected [rows, heads, width], last stride 1")
-    return RowsStruct(_ptr(t), t.shape[0], t.stride(0), t.stride(1), _ptr(index))
-
-
 def lrkv_rope(plan: RopePlan, x, y, positions, begin: int = 0, x_rows=None, y_rows=None, transpose: bool = False,
               status=None, stream=None):
     """y = x with values [begin, begin + plan.d_rot) of every head rotated at positions [n] (int32): x, y
     [rows, heads, width] of bf16 or fp32 (y is x: in place); x_rows, y_rows [n] int32 pick rows."""
     n = positions.shape[0]
-    for index in (x_rows, y_rows):
-        if index is not None and index.shape[0] != n:
-            raise ValueError(f"{index.shape[0]} row indices for {n} positions")
-    if x.dtype is not y.dtype or x.dtype not in _ROPE_TYPES or x.shape[1:] != y.shape[1:]:
-        raise ValueError(f"x {tuple(x.shape)} of {x.dtype}, y {tuple(y.shape)} of {y.dtype}: expected equal heads and "
-                         "widths in bfloat16 or float32")
-    xs, ys = _rows(x, x_rows), _rows(y, y_rows)
-    rc = load().lrkv_rope(ctypes.byref(plan), _ROPE_TYPES[x.dtype], n, x.shape[1], x.shape[2], begin,
-                          ctypes.byref(xs), ctypes.byref(ys), _ptr(positions), int(transpose), _ptr(status),
-                          _stream(stream))
+    xs, xt = x.shape, x.stride()
+    ys, yt = (xs, xt) if y is x else (y.shape, y.stride())
+    kind = _ROPE_TYPES.get(x.dtype)
+    if (kind is None or y.dtype is not x.dtype or len(xs) != 3 or len(ys) != 3 or xs[1] != ys[1] or xs[2] != ys[2] or
+            xt[2] != 1 or yt[2] != 1):
+        raise ValueError(f"x {tuple(xs)} of {x.dtype}, strides {xt}; y {tuple(ys)} of {y.dtype}, strides {yt}: expected "
+                         "[rows, heads, width] of equal heads and widths, bfloat16 or float32, last stride 1")
+    if (x_rows is not None and x_rows.shape[0] != n) or (y_rows is not None and y_rows.shape[0] != n):
+        raise ValueError(f"row indices for other than {n} positions")
+    xr = RowsStruct(x.data_ptr(), xs[0], xt[0], xt[1], _ptr(x_rows))
+    yr = RowsStruct(y.data_ptr(), ys[0], yt[0], yt[1], _ptr(y_rows))
+    rc = load().lrkv_rope(ctypes.byref(plan), kind, n, xs[1], xs[2], begin, ctypes.byref(xr), ctypes.byref(yr),
+                          _ptr(positions), 1 if transpose else 0, _ptr(status), _stream(stream))
     _check(rc, "lrkv_rope")
 
 
@@ -587,41 +584,47 @@ class Pools:
         return cls([(cache.rows if isinstance(cache, QuantCache) else cache).unsqueeze(0)])
 
 
+_I32 = torch.int32
+
+
 def _page_table(refs, block_table, seq_lens):
-    for t in (refs, block_table, seq_lens):
-        if t.dtype is not torch.int32 or not t.is_contiguous():
-            raise ValueError(f"{tuple(t.shape)} of {t.dtype}: refs, block table and lengths are contiguous int32")
-    if block_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError(f"block table of {block_table.shape[0]} sequences, {seq_lens.shape[0]} lengths")
-    return block_table.shape[0]
+    """Checks of what the page calls write; the table's shape."""
+    if (refs.dtype is not _I32 or block_table.dtype is not _I32 or seq_lens.dtype is not _I32 or
+            not refs.is_contiguous() or not block_table.is_contiguous() or not seq_lens.is_contiguous()):
+        raise ValueError(f"counts or paths of {refs.dtype}, block table of {block_table.dtype}, lengths of "
+                         f"{seq_lens.dtype}: expected contiguous int32")
+    shape = block_table.shape
+    if shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"block table of {shape[0]} sequences, {seq_lens.shape[0]} lengths")
+    return shape
 
 
 def lrkv_pages_reserve(refs, block_table, seq_lens, new_tokens, status=None, stream=None):
     """Pages for new_tokens [B] more tokens of every sequence, from the pages with count 0 in refs [num_blocks]."""
-    B = _page_table(refs, block_table, seq_lens)
+    B, width = _page_table(refs, block_table, seq_lens)
     _same_length(seq_lens, new_tokens)
-    rc = load().lrkv_pages_reserve(refs.shape[0], _ptr(refs), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+    rc = load().lrkv_pages_reserve(refs.shape[0], _ptr(refs), _ptr(block_table), width, _ptr(seq_lens),
                                    _ptr(new_tokens), B, _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_reserve")
 
 
 def lrkv_pages_fork(pools: Pools, refs, block_table, seq_lens, parents, children, status=None, stream=None):
     """Sequences children [n] become copies of sequences parents [n], sharing their full pages."""
-    B = _page_table(refs, block_table, seq_lens)
+    B, width = _page_table(refs, block_table, seq_lens)
     if refs.shape[0] != pools.c.num_blocks:
         raise ValueError(f"{refs.shape[0]} counts for {pools.c.num_blocks} pages")
-    rc = load().lrkv_pages_fork(ctypes.byref(pools.c), _ptr(refs), _ptr(block_table), block_table.shape[1],
-                                _ptr(seq_lens), B, _ptr(parents), _ptr(children), _same_length(parents, children),
+    rc = load().lrkv_pages_fork(ctypes.byref(pools.c), _ptr(refs), _ptr(block_table), width, _ptr(seq_lens),
+                                B, _ptr(parents), _ptr(children), _same_length(parents, children),
                                 _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_fork")
 
 
 def lrkv_pages_free(refs, block_table, seq_lens, seqs, keep_lens=None, status=None, stream=None):
     """Sequences seqs [n] give back their pages behind keep_lens [B] tokens (None: all)."""
-    B = _page_table(refs, block_table, seq_lens)
+    B, width = _page_table(refs, block_table, seq_lens)
     if keep_lens is not None:
         _same_length(seq_lens, keep_lens)
-    rc = load().lrkv_pages_free(refs.shape[0], _ptr(refs), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+    rc = load().lrkv_pages_free(refs.shape[0], _ptr(refs), _ptr(block_table), width, _ptr(seq_lens), B,
                                 _ptr(seqs), seqs.shape[0], _ptr(keep_lens), _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_free")
 
@@ -636,10 +639,10 @@ def lrkv_pages_copy(src: Pools, src_pages, dst: Pools, dst_pages, status=None, s
 def lrkv_cache_compact(pools: Pools, block_table, seq_lens, path, path_lens, new_lens=None, status=None, stream=None):
     """Rows seq_lens[b] + path[b, i] -> seq_lens[b] + i, i < path_lens[b]; new_lens = seq_lens + path_lens (None: in
     place)."""
-    B = _page_table(path, block_table, seq_lens)
+    B, width = _page_table(path, block_table, seq_lens)
     _same_length(seq_lens, path)
     _same_length(seq_lens, path_lens)
-    rc = load().lrkv_cache_compact(ctypes.byref(pools.c), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+    rc = load().lrkv_cache_compact(ctypes.byref(pools.c), _ptr(block_table), width, _ptr(seq_lens), B,
                                    _ptr(path), _ptr(path_lens), path.shape[1], _ptr(new_lens), _ptr(status),
                                    _stream(stream))
     _check(rc, "lrkv_cache_compact")

@@ -1127,7 +1127,9 @@ lrkv_status lrkv_pages_copy(const lrkv_pools* src, const int32_t* src_pages, con
     if (n < 0 || n > (1 << 20)) return fail(LRKV_ERR_INVALID_ARG, "n %d (0..2^20)", n);
     if (n == 0) return ok();
     if (!src_pages || !dst_pages) return fail(LRKV_ERR_INVALID_ARG, "src_pages or dst_pages is NULL");
-    return cuda_status(lrkv::launch_pages_copy(f, t, src_pages, dst_pages, n, status_dev,
+    DeviceInfo di;
+    if ((s = device_info(&di)) != LRKV_OK) return s;
+    return cuda_status(lrkv::launch_pages_copy(f, t, src_pages, dst_pages, n, di.sms, status_dev,
                                                static_cast<cudaStream_t>(stream)),
                        "lrkv_pages_copy launch");
 }

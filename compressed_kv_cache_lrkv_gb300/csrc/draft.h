@@ -46,7 +46,7 @@ cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PoolArgs& src, const PoolArgs& dst, const int32_t* src_pages,
-                              const int32_t* dst_pages, int n, uint32_t* status, cudaStream_t stream);
+                              const int32_t* dst_pages, int n, int sms, uint32_t* status, cudaStream_t stream);
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t stream);
 
 }  // namespace lrkv

@@ -7,6 +7,7 @@
 
 #include "draft.h"
 #include "lrkv_internal.cuh"
+#include "tile_attn.cuh"
 
 namespace lrkv {
 
@@ -60,16 +61,18 @@ __device__ int search_free(const int32_t* refs, int num_blocks, int want, int* w
     for (int p0 = 0; p0 < num_blocks && found < want; p0 += kPlanThreads * kPerThread) {
         const int p = p0 + threadIdx.x * kPerThread;
         uint32_t free = 0;
+        if (p + kPerThread <= num_blocks) {
+            int4 r[kPerThread / 4];
 #pragma unroll
-        for (int k = 0; k < kPerThread; k += 4) {
-            if (p + k + 4 <= num_blocks) {
-                const int4 r = __ldcg(reinterpret_cast<const int4*>(refs + p + k));
-                free |= (uint32_t)(r.x == 0) << k | (uint32_t)(r.y == 0) << (k + 1) | (uint32_t)(r.z == 0) << (k + 2) |
-                        (uint32_t)(r.w == 0) << (k + 3);
-            } else {
-                for (int e = k; e < k + 4; ++e)
-                    if (p + e < num_blocks && __ldcg(refs + p + e) == 0) free |= 1u << e;
-            }
+            for (int k = 0; k < kPerThread / 4; ++k) r[k] = __ldcg(reinterpret_cast<const int4*>(refs + p) + k);
+#pragma unroll
+            for (int k = 0; k < kPerThread / 4; ++k)
+                free |= ((uint32_t)(r[k].x == 0) | (uint32_t)(r[k].y == 0) << 1 | (uint32_t)(r[k].z == 0) << 2 |
+                         (uint32_t)(r[k].w == 0) << 3)
+                        << (4 * k);
+        } else {
+            for (int e = 0; e < kPerThread; ++e)
+                if (p + e < num_blocks && __ldcg(refs + p + e) == 0) free |= 1u << e;
         }
         const int c = __popc(free);
         int total;
@@ -97,18 +100,24 @@ __device__ __forceinline__ int owner(const int* pre, int n, int rank) {
     return lo;
 }
 
-// need[0..n) granted from the free pages, whole requests or none, in order; afterwards need holds exclusive
-// prefix sums of what is granted.  Returns the total; refused(i) for requests that do not fit.
-template <class F>
-__device__ int grant(int* need, int n, const int32_t* refs, int num_blocks, int* warp_sums, F&& refused) {
+// need[0..n) granted from the free pages, whole requests or none, in order (refused(i) for those that do not fit);
+// give(i, k, granted, page) is called for the k-th of the `granted` pages of request i.  The first search keeps the pages it finds, up to kPicked: they are all that most calls need.
+constexpr int kPicked = 2048;
+template <class F, class G>
+__device__ void grant(int* need, int n, const int32_t* refs, int num_blocks, int* warp_sums, int* picked, F&& refused,
+                      G&& give) {
     int total = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
         int t;
         block_scan(i0 + (int)threadIdx.x < n ? need[i0 + threadIdx.x] : 0, warp_sums, &t);
         total += t;
     }
-    const int have = search_free(refs, num_blocks, total, warp_sums, [](int, int) {});
+    if (total == 0) return;
+    const int have = search_free(refs, num_blocks, total, warp_sums, [&](int page, int rank) {
+        if (rank < kPicked) picked[rank] = page;
+    });
     if (have < total) {
+        __syncthreads();
         if (threadIdx.x == 0) {
             int left = have;
             for (int i = 0; i < n; ++i) {
@@ -122,7 +131,16 @@ __device__ int grant(int* need, int n, const int32_t* refs, int num_blocks, int*
         }
         __syncthreads();
     }
-    return prefix_of_needs(need, n, warp_sums);
+    total = prefix_of_needs(need, n, warp_sums);
+    auto hand = [&](int page, int rank) {
+        const int i = owner(need, n, rank);
+        give(i, rank - need[i], (i + 1 < n ? need[i + 1] : total) - need[i], page);
+    };
+    if (total <= kPicked) {
+        for (int rank = threadIdx.x; rank < total; rank += kPlanThreads) hand(picked[rank], rank);
+    } else {
+        search_free(refs, num_blocks, total, warp_sums, hand);
+    }
 }
 
 __device__ __forceinline__ int pages_of(long long tokens) { return (int)((tokens + kBlockSize - 1) / kBlockSize); }
@@ -138,7 +156,7 @@ __device__ __forceinline__ void give_back(int32_t* refs, int num_blocks, int pag
 
 // ---------------------------------------------------------------- reserve: one block
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a) {
-    __shared__ int need[LRKV_MAX_PAGE_BATCH], warp_sums[32];
+    __shared__ int need[LRKV_MAX_PAGE_BATCH], warp_sums[32], picked[kPicked];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // a warp per sequence: its first empty entry from the page of its length on
     for (int b = warp; b < a.batch; b += kPlanThreads / 32) {
@@ -161,16 +179,13 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a)
         if (lane == 0) need[b] = want - held;
     }
     __syncthreads();
-    const int total = grant(need, a.batch, a.refs, a.num_blocks, warp_sums,
-                            [&](int) { set_status(a.status, LRKV_DEV_NO_PAGES); });
-    search_free(a.refs, a.num_blocks, total, warp_sums, [&](int page, int rank) {
-        const int b = owner(need, a.batch, rank);
-        // the granted entries are the last ones of what the sequence asked for
-        const int granted = (b + 1 < a.batch ? need[b + 1] : total) - need[b];
-        const int last = pages_of((long long)a.lens[b] + a.b[b]);
-        a.table[(size_t)b * a.max_pages + last - granted + (rank - need[b])] = page;
-        a.refs[page] = 1;
-    });
+    grant(need, a.batch, a.refs, a.num_blocks, warp_sums, picked, [&](int) { set_status(a.status, LRKV_DEV_NO_PAGES); },
+          [&](int b, int k, int granted, int page) {
+              // (the granted entries are the last ones of what the sequence asked for)
+              const int want = pages_of((long long)a.lens[b] + a.b[b]);
+              a.table[(size_t)b * a.max_pages + want - granted + k] = page;
+              a.refs[page] = 1;
+          });
 }
 
 // ---------------------------------------------------------------- fork
@@ -194,11 +209,17 @@ __device__ uint32_t fork_refused(const PageArgs& a, int i, int lane, int lanes, 
     return all(bad);
 }
 
+// One block: a warp per fork looks, gives the child's pages back, and passes the parent's on; eight entries of a row
+// per lane on their way at once (one after the other: 64 forks of 100 pages 26 us).
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs a) {
-    // need: pages asked for, then their prefix sums; full: the full pages that a fork passes on (-1: left out)
-    __shared__ int need[LRKV_MAX_PAGE_BATCH], warp_sums[32];
-    extern __shared__ int full[];
+    // need: pages asked for, then their prefix sums; full: the full pages that a fork passes on (-1: left out, -2: no
+    // page was left for the last, partly filled one)
+    extern __shared__ int sh[];
+    int *const need = sh, *const full = sh + a.n;
+    __shared__ int warp_sums[32], picked[kPicked];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto row_of = [&](int s) { return a.table + (size_t)s * a.max_pages; };
+    constexpr int E = 8;
     for (int i = warp; i < a.n; i += kPlanThreads / 32) {
         const uint32_t bad = fork_refused(a, i, lane, 32, [](uint32_t x) { return __reduce_or_sync(0xffffffffu, x); });
         if (lane == 0) {
@@ -207,39 +228,56 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
             full[i] = bad ? -1 : L / kBlockSize;
             need[i] = L % kBlockSize != 0;
         }
-    }
-    __syncthreads();
-    // what the children held goes back first
-    for (int i = warp; i < a.n; i += kPlanThreads / 32) {
-        if (full[i] < 0) continue;
-        int32_t* row = a.table + (size_t)a.b[i] * a.max_pages;
-        for (int k = lane; k < a.max_pages; k += 32) {
-            const int page = row[k];
-            if (page >= 0) give_back(a.refs, a.num_blocks, page, a.status);
-            row[k] = -1;
+        if (bad) continue;
+        // what the child held goes back (parents' rows are not written here: no child is a parent)
+        int32_t* row = row_of(a.b[i]);
+        for (int k0 = 0; k0 < a.max_pages; k0 += 32 * E) {
+            int page[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int k = k0 + e * 32 + lane;
+                page[e] = k < a.max_pages ? row[k] : -1;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (page[e] >= 0) {
+                    give_back(a.refs, a.num_blocks, page[e], a.status);
+                    row[k0 + e * 32 + lane] = -1;
+                }
         }
     }
     __threadfence();
     __syncthreads();
-    const int total = grant(need, a.n, a.refs, a.num_blocks, warp_sums, [&](int i) {
-        set_status(a.status, LRKV_DEV_NO_PAGES);
-        full[i] = -2;  // the child stays empty
-    });
-    search_free(a.refs, a.num_blocks, total, warp_sums, [&](int page, int rank) {
-        const int i = owner(need, a.n, rank);
-        a.table[(size_t)a.b[i] * a.max_pages + full[i]] = page;
-        a.refs[page] = 1;
-    });
+    grant(need, a.n, a.refs, a.num_blocks, warp_sums, picked,
+          [&](int i) {
+              set_status(a.status, LRKV_DEV_NO_PAGES);
+              full[i] = -2;  // the child stays empty
+          },
+          [&](int i, int, int, int page) {
+              row_of(a.b[i])[full[i]] = page;
+              a.refs[page] = 1;
+          });
     __syncthreads();
     for (int i = warp; i < a.n; i += kPlanThreads / 32) {
-        if (full[i] == -1) continue;
-        const int p = a.a[i], c = a.b[i];
-        for (int k = lane; k < full[i]; k += 32) {
-            const int page = a.table[(size_t)p * a.max_pages + k];
-            a.table[(size_t)c * a.max_pages + k] = page;
-            atomicAdd(a.refs + page, 1);
+        const int f = full[i];
+        if (f == -1) continue;
+        const int32_t* from = row_of(a.a[i]);
+        int32_t* to = row_of(a.b[i]);
+        for (int k0 = 0; k0 < f; k0 += 32 * E) {
+            int page[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int k = k0 + e * 32 + lane;
+                page[e] = k < f ? from[k] : -1;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (page[e] >= 0) {
+                    to[k0 + e * 32 + lane] = page[e];
+                    atomicAdd(a.refs + page[e], 1);
+                }
         }
-        if (lane == 0) a.lens[c] = full[i] < 0 ? 0 : a.lens[p];
+        if (lane == 0) a.lens[a.b[i]] = f < 0 ? 0 : a.lens[a.a[i]];
     }
 }
 
@@ -253,18 +291,29 @@ __device__ __forceinline__ int pool_of(const PoolArgs& p, int* u) {
 // Rows of the children's last pages: grid (units in pieces, forks, layers).
 __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, const PageArgs a) {
     const int i = blockIdx.y;
+    pdl_wait();
     if (fork_refused(a, i, threadIdx.x, 256, [](uint32_t x) { return (uint32_t)__syncthreads_or(x != 0); })) return;
     const int par = a.a[i], c = a.b[i], L = a.lens[c];  // (0 where no page was left for the child)
     if (L % kBlockSize == 0) return;
     const int k = L / kBlockSize, from = a.table[(size_t)par * a.max_pages + k], to = a.table[(size_t)c * a.max_pages + k];
     const int rows = L % kBlockSize, n = rows * p.units;
-    for (int e = blockIdx.x * 256 + threadIdx.x; e < n; e += gridDim.x * 256) {
-        int pool = 0, u = e;
+    constexpr int E = 8;
+    uint4 v[E];
+    uint4* out[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        int pool = 0, u = (blockIdx.x * E + e) * 256 + threadIdx.x;
+        out[e] = nullptr;
+        if (u >= n) continue;
         while (pool + 1 < p.pools && u >= p.u[pool] * rows) u -= p.u[pool++] * rows;
         uint4* b = p.base[pool] + (size_t)blockIdx.z * p.layer[pool];
         const size_t page = (size_t)kBlockSize * p.u[pool];
-        b[to * page + u] = b[from * page + u];
+        v[e] = b[from * page + u];
+        out[e] = b + to * page + u;
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (out[e]) *out[e] = v[e];
 }
 
 // ---------------------------------------------------------------- free: a block per sequence
@@ -292,33 +341,86 @@ __global__ void __launch_bounds__(256) free_kernel(const PageArgs a) {
 }
 
 // ---------------------------------------------------------------- copy of whole pages
-constexpr int kCopyUnroll = 4;
-__global__ void __launch_bounds__(256) copy_kernel(const PoolArgs src, const PoolArgs dst, const int32_t* from,
-                                                   const int32_t* to, const int pieces, uint32_t* status) {
-    const int i = blockIdx.x / pieces, piece = blockIdx.x - i * pieces;
-    const int f = from[i], t = to[i];
-    if (f < 0 || t < 0) return;
-    if (f >= src.num_blocks || t >= dst.num_blocks) {
-        if (threadIdx.x == 0) set_status(status, LRKV_DEV_BAD_BLOCK);
-        return;
+// A page's rows lie together in each pool, so it is moved in pieces of up to 16 KB by bulk copies, through a ring of
+// stages in shared memory.  A warp is a block: its lanes work out the next 32 pieces, one of them issues the copies.
+// 1,024 pages of 295 KB: 164 us with four 16-byte loads a thread, whose blocks came and went.
+constexpr uint32_t kPiece = 16384;
+constexpr int kStages = 6, kLag = 4;  // stages; pieces between a load's issue and its store's
+struct CopyArgs {
+    PoolArgs src, dst;
+    const int32_t *from, *to;
+    long long items;
+    int parts;  // pieces of a page in all pools
+    uint32_t* status;
+};
+__global__ void __launch_bounds__(32) copy_kernel(const __grid_constant__ CopyArgs a) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* const ring = raw + ((128u - (smem_u32(raw) & 127u)) & 127u);
+    __shared__ uint64_t full[kStages];
+    __shared__ uint4* dst[kStages];
+    __shared__ uint32_t size[kStages];
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(full + i), 1);
+        fence_mbar_init();
     }
-    const int n = kBlockSize * src.units;
-    uint4 v[kCopyUnroll];
-    uint4* out[kCopyUnroll];
-#pragma unroll
-    for (int e = 0; e < kCopyUnroll; ++e) {
-        int u = (piece * kCopyUnroll + e) * 256 + threadIdx.x;
-        out[e] = nullptr;
-        if (u >= n) continue;
-        int p = 0;
-        while (p + 1 < src.pools && u >= kBlockSize * src.u[p]) u -= kBlockSize * src.u[p++];
-        const size_t page = (size_t)kBlockSize * src.u[p];
-        v[e] = __ldcs(src.base[p] + (size_t)blockIdx.y * src.layer[p] + f * page + u);
-        out[e] = dst.base[p] + (size_t)blockIdx.y * dst.layer[p] + t * page + u;
+    __syncwarp();
+    int loaded = 0, stored = 0;
+    bool ok = true;
+    auto store = [&]() {  // the oldest piece on its way
+        const int st = stored % kStages;
+        if (!mbar_wait(smem_u32(full + st), (stored / kStages) & 1, a.status)) return false;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst[st]),
+                     "r"(smem_u32(ring) + st * kPiece), "r"(size[st])
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        ++stored;
+        return true;
+    };
+    for (long long base = blockIdx.x; base < a.items; base += (long long)gridDim.x * 32) {
+        const long long item = base + (long long)gridDim.x * lane;
+        const uint4* s = nullptr;
+        uint4* t = nullptr;
+        uint32_t bytes = 0;
+        if (item < a.items) {
+            const long long page = item / a.parts, i = page / a.src.layers;
+            int part = (int)(item - page * a.parts);
+            const int layer = (int)(page - i * a.src.layers), f = a.from[i], to = a.to[i];
+            if (f >= 0 && to >= 0) {
+                if (f >= a.src.num_blocks || to >= a.dst.num_blocks) {
+                    set_status(a.status, LRKV_DEV_BAD_BLOCK);
+                } else {
+                    int p = 0;
+                    auto pieces = [&](int k) { return (int)((kBlockSize * a.src.u[k] * 16 + kPiece - 1) / kPiece); };
+                    while (part >= pieces(p)) part -= pieces(p++);
+                    const size_t u = (size_t)kBlockSize * a.src.u[p], at = (size_t)part * (kPiece / 16);
+                    s = a.src.base[p] + (size_t)layer * a.src.layer[p] + f * u + at;
+                    t = a.dst.base[p] + (size_t)layer * a.dst.layer[p] + to * u + at;
+                    bytes = (uint32_t)((u - at < kPiece / 16 ? u - at : kPiece / 16) * 16);
+                }
+            }
+        }
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t n = __shfl_sync(0xffffffffu, bytes, j);
+            const uint64_t sp = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(s), j);
+            const uint64_t tp = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(t), j);
+            if (lane != 0 || n == 0 || !ok) continue;
+            const int st = loaded % kStages;
+            // the stage's last store has read it: behind it kStages - kLag - 1 others have been issued
+            if (loaded >= kStages) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kStages - kLag - 1) : "memory");
+            dst[st] = reinterpret_cast<uint4*>(tp);
+            size[st] = n;
+            mbar_arrive_expect_tx(smem_u32(full + st), n);
+            bulk_load(smem_u32(ring) + st * kPiece, reinterpret_cast<const void*>(sp), n, smem_u32(full + st));
+            if (++loaded > kLag) ok = store();
+        }
     }
-#pragma unroll
-    for (int e = 0; e < kCopyUnroll; ++e)
-        if (out[e]) __stcs(out[e], v[e]);
+    if (lane == 0) {
+        while (ok && stored < loaded) ok = store();
+        // (after an expired wait: what is still on its way lands before the block gives up its shared memory)
+        for (; stored < loaded; ++stored) mbar_wait(smem_u32(full + stored % kStages), (stored / kStages) & 1, a.status);
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
 }
 
 // ---------------------------------------------------------------- compact: a cluster per sequence
@@ -388,14 +490,17 @@ cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t stream) {
-    const int smem = a.n * (int)sizeof(int);
-    const cudaError_t e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               LRKV_MAX_PAGE_BATCH * (int)sizeof(int));
-    if (e != cudaSuccess) return e;
+    const size_t smem = 2 * (size_t)a.n * sizeof(int);
+    if (smem > 32768) {  // (beside 8 KB of its own)
+        const cudaError_t e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   2 * LRKV_MAX_PAGE_BATCH * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
     fork_plan_kernel<<<1, kPlanThreads, smem, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     const int pieces = (kBlockSize * p.units + 256 * 8 - 1) / (256 * 8);
-    fork_copy_kernel<<<dim3(pieces, a.n, p.layers), 256, 0, stream>>>(p, a);
-    return cudaGetLastError();
+    return launch_dependent(fork_copy_kernel, dim3(pieces, a.n, p.layers), dim3(256), 0, stream, p, a);
 }
 
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream) {
@@ -404,10 +509,14 @@ cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_pages_copy(const PoolArgs& src, const PoolArgs& dst, const int32_t* src_pages,
-                              const int32_t* dst_pages, int n, uint32_t* status, cudaStream_t stream) {
-    const int pieces = (kBlockSize * src.units + 256 * kCopyUnroll - 1) / (256 * kCopyUnroll);
-    copy_kernel<<<dim3((unsigned)pieces * n, src.layers), 256, 0, stream>>>(src, dst, src_pages, dst_pages, pieces,
-                                                                            status);
+                              const int32_t* dst_pages, int n, int sms, uint32_t* status, cudaStream_t stream) {
+    CopyArgs a{src, dst, src_pages, dst_pages, 0, 0, status};
+    for (int p = 0; p < src.pools; ++p) a.parts += (int)((kBlockSize * src.u[p] * 16 + kPiece - 1) / kPiece);
+    a.items = (long long)n * src.layers * a.parts;
+    constexpr int smem = kStages * (int)kPiece + 128;
+    const cudaError_t e = cudaFuncSetAttribute(copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    copy_kernel<<<(unsigned)(a.items < 2 * sms ? a.items : 2 * sms), 32, smem, stream>>>(a);
     return cudaGetLastError();
 }
 

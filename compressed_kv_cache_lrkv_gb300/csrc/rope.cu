@@ -34,57 +34,66 @@ __device__ __forceinline__ void cos_sin_turn(unsigned long long f, float& c, flo
     if (q >= 2) s = -s;
 }
 
-// N consecutive values of a row, as fp32: N = 4 or 8, the address a multiple of N elements.
-template <int N>
-struct Vals {
-    float v[N];
+// Eight values of a head as they lie in memory, four from p + at0 and four from p + at1.
+template <typename T>
+struct Raw {
+    uint32_t r[2 * sizeof(T)];
 };
-template <int N>
-__device__ __forceinline__ Vals<N> load(const uint16_t* p) {
-    Vals<N> r;
-    if constexpr (N == 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.v[2 * i] = bf16lo(w[i]), r.v[2 * i + 1] = bf16hi(w[i]);
+template <bool HALF>
+__device__ __forceinline__ void get(Raw<uint16_t>& v, const uint16_t* p, int at0, int at1) {
+    if (HALF) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + at0), y = *reinterpret_cast<const uint2*>(p + at1);
+        v.r[0] = x.x, v.r[1] = x.y, v.r[2] = y.x, v.r[3] = y.y;
     } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        r.v[0] = bf16lo(x.x), r.v[1] = bf16hi(x.x), r.v[2] = bf16lo(x.y), r.v[3] = bf16hi(x.y);
+        const uint4 x = *reinterpret_cast<const uint4*>(p + at0);
+        v.r[0] = x.x, v.r[1] = x.y, v.r[2] = x.z, v.r[3] = x.w;
     }
-    return r;
 }
-template <int N>
-__device__ __forceinline__ Vals<N> load(const float* p) {
-    Vals<N> r;
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        const float4 x = reinterpret_cast<const float4*>(p)[i];
-        r.v[4 * i] = x.x, r.v[4 * i + 1] = x.y, r.v[4 * i + 2] = x.z, r.v[4 * i + 3] = x.w;
+template <bool HALF>
+__device__ __forceinline__ void put(const Raw<uint16_t>& v, uint16_t* p, int at0, int at1) {
+    if (HALF) {
+        *reinterpret_cast<uint2*>(p + at0) = make_uint2(v.r[0], v.r[1]);
+        *reinterpret_cast<uint2*>(p + at1) = make_uint2(v.r[2], v.r[3]);
+    } else {
+        *reinterpret_cast<uint4*>(p + at0) = make_uint4(v.r[0], v.r[1], v.r[2], v.r[3]);
     }
-    return r;
 }
-template <int N>
-__device__ __forceinline__ void store(uint16_t* p, const Vals<N>& r) {
-    if constexpr (N == 8)
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(r.v[0], r.v[1]), pack_bf16x2(r.v[2], r.v[3]),
-                                                  pack_bf16x2(r.v[4], r.v[5]), pack_bf16x2(r.v[6], r.v[7]));
-    else
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r.v[0], r.v[1]), pack_bf16x2(r.v[2], r.v[3]));
+template <bool HALF>
+__device__ __forceinline__ void get(Raw<float>& v, const float* p, int at0, int at1) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p + at0), y = *reinterpret_cast<const uint4*>(p + at1);
+    v.r[0] = x.x, v.r[1] = x.y, v.r[2] = x.z, v.r[3] = x.w, v.r[4] = y.x, v.r[5] = y.y, v.r[6] = y.z, v.r[7] = y.w;
 }
-template <int N>
-__device__ __forceinline__ void store(float* p, const Vals<N>& r) {
+template <bool HALF>
+__device__ __forceinline__ void put(const Raw<float>& v, float* p, int at0, int at1) {
+    *reinterpret_cast<uint4*>(p + at0) = make_uint4(v.r[0], v.r[1], v.r[2], v.r[3]);
+    *reinterpret_cast<uint4*>(p + at1) = make_uint4(v.r[4], v.r[5], v.r[6], v.r[7]);
+}
+__device__ __forceinline__ void widen(const Raw<uint16_t>& v, float* x) {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i)
-        reinterpret_cast<float4*>(p)[i] = make_float4(r.v[4 * i], r.v[4 * i + 1], r.v[4 * i + 2], r.v[4 * i + 3]);
+    for (int i = 0; i < 4; ++i) x[2 * i] = bf16lo(v.r[i]), x[2 * i + 1] = bf16hi(v.r[i]);
+}
+__device__ __forceinline__ void widen(const Raw<float>& v, float* x) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v.r[i]);
+}
+__device__ __forceinline__ void narrow(const float* x, Raw<uint16_t>& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void narrow(const float* x, Raw<float>& v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.r[i] = __float_as_uint(x[i]);
 }
 
-// A block: x units (4 pairs, or 8 values that are copied) of a head, y heads, z rows; a thread takes its unit of
-// every blockDim.y-th head, HB of them in flight, with the sines of its four pairs formed once.
-// HALF: a unit's pairs are 4 values of the lower half and 4 of the upper one; else 8 neighbouring values.
-template <typename T, bool HALF, int HB>
-__global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeArgs a) {
+// A block: x units of a head (four pairs, or eight values that are copied), y heads, z rows; a thread takes its unit of
+// RB rows and every blockDim.y-th head, HB of them, RB x HB units in flight at once and before the sines are formed
+// (once for all heads of a row).  HALF: a unit's pairs are four values of the lower half and four of the upper one;
+// else eight neighbouring values.  Bound by the memory: what carries it is bytes in flight, so the values wait in their
+// own type.  (With one unit after another behind the position's load: 8,192 rows x 32 heads of 192 98 us.)
+template <typename T, bool HALF, int RB, int HB>
+__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
     const int un = threadIdx.x, rot = a.plan.d_rot / 8;
-    // units: first the rotated ones, then 8 copied values each, those before `begin` and those behind the part
+    // units: first the rotated ones, then eight copied values each, those before `begin` and those behind the part
     const bool turns = un < rot;
     int at0, at1;
     if (turns) {
@@ -101,64 +110,56 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
     unsigned long long speed[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) speed[k] = turns ? a.plan.turn[un * 4 + k] : 0;
-    for (long long i = (long long)blockIdx.x * blockDim.z + threadIdx.z; i < a.n;
-         i += (long long)gridDim.x * blockDim.z) {
-        const long long xr = a.x_index ? a.x_index[i] : i, yr = a.y_index ? a.y_index[i] : i;
-        if (xr < 0 || yr < 0) continue;
-        if (xr >= a.x_rows || yr >= a.y_rows) {
-            set_status(a.status, LRKV_DEV_BAD_SLOT);
-            continue;
+    const long long rstep = (long long)gridDim.x * blockDim.z;
+    for (long long i0 = (long long)blockIdx.x * blockDim.z + threadIdx.z; i0 < a.n; i0 += rstep * RB) {
+        const T* xp[RB];
+        T* yp[RB];
+        int pos[RB];
+        bool ok[RB];
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const long long i = i0 + r * rstep;
+            ok[r] = i < a.n;
+            long long xr = i, yr = i;
+            if (ok[r] && a.x_index) xr = a.x_index[i];
+            if (ok[r] && a.y_index) yr = a.y_index[i];
+            if (ok[r] && xr >= 0 && yr >= 0 && (xr >= a.x_rows || yr >= a.y_rows)) set_status(a.status, LRKV_DEV_BAD_SLOT);
+            pos[r] = ok[r] ? a.positions[i] : 0;
+            ok[r] = ok[r] && xr >= 0 && yr >= 0 && xr < a.x_rows && yr < a.y_rows;
+            xp[r] = xb + xr * a.x_row;
+            yp[r] = yb + yr * a.y_row;
         }
-        float c[4], s[4];
-        if (turns) {
-            const long long pos = a.positions[i];
+        for (int h0 = blockIdx.y * blockDim.y + threadIdx.y; h0 < a.heads; h0 += hstep * HB) {
+            Raw<T> v[RB][HB];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                cos_sin_turn((unsigned long long)pos * speed[k], c[k], s[k]);
-                c[k] *= a.plan.magnitude;
-                s[k] *= a.transpose ? -a.plan.magnitude : a.plan.magnitude;
-            }
-        }
-        const T* xp = xb + xr * a.x_row;
-        T* yp = yb + yr * a.y_row;
-        for (int h = blockIdx.y * blockDim.y + threadIdx.y; h < a.heads; h += hstep * HB) {
-            Vals<8> v[HB];
+            for (int r = 0; r < RB; ++r)
 #pragma unroll
-            for (int b = 0; b < HB; ++b) {
-                if (h + b * hstep >= a.heads) break;
-                const T* p = xp + (h + b * hstep) * a.x_head;
-                if (HALF && turns) {
-                    const Vals<4> lo = load<4>(p + at0), hi = load<4>(p + at1);
+                for (int b = 0; b < HB; ++b)
+                    if (ok[r] && h0 + b * hstep < a.heads) get<HALF>(v[r][b], xp[r] + (h0 + b * hstep) * a.x_head, at0, at1);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[b].v[k] = lo.v[k], v[b].v[4 + k] = hi.v[k];
-                } else {
-                    v[b] = load<8>(p + at0);
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < HB; ++b) {
-                if (h + b * hstep >= a.heads) break;
-                T* p = yp + (h + b * hstep) * a.y_head;
-                if (!turns) {
-                    store<8>(p + at0, v[b]);
-                    continue;
-                }
-                Vals<8> o;
+            for (int r = 0; r < RB; ++r) {
+                float c[4], s[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int i0 = HALF ? k : 2 * k, i1 = HALF ? 4 + k : 2 * k + 1;
-                    const float x0 = v[b].v[i0], x1 = v[b].v[i1];
-                    o.v[i0] = fmaf(x0, c[k], -(x1 * s[k]));
-                    o.v[i1] = fmaf(x0, s[k], x1 * c[k]);
+                    cos_sin_turn((unsigned long long)(long long)pos[r] * speed[k], c[k], s[k]);
+                    c[k] *= a.plan.magnitude;
+                    s[k] *= a.transpose ? -a.plan.magnitude : a.plan.magnitude;
                 }
-                if (HALF) {
-                    Vals<4> lo, hi;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) lo.v[k] = o.v[k], hi.v[k] = o.v[4 + k];
-                    store<4>(p + at0, lo);
-                    store<4>(p + at1, hi);
-                } else {
-                    store<8>(p + at0, o);
+                for (int b = 0; b < HB; ++b) {
+                    if (!ok[r] || h0 + b * hstep >= a.heads) continue;
+                    if (turns) {
+                        float x[8], o[8];
+                        widen(v[r][b], x);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int e0 = HALF ? k : 2 * k, e1 = HALF ? 4 + k : 2 * k + 1;
+                            o[e0] = fmaf(x[e0], c[k], -(x[e1] * s[k]));
+                            o[e1] = fmaf(x[e0], s[k], x[e1] * c[k]);
+                        }
+                        narrow(o, v[r][b]);
+                    }
+                    put<HALF>(v[r][b], yp[r] + (h0 + b * hstep) * a.y_head, at0, at1);
                 }
             }
         }
@@ -168,20 +169,26 @@ __global__ void __launch_bounds__(512) rope_kernel(const __grid_constant__ RopeA
 template <typename T, bool HALF>
 cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t stream) {
     const int units = a.in_place ? a.plan.d_rot / 8 : a.width / 8;
-    // a head a thread while that fits on the GPU at once, else four in flight and the sines shared by all
-    const bool few = (long long)a.n * a.heads * units <= (long long)sms * 2048;
+    // one unit a thread while all fit on the GPU at once (latency counts); else four rows of few heads, or four (fp32)
+    // or eight heads of a row
+    const long long all = (long long)a.n * a.heads * units;
+    constexpr int HB = sizeof(T) == 2 ? 8 : 4;
+    const int rb = all <= (long long)sms * 1024 || a.heads >= 4 ? 1 : 4;
+    const int hb = all <= (long long)sms * 1024 || a.heads < 4 ? 1 : HB;
     int ny = 1;
-    while (ny * (few ? 1 : 4) < a.heads && units * ny * 2 <= 256) ny *= 2;
+    while (ny * hb < a.heads && units * ny * 2 <= 256) ny *= 2;
     int nz = 1;
     while (units * ny * nz * 2 <= 256 && nz < 64) nz *= 2;
-    const long long rows = ((long long)a.n + nz - 1) / nz;
+    const long long rows = ((long long)a.n + nz * rb - 1) / (nz * rb);
     const unsigned gx = (unsigned)(rows < (1 << 20) ? rows : 1 << 20);
-    const unsigned gy = few ? (unsigned)((a.heads + ny - 1) / ny) : 1u;
+    const unsigned gy = hb == 1 ? (unsigned)((a.heads + ny - 1) / ny) : 1u;
     const dim3 grid(gx, gy), block(units, ny, nz);
-    if (few)
-        rope_kernel<T, HALF, 1><<<grid, block, 0, stream>>>(a);
+    if (rb == 4)
+        rope_kernel<T, HALF, 4, 1><<<grid, block, 0, stream>>>(a);
+    else if (hb == 1)
+        rope_kernel<T, HALF, 1, 1><<<grid, block, 0, stream>>>(a);
     else
-        rope_kernel<T, HALF, 4><<<grid, block, 0, stream>>>(a);
+        rope_kernel<T, HALF, 1, HB><<<grid, block, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
