@@ -13,6 +13,13 @@ namespace lrkv {
 
 namespace {
 
+// These kernels are short and follow one another: each is launched while the one before it on the stream still runs, waits
+// for its end before it touches memory, and only then lets the next one be launched.
+__device__ __forceinline__ void begin_dependent() {
+    pdl_wait();
+    pdl_trigger();
+}
+
 constexpr int kPlanThreads = 1024;
 constexpr int kPerThread = 16;  // counts a thread looks at in one round of the search
 
@@ -157,6 +164,7 @@ __device__ __forceinline__ void give_back(int32_t* refs, int num_blocks, int pag
 // ---------------------------------------------------------------- reserve: one block
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a) {
     __shared__ int need[LRKV_MAX_PAGE_BATCH], warp_sums[32], picked[kPicked];
+    begin_dependent();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // a warp per sequence: its first empty entry from the page of its length on
     for (int b = warp; b < a.batch; b += kPlanThreads / 32) {
@@ -209,19 +217,23 @@ __device__ uint32_t fork_refused(const PageArgs& a, int i, int lane, int lanes, 
     return all(bad);
 }
 
-// One block: a warp per fork looks, gives the child's pages back, and passes the parent's on; eight entries of a row
-// per lane on their way at once (one after the other: 64 forks of 100 pages 26 us).
+// One block: a warp per fork, or a half or quarter of one where there are more forks, looks, gives the child's pages
+// back, and passes the parent's on; eight entries of a row per lane on their way at once (one after the other, a warp per
+// fork: 64 forks of 100 pages 26 us).
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs a) {
     // need: pages asked for, then their prefix sums; full: the full pages that a fork passes on (-1: left out, -2: no
     // page was left for the last, partly filled one)
     extern __shared__ int sh[];
     int *const need = sh, *const full = sh + a.n;
     __shared__ int warp_sums[32], picked[kPicked];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    begin_dependent();
+    const int lanes = a.n <= 32 ? 32 : a.n <= 64 ? 16 : 8, lane = threadIdx.x & (lanes - 1);
+    const int first = threadIdx.x / lanes, step = kPlanThreads / lanes;
+    const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1) << (threadIdx.x & 31 & ~(lanes - 1));
     auto row_of = [&](int s) { return a.table + (size_t)s * a.max_pages; };
     constexpr int E = 8;
-    for (int i = warp; i < a.n; i += kPlanThreads / 32) {
-        const uint32_t bad = fork_refused(a, i, lane, 32, [](uint32_t x) { return __reduce_or_sync(0xffffffffu, x); });
+    for (int i = first; i < a.n; i += step) {
+        const uint32_t bad = fork_refused(a, i, lane, lanes, [&](uint32_t x) { return __reduce_or_sync(mask, x); });
         if (lane == 0) {
             if (bad) set_status(a.status, bad & LRKV_DEV_BAD_INDEX ? LRKV_DEV_BAD_INDEX : bad);
             const int L = bad ? 0 : a.lens[a.a[i]];
@@ -231,18 +243,18 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
         if (bad) continue;
         // what the child held goes back (parents' rows are not written here: no child is a parent)
         int32_t* row = row_of(a.b[i]);
-        for (int k0 = 0; k0 < a.max_pages; k0 += 32 * E) {
+        for (int k0 = 0; k0 < a.max_pages; k0 += lanes * E) {
             int page[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int k = k0 + e * 32 + lane;
+                const int k = k0 + e * lanes + lane;
                 page[e] = k < a.max_pages ? row[k] : -1;
             }
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (page[e] >= 0) {
                     give_back(a.refs, a.num_blocks, page[e], a.status);
-                    row[k0 + e * 32 + lane] = -1;
+                    row[k0 + e * lanes + lane] = -1;
                 }
         }
     }
@@ -258,22 +270,22 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
               a.refs[page] = 1;
           });
     __syncthreads();
-    for (int i = warp; i < a.n; i += kPlanThreads / 32) {
+    for (int i = first; i < a.n; i += step) {
         const int f = full[i];
         if (f == -1) continue;
         const int32_t* from = row_of(a.a[i]);
         int32_t* to = row_of(a.b[i]);
-        for (int k0 = 0; k0 < f; k0 += 32 * E) {
+        for (int k0 = 0; k0 < f; k0 += lanes * E) {
             int page[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int k = k0 + e * 32 + lane;
+                const int k = k0 + e * lanes + lane;
                 page[e] = k < f ? from[k] : -1;
             }
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (page[e] >= 0) {
-                    to[k0 + e * 32 + lane] = page[e];
+                    to[k0 + e * lanes + lane] = page[e];
                     atomicAdd(a.refs + page[e], 1);
                 }
         }
@@ -291,7 +303,7 @@ __device__ __forceinline__ int pool_of(const PoolArgs& p, int* u) {
 // Rows of the children's last pages: grid (units in pieces, forks, layers).
 __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, const PageArgs a) {
     const int i = blockIdx.y;
-    pdl_wait();
+    begin_dependent();
     if (fork_refused(a, i, threadIdx.x, 256, [](uint32_t x) { return (uint32_t)__syncthreads_or(x != 0); })) return;
     const int par = a.a[i], c = a.b[i], L = a.lens[c];  // (0 where no page was left for the child)
     if (L % kBlockSize == 0) return;
@@ -318,6 +330,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, const 
 
 // ---------------------------------------------------------------- free: a block per sequence
 __global__ void __launch_bounds__(256) free_kernel(const PageArgs a) {
+    begin_dependent();
     const int b = a.a[blockIdx.x];
     if (b < 0 || b >= a.batch) {
         if (threadIdx.x == 0) set_status(a.status, LRKV_DEV_BAD_INDEX);
@@ -359,6 +372,7 @@ __global__ void __launch_bounds__(32) copy_kernel(const __grid_constant__ CopyAr
     __shared__ uint64_t full[kStages];
     __shared__ uint4* dst[kStages];
     __shared__ uint32_t size[kStages];
+    begin_dependent();
     const int lane = threadIdx.x;
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(full + i), 1);
@@ -430,6 +444,7 @@ __global__ void __launch_bounds__(32) copy_kernel(const __grid_constant__ CopyAr
 constexpr int kCompactCtas = 8, kCompactBatch = 8;
 __global__ void __cluster_dims__(kCompactCtas, 1, 1) __launch_bounds__(256) compact_kernel(const CompactArgs a) {
     __shared__ int from[1024], to[1024];
+    begin_dependent();
     const int b = blockIdx.y, L = a.lens[b], n = a.path_lens[b];
     const int32_t* path = a.path + (size_t)b * a.max_path;
     const int32_t* row = a.table + (size_t)b * a.max_pages;
@@ -485,8 +500,7 @@ __global__ void __cluster_dims__(kCompactCtas, 1, 1) __launch_bounds__(256) comp
 }  // namespace
 
 cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream) {
-    reserve_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
 }
 
 cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t stream) {
@@ -496,16 +510,14 @@ cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t
                                                    2 * LRKV_MAX_PAGE_BATCH * (int)sizeof(int));
         if (e != cudaSuccess) return e;
     }
-    fork_plan_kernel<<<1, kPlanThreads, smem, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_dependent(fork_plan_kernel, dim3(1), dim3(kPlanThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
     const int pieces = (kBlockSize * p.units + 256 * 8 - 1) / (256 * 8);
     return launch_dependent(fork_copy_kernel, dim3(pieces, a.n, p.layers), dim3(256), 0, stream, p, a);
 }
 
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream) {
-    free_kernel<<<a.n, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(free_kernel, dim3(a.n), dim3(256), 0, stream, a);
 }
 
 cudaError_t launch_pages_copy(const PoolArgs& src, const PoolArgs& dst, const int32_t* src_pages,
@@ -516,13 +528,11 @@ cudaError_t launch_pages_copy(const PoolArgs& src, const PoolArgs& dst, const in
     constexpr int smem = kStages * (int)kPiece + 128;
     const cudaError_t e = cudaFuncSetAttribute(copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    copy_kernel<<<(unsigned)(a.items < 2 * sms ? a.items : 2 * sms), 32, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(copy_kernel, dim3((unsigned)(a.items < 2 * sms ? a.items : 2 * sms)), dim3(32), smem, stream, a);
 }
 
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t stream) {
-    compact_kernel<<<dim3(kCompactCtas, a.batch), 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(compact_kernel, dim3(kCompactCtas, a.batch), dim3(256), 0, stream, a);
 }
 
 }  // namespace lrkv

@@ -7,6 +7,7 @@
 // a turn) and through the Taylor polynomials of sine and cosine.
 #include "draft.h"
 #include "lrkv_internal.cuh"
+#include "tile_attn.cuh"
 
 namespace lrkv {
 
@@ -111,6 +112,8 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 #pragma unroll
     for (int k = 0; k < 4; ++k) speed[k] = turns ? a.plan.turn[un * 4 + k] : 0;
     const long long rstep = (long long)gridDim.x * blockDim.z;
+    pdl_wait();  // (launched while the kernel before it on the stream still runs)
+    pdl_trigger();
     for (long long i0 = (long long)blockIdx.x * blockDim.z + threadIdx.z; i0 < a.n; i0 += rstep * RB) {
         const T* xp[RB];
         T* yp[RB];
@@ -183,13 +186,9 @@ cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t stream) {
     const unsigned gx = (unsigned)(rows < (1 << 20) ? rows : 1 << 20);
     const unsigned gy = hb == 1 ? (unsigned)((a.heads + ny - 1) / ny) : 1u;
     const dim3 grid(gx, gy), block(units, ny, nz);
-    if (rb == 4)
-        rope_kernel<T, HALF, 4, 1><<<grid, block, 0, stream>>>(a);
-    else if (hb == 1)
-        rope_kernel<T, HALF, 1, 1><<<grid, block, 0, stream>>>(a);
-    else
-        rope_kernel<T, HALF, 1, HB><<<grid, block, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (rb == 4) return launch_dependent(rope_kernel<T, HALF, 4, 1>, grid, block, 0, stream, a);
+    if (hb == 1) return launch_dependent(rope_kernel<T, HALF, 1, 1>, grid, block, 0, stream, a);
+    return launch_dependent(rope_kernel<T, HALF, 1, HB>, grid, block, 0, stream, a);
 }
 
 }  // namespace
