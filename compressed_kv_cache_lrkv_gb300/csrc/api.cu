@@ -915,7 +915,7 @@ lrkv_status lrkv_decode_tree(const lrkv_dims* dims, const void* q, const void* B
     const uint32_t zbox = a.zw == 32 ? 32 : 64;
     const CUtensorMapSwizzle zswz = a.zw == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     if ((s = make_tmap(&mp.sK, cache->sK, dk, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "sK")) != LRKV_OK ||
-        (s = make_tmap(&mp.sV, cache->sV, dh, rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B, "sV")) != LRKV_OK ||
+        (s = make_tmap(&mp.sV, cache->sV, dh, rows, zbox, 64, zswz, "sV")) != LRKV_OK ||
         (s = make_tmap(&mp.zK, cache->zK, HR, rows, zbox, 64, zswz, "zK")) != LRKV_OK ||
         (s = make_tmap(&mp.zV, cache->zV, HR, rows, zbox, 64, zswz, "zV")) != LRKV_OK)
         return s;

@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int oob_row = d.num_blocks * kBlockSize;  // whole box out of bounds: zeros
         const int depth = keys ? KST : VST;
         const uint32_t stage_bytes = keys ? Lay::K_BYTES : Lay::V_BYTES;
-        const int nblk = keys ? D_K / 64 : D_H / 64;
+        // with zw = 32 the values come in blocks of 32 columns, 64-byte swizzle, s^V as z^V: one MMA takes them all
+        const int cols = !keys && ZW == 32 ? 32 : 64, nblk = (keys ? D_K : D_H) / cols;
         uint64_t* full = keys ? k_full : v_full;
         uint64_t* empty = keys ? s_done : o_done;
         const CUtensorMap* ms = keys ? &m.sK : &m.sV;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t dst = ring + st * stage_bytes;
                     const uint32_t bar = B(full + st);
                     mbar_arrive_expect_tx(bar, stage_bytes);
-                    for (int bk = 0; bk < nblk; ++bk, dst += 8192) tma_load_2d(dst, ms, 64 * bk, prow, bar);
+                    for (int bk = 0; bk < nblk; ++bk, dst += cols * 128) tma_load_2d(dst, ms, cols * bk, prow, bar);
                     for (int bk = 0; bk < Lay::ZBLK; ++bk, dst += Lay::ZBLK_BYTES)
                         tma_load_2d(dst, mz, x0 + 64 * bk, prow, bar);
                 }
@@ -292,12 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (With a vote of the warp at every wait and MMA the issue took 1,970 cycles a page of 12 + 8 MMAs, of which the
         // tensor cores need 704; from one thread 1,390.)
         constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
-        constexpr uint32_t id_PV = idesc_bf16_f32(128, ZW == 32 ? D_H : D_H + ZW) | (1u << 16);  // B is MN-major
-        constexpr uint32_t id_PZ = idesc_bf16_f32(128, 32) | (1u << 16);
+        constexpr uint32_t id_PV = idesc_bf16_f32(128, D_H + ZW) | (1u << 16);  // B is MN-major
         if (elect_one_sync()) {
             constexpr uint32_t U128 = desc_upper(1024, 2), U64 = desc_upper(512, 4);
             const uint32_t dQ = desc_lower(S0, 16), dK = desc_lower(S0 + Lay::OFF_K, 16);
-            const uint32_t dV = desc_lower(S0 + Lay::OFF_V, 8192), dVz = desc_lower(S0 + Lay::OFF_V + D_H / 64 * 8192, 16);
+            const uint32_t dV = desc_lower(S0 + Lay::OFF_V, ZW == 32 ? 4096 : 8192);
             int kst = 0, vst = 0, sb = 0, pb = 0;  // stages and S buffers in turn
             uint32_t kphase = 0, vphase = 0, qphase = 0, pphase = 0;
             auto s_tile = [&]() -> bool {
@@ -334,12 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t so = vst * (Lay::V_BYTES >> 4), tp = Lay::TM_S + pb * 64;
 #pragma unroll
                 for (int kk = 0; kk < kBlockSize / 16; ++kk)
-                    mma_ts_h<U128>(Lay::TM_O, tp + kk * 8, dV + so + (kk * 2048 >> 4), id_PV, !first || kk > 0);
-                if (ZW == 32) {
-#pragma unroll
-                    for (int kk = 0; kk < kBlockSize / 16; ++kk)
-                        mma_ts_h<U64>(Lay::TM_O + D_H, tp + kk * 8, dVz + so + (kk * 1024 >> 4), id_PZ, !first || kk > 0);
-                }
+                    mma_ts_h<ZW == 32 ? U64 : U128>(Lay::TM_O, tp + kk * 8, dV + so + (kk * (ZW == 32 ? 1024 : 2048) >> 4),
+                                                    id_PV, !first || kk > 0);
                 tc_commit(B(o_done + vst));
                 if (++pb == NSB) {
                     pb = 0;
@@ -529,12 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (hit) *p = make_uint4(x[0], x[1], x[2], x[3]);
                                 found |= hit;
                             };
-                            for (int bk = row >> 6; bk < D_H / 64 + (ZW == 32 ? 0 : Lay::ZBLK); bk += 2)
-                                for (int c8 = 0; c8 < 8; ++c8)
-                                    clean(reinterpret_cast<uint4*>(v0 + bk * 8192 + vr * 128) + c8);
-                            if (ZW == 32)
-                                for (int c8 = row >> 6; c8 < 4; c8 += 2)
-                                    clean(reinterpret_cast<uint4*>(v0 + D_H / 64 * 8192 + vr * 64) + c8);
+                            constexpr int PB = ZW == 32 ? 64 : 128;  // bytes of a row in a block
+                            for (int bk = row >> 6; bk < (D_H + ZW) * 2 / PB; bk += 2)
+                                for (int c8 = 0; c8 < PB / 16; ++c8)
+                                    clean(reinterpret_cast<uint4*>(v0 + bk * (PB * 64) + vr * PB) + c8);
                             if (found) atomicOr(poison + (piece & 1), 1ull << t);
                         }
                         __syncwarp();

@@ -29,8 +29,8 @@ size_t tree_workspace_bytes(int H, int D_H, int R, int D_R, int batch, int T, in
 void tree_carve_workspace(TreeArgs* a, void* ws, int D_H, int R, int D_R, int sms);
 
 // Maps over the pools: [s^K | k^R], s^V as [num_blocks * 64][d_h (+ d_rope)], box 64 columns x 64 tokens, 128-byte
-// swizzle; z^K, z^V as [num_blocks * 64][H r], the same box, or 32 columns x 64 tokens with 64-byte swizzle for
-// zw = 32.
+// swizzle; z^K, z^V as [num_blocks * 64][H r], the same box.  For zw = 32 s^V, z^K and z^V have boxes of 32 columns x 64
+// tokens with 64-byte swizzle.
 struct TreeMaps {
     CUtensorMap sK, sV, zK, zV;
 };
