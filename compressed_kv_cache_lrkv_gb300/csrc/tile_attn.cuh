@@ -87,6 +87,12 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x4(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
 // Pairs of fp32 values in one register pair, and what works on both at once.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
     uint64_t r;

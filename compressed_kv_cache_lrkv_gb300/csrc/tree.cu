@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.
-constexpr int kStartPages = 8;
+constexpr int kStartPages = 11;
 
 __device__ __forceinline__ void named_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -128,6 +128,94 @@ struct Walk {
         ++t;
     }
 };
+
+// The row's largest logit (log2 units), NaN where one is: of 64 in TMEM, of which those that are not seen become
+// -infinity there.
+__device__ __forceinline__ float look(uint32_t tS, bool all, unsigned long long seen, float scale_log2) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32, seen >>= 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tS + c, v);
+        if (!all) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = (uint32_t)seen >> e & 1 ? v[e] : 0xff800000u;
+            tmem_st_32x32b_x32(tS + c, v);
+            tmem_wait_st();
+        }
+        float m4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            m4[e] = max3_nan(__uint_as_float(v[e]), __uint_as_float(v[4 + e]), __uint_as_float(v[8 + e]));
+#pragma unroll
+        for (int e = 12; e < 28; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = max3_nan(m4[k], __uint_as_float(v[e + k]), __uint_as_float(v[e + 4 + k]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = max_nan(m4[k], __uint_as_float(v[28 + k]));
+        mx = max3_nan(mx, max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
+    }
+    return mx * scale_log2;
+}
+
+// Those that are NaN, formed again from q, q~ and the pools; `slot`: of the first.
+__device__ __noinline__ void form_again(uint32_t tS, bool live, size_t slot, const uint16_t* q, const float* qt,
+                                        const uint16_t* sK, const uint16_t* zK, int D_K, int R, int H, int h) {
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 8) {
+        uint32_t v[8];
+        tmem_ld_32x32b_x8(tS + c, v);
+        uint32_t nans = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nans |= (__uint_as_float(v[e]) != __uint_as_float(v[e]) ? 1u : 0u) << e;
+        for (uint32_t todo = live ? nans : 0u; todo != 0; todo &= todo - 1) {
+            const int e = __ffs(todo) - 1;
+            const size_t t = slot + c + e;
+            const uint32_t x = __float_as_uint(dot8(q, sK + t * D_K, D_K) + dot8(qt, zK + (t * H + h) * R, R));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = k == e ? x : v[k];
+        }
+        __syncwarp();
+        tmem_st_32x32b_x8(tS + c, v);
+    }
+    tmem_wait_st();
+}
+
+// Half `part` of row vr of a value stage: cleared wholly, or its NaNs and infinities; whether there were any.
+template <int D_H, int ZW>
+__device__ __noinline__ bool clean_values(uint8_t* stage, int vr, int part, bool wholly) {
+    constexpr int PB = ZW == 32 ? 64 : 128, PC = PB / 16;  // bytes of a row in a block, 16-byte pieces
+    bool found = false;
+#pragma unroll 1
+    for (int bk = 0; bk < (D_H + ZW) * 2 / PB; ++bk) {
+        // (rows are PB bytes apart: each begins with another of its pieces, and so in another bank)
+        uint4* const r = reinterpret_cast<uint4*>(stage + bk * (PB * 64) + vr * PB);
+        uint4 y[PC / 2];
+#pragma unroll
+        for (int i = 0; i < PC / 2; ++i) {
+            uint4* const p = r + ((part * (PC / 2) + i + vr) & (PC - 1));
+            if (wholly)
+                *p = make_uint4(0, 0, 0, 0);
+            else
+                y[i] = *p;
+        }
+        if (wholly) continue;
+#pragma unroll
+        for (int i = 0; i < PC / 2; ++i) {
+            uint32_t x[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool lo = (x[e] & 0x7f80u) == 0x7f80u, hi = (x[e] & 0x7f800000u) == 0x7f800000u;
+                hit |= lo | hi;
+                x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
+            }
+            if (hit) r[(part * (PC / 2) + i + vr) & (PC - 1)] = make_uint4(x[0], x[1], x[2], x[3]);
+            found |= hit;
+        }
+    }
+    return found;
+}
 
 template <int D_H, int D_R, int ZW>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -374,10 +462,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hl = row / a.ns, il = row - hl * a.ns;
         volatile float* const refs = reinterpret_cast<float*>(smem + Lay::OFF_ROW);
         float2* const sums = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
-        bool ok = true, waited = false;
+        bool ok = true;
         int g = 0, sb = 0, kst = 0, vst = 0, piece = 0;  // pages so far, its S buffer and stages, pieces so far
         uint32_t kphase = 0, vphase = 0;
+        // 64 columns of a block into TMEM (two columns a register), or K-major with 128-byte swizzle (16-byte chunk c
+        // at c ^ (row mod 8))
+        auto put_block = [&](int bk, const uint4* x) {
+            if (bk < Lay::QBT) {
+                tmem_st_32x32b_x32(tmem + tl + Lay::TM_Q + bk * 32, reinterpret_cast<const uint32_t*>(x));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(smem + (bk - Lay::QBT) * 16384 + row * 128 + ((c ^ (row & 7)) << 4)) = x[c];
+            }
+        };
         bool have = w.next(a);
+        if (have && half == 1) {
+            const uint4 zeros[8] = {};
+#pragma unroll
+            for (int bk = D_K / 64; bk < NBQ; ++bk) put_block(bk, zeros);
+            tmem_wait_st();
+        }
+        pdl_wait();  // q~ (and this grid's end stands for that of the launches before it)
+        if (have) pdl_trigger();  // the merge may be set up: its blocks wait for this grid's end
         while (have) {
             const int b = w.b, L = w.s.L, n = w.s.n, st_b = (n + a.ns - 1) / a.ns;
             const int tile = w.tile(a), h = tile / st_b * a.hb + hl, i = tile % st_b * a.ns + il;
@@ -388,70 +495,75 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the drafted tokens that the row sees
             unsigned long long tree = ~0ull >> (64 - n);  // (n >= 1)
             if (live) tree &= a.mask ? a.mask[(size_t)b * a.T + i] : ~0ull >> (63 - i);
+            {
+                // Its share of [Q | diag(Q~)]: group 0 has the first 128 columns of q, group 1 the last 64 of 192 and q~, of
+                // which a row only ever writes its own head's columns (the others are zeroed once).
+                uint4 qv[16];  // (of group 1: eight of q, eight of q~'s fp32 values)
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+                const uint4* const q = reinterpret_cast<const uint4*>(d.q + qr * D_K) + (half == 0 ? 0 : 16);
+                const uint4* const y = reinterpret_cast<const uint4*>(d.qt + qr * R);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    qv[c] = live && (half == 0 || D_K == 192) ? q[c] : zero;
+                    qv[8 + c] = !live ? zero : half == 0 ? (D_K >= 128 ? q[8 + c] : zero) : c < R / 4 ? y[c] : zero;
+                }
+                if (half == 0) {
+                    put_block(0, qv);
+                    if (D_K >= 128) put_block(1, qv + 8);
+                } else {
+                    if (D_K == 192) put_block(2, qv);
+                    // q~ rounded to bf16, and what that left, rounded: R / 2 registers each
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float4 y = make_float4(__uint_as_float(qv[8 + c].x), __uint_as_float(qv[8 + c].y),
+                                                     __uint_as_float(qv[8 + c].z), __uint_as_float(qv[8 + c].w));
+                        hi[2 * c] = pack_bf16x2(y.x, y.y);
+                        hi[2 * c + 1] = pack_bf16x2(y.z, y.w);
+                        lo[2 * c] = pack_bf16x2(y.x - bf16lo(hi[2 * c]), y.y - bf16hi(hi[2 * c]));
+                        lo[2 * c + 1] = pack_bf16x2(y.z - bf16lo(hi[2 * c + 1]), y.w - bf16hi(hi[2 * c + 1]));
+                    }
+                    // (a warp's rows are of 32 / ns heads or of one, whose columns lie in one block)
+                    const int h1 = (qq * 32) / a.ns, h2 = (qq * 32 + 31) / a.ns;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t* const x = part ? lo : hi;
+                        const int col = D_K + part * ZW + h1 * R;
+                        if (col / 64 < Lay::QBT) {
+                            for (int hh = h1; hh <= h2; ++hh) {
+                                uint32_t v[16];
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) v[c] = hl == hh ? x[c] : 0u;
+                                const uint32_t at = tmem + tl + Lay::TM_Q + (D_K + part * ZW + hh * R) / 2;
+                                if (R == 8)
+                                    tmem_st_32x32b_x4(at, v);
+                                else if (R == 16)
+                                    tmem_st_32x32b_x8(at, v);
+                                else
+                                    tmem_st_32x32b_x16(at, v);
+                            }
+                        } else {
+                            const int mine = D_K + part * ZW + hl * R, c0 = mine % 64 / 8;
+                            uint8_t* const r = smem + (mine / 64 - Lay::QBT) * 16384 + row * 128;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c < R / 8)
+                                    *reinterpret_cast<uint4*>(r + (((c0 + c) ^ (row & 7)) << 4)) =
+                                        make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                arrive(q_ready);
+            }
             if (p0 == 0 && warp == 2 && lane == 0) {
                 const int last = work.range_of(w.seg + w.s.pages - 1);
                 a.seg_table[b * a.tmax + tile] = make_int2(slot, last - gang + 1);
             }
             w.step();
             have = w.next(a);  // (from here on the walk shows the next piece)
-            {
-                // [Q | diag(Q~)] row, block by block of 64 columns: into TMEM (two columns a register), or K-major with
-                // 128-byte swizzle (16-byte chunk c at c ^ (row mod 8)).  The groups take every other block.
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                const uint4* q = reinterpret_cast<const uint4*>(d.q + qr * D_K);
-                const float* qt = d.qt + qr * R;
-#pragma unroll
-                for (int bk = 0; bk < NBQ; ++bk) {
-                    if ((bk & 1) != half) continue;
-                    if (bk >= D_K / 64 && !waited) {
-                        pdl_wait();  // q~
-                        waited = true;
-                    }
-                    uint32_t v[32];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        uint4 x = zero;
-                        const int gc = bk * 64 + c * 8;
-                        if (gc < D_K) {
-                            if (live) x = q[bk * 8 + c];
-                        } else {
-                            const bool rest = gc - D_K >= ZW;
-                            const int col = gc - D_K - (rest ? ZW : 0) - hl * R;
-                            if (live && col >= 0 && col < R) {
-                                const float4 y = *reinterpret_cast<const float4*>(qt + col);
-                                const float4 z = *reinterpret_cast<const float4*>(qt + col + 4);
-                                x = make_uint4(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w), pack_bf16x2(z.x, z.y),
-                                               pack_bf16x2(z.z, z.w));
-                                if (rest)  // what the rounding left
-                                    x = make_uint4(pack_bf16x2(y.x - bf16lo(x.x), y.y - bf16hi(x.x)),
-                                                   pack_bf16x2(y.z - bf16lo(x.y), y.w - bf16hi(x.y)),
-                                                   pack_bf16x2(z.x - bf16lo(x.z), z.y - bf16hi(x.z)),
-                                                   pack_bf16x2(z.z - bf16lo(x.w), z.w - bf16hi(x.w)));
-                            }
-                        }
-                        v[4 * c] = x.x;
-                        v[4 * c + 1] = x.y;
-                        v[4 * c + 2] = x.z;
-                        v[4 * c + 3] = x.w;
-                    }
-                    if (bk < Lay::QBT) {
-                        tmem_st_32x32b_x32(tmem + tl + Lay::TM_Q + bk * 32, v);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            *reinterpret_cast<uint4*>(smem + (bk - Lay::QBT) * 16384 + row * 128 +
-                                                      ((c ^ (row & 7)) << 4)) =
-                                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-                    }
-                }
-                if (!waited) pdl_wait();  // (this grid's end stands for that of the launches before it)
-                if (piece == 0) pdl_trigger();  // the merge may be set up: its blocks wait for this grid's end
-                waited = true;
-                tmem_wait_st();
-                fence_proxy_async_smem();
-                tc_fence_before();
-                arrive(q_ready);
-            }
             float mref = -INFINITY, l = 0.f;  // the reference that this group knows, and its sum relative to that
             // After an expired wait the loop goes on without work, so that the groups still meet at their barriers.
             auto turn = [&]() {
@@ -486,86 +598,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool good = blk >= 0 && blk < d.num_blocks;
                 const bool inner = good && base + kBlockSize <= L;  // every row sees every token
                 ok = ok && wait_warp(B(s_done + kst), kphase, d, abort_flag);
-                uint32_t sv[64];
                 float mx = -INFINITY;
                 if (ok) {
                     if (j == 0 && row == 0) poison[(piece + 1) & 1] = 0;  // (every row is done with the piece before)
                     tc_fence_after();
-                    tmem_ld_32x32b_x32_nowait(tS, sv);
-                    tmem_ld_32x32b_x32_nowait(tS + 32, sv + 32);
-                    tmem_wait_ld();
+                    const int c = L - base;  // tokens of the page before the drafted ones
+                    unsigned long long seen = ~0ull;
                     if (!inner) {
-                        const int c = L - base;  // tokens of the page before the drafted ones
-                        unsigned long long seen = c >= 0 ? (c < 64 ? tree << c : 0) | (c < 64 ? (1ull << c) - 1 : ~0ull)
-                                                         : (c > -64 ? tree >> -c : 0);
+                        seen = c >= 0 ? (c < 64 ? tree << c : 0) | (c < 64 ? (1ull << c) - 1 : ~0ull)
+                                      : (c > -64 ? tree >> -c : 0);
                         if (!good) seen = 0;
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) sv[e] = seen >> e & 1 ? sv[e] : 0xff800000u;
                         // Values that not every row sees, or none: cleared where they could spoil a product with a
                         // probability of 0.  Rows behind the end wholly; of a drafted token what is not finite,
                         // which is noted and added at the end to the rows that do see it.
                         ok = wait_warp(B(v_full + vst), vphase, d, abort_flag);
-                        const int vr = row & 63, t = base + vr - L;
-                        if (ok && t >= 0) {
-                            uint8_t* const v0 = smem + Lay::OFF_V + vst * Lay::V_BYTES;
-                            bool found = false;
-                            auto clean = [&](uint4* p) {
-                                if (t >= n) {
-                                    *p = make_uint4(0, 0, 0, 0);
-                                    return;
-                                }
-                                uint32_t x[4] = {p->x, p->y, p->z, p->w};
-                                bool hit = false;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const bool lo = (x[e] & 0x7f80u) == 0x7f80u, hi = (x[e] & 0x7f800000u) == 0x7f800000u;
-                                    hit |= lo | hi;
-                                    x[e] &= (lo ? 0xffff0000u : ~0u) & (hi ? 0xffffu : ~0u);
-                                }
-                                if (hit) *p = make_uint4(x[0], x[1], x[2], x[3]);
-                                found |= hit;
-                            };
-                            constexpr int PB = ZW == 32 ? 64 : 128;  // bytes of a row in a block
-                            for (int bk = row >> 6; bk < (D_H + ZW) * 2 / PB; bk += 2)
-                                for (int c8 = 0; c8 < PB / 16; ++c8)
-                                    clean(reinterpret_cast<uint4*>(v0 + bk * (PB * 64) + vr * PB) + c8);
-                            if (found) atomicOr(poison + (piece & 1), 1ull << t);
-                        }
+                        const int t = base + (row & 63) - L;
+                        if (ok && t >= 0 &&
+                            clean_values<D_H, ZW>(smem + Lay::OFF_V + vst * Lay::V_BYTES, row & 63, row >> 6, t >= n))
+                            atomicOr(poison + (piece & 1), 1ull << t);
                         __syncwarp();
                     }
-                    float m4[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        m4[e] = max3_nan(__uint_as_float(sv[e]), __uint_as_float(sv[4 + e]), __uint_as_float(sv[8 + e]));
-#pragma unroll
-                    for (int e = 12; e < 60; e += 8)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            m4[k] = max3_nan(m4[k], __uint_as_float(sv[e + k]), __uint_as_float(sv[e + 4 + k]));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) m4[k] = max_nan(m4[k], __uint_as_float(sv[60 + k]));
-                    mx = max_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3]);
+                    // (in halves, and again for the exponentials: a loop that stays in the instruction cache is worth
+                    // more than the loads from TMEM)
+                    mx = look(tS, inner, seen, d.scale_log2);
                     // diag(Q~)'s zeros times another head's NaN or infinity are NaN (and so is what rounding an
-                    // infinite product left): such logits are formed again from the row's own head alone.
+                    // infinite product left): such logits are formed again from the row's own head alone.  A
+                    // second look is over numbers, or over what is NaN by itself, which decides through the sum.
                     if (__any_sync(0xffffffffu, mx != mx)) {
-                        unsigned long long nans = 0;
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            nans |= (unsigned long long)(__uint_as_float(sv[e]) != __uint_as_float(sv[e])) << e;
-                        for (unsigned long long todo = live ? nans : 0ull; todo != 0; todo &= todo - 1) {
-                            const int e = __ffsll(todo) - 1;
-                            const size_t t = (size_t)blk * kBlockSize + e;
-                            const float x = dot8(d.q + qr * D_K, a.sK + t * D_K, D_K) +
-                                            dot8(d.qt + qr * R, a.zK + (t * H + h) * R, R);
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) sv[k] = k == e ? __float_as_uint(x) : sv[k];
-                        }
-                        __syncwarp();
-                        mx = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(sv[e]));
+                        form_again(tS, live, (size_t)blk * kBlockSize, d.q + qr * D_K, d.qt + qr * R, a.sK, a.zK, D_K, R, H,
+                                   h);
+                        mx = look(tS, true, ~0ull, d.scale_log2);
+                        mx = mx != mx ? INFINITY : mx;
                     }
-                    mx *= d.scale_log2;
                 }
                 if (g > 0) named_bar(1 + qq + 4 * half, 64);  // the other group has decided for the page before
                 const float before = j > 0 ? refs[row] : -INFINITY;
@@ -584,17 +648,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t nm2 = pair(__float_as_uint(nm), __float_as_uint(nm));
                 const uint64_t sc2 = pair(__float_as_uint(d.scale_log2), __float_as_uint(d.scale_log2));
                 uint64_t l2[2] = {0, 0};
-                uint32_t pk[32];
+#pragma unroll 1
+                for (int e0 = 0; e0 < 64; e0 += 32) {
+                    uint32_t sv[32], pk[16];
+                    tmem_ld_32x32b_x32(tS + e0, sv);
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    float x0, x1;
-                    unpair(fma2(pair(sv[e], sv[e + 1]), sc2, nm2), x0, x1);
-                    x0 = ex2_approx(x0);
-                    x1 = ex2_approx(x1);
-                    l2[e / 2 & 1] = add2(l2[e / 2 & 1], pair(__float_as_uint(x0), __float_as_uint(x1)));
-                    pk[e / 2] = pack_bf16x2(x0, x1);
+                    for (int e = 0; e < 32; e += 2) {
+                        float x0, x1;
+                        unpair(fma2(pair(sv[e], sv[e + 1]), sc2, nm2), x0, x1);
+                        x0 = ex2_approx(x0);
+                        x1 = ex2_approx(x1);
+                        l2[e / 2 & 1] = add2(l2[e / 2 & 1], pair(__float_as_uint(x0), __float_as_uint(x1)));
+                        pk[e / 2] = pack_bf16x2(x0, x1);
+                    }
+                    tmem_st_32x32b_x16(tS + e0 / 2, pk);
                 }
-                tmem_st_32x32b_x32(tS, pk);
                 {
                     float x0, x1;
                     unpair(add2(l2[0], l2[1]), x0, x1);
@@ -683,7 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++piece;
         }
-        if (!waited) pdl_wait();  // (a range without work)
     }
     tc_fence_before();
     __syncthreads();
@@ -935,7 +1002,7 @@ cudaError_t launch_tree(const TreeMaps& maps, const TreeArgs& a, int D_H, int R,
     if (D_H == DH && R == RR)                                                                                       \
         return few ? launch_dependent(tree_combine_kernel<DH, RR, 32>, dim3(4 * (DH / 32), a.tmax, a.batch),        \
                                       dim3(32, 8), 0, stream, a)                                                    \
-                   : launch_dependent(tree_combine_kernel<DH, RR, DH>, dim3(4, a.tmax, a.batch), dim3(32, 8), 0,    \
+                   : launch_dependent(tree_combine_kernel<DH, RR, 64>, dim3(4 * (DH / 64), a.tmax, a.batch), dim3(32, 8), 0,    \
                                       stream, a);
     LRKV_TC(64, 8) LRKV_TC(64, 16) LRKV_TC(64, 32) LRKV_TC(128, 8) LRKV_TC(128, 16) LRKV_TC(128, 32)
 #undef LRKV_TC
