@@ -217,6 +217,29 @@ __device__ __noinline__ bool clean_values(uint8_t* stage, int vr, int part, bool
     return found;
 }
 
+// A row's sums, as this thread has stored them (every second 32 columns of s^V and of the tile's latents), quads `rs`
+// apart: what is not finite in the values of the drafted tokens `spoilt` is added.
+__device__ __noinline__ void add_spoilt(float4* dst, int rs, unsigned long long spoilt, int part, int hl,
+                                        const int32_t* pages, int L, const uint16_t* sV, const uint16_t* zV, int D_H,
+                                        int R, int H, int h) {
+    for (; spoilt != 0; spoilt &= spoilt - 1) {
+        const int t = L + __ffsll(spoilt) - 1;
+        const size_t at = (size_t)pages[t / kBlockSize] * kBlockSize + t % kBlockSize;
+#pragma unroll 1
+        for (int c = 0; c < D_H + R; c += 4) {
+            if (((c < D_H ? c : hl * R + c - D_H) / 32 & 1) != part) continue;
+            const uint2 y = *reinterpret_cast<const uint2*>(c < D_H ? sV + at * D_H + c : zV + (at * H + h) * R + c - D_H);
+            float4 x = dst[(size_t)(c / 4) * rs];
+            auto add = [](float& z, float e) { z += fabsf(e) < INFINITY ? 0.f : e; };
+            add(x.x, bf16lo(y.x));
+            add(x.y, bf16hi(y.x));
+            add(x.z, bf16lo(y.y));
+            add(x.w, bf16hi(y.y));
+            dst[(size_t)(c / 4) * rs] = x;
+        }
+    }
+}
+
 template <int D_H, int D_R, int ZW>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_scan_kernel(const __grid_constant__ TreeMaps m, const __grid_constant__ TreeArgs a, const int R) {
@@ -463,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile float* const refs = reinterpret_cast<float*>(smem + Lay::OFF_ROW);
         float2* const sums = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
         bool ok = true;
-        int g = 0, sb = 0, kst = 0, vst = 0, piece = 0;  // pages so far, its S buffer and stages, pieces so far
-        uint32_t kphase = 0, vphase = 0;
+        int g0 = 0, sb0 = 0, kst0 = 0, vst0 = 0, piece = 0;  // pages so far, S buffer and stages of the next, pieces so far
+        uint32_t kphase0 = 0, vphase0 = 0;
         // 64 columns of a block into TMEM (two columns a register), or K-major with 128-byte swizzle (16-byte chunk c
         // at c ^ (row mod 8))
         auto put_block = [&](int bk, const uint4* x) {
@@ -566,35 +589,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             have = w.next(a);  // (from here on the walk shows the next piece)
             float mref = -INFINITY, l = 0.f;  // the reference that this group knows, and its sum relative to that
             // After an expired wait the loop goes on without work, so that the groups still meet at their barriers.
-            auto turn = [&]() {
-                ++g;
-                if (++sb == NSB) sb = 0;
-                if (++kst == KST) {
-                    kst = 0;
-                    kphase ^= 1;
-                }
-                if (++vst == VST) {
-                    vst = 0;
-                    vphase ^= 1;
-                }
+            // S buffer and stages of page g; the thread's own pages are every second one
+            int sb = sb0, kst = kst0, vst = vst0;
+            uint32_t kphase = kphase0, vphase = vphase0;
+            auto advance = [&](int pages) {  // by 1 or 2
+                sb += pages;
+                sb -= sb >= NSB ? NSB : 0;
+                kst += pages;
+                kphase ^= kst >= KST;
+                kst -= kst >= KST ? KST : 0;
+                vst += pages;
+                vphase ^= vst >= VST;
+                vst -= vst >= VST ? VST : 0;
             };
             auto wait_before = [&]() {  // until the page before has been added to O
                 return wait_warp(B(o_done + (vst > 0 ? vst - 1 : VST - 1)), vst > 0 ? vphase : vphase ^ 1, d, abort_flag);
             };
-            // page ids of 32 pages at a time, the next ones on their way (a load per page, some 700 cycles late, was
-            // half of a page's time)
             const int32_t* const pages = d.block_table + (size_t)b * d.max_pages + p0;
-            auto fetch = [&](int k) { return k < nt ? pages[k] : -1; };
-            int ids = fetch(lane), ids_next = fetch(32 + lane);
-            for (int j = 0; j < nt; ++j, turn()) {
-                if (j > 0 && (j & 31) == 0) {
-                    ids = ids_next;
-                    ids_next = fetch(j + 32 + lane);
-                }
-                if ((g & 1) != half) continue;
+            const int j0 = (g0 ^ half) & 1;
+            if (j0) advance(1);
+            // (a page's id is loaded a page ahead: some 700 cycles late, it was half of a page's time)
+            int blk_next = j0 < nt ? pages[j0] : -1;
+            for (int j = j0; j < nt; j += 2, advance(2)) {
+                const int g = g0 + j, blk = blk_next;
+                blk_next = j + 2 < nt ? pages[j + 2] : -1;
                 const uint32_t tS = tmem + tl + Lay::TM_S + sb * 64;
                 const int base = (p0 + j) * kBlockSize;
-                const int blk = __shfl_sync(0xffffffffu, ids, j & 31);
                 const bool good = blk >= 0 && blk < d.num_blocks;
                 const bool inner = good && base + kBlockSize <= L;  // every row sees every token
                 ok = ok && wait_warp(B(s_done + kst), kphase, d, abort_flag);
@@ -638,7 +658,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 refs[row] = now;
                 if (j + 1 < nt || have) named_arrive(1 + qq + 4 * (half ^ 1), 64);
                 if (!ok) continue;
-                const float alpha = raise && before != -INFINITY ? ex2_approx(before - now) : 1.f;
                 if (mref != now) {
                     l = mref == -INFINITY ? 0.f : l * ex2_approx(mref - now);
                     mref = now;
@@ -673,6 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = wait_before();
                     if (ok) {
                         tc_fence_after();
+                        const float alpha = raise && before != -INFINITY ? ex2_approx(before - now) : 1.f;
                         uint32_t v[32];
 #pragma unroll 1
                         for (int c = 0; c < (D_H + ZW) / 32; ++c) {
@@ -689,6 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 arrive(p_full + sb);
             }
+            g0 += nt;
+            sb0 = (sb0 + nt) % NSB;
+            kphase0 ^= (kst0 + nt) / KST & 1;
+            kst0 = (kst0 + nt) % KST;
+            vphase0 ^= (vst0 + nt) / VST & 1;
+            vst0 = (vst0 + nt) % VST;
             // the row's sum over both groups' pages
             sums[half * 128 + row] = make_float2(l, mref);
             named_bar(9 + qq, 64);
@@ -697,32 +723,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             float ls = (mref == -INFINITY ? 0.f : l * ex2_approx(mref - M)) +
                        (other.y == -INFINITY ? 0.f : other.x * ex2_approx(other.y - M));
             // ---- partials, unnormalised: [column quad][row], so that a warp's stores are consecutive
+            vst = vst0;
+            vphase = vphase0;
             if (ok) ok = wait_before();
             if (ok) {
                 tc_fence_after();
                 const bool nan = ls != ls;  // handed on as NaN values with a weight, not as an empty part
                 const float mo = nan && !(fabsf(M) < INFINITY) ? 0.f : M;
-                if (half == 0) a.ml[(size_t)slot * 128 + row] = make_float2(mo, nan ? 1.f : ls);
-                float4* const dst = a.acc + (size_t)slot * (W / 4) * 128 + row;
-                const unsigned long long spoilt = live ? poison[piece & 1] & tree : 0ull;
+                // (rows without a drafted token or head are not stored)
+                if (half == 0 && live) a.ml[(size_t)slot * a.rs + hl * a.tn + il] = make_float2(mo, nan ? 1.f : ls);
+                float4* const dst = a.acc + (size_t)slot * (W / 4) * a.rs + hl * a.tn + il;
                 const float bad = __uint_as_float(0x7fc00000u);
                 auto put = [&](const uint32_t* v, int c) {  // columns c .. c + 3 of [s^V | z^V of the row's head]
-                    float4 x = make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
-                                           __uint_as_float(v[3]));
-                    if (nan) x = make_float4(bad, bad, bad, bad);
-                    for (unsigned long long todo = spoilt; todo != 0; todo &= todo - 1) {
-                        const int t = L + __ffsll(todo) - 1;
-                        const size_t at = (size_t)d.block_table[(size_t)b * d.max_pages + t / kBlockSize] * kBlockSize +
-                                          t % kBlockSize;
-                        const uint2 y = *reinterpret_cast<const uint2*>(c < D_H ? a.sV + at * D_H + c
-                                                                                : a.zV + (at * H + h) * R + c - D_H);
-                        auto add = [](float& z, float e) { z += fabsf(e) < INFINITY ? 0.f : e; };
-                        add(x.x, bf16lo(y.x));
-                        add(x.y, bf16hi(y.x));
-                        add(x.z, bf16lo(y.y));
-                        add(x.w, bf16hi(y.y));
-                    }
-                    dst[(size_t)(c / 4) * 128] = x;
+                    if (live)
+                        dst[(size_t)(c / 4) * a.rs] = nan ? make_float4(bad, bad, bad, bad)
+                                                          : make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]),
+                                                                        __uint_as_float(v[2]), __uint_as_float(v[3]));
                 };
 #pragma unroll 1
                 for (int c = half; c < D_H / 32; c += 2) {
@@ -746,6 +762,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
+                const unsigned long long spoilt = live ? poison[piece & 1] & tree : 0ull;
+                if (spoilt)
+                    add_spoilt(dst, a.rs, spoilt, half, hl, d.block_table + (size_t)b * d.max_pages, L, a.sV, a.zV, D_H, R, H,
+                               h);
             } else {
                 *abort_flag = 1;
             }
@@ -766,8 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Merge of a tile's pieces, B_h^V, division by the sum: grid (4 groups of 32 rows x D_H / DC groups of DC output columns,
-// tiles, sequences), block (32, 8).  A lane is a row while the pieces are read (consecutive rows' quads lie side by
+// Merge of a tile's pieces, B_h^V, division by the sum: grid (groups of 32 rows x D_H / DC groups of DC output columns, tiles,
+// sequences), block (32, 8).  A lane is a row while the pieces are read (consecutive rows' quads lie side by
 // side), output columns after.  Where there are few tiles a block takes few columns (and reads the latents' sums again) and
 // has the loads of four pieces in flight; many tiles are of one or two pieces each, and more blocks fit with one.
 template <int D_H, int R, int DC>
@@ -775,21 +795,23 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
     constexpr int W4 = (D_H + R) / 4, C4 = (DC + R) / 4, QPW = (C4 + 7) / 8, DPL = DC / 32, kPieces = DC == 32 ? 4 : 1;
     const DecodeArgs& d = a.d;
     const int lane = threadIdx.x, warp = threadIdx.y, b = blockIdx.z, t = blockIdx.y;
-    const int row0 = (blockIdx.x & 3) * 32, row = row0 + lane, d0 = (blockIdx.x >> 2) * DC;
+    // rows: head x drafted token of the tile, tn tokens a head
+    const int groups = a.rs / 32, row0 = blockIdx.x % groups * 32, row = row0 + lane, d0 = blockIdx.x / groups * DC;
     __shared__ float tile[32][DC + R + 1];
     const Seq s = seq_of(a, b);  // (the caller's, not of a launch before this one)
     const int st_b = max(1, (s.n + a.ns - 1) / a.ns), h0 = t / st_b * a.hb, i0 = t % st_b * a.ns;
-    // four rows of one head per warp (ns is a multiple of 4), DPL output columns per lane
-    const int r0 = warp * 4, h = h0 + (row0 + r0) / a.ns;
-    const bool mine = !s.bad && t < tiles_of(a, s.n) && h < d.H;
+    // four rows per warp, mostly of one head, DPL output columns per lane
+    const int r0 = warp * 4;
+    int h = h0 + (row0 + r0) / a.tn;
     uint4 f[DPL][R / 8];
-    if (mine) {
+    auto factors = [&]() {
         const uint16_t* bv = d.BV + ((size_t)h * D_H + d0 + lane * DPL) * R;
 #pragma unroll
         for (int e = 0; e < DPL; ++e)
 #pragma unroll
             for (int k = 0; k < R / 8; ++k) f[e][k] = *reinterpret_cast<const uint4*>(bv + e * R + k * 8);
-    }
+    };
+    if (!s.bad && t < tiles_of(a, s.n) && h < d.H) factors();
     pdl_wait();  // the scan (in every block: this grid's end stands for that of the launches before it)
     if (s.bad) {  // zeros in all T rows: the tiles of a full sequence share them
         if (t == 0 && blockIdx.x == 0 && lane == 0 && warp == 0) set_status(d.status, LRKV_DEV_BAD_SEQLEN);
@@ -799,26 +821,27 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
             out[i] = make_uint4(0, 0, 0, 0);
         return;
     }
-    if (t >= tiles_of(a, s.n) || h0 + row0 / a.ns >= d.H || (a.ns >= 32 && i0 + row0 % a.ns >= s.n)) return;
-    const bool live = h0 + row / a.ns < d.H && i0 + row % a.ns < s.n;
+    if (t >= tiles_of(a, s.n) || h0 + row0 / a.tn >= d.H) return;
+    const bool live = row < a.hb * a.tn && h0 + row / a.tn < d.H && i0 + row % a.tn < s.n;
+    if (!__syncthreads_or(live)) return;
     const int2 fe = a.seg_table[b * a.tmax + t];
     float M = -INFINITY, ls = 0.f;
     float4 x[QPW];
 #pragma unroll
     for (int e = 0; e < QPW; ++e) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float2* const ml0 = a.ml + (size_t)fe.x * 128 + row;
-    const float4* const acc0 = a.acc + (size_t)fe.x * W4 * 128 + row;
+    const float2* const ml0 = a.ml + (size_t)fe.x * a.rs + row;
+    const float4* const acc0 = a.acc + (size_t)fe.x * W4 * a.rs + row;
     for (int k0 = 0; live && k0 < fe.y; k0 += kPieces) {
         float2 ml[kPieces];
         float4 y[kPieces][QPW];
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) {
             const bool there = k0 + k < fe.y;
-            ml[k] = there ? ml0[(size_t)(k0 + k) * a.gang * 128] : make_float2(-INFINITY, 0.f);
+            ml[k] = there ? ml0[(size_t)(k0 + k) * a.gang * a.rs] : make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int e = 0; e < QPW; ++e) {
                 const int c = e * 8 + warp, at = c < DC / 4 ? d0 / 4 + c : D_H / 4 + c - DC / 4;
-                y[k][e] = there && c < C4 ? acc0[((size_t)(k0 + k) * a.gang * W4 + at) * 128]
+                y[k][e] = there && c < C4 ? acc0[((size_t)(k0 + k) * a.gang * W4 + at) * a.rs]
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
@@ -862,11 +885,14 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
         tile[lane][c + 3] = x[e].w * inv;
     }
     __syncthreads();
-    if (!mine) return;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int i = i0 + (row0 + r0 + r) % a.ns;
-        if (i >= s.n) continue;
+        const int rr = row0 + r0 + r, i = i0 + rr % a.tn, hr = h0 + rr / a.tn;
+        if (rr >= a.hb * a.tn || i >= s.n || hr >= d.H) continue;
+        if (hr != h) {
+            h = hr;
+            factors();
+        }
         float y[DPL];
 #pragma unroll
         for (int e = 0; e < DPL; ++e) y[e] = tile[r0 + r][lane * DPL + e];
@@ -937,6 +963,7 @@ static int tree_gang(int tiles, int sms) {
 
 struct TreeSizes {
     int gang, gangs, gmax;  // CTAs of a gang, gangs, groups of tiles of a sequence
+    int tn, rs;             // drafted tokens of a tile at most, rows kept of it
     size_t qt, seg, ml, acc;
 };
 static TreeSizes tree_sizes(int H, int D_H, int R, int batch, int T, const TreePlan& p, int sms) {
@@ -945,11 +972,13 @@ static TreeSizes tree_sizes(int H, int D_H, int R, int batch, int T, const TreeP
     z.gang = tree_gang(tiles, sms);
     z.gangs = sms / z.gang;
     z.gmax = (tiles + z.gang - 1) / z.gang;
+    z.tn = T < p.ns ? T : p.ns;
+    z.rs = (p.hb * z.tn + 31) / 32 * 32;
     const size_t slots = ((size_t)z.gangs + (size_t)batch * z.gmax) * z.gang;
     z.qt = align256((size_t)batch * T * H * R * sizeof(float));
     z.seg = align256((size_t)batch * tiles * sizeof(int2));
-    z.ml = align256(slots * 128 * sizeof(float2));
-    z.acc = align256(slots * 128 * (D_H + R) * sizeof(float));
+    z.ml = align256(slots * z.rs * sizeof(float2));
+    z.acc = align256(slots * z.rs * (D_H + R) * sizeof(float));
     return z;
 }
 
@@ -969,6 +998,8 @@ void tree_carve_workspace(TreeArgs* a, void* ws, int D_H, int R, int D_R, int sm
     a->gang = z.gang;
     a->gangs = z.gangs;
     a->gmax = z.gmax;
+    a->tn = z.tn;
+    a->rs = z.rs;
     uint8_t* at = static_cast<uint8_t*>(ws);
     a->d.qt = reinterpret_cast<float*>(at);
     a->seg_table = reinterpret_cast<int2*>(at += z.qt);
@@ -997,12 +1028,13 @@ cudaError_t launch_tree(const TreeMaps& maps, const TreeArgs& a, int D_H, int R,
     LRKV_TS(64, 0) LRKV_TS(64, 64) LRKV_TS(128, 0) LRKV_TS(128, 64)
 #undef LRKV_TS
     if (e != cudaSuccess) return e;
-    const bool few = (long long)a.tmax * a.batch * 4 <= 4 * a.gang * a.gangs;  // blocks for fewer than four an SM
+    const int groups = a.rs / 32;
+    const bool few = (long long)a.tmax * a.batch * groups <= 4 * a.gang * a.gangs;  // blocks for fewer than four an SM
 #define LRKV_TC(DH, RR)                                                                                             \
     if (D_H == DH && R == RR)                                                                                       \
-        return few ? launch_dependent(tree_combine_kernel<DH, RR, 32>, dim3(4 * (DH / 32), a.tmax, a.batch),        \
+        return few ? launch_dependent(tree_combine_kernel<DH, RR, 32>, dim3(groups * (DH / 32), a.tmax, a.batch),        \
                                       dim3(32, 8), 0, stream, a)                                                    \
-                   : launch_dependent(tree_combine_kernel<DH, RR, 64>, dim3(4 * (DH / 64), a.tmax, a.batch), dim3(32, 8), 0,    \
+                   : launch_dependent(tree_combine_kernel<DH, RR, 64>, dim3(groups * (DH / 64), a.tmax, a.batch), dim3(32, 8), 0,    \
                                       stream, a);
     LRKV_TC(64, 8) LRKV_TC(64, 16) LRKV_TC(64, 32) LRKV_TC(128, 8) LRKV_TC(128, 16) LRKV_TC(128, 32)
 #undef LRKV_TC

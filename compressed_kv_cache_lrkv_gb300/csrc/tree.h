@@ -15,9 +15,10 @@ struct TreeArgs {
     int batch, T;
     int zw, hb, ns, htiles, tmax;  // the tile (below); tmax: tiles of a sequence with T drafted tokens
     int gang, gangs, gmax;         // CTAs that take neighbouring tiles together, gangs, groups of a sequence's tiles
+    int tn, rs;                    // drafted tokens of a tile at most (T or ns), rows kept of a tile (hb tn and up to 31)
     int2* seg_table;               // [batch * tmax] first partial and their number
-    float2* ml;                    // [slot][128] running max (log2 domain) and sum
-    float4* acc;                   // [slot][(D_H + R) / 4][128]
+    float2* ml;                    // [slot][rs] running max (log2 domain) and sum
+    float4* acc;                   // [slot][(D_H + R) / 4][rs]
 };
 
 // A CTA's 128 query rows are hb heads x ns drafted tokens of one sequence, with hb r = zw columns of latents.

@@ -329,3 +329,44 @@ def test_workspace_is_checked():
             b.lrkv_decode_tree(c.dims, c.q, c.BK, c.BV, c.cache, c.bt, c.sl, c.mask, c.tl, c.out, ws)
         assert e.value.status in (1, 3)
     assert (c.out == MARK).all()
+
+
+@pytest.mark.parametrize("H,d_h,r,d_rope,lens,T", [(32, 128, 16, 0, [4000, 200], 20), (32, 128, 32, 0, [3000], 8),
+                                                   (8, 64, 16, 64, [900] * 8, 64), (128, 128, 16, 0, [700, 90], 64)])
+def test_expired_wait_reports_timeout_and_gpu_stays_usable(monkeypatch, H, d_h, r, d_rope, lens, T):
+    """With the debugging limit LRKV_DEBUG_WAIT_LIMIT_NS=0 the scan's waits give up as soon as something is not already
+    there.  The call ends, reports LRKV_DEV_TIMEOUT and nothing else, and the next one is right to the bit."""
+    c = Case(16, H, d_h, r, d_rope, lens, [T] * len(lens))
+    c.run()
+    assert int(c.st.item()) == 0
+    want = c.out.clone()
+    c.verify(every=7)
+    monkeypatch.setenv("LRKV_DEBUG_WAIT_LIMIT_NS", "0")
+    seen = 0
+    for _ in range(5):
+        c.run()
+        seen |= int(c.st.item())
+    assert seen == b.DEV_TIMEOUT
+    monkeypatch.delenv("LRKV_DEBUG_WAIT_LIMIT_NS")
+    c.st.zero_()
+    c.out.fill_(MARK)
+    c.run()
+    assert int(c.st.item()) == 0 and torch.equal(c.out, want)
+
+
+def test_many_short_sequences():
+    """More tiles than the GPU takes at once, of a page or two each, one drafted token and several; odd head counts."""
+    for H, r, T in ((33, 32, 1), (17, 16, 3)):
+        c = Case(17, H, 128, r, 0, [5 * i % 130 for i in range(150)], [1 + i % T for i in range(150)])
+        c.run()
+        assert int(c.st.item()) == 0
+        c.verify(seqs=range(0, 150, 7))
+
+
+def test_workspace_stays_in_proportion():
+    """The workspace grows with the queries, not with the rows of the kernel's tiles: for one drafted token at most
+    32 rows a tile are kept."""
+    dims = b.make_dims(128, 128, 16, 128 * 128)
+    for T in (1, 8, 64):
+        per_query = b.decode_tree_workspace_bytes(dims, 256, T) / (256 * T * 128)
+        assert per_query <= 4 * (128 + 16 + 16 + 2) * (32 / min(32, 8 * T)) * 1.2 + 64, T
