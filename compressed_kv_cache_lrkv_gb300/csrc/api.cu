@@ -1099,7 +1099,9 @@ lrkv_status lrkv_pages_fork(const lrkv_pools* pools, int32_t* refs, int32_t* blo
     if (!parents || !children) return fail(LRKV_ERR_INVALID_ARG, "parents or children is NULL");
     const lrkv::PageArgs a{refs, block_table, seq_lens, parents, children, status_dev, pools->num_blocks,
                            max_blocks_per_seq, batch, n};
-    return cuda_status(lrkv::launch_pages_fork(p, a, static_cast<cudaStream_t>(stream)), "lrkv_pages_fork launch");
+    DeviceInfo di;
+    if ((s = device_info(&di)) != LRKV_OK) return s;
+    return cuda_status(lrkv::launch_pages_fork(p, a, di.sms, static_cast<cudaStream_t>(stream)), "lrkv_pages_fork launch");
 }
 
 lrkv_status lrkv_pages_free(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,

@@ -43,7 +43,7 @@ struct CompactArgs {
     int max_pages, batch, max_path;
 };
 cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream);
-cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t stream);
+cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream);
 cudaError_t launch_pages_copy(const PoolArgs& src, const PoolArgs& dst, const int32_t* src_pages,
                               const int32_t* dst_pages, int n, int sms, uint32_t* status, cudaStream_t stream);

@@ -152,12 +152,19 @@ __device__ void grant(int* need, int n, const int32_t* refs, int num_blocks, int
 
 __device__ __forceinline__ int pages_of(long long tokens) { return (int)((tokens + kBlockSize - 1) / kBlockSize); }
 
-__device__ __forceinline__ void give_back(int32_t* refs, int num_blocks, int page, uint32_t* status) {
-    if (page >= num_blocks) {
-        set_status(status, LRKV_DEV_BAD_BLOCK);
-    } else if (atomicSub(refs + page, 1) <= 0) {
-        atomicAdd(refs + page, 1);
-        set_status(status, LRKV_DEV_BAD_INDEX);
+// E pages (negative: none) given back, their atomics on the way together.
+template <int E>
+__device__ __forceinline__ void give_back(int32_t* refs, int num_blocks, const int* page, uint32_t* status) {
+    int old[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) old[e] = page[e] >= 0 && page[e] < num_blocks ? atomicSub(refs + page[e], 1) : 1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (page[e] >= num_blocks) set_status(status, LRKV_DEV_BAD_BLOCK);
+        if (old[e] <= 0) {
+            atomicAdd(refs + page[e], 1);
+            set_status(status, LRKV_DEV_BAD_INDEX);
+        }
     }
 }
 
@@ -252,10 +259,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const PageArgs 
             }
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (page[e] >= 0) {
-                    give_back(a.refs, a.num_blocks, page[e], a.status);
-                    row[k0 + e * lanes + lane] = -1;
-                }
+                if (page[e] >= 0) row[k0 + e * lanes + lane] = -1;
+            give_back<E>(a.refs, a.num_blocks, page, a.status);
         }
     }
     __threadfence();
@@ -300,32 +305,36 @@ __device__ __forceinline__ int pool_of(const PoolArgs& p, int* u) {
     return k;
 }
 
-// Rows of the children's last pages: grid (units in pieces, forks, layers).
-__global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, const PageArgs a) {
-    const int i = blockIdx.y;
+// Rows of the children's last pages: grid (forks, layers, parts of a page's rows), about as many blocks as run at once, since
+// each begins with a chain of loads (in pieces of 32 KB, 64 forks of 4 layers 20 us).
+constexpr int kForkThreads = 512;
+__global__ void __launch_bounds__(kForkThreads) fork_copy_kernel(const PoolArgs p, const PageArgs a) {
+    const int i = blockIdx.x;
     begin_dependent();
-    if (fork_refused(a, i, threadIdx.x, 256, [](uint32_t x) { return (uint32_t)__syncthreads_or(x != 0); })) return;
+    if (fork_refused(a, i, threadIdx.x, kForkThreads, [](uint32_t x) { return (uint32_t)__syncthreads_or(x != 0); })) return;
     const int par = a.a[i], c = a.b[i], L = a.lens[c];  // (0 where no page was left for the child)
     if (L % kBlockSize == 0) return;
     const int k = L / kBlockSize, from = a.table[(size_t)par * a.max_pages + k], to = a.table[(size_t)c * a.max_pages + k];
-    const int rows = L % kBlockSize, n = rows * p.units;
-    constexpr int E = 8;
-    uint4 v[E];
-    uint4* out[E];
+    const int rows = L % kBlockSize, n = rows * p.units, step = gridDim.z * kForkThreads;
+    constexpr int E = 6;
+    for (int u0 = blockIdx.z * kForkThreads + threadIdx.x; u0 < n; u0 += step * E) {
+        uint4 v[E];
+        uint4* out[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        int pool = 0, u = (blockIdx.x * E + e) * 256 + threadIdx.x;
-        out[e] = nullptr;
-        if (u >= n) continue;
-        while (pool + 1 < p.pools && u >= p.u[pool] * rows) u -= p.u[pool++] * rows;
-        uint4* b = p.base[pool] + (size_t)blockIdx.z * p.layer[pool];
-        const size_t page = (size_t)kBlockSize * p.u[pool];
-        v[e] = b[from * page + u];
-        out[e] = b + to * page + u;
+        for (int e = 0; e < E; ++e) {
+            int pool = 0, u = u0 + e * step;
+            out[e] = nullptr;
+            if (u >= n) continue;
+            while (pool + 1 < p.pools && u >= p.u[pool] * rows) u -= p.u[pool++] * rows;
+            uint4* b = p.base[pool] + (size_t)blockIdx.y * p.layer[pool];
+            const size_t page = (size_t)kBlockSize * p.u[pool];
+            v[e] = b[from * page + u];
+            out[e] = b + to * page + u;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (out[e]) *out[e] = v[e];
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (out[e]) *out[e] = v[e];
 }
 
 // ---------------------------------------------------------------- free: a block per sequence
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(256) free_kernel(const PageArgs a) {
     for (int k = pages_of(keep) + threadIdx.x; k < a.max_pages; k += 256) {
         if (row[k] < 0) continue;
         const int page = atomicExch(row + k, -1);  // (the sequence may be listed twice)
-        if (page >= 0) give_back(a.refs, a.num_blocks, page, a.status);
+        give_back<1>(a.refs, a.num_blocks, &page, a.status);
     }
     if (threadIdx.x == 0) {
         const int L = a.lens[b];
@@ -503,7 +512,7 @@ cudaError_t launch_pages_reserve(const PageArgs& a, cudaStream_t stream) {
     return launch_dependent(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a);
 }
 
-cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t stream) {
+cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, int sms, cudaStream_t stream) {
     const size_t smem = 2 * (size_t)a.n * sizeof(int);
     if (smem > 32768) {  // (beside 8 KB of its own)
         const cudaError_t e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -512,8 +521,10 @@ cudaError_t launch_pages_fork(const PoolArgs& p, const PageArgs& a, cudaStream_t
     }
     const cudaError_t e = launch_dependent(fork_plan_kernel, dim3(1), dim3(kPlanThreads), smem, stream, a);
     if (e != cudaSuccess) return e;
-    const int pieces = (kBlockSize * p.units + 256 * 8 - 1) / (256 * 8);
-    return launch_dependent(fork_copy_kernel, dim3(pieces, a.n, p.layers), dim3(256), 0, stream, p, a);
+    const long long pages = (long long)a.n * p.layers;
+    const int most = (kBlockSize * p.units + kForkThreads - 1) / kForkThreads;
+    const int parts = pages >= 2 * sms ? 1 : (int)(2 * sms / pages) < most ? (int)(2 * sms / pages) : most;
+    return launch_dependent(fork_copy_kernel, dim3(a.n, p.layers, parts), dim3(kForkThreads), 0, stream, p, a);
 }
 
 cudaError_t launch_pages_free(const PageArgs& a, cudaStream_t stream) {
