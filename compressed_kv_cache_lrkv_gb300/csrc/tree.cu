@@ -39,13 +39,13 @@ struct TrLayout {
     static constexpr int NSB = (512 - 192 - D_H - ZW) / 32 >= NBQ ? 3 : 2, QROOM = (512 - 64 * NSB - D_H - ZW) / 32;
     static constexpr int QBT = NBQ < QROOM ? NBQ : QROOM, QBS = NBQ - QBT;  // blocks in TMEM, in shared memory
     static constexpr uint32_t Q_BYTES = QBS * 16384;
-    static constexpr uint32_t ROOM = 232448 - 1024 - 4096 - Q_BYTES;
+    static constexpr uint32_t ROOM = 232448 - 1024 - 5120 - Q_BYTES;
     static constexpr int BOTH = ROOM / (K_BYTES + V_BYTES);
     static constexpr int VST = BOTH > 6 ? 6 : BOTH;
     static constexpr int KST = VST < 6 && ROOM - VST * (K_BYTES + V_BYTES) >= K_BYTES ? VST + 1 : VST;
     static constexpr uint32_t OFF_K = Q_BYTES, OFF_V = OFF_K + KST * K_BYTES, OFF_BAR = OFF_V + VST * V_BYTES;
-    static constexpr uint32_t OFF_ROW = OFF_BAR + 512;  // 128 references, then 2 x 128 (sum, reference)
-    static constexpr uint32_t SMEM = OFF_ROW + 512 + 2048 + 1024;
+    static constexpr uint32_t OFF_ROW = OFF_BAR + 512;  // 128 references, then [piece's parity][group][128] (sum, reference)
+    static constexpr uint32_t SMEM = OFF_ROW + 512 + 4096 + 1024;
     static_assert(VST >= 2 && KST >= NSB && SMEM <= 232448, "stages");
     static constexpr uint32_t TM_S = 0, TM_O = 64 * NSB, TM_Q = TM_O + D_H + ZW;
     static_assert(TM_Q + QBT * 32 <= 512, "TMEM");
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tl = (uint32_t)(qq * 32) << 16;
         const int hl = row / a.ns, il = row - hl * a.ns;
         volatile float* const refs = reinterpret_cast<float*>(smem + Lay::OFF_ROW);
-        float2* const sums = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
+        float2* const sums2 = reinterpret_cast<float2*>(smem + Lay::OFF_ROW + 512);
         bool ok = true;
         int g0 = 0, sb0 = 0, kst0 = 0, vst0 = 0, piece = 0;  // pages so far, S buffer and stages of the next, pieces so far
         uint32_t kphase0 = 0, vphase0 = 0;
@@ -716,6 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             vphase0 ^= (vst0 + nt) / VST & 1;
             vst0 = (vst0 + nt) % VST;
             // the row's sum over both groups' pages
+            // (by the piece's parity: a group without a page in the next piece gets there while the other may still read)
+            float2* const sums = sums2 + (piece & 1) * 256;
             sums[half * 128 + row] = make_float2(l, mref);
             named_bar(9 + qq, 64);
             const float2 other = sums[(half ^ 1) * 128 + row];

@@ -363,6 +363,17 @@ def test_many_short_sequences():
         c.verify(seqs=range(0, 150, 7))
 
 
+def test_consecutive_one_page_pieces_repeat_exactly():
+    """CTAs with many pieces of one page each: the group of rows without a page goes ahead into the next piece, whose
+    sums must not reach the piece before.  Every sequence is compared with 64 bits, and runs with one another."""
+    c = Case(23, 33, 128, 16, 0, [7 * i % 60 for i in range(300)], [1 + i % 3 for i in range(300)])
+    first = c.run().clone()
+    assert int(c.st.item()) == 0
+    c.verify(seqs=range(0, 300, 3))
+    for _ in range(20):
+        assert torch.equal(c.run(), first)
+
+
 def test_workspace_stays_in_proportion():
     """The workspace grows with the queries, not with the rows of the kernel's tiles: for one drafted token at most
     32 rows a tile are kept."""
