@@ -6,7 +6,19 @@
 // The cached rows are the same for all heads and drafted tokens, so 128 query rows, hb heads x ns tokens of one
 // sequence, are one attention tile of width d_h + zw, zw = hb r (as in prefix.cu, there over sequences):
 //     S = [Q | diag(Q~)] . [s^K | z^K of the hb heads]^T,   O += P . [s^V | z^V of the hb heads]
-// on tcgen05, M = 128, 64 tokens (a page) at a time.
+// on tcgen05, M = 128, 64 tokens (a page) at a time.  zw is 32, 64 or 128 (tree_plan); 32 for up to 64 drafted tokens of
+// r = 16, so that each latent is read by one tile.
+//
+// Three dependent launches: q~ (decode.cu's absorb, every drafted token a query), the scan, the merge.  The scan is
+// persistent, one CTA an SM, with the tiles' pages divided evenly (Work).  Warps: 0 keys and 6 values (TMA), 1 issues
+// all MMAs, 2 .. 5 and 8 .. 11 are two groups of 128 query rows that take the pages in turn.
+//
+// Measured (a call in a stream of others): 8 heads of 64, r = 16, 1 x 4 drafted behind 256 tokens 13 us; 16 x 16 behind
+// 2,048 20 us; 32 heads of 128, r = 16, positional key, 24 x up to 26 behind 1 to 8,191 92 us; 32 heads, r = 32, 4 x 8
+// behind 16 to 32 K 99 us (475 MB read, 70 us at the copy rate); 128 heads, r = 16, 8 x up to 64 behind 8,192 327 us.
+// In the last no single part bounds the scan: with the call at 305 us in a test, it took 269 without the softmax and 290
+// with most products left out.  More warps of rows (two threads a row, or a third group) were slower; issuing the two
+// products from two warps, P beside S, gained 1%.
 #include "lrkv_internal.cuh"
 #include "tile_attn.cuh"
 #include "tree.h"
@@ -17,7 +29,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.
+// What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.  (24 sequences of 1 to
+// 8,191 tokens: 91 us with 8 or 11, 95 with 4; 1 x 4 tokens behind 256: 17 us with 4, 15.8 with 8, 14.7 with 11.)
 constexpr int kStartPages = 11;
 
 __device__ __forceinline__ void named_arrive(int id, int threads) {
@@ -290,12 +303,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // the units of all sequences, and the sequence that holds this range's first
         long long total = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-            long long v = b0 + lane < a.batch ? units_of(a, seq_of(a, b0 + lane)) : 0;
+#pragma unroll 4
+        for (int b = lane; b < a.batch; b += 32) total += units_of(a, seq_of(a, b));
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            total += v;
-        }
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         const Work w(total, a.gangs);
         const long long lo = w.start(blockIdx.x / a.gang);
         long long base = 0;
@@ -401,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------------- MMAs
         // One thread issues all of them, so they run in this order: S_0 .. S_{NSB-1} | P_0 V_0, S_NSB | P_1 V_1, ..: S_{g+NSB}
         // overwrites the buffer that P_g V_g has read; while the rows work on S_g, the products of its neighbours run.
-        // (With a vote of the warp at every wait and MMA the issue took 1,970 cycles a page of 12 + 8 MMAs, of which the
-        // tensor cores need 704; from one thread 1,390.)
+        // (128 heads x 64 tokens: 481 us with a vote of the warp at every wait and MMA and two S buffers, 357 from one
+        // thread and with three.)
         constexpr uint32_t id_S = idesc_bf16_f32(128, 64);
         constexpr uint32_t id_PV = idesc_bf16_f32(128, D_H + ZW) | (1u << 16);  // B is MN-major
         if (elect_one_sync()) {
