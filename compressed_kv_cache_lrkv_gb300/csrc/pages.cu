@@ -108,7 +108,8 @@ __device__ __forceinline__ int owner(const int* pre, int n, int rank) {
 }
 
 // need[0..n) granted from the free pages, whole requests or none, in order (refused(i) for those that do not fit);
-// give(i, k, granted, page) is called for the k-th of the `granted` pages of request i.  The first search keeps the pages it finds, up to kPicked: they are all that most calls need.
+// give(i, k, granted, page) is called for the k-th of the `granted` pages of request i.  The first search keeps the pages it
+// finds, up to kPicked: they are all that most calls need.
 constexpr int kPicked = 2048;
 template <class F, class G>
 __device__ void grant(int* need, int n, const int32_t* refs, int num_blocks, int* warp_sums, int* picked, F&& refused,
@@ -306,7 +307,8 @@ __device__ __forceinline__ int pool_of(const PoolArgs& p, int* u) {
 }
 
 // Rows of the children's last pages: grid (forks, layers, parts of a page's rows), about as many blocks as run at once, since
-// each begins with a chain of loads (in pieces of 32 KB, 64 forks of 4 layers 20 us).
+// each begins with a chain of loads (in pieces of 32 KB, 64 forks of 4 layers 20 us).  The whole call, 64 forks, 35 us in a
+// stream of others, 32 in a graph; 11 for the bytes, the rest is the plan's chain of loads and this one's.
 constexpr int kForkThreads = 512;
 __global__ void __launch_bounds__(kForkThreads) fork_copy_kernel(const PoolArgs p, const PageArgs a) {
     const int i = blockIdx.x;
@@ -365,7 +367,8 @@ __global__ void __launch_bounds__(256) free_kernel(const PageArgs a) {
 // ---------------------------------------------------------------- copy of whole pages
 // A page's rows lie together in each pool, so it is moved in pieces of up to 16 KB by bulk copies, through a ring of
 // stages in shared memory.  A warp is a block: its lanes work out the next 32 pieces, one of them issues the copies.
-// 1,024 pages of 295 KB: 164 us with four 16-byte loads a thread, whose blocks came and went.
+// 1,024 pages of 295 KB: 99 us (89 for the bytes at the copy rate); 164 with four 16-byte loads a thread, whose blocks came
+// and went.
 constexpr uint32_t kPiece = 16384;
 constexpr int kStages = 6, kLag = 4;  // stages; pieces between a load's issue and its store's
 struct CopyArgs {

@@ -13,12 +13,12 @@
 // persistent, one CTA an SM, with the tiles' pages divided evenly (Work).  Warps: 0 keys and 6 values (TMA), 1 issues
 // all MMAs, 2 .. 5 and 8 .. 11 are two groups of 128 query rows that take the pages in turn.
 //
-// Measured (a call in a stream of others): 8 heads of 64, r = 16, 1 x 4 drafted behind 256 tokens 13 us; 16 x 16 behind
+// Measured (a call in a stream of others): 8 heads of 64, r = 16, 1 x 4 drafted behind 256 tokens 14 us; 16 x 16 behind
 // 2,048 20 us; 32 heads of 128, r = 16, positional key, 24 x up to 26 behind 1 to 8,191 92 us; 32 heads, r = 32, 4 x 8
-// behind 16 to 32 K 99 us (475 MB read, 70 us at the copy rate); 128 heads, r = 16, 8 x up to 64 behind 8,192 327 us.
-// In the last no single part bounds the scan: with the call at 305 us in a test, it took 269 without the softmax and 290
-// with most products left out.  More warps of rows (two threads a row, or a third group) were slower; issuing the two
-// products from two warps, P beside S, gained 1%.
+// behind 16 to 32 K 100 us (475 MB read, 70 us at the copy rate); 128 heads, r = 16, 8 x up to 64 behind 8,192 326 to 334 us.
+// In the last no single part bounds the scan: a variant that issues the two products from two warps took 305 us, 269 of
+// them without the softmax and 290 with most products left out.  That variant is within 1% of this one (306 then) and
+// was not kept; more warps of rows (two threads a row, or a third group) were slower.
 #include "lrkv_internal.cuh"
 #include "tile_attn.cuh"
 #include "tree.h"
