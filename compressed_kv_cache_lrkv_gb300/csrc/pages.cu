@@ -5,6 +5,8 @@
 // pages go to the requests in the order of the call by a prefix sum, so results do not depend on timing.
 #include <cooperative_groups.h>
 
+#include <climits>
+
 #include "draft.h"
 #include "lrkv_internal.cuh"
 #include "tile_attn.cuh"
@@ -170,31 +172,69 @@ __device__ __forceinline__ void give_back(int32_t* refs, int num_blocks, const i
 }
 
 // ---------------------------------------------------------------- reserve: one block
+// The empty entries of a row are counted from its first one on: a caller may set a length before the row has pages for
+// it.  They have to be the last ones of what is asked for, as in every row that these calls leave; a page that stands
+// behind an empty entry is not written over.
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a) {
     __shared__ int need[LRKV_MAX_PAGE_BATCH], warp_sums[32], picked[kPicked];
+    __shared__ int first_of[16], empty_of[16];
     begin_dependent();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // a warp per sequence: its first empty entry from the page of its length on
-    for (int b = warp; b < a.batch; b += kPlanThreads / 32) {
-        const int L = a.lens[b], add = a.b[b];
-        const int want = L >= 0 && add >= 0 ? pages_of((long long)L + add) : -1;
-        int held = want;
-        if (want < 0 || want > a.max_pages) {
-            if (lane == 0) set_status(a.status, LRKV_DEV_BAD_SEQLEN);
-            held = want;
-        } else {
-            for (int k = pages_of(L); k < want; k += 32) {
-                const bool empty = k + lane < want && a.table[(size_t)b * a.max_pages + k + lane] < 0;
-                const unsigned m = __ballot_sync(0xffffffffu, empty);
-                if (m) {
-                    held = k + __ffs(m) - 1;
-                    break;
-                }
-            }
-        }
-        if (lane == 0) need[b] = want - held;
+    // `parts` warps a sequence (of at most 16 where there are several), kEntries x 32 entries at a time
+    constexpr int kWarps = kPlanThreads / 32, kEntries = 8;
+    const int parts = a.batch < kWarps ? kWarps / a.batch : 1, part = warp % parts;
+    if (threadIdx.x < 16) {
+        first_of[threadIdx.x] = INT_MAX;
+        empty_of[threadIdx.x] = 0;
     }
     __syncthreads();
+    auto want_of = [&](int b) {
+        const int L = a.lens[b], add = a.b[b];
+        const int want = L >= 0 && add >= 0 ? pages_of((long long)L + add) : -1;
+        return want <= a.max_pages ? want : -1;
+    };
+    auto decide = [&](int b, int want, int first, int empty) {
+        need[b] = 0;
+        if (want < 0)
+            set_status(a.status, LRKV_DEV_BAD_SEQLEN);
+        else if (empty > 0 && first + empty != want)
+            set_status(a.status, LRKV_DEV_BAD_BLOCK);
+        else
+            need[b] = empty;
+    };
+    for (int b = warp / parts; b < a.batch && warp < parts * a.batch; b += kWarps / parts) {
+        const int want = want_of(b);
+        const int32_t* row = a.table + (size_t)b * a.max_pages;
+        int first = INT_MAX, empty = 0;  // of this lane's entries
+        for (int k0 = part * 32 * kEntries; k0 < want; k0 += parts * 32 * kEntries) {
+            int page[kEntries];
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) {
+                const int k = k0 + e * 32 + lane;
+                page[e] = k < want ? row[k] : 0;
+            }
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e) {
+                if (page[e] >= 0) continue;
+                first = min(first, k0 + e * 32 + lane);
+                ++empty;
+            }
+        }
+        first = __reduce_min_sync(0xffffffffu, first);
+        empty = __reduce_add_sync(0xffffffffu, empty);
+        if (lane != 0) continue;
+        if (parts == 1) {
+            decide(b, want, first, empty);
+        } else {
+            atomicMin(first_of + b, first);
+            atomicAdd(empty_of + b, empty);
+        }
+    }
+    __syncthreads();
+    if (parts > 1) {
+        if (threadIdx.x < a.batch) decide(threadIdx.x, want_of(threadIdx.x), first_of[threadIdx.x], empty_of[threadIdx.x]);
+        __syncthreads();
+    }
     grant(need, a.batch, a.refs, a.num_blocks, warp_sums, picked, [&](int) { set_status(a.status, LRKV_DEV_NO_PAGES); },
           [&](int b, int k, int granted, int page) {
               // (the granted entries are the last ones of what the sequence asked for)

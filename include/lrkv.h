@@ -536,9 +536,10 @@ typedef struct lrkv_pools {
 
 /*
  * lrkv_pages_reserve -- pages for seq_lens[b] + new_tokens[b] tokens of every sequence: the empty entries below
- *   ceil((seq_lens[b] + new_tokens[b]) / 64) of its row are filled.  A sequence for whose pages too few are
- *   left gets none (LRKV_DEV_NO_PAGES) and the next one is tried; one that asks for more than its row
- *   holds, or a negative length or count, gets none (LRKV_DEV_BAD_SEQLEN).
+ *   ceil((seq_lens[b] + new_tokens[b]) / 64) of its row are filled, those below its length included.  A
+ *   sequence for whose pages too few are left gets none (LRKV_DEV_NO_PAGES) and the next one is tried; one
+ *   that asks for more than its row holds, or a negative length or count, gets none (LRKV_DEV_BAD_SEQLEN),
+ *   as does one with a page behind an empty entry below that bound (LRKV_DEV_BAD_BLOCK).
  */
 lrkv_status lrkv_pages_reserve(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
                                const int32_t* seq_lens, const int32_t* new_tokens, int32_t batch,
