@@ -48,7 +48,23 @@ __device__ int block_scan(int v, int* warp_sums, int* total) {
     return r;
 }
 
-// need[0..n) (shared memory): pages asked for by request i -> exclusive prefix sums; returns their total.
+// Sum of need[0..n) (shared memory) to every thread, in 64 bits: 8,192 requests of up to 2^24 + 1 pages each.
+__device__ long long sum_of_needs(const int* need, int n) {
+    __shared__ long long sums[kPlanThreads / 32];
+    long long v = 0;
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) v += need[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = sums[threadIdx.x & 31];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// need[0..n) (shared memory), at most num_blocks together: pages of request i -> exclusive prefix sums; returns their
+// total.
 __device__ int prefix_of_needs(int* need, int n, int* warp_sums) {
     int base = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
@@ -116,17 +132,13 @@ constexpr int kPicked = 2048;
 template <class F, class G>
 __device__ void grant(int* need, int n, const int32_t* refs, int num_blocks, int* warp_sums, int* picked, F&& refused,
                       G&& give) {
-    int total = 0;
-    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
-        int t;
-        block_scan(i0 + (int)threadIdx.x < n ? need[i0 + threadIdx.x] : 0, warp_sums, &t);
-        total += t;
-    }
-    if (total == 0) return;
+    const long long asked = sum_of_needs(need, n);
+    if (asked == 0) return;
+    int total = (int)(asked < num_blocks ? asked : num_blocks);
     const int have = search_free(refs, num_blocks, total, warp_sums, [&](int page, int rank) {
         if (rank < kPicked) picked[rank] = page;
     });
-    if (have < total) {
+    if (have < asked) {
         __syncthreads();
         if (threadIdx.x == 0) {
             int left = have;
@@ -197,6 +209,8 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a)
         need[b] = 0;
         if (want < 0)
             set_status(a.status, LRKV_DEV_BAD_SEQLEN);
+        else if (empty > a.num_blocks)
+            need[b] = a.num_blocks + 1;
         else if (empty > 0 && first + empty != want)
             set_status(a.status, LRKV_DEV_BAD_BLOCK);
         else
@@ -219,6 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a)
                 first = min(first, k0 + e * 32 + lane);
                 ++empty;
             }
+            if (__reduce_add_sync(0xffffffffu, empty) > a.num_blocks) break;  // more than there are
         }
         first = __reduce_min_sync(0xffffffffu, first);
         empty = __reduce_add_sync(0xffffffffu, empty);

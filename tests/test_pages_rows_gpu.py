@@ -2,6 +2,7 @@
 empty entry."""
 import numpy as np
 import pytest
+import torch
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,16 @@ def test_reserve_leaves_rows_with_a_page_behind_an_empty_entry():
             if m.table[s, k] < 0:
                 m.table[s, k] = m.take()
     m.check()
+
+
+@pytest.mark.parametrize("rows", [128, 129, 256])
+def test_reserve_of_more_than_32_bits_of_pages(rows):
+    """Requests that sum to 2^31 pages and more (129 rows of 2^24 entries: 8.7 GB), and two that can be served."""
+    table = torch.full((rows + 1, 1 << 24), -1, dtype=torch.int32, device="cuda")
+    refs, lens, st = i32(np.zeros(70)), i32(np.zeros(rows + 1)), i32([0])
+    add = torch.full((rows + 1,), 1 << 30, dtype=torch.int32, device="cuda")
+    add[[3, rows]] = i32([64 * 40, 64 * 30])
+    b.lrkv_pages_reserve(refs, table, lens, add, status=st)
+    assert int(st) == NO_PAGES and (refs == 1).all()
+    assert torch.equal(table[3, :40], i32(range(40))) and torch.equal(table[rows, :30], i32(range(40, 70)))
+    assert int((table[:, :64] >= 0).sum()) == 70 and int((table[:, -1] >= 0).sum()) == 0
