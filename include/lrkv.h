@@ -520,6 +520,12 @@ lrkv_status lrkv_rope(const lrkv_rope_plan* plan, int32_t dtype, int32_t n, int3
  * of the block table; the entries behind them are -1.  Free pages are taken lowest first, by the
  * sequences in the order of the call, so the outcome does not depend on timing.  Counts may be raised
  * by the caller to keep pages (a shared prefix).  Calls on the same refs or tables must not overlap.
+ *
+ * Rows are written (lrkv_append, lrkv_cache_compact) only to pages that one sequence holds.  The pages that
+ * lrkv_pages_reserve takes and the last, partly filled page of a fork are of that kind.  A sequence that is
+ * cut (lrkv_pages_free with keep_lens, a smaller seq_lens) to a length inside a page that others hold too is
+ * not: that page's further rows are theirs.  No call tells, as a raised count may be the caller's own.  Such
+ * a sequence is forked before it goes on, and given back: the fork's last page is its own.
  * ====================================================================== */
 #define LRKV_MAX_POOLS 4
 #define LRKV_MAX_PAGE_BATCH 8192
@@ -540,6 +546,7 @@ typedef struct lrkv_pools {
  *   sequence for whose pages too few are left gets none (LRKV_DEV_NO_PAGES) and the next one is tried; one
  *   that asks for more than its row holds, or a negative length or count, gets none (LRKV_DEV_BAD_SEQLEN),
  *   as does one with a page behind an empty entry below that bound (LRKV_DEV_BAD_BLOCK).
+ *   Pages that the row already holds are taken as they are, shared ones too (see above).
  */
 lrkv_status lrkv_pages_reserve(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
                                const int32_t* seq_lens, const int32_t* new_tokens, int32_t batch,
@@ -565,6 +572,7 @@ lrkv_status lrkv_pages_fork(const lrkv_pools* pools, int32_t* refs, int32_t* blo
  *   min(seq_lens, keep_lens) (0).  A sequence listed twice gives its pages back once.  A page with count 0
  *   keeps it and sets LRKV_DEV_BAD_INDEX, as does a sequence out of range; a negative keep length sets
  *   LRKV_DEV_BAD_SEQLEN and leaves that sequence alone.
+ *   A keep length inside a page that other sequences hold leaves it shared: see above before rows are added.
  */
 lrkv_status lrkv_pages_free(int32_t num_blocks, int32_t* refs, int32_t* block_table, int32_t max_blocks_per_seq,
                             int32_t* seq_lens, int32_t batch, const int32_t* seqs, int32_t n,
@@ -587,6 +595,7 @@ lrkv_status lrkv_pages_copy(const lrkv_pools* src, const int32_t* src_pages, con
  *   A path that is out of order, out of range or longer than max_path sets LRKV_DEV_BAD_INDEX, rows beyond
  *   the table or a negative length LRKV_DEV_BAD_SEQLEN, a bad page id LRKV_DEV_BAD_BLOCK; that sequence's
  *   rows stay as they are and new_lens[b] = seq_lens[b].
+ *   The pages of the rows moved to must not be held by other sequences (see above).
  */
 lrkv_status lrkv_cache_compact(const lrkv_pools* pools, const int32_t* block_table, int32_t max_blocks_per_seq,
                                int32_t* seq_lens, int32_t batch, const int32_t* path, const int32_t* path_lens,

@@ -72,3 +72,47 @@ def test_reserve_of_more_than_32_bits_of_pages(rows):
     assert int(st) == NO_PAGES and (refs == 1).all()
     assert torch.equal(table[3, :40], i32(range(40))) and torch.equal(table[rows, :30], i32(range(40, 70)))
     assert int((table[:, :64] >= 0).sum()) == 70 and int((table[:, -1] >= 0).sum()) == 0
+
+
+@pytest.mark.parametrize("cut", [65, 70, 127, 128])
+def test_a_sequence_cut_inside_a_shared_page_goes_on_in_a_fork(cut):
+    """Forks of 128 tokens share two full pages; the one cut to `cut` tokens is forked and given back, and what is appended
+    and moved then reaches no row of the others."""
+    H, d_h, r, d = 2, 64, 8, 128
+    dims = b.make_dims(H, d_h, r, d)
+    g = torch.Generator(device="cuda").manual_seed(cut)
+    cache = b.PagedCache.empty(10, H, d_h, r)
+    for t in cache.tensors():
+        t.zero_()
+    pools, st = b.Pools.of(cache), i32([0])
+    W = (torch.randn(2 * (d_h + H * r), d, generator=g, device="cuda") * d ** -0.5).to(torch.bfloat16)
+    refs, table, lens = i32(np.zeros(10)), torch.full((3, 4), -1, dtype=torch.int32, device="cuda"), i32([0, 0, 0])
+
+    def append(s, first, n):
+        t = torch.arange(first, first + n, device="cuda")
+        x = torch.randn(n, d, generator=g, device="cuda").to(torch.bfloat16)
+        b.lrkv_append(dims, x, W, (table[s][t // 64] * 64 + t % 64).int(), cache, status=st)
+
+    def rows(s, n):
+        return [t[table[s, :-(-n // 64)].long()].flatten(0, 1)[:n].clone() for t in cache.tensors()]
+
+    b.lrkv_pages_reserve(refs, table, lens, i32([128, 0, 0]), status=st)
+    append(0, 0, 128)
+    lens[0] = 128
+    b.lrkv_pages_fork(pools, refs, table, lens, i32([0]), i32([1]), status=st)
+    assert torch.equal(table[0], table[1])
+    b.lrkv_pages_free(refs, table, lens, i32([1]), keep_lens=i32([0, cut, 0]), status=st)
+    parent = rows(0, 128)
+    b.lrkv_pages_fork(pools, refs, table, lens, i32([1]), i32([2]), status=st)
+    b.lrkv_pages_free(refs, table, lens, i32([1]), status=st)
+    b.lrkv_pages_reserve(refs, table, lens, i32([0, 0, 60]), status=st)
+    held = table[2, :-(-(cut + 60) // 64)].long()
+    assert lens.tolist() == [128, 0, cut] and (refs[held[cut // 64:]] == 1).all()
+    append(2, cut, 60)
+    kept = rows(2, cut + 60)
+    b.lrkv_cache_compact(pools, table, lens, i32([[0] * 20, [0] * 20, range(1, 60, 3)]), i32([0, 0, 20]), status=st)
+    assert lens.tolist() == [128, 0, cut + 20] and int(st) == 0
+    for x, y, z, k in zip(rows(0, 128), parent, rows(2, cut + 20), kept):
+        assert torch.equal(x, y) and torch.equal(z[:cut], x[:cut]) and torch.equal(z[cut:], k[cut + 1:cut + 60:3])
+    b.lrkv_pages_free(refs, table, lens, i32([0, 2]), status=st)
+    assert (refs == 0).all() and (table == -1).all() and int(st) == 0
