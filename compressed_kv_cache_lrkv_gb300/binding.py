@@ -587,6 +587,15 @@ class Pools:
 _I32 = torch.int32
 
 
+def _indices(t, n: int | None = None) -> int:
+    """Check of what is read (or written) as one 32-bit word per item, n of them where given; how many."""
+    shape = t.shape
+    if t.dtype is not _I32 or len(shape) != 1 or not t.is_contiguous() or (n is not None and shape[0] != n):
+        raise ValueError(f"{tuple(shape)} of {t.dtype}, strides {t.stride()}: expected contiguous int32 "
+                         f"[{'n' if n is None else n}]")
+    return shape[0]
+
+
 def _page_table(refs, block_table, seq_lens):
     """Checks of what the page calls write; the table's shape."""
     if (refs.dtype is not _I32 or block_table.dtype is not _I32 or seq_lens.dtype is not _I32 or
@@ -602,7 +611,7 @@ def _page_table(refs, block_table, seq_lens):
 def lrkv_pages_reserve(refs, block_table, seq_lens, new_tokens, status=None, stream=None):
     """Pages for new_tokens [B] more tokens of every sequence, from the pages with count 0 in refs [num_blocks]."""
     B, width = _page_table(refs, block_table, seq_lens)
-    _same_length(seq_lens, new_tokens)
+    _indices(new_tokens, B)
     rc = load().lrkv_pages_reserve(refs.shape[0], _ptr(refs), _ptr(block_table), width, _ptr(seq_lens),
                                    _ptr(new_tokens), B, _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_reserve")
@@ -613,9 +622,9 @@ def lrkv_pages_fork(pools: Pools, refs, block_table, seq_lens, parents, children
     B, width = _page_table(refs, block_table, seq_lens)
     if refs.shape[0] != pools.c.num_blocks:
         raise ValueError(f"{refs.shape[0]} counts for {pools.c.num_blocks} pages")
+    n = _indices(children, _indices(parents))
     rc = load().lrkv_pages_fork(ctypes.byref(pools.c), _ptr(refs), _ptr(block_table), width, _ptr(seq_lens),
-                                B, _ptr(parents), _ptr(children), _same_length(parents, children),
-                                _ptr(status), _stream(stream))
+                                B, _ptr(parents), _ptr(children), n, _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_fork")
 
 
@@ -623,16 +632,16 @@ def lrkv_pages_free(refs, block_table, seq_lens, seqs, keep_lens=None, status=No
     """Sequences seqs [n] give back their pages behind keep_lens [B] tokens (None: all)."""
     B, width = _page_table(refs, block_table, seq_lens)
     if keep_lens is not None:
-        _same_length(seq_lens, keep_lens)
+        _indices(keep_lens, B)
     rc = load().lrkv_pages_free(refs.shape[0], _ptr(refs), _ptr(block_table), width, _ptr(seq_lens), B,
-                                _ptr(seqs), seqs.shape[0], _ptr(keep_lens), _ptr(status), _stream(stream))
+                                _ptr(seqs), _indices(seqs), _ptr(keep_lens), _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_free")
 
 
 def lrkv_pages_copy(src: Pools, src_pages, dst: Pools, dst_pages, status=None, stream=None):
     """Pages src_pages [n] of src -> pages dst_pages [n] of dst, in all pools and layers."""
     rc = load().lrkv_pages_copy(ctypes.byref(src.c), _ptr(src_pages), ctypes.byref(dst.c), _ptr(dst_pages),
-                                _same_length(src_pages, dst_pages), _ptr(status), _stream(stream))
+                                _indices(dst_pages, _indices(src_pages)), _ptr(status), _stream(stream))
     _check(rc, "lrkv_pages_copy")
 
 
@@ -640,10 +649,14 @@ def lrkv_cache_compact(pools: Pools, block_table, seq_lens, path, path_lens, new
     """Rows seq_lens[b] + path[b, i] -> seq_lens[b] + i, i < path_lens[b]; new_lens = seq_lens + path_lens (None: in
     place)."""
     B, width = _page_table(path, block_table, seq_lens)
-    _same_length(seq_lens, path)
-    _same_length(seq_lens, path_lens)
+    rows, max_path = path.shape
+    if rows != B:
+        raise ValueError(f"paths of {rows} sequences, {B} lengths")
+    _indices(path_lens, B)
+    if new_lens is not None:
+        _indices(new_lens, B)
     rc = load().lrkv_cache_compact(ctypes.byref(pools.c), _ptr(block_table), width, _ptr(seq_lens), B,
-                                   _ptr(path), _ptr(path_lens), path.shape[1], _ptr(new_lens), _ptr(status),
+                                   _ptr(path), _ptr(path_lens), max_path, _ptr(new_lens), _ptr(status),
                                    _stream(stream))
     _check(rc, "lrkv_cache_compact")
 
