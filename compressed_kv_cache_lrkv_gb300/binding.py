@@ -518,6 +518,18 @@ def lrkv_decode_tree(dims: Dims, q, BK, BV, cache: PagedCache, block_table, seq_
     _check(rc, "lrkv_decode_tree")
 
 
+_I32 = torch.int32
+
+
+def _indices(t, n: int | None = None) -> int:
+    """Check of what is read (or written) as one 32-bit word per item, n of them where given; how many."""
+    shape = t.shape
+    if t.dtype is not _I32 or len(shape) != 1 or not t.is_contiguous() or (n is not None and shape[0] != n):
+        raise ValueError(f"{tuple(shape)} of {t.dtype}, strides {t.stride()}: expected contiguous int32 "
+                         f"[{'n' if n is None else n}]")
+    return shape[0]
+
+
 _ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "parts": 2}
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -538,7 +550,7 @@ def lrkv_rope(plan: RopePlan, x, y, positions, begin: int = 0, x_rows=None, y_ro
               status=None, stream=None):
     """y = x with values [begin, begin + plan.d_rot) of every head rotated at positions [n] (int32): x, y
     [rows, heads, width] of bf16 or fp32 (y is x: in place); x_rows, y_rows [n] int32 pick rows."""
-    n = positions.shape[0]
+    n = _indices(positions)
     xs, xt = x.shape, x.stride()
     ys, yt = (xs, xt) if y is x else (y.shape, y.stride())
     kind = _ROPE_TYPES.get(x.dtype)
@@ -546,8 +558,10 @@ def lrkv_rope(plan: RopePlan, x, y, positions, begin: int = 0, x_rows=None, y_ro
             xt[2] != 1 or yt[2] != 1):
         raise ValueError(f"x {tuple(xs)} of {x.dtype}, strides {xt}; y {tuple(ys)} of {y.dtype}, strides {yt}: expected "
                          "[rows, heads, width] of equal heads and widths, bfloat16 or float32, last stride 1")
-    if (x_rows is not None and x_rows.shape[0] != n) or (y_rows is not None and y_rows.shape[0] != n):
-        raise ValueError(f"row indices for other than {n} positions")
+    if x_rows is not None:
+        _indices(x_rows, n)
+    if y_rows is not None:
+        _indices(y_rows, n)
     xr = RowsStruct(x.data_ptr(), xs[0], xt[0], xt[1], _ptr(x_rows))
     yr = RowsStruct(y.data_ptr(), ys[0], yt[0], yt[1], _ptr(y_rows))
     rc = load().lrkv_rope(ctypes.byref(plan), kind, n, xs[1], xs[2], begin, ctypes.byref(xr), ctypes.byref(yr),
@@ -582,18 +596,6 @@ class Pools:
         if isinstance(cache, PagedCache):
             return cls(t.unsqueeze(0) for t in cache.tensors())
         return cls([(cache.rows if isinstance(cache, QuantCache) else cache).unsqueeze(0)])
-
-
-_I32 = torch.int32
-
-
-def _indices(t, n: int | None = None) -> int:
-    """Check of what is read (or written) as one 32-bit word per item, n of them where given; how many."""
-    shape = t.shape
-    if t.dtype is not _I32 or len(shape) != 1 or not t.is_contiguous() or (n is not None and shape[0] != n):
-        raise ValueError(f"{tuple(shape)} of {t.dtype}, strides {t.stride()}: expected contiguous int32 "
-                         f"[{'n' if n is None else n}]")
-    return shape[0]
 
 
 def _page_table(refs, block_table, seq_lens):

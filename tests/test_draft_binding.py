@@ -51,3 +51,18 @@ def test_empty_lists_are_taken():
     b.lrkv_pages_free(z(4), z(3, 2), z(3), z(0), stream=0)
     b.lrkv_pages_fork(P, z(4), z(3, 2), z(3), z(0), z(0), stream=0)
     b.lrkv_pages_copy(P, z(0), P, z(0), stream=0)
+
+
+@pytest.mark.parametrize("k", range(8))
+def test_rotation(k):
+    """Positions may be of any number, row indices of theirs."""
+    bad, plan, x = bad_arrays(3)[k], b.rope_plan(8), z(6, 2, 8, t=torch.bfloat16)
+    if k not in (4, 5):
+        refused(b.lrkv_rope, plan, x, x, bad)
+    refused(b.lrkv_rope, plan, x, x, z(3), x_rows=bad)
+    refused(b.lrkv_rope, plan, x, x, z(3), y_rows=bad)
+    refused(b.lrkv_rope, plan, x, x, z(3), x_rows=z(3), y_rows=bad)
+
+
+def test_no_rows_are_taken():
+    b.lrkv_rope(b.rope_plan(8), z(6, 2, 8, t=torch.float32), z(6, 2, 8, t=torch.float32), z(0), x_rows=z(0), stream=0)
