@@ -504,20 +504,6 @@ def decode_tree_workspace_bytes(dims: Dims, batch: int, T: int) -> int:
     return int(load().lrkv_decode_tree_workspace_bytes(ctypes.byref(dims), batch, T))
 
 
-def lrkv_decode_tree(dims: Dims, q, BK, BV, cache: PagedCache, block_table, seq_lens, tree_mask, tree_lens, out,
-                     workspace, status=None, stream=None):
-    """Drafted tokens over the cache: q [B, T, H, d_h + d_rope] -> out [B, T, H, d_h]; tree_mask [B, T] int64 bit sets
-    of the drafted tokens seen (None: a chain), tree_lens [B] int32 drafted tokens of each sequence (None: T)."""
-    c = cache.struct()
-    B, T = q.shape[0], q.shape[1]
-    if tree_mask is not None and (tree_mask.element_size() != 8 or tuple(tree_mask.shape) != (B, T)):
-        raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype}: expected 64-bit words [{B}, {T}]")
-    rc = load().lrkv_decode_tree(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(c), _ptr(block_table),
-                                 block_table.shape[1], _ptr(seq_lens), _ptr(tree_mask), _ptr(tree_lens), B, T,
-                                 _ptr(out), _ptr(workspace), workspace.nbytes, _ptr(status), _stream(stream))
-    _check(rc, "lrkv_decode_tree")
-
-
 _I32 = torch.int32
 
 
@@ -528,6 +514,31 @@ def _indices(t, n: int | None = None) -> int:
         raise ValueError(f"{tuple(shape)} of {t.dtype}, strides {t.stride()}: expected contiguous int32 "
                          f"[{'n' if n is None else n}]")
     return shape[0]
+
+
+_MASK_TYPES = (torch.int64, torch.uint64)
+
+
+def lrkv_decode_tree(dims: Dims, q, BK, BV, cache: PagedCache, block_table, seq_lens, tree_mask, tree_lens, out,
+                     workspace, status=None, stream=None):
+    """Drafted tokens over the cache: q [B, T, H, d_h + d_rope] -> out [B, T, H, d_h]; tree_mask [B, T] int64 bit sets
+    of the drafted tokens seen (None: a chain), tree_lens [B] int32 drafted tokens of each sequence (None: T)."""
+    c = cache.struct()
+    B, T = q.shape[0], q.shape[1]
+    if tree_mask is not None and (tree_mask.dtype not in _MASK_TYPES or tree_mask.shape != (B, T) or
+                                  not tree_mask.is_contiguous()):
+        raise ValueError(f"tree_mask {tuple(tree_mask.shape)} of {tree_mask.dtype}, strides {tree_mask.stride()}: "
+                         f"expected contiguous 64-bit words [{B}, {T}]")
+    if tree_lens is not None:
+        _indices(tree_lens, B)
+    _indices(seq_lens, B)
+    if block_table.dtype is not _I32 or block_table.shape[0] != B or not block_table.is_contiguous():
+        raise ValueError(f"block table {tuple(block_table.shape)} of {block_table.dtype}, strides "
+                         f"{block_table.stride()}: expected contiguous int32 [{B}, ...]")
+    rc = load().lrkv_decode_tree(ctypes.byref(dims), _ptr(q), _ptr(BK), _ptr(BV), ctypes.byref(c), _ptr(block_table),
+                                 block_table.shape[1], _ptr(seq_lens), _ptr(tree_mask), _ptr(tree_lens), B, T,
+                                 _ptr(out), _ptr(workspace), workspace.nbytes, _ptr(status), _stream(stream))
+    _check(rc, "lrkv_decode_tree")
 
 
 _ROPE_LAYOUTS = {"interleaved": 0, "half": 1}

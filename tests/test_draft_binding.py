@@ -66,3 +66,31 @@ def test_rotation(k):
 
 def test_no_rows_are_taken():
     b.lrkv_rope(b.rope_plan(8), z(6, 2, 8, t=torch.float32), z(6, 2, 8, t=torch.float32), z(0), x_rows=z(0), stream=0)
+
+
+def tree(**kw):
+    bf = torch.bfloat16
+    cache = b.PagedCache(*(z(4, 64, 8, t=bf) for _ in range(4)))
+    a = dict(table=TABLE, lens=LENS, mask=z(3, 5, t=I64), counts=z(3))
+    a.update(kw)
+    q, x = z(3, 5, 8, 64, t=bf), z(8, 64, 16, t=bf)
+    return (b.make_dims(8, 64, 16, 512), q, x, x, cache, a["table"], a["lens"], a["mask"], a["counts"], q, z(256))
+
+
+@pytest.mark.parametrize("bad", [z(3, 5, t=torch.float64), z(3, 5), z(3, 10), z(5, 3, t=I64).t(), z(3, 6, t=I64)[:, :5],
+                                 z(15, t=I64), z(3, 4, t=I64), z(2, 5, t=I64)])
+def test_tree_masks(bad):
+    with pytest.raises(ValueError, match="64-bit"):
+        b.lrkv_decode_tree(*tree(mask=bad), stream=0)
+
+
+@pytest.mark.parametrize("k", range(8))
+def test_tree_lengths(k):
+    bad = bad_arrays(3)[k]
+    refused(b.lrkv_decode_tree, *tree(counts=bad))
+    refused(b.lrkv_decode_tree, *tree(lens=bad))
+
+
+@pytest.mark.parametrize("bad", [z(3, 2, t=I64), z(2, 3).t(), z(3, 4)[:, :2], z(2, 2), z(4, 2), z(3, 2, t=torch.float32)])
+def test_tree_tables(bad):
+    refused(b.lrkv_decode_tree, *tree(table=bad))
