@@ -806,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D_H, int R, int DC>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int W4 = (D_H + R) / 4, C4 = (DC + R) / 4, QPW = (C4 + 7) / 8, DPL = DC / 32, kPieces = DC == 32 ? 4 : 1;
+    static_assert(DPL == 1 || DPL == 2, "output columns of a lane");
     const DecodeArgs& d = a.d;
     const int lane = threadIdx.x, warp = threadIdx.y, b = blockIdx.z, t = blockIdx.y;
     // rows: head x drafted token of the tile, tn tokens a head
@@ -923,10 +924,8 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
             }
         }
         uint16_t* out = d.out + (((size_t)b * a.T + i) * d.H + h) * D_H + d0 + lane * DPL;
-        if (DPL == 4) {
-            *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[DPL - 2], y[DPL - 1]));
-        } else if (DPL == 2) {
-            *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(y[0], y[DPL - 1]);
+        if constexpr (DPL == 2) {
+            *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(y[0], y[1]);
         } else {
             const __nv_bfloat16 o = __float2bfloat16_rn(y[0]);
             *out = *reinterpret_cast<const uint16_t*>(&o);
