@@ -15,7 +15,8 @@ def z(*s, t=I32):
 
 def bad_arrays(n):
     """What a call must not take for n 32-bit words."""
-    return [z(n, t=I64), z(n, t=torch.float32), z(n, t=torch.int16), z(2 * n)[::2], z(n + 1), z(n - 1), z(n, 1), z(1, n)]
+    return [z(n, t=I64), z(n, t=torch.float32), z(n, t=torch.int16), z(2 * n)[::2], z(n + 1), z(n - 1), z(n, 2),
+            z(n, n).t()[0]]
 
 
 def refused(call, *args, **kw):
