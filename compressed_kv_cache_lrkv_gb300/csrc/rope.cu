@@ -173,12 +173,14 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 template <typename T, bool HALF>
 cudaError_t launch_t(const RopeArgs& a, int sms, cudaStream_t stream) {
     const int units = a.in_place ? a.plan.d_rot / 8 : a.width / 8;
-    // one unit a thread while all fit on the GPU at once (latency counts); else four rows of few heads, or four (fp32)
-    // or eight heads of a row
-    const long long all = (long long)a.n * a.heads * units;
+    // One unit a thread up to 512 of them for an SM (latency counts), else four rows of one or two heads, or four
+    // (fp32) or eight heads of a row.  In a graph, us, one unit | several: 1 head of 64, 500 an SM 2.4 | 3.1, 700
+    // 3.6 | 3.2, 9,600 24 | 20; 8 heads of 128, 64 turned, 500 2.4 | 2.6, 700 3.6 | 2.8; 32 heads of 192, 300 2.2 | 2.5,
+    // 500 3.3 | 2.6, 9,600 23 | 10.5; fp32, 8 heads of 128, 500 3.1 | 3.2, 700 4.2 | 3.5.  2,400 an SM by rows | by heads:
+    // 2 heads of 64 7.1 | 8.0, 3 of 128 9.4 | 7.4; fp32, 2 of 128 8.9 | 9.1, 3 of 64 9.0 | 7.5.
+    const bool few = (long long)a.n * a.heads * units <= (long long)sms * 512;
     constexpr int HB = sizeof(T) == 2 ? 8 : 4;
-    const int rb = all <= (long long)sms * 1024 || a.heads >= 4 ? 1 : 4;
-    const int hb = all <= (long long)sms * 1024 || a.heads < 4 ? 1 : HB;
+    const int rb = few || a.heads >= 3 ? 1 : 4, hb = few || a.heads < 3 ? 1 : HB;
     int ny = 1;
     while (ny * hb < a.heads && units * ny * 2 <= 256) ny *= 2;
     int nz = 1;
