@@ -1042,7 +1042,10 @@ cudaError_t launch_tree(const TreeMaps& maps, const TreeArgs& a, int D_H, int R,
 #undef LRKV_TS
     if (e != cudaSuccess) return e;
     const int groups = a.rs / 32;
-    const bool few = (long long)a.tmax * a.batch * groups <= 4 * a.gang * a.gangs;  // blocks for fewer than four an SM
+    // Up to one group of 32 rows for an SM: blocks of 32 output columns with four pieces in flight, else of 64 with one.  (In
+    // a graph, us, 32 | 64 columns: 0.03 groups an SM 17.9 | 28.5, 0.2 95.7 | 101, 0.4 18.8 | 21.6; 1.2 58.0 | 53.2, 2.1
+    // 31.6 | 26.8, 3.4 42.5 | 30.6, 5 109 | 92.)
+    const bool few = (long long)a.tmax * a.batch * groups <= a.gang * a.gangs;
 #define LRKV_TC(DH, RR)                                                                                             \
     if (D_H == DH && R == RR)                                                                                       \
         return few ? launch_dependent(tree_combine_kernel<DH, RR, 32>, dim3(groups * (DH / 32), a.tmax, a.batch),        \
