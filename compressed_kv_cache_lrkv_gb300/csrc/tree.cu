@@ -29,8 +29,9 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.  (24 sequences of 1 to
-// 8,191 tokens: 91 us with 8 or 11, 95 with 4; 1 x 4 tokens behind 256: 17 us with 4, 15.8 with 8, 14.7 with 11.)
+// What a piece's start and end cost, in pages: the work is cut as if every tile had that many more.  (In a graph, us, with
+// 4 | 8 | 11 | 16: 24 sequences of 1 to 8,191 tokens 96.5 | 92.5 | 92.4 | 94.7, 16 x 16 tokens behind 2,048 19.7 | 19.4 |
+// 18.8 | 19.4; 128 heads, the long context and short sequences within 2%.)
 constexpr int kStartPages = 11;
 
 __device__ __forceinline__ void named_arrive(int id, int threads) {
