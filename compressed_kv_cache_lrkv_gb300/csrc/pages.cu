@@ -50,17 +50,14 @@ __device__ int block_scan(int v, int* warp_sums, int* total) {
 
 // Sum of need[0..n) (shared memory) to every thread, in 64 bits: 8,192 requests of up to 2^24 + 1 pages each.
 __device__ long long sum_of_needs(const int* need, int n) {
-    __shared__ long long sums[kPlanThreads / 32];
-    long long v = 0;
+    __shared__ uint2 sums[kPlanThreads / 32];
+    unsigned v = 0;  // (at most eight requests of a thread)
     for (int i = threadIdx.x; i < n; i += kPlanThreads) v += need[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+    uint2 x = make_uint2(__reduce_add_sync(0xffffffffu, v & 0xffff), __reduce_add_sync(0xffffffffu, v >> 16));
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
     __syncthreads();
-    v = sums[threadIdx.x & 31];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    x = sums[threadIdx.x & 31];
+    return (long long)__reduce_add_sync(0xffffffffu, x.y) * 65536 + __reduce_add_sync(0xffffffffu, x.x);
 }
 
 // need[0..n) (shared memory), at most num_blocks together: pages of request i -> exclusive prefix sums; returns their
@@ -192,14 +189,16 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a)
     __shared__ int first_of[16], empty_of[16];
     begin_dependent();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // `parts` warps a sequence (of at most 16 where there are several), kEntries x 32 entries at a time
-    constexpr int kWarps = kPlanThreads / 32, kEntries = 8;
-    const int parts = a.batch < kWarps ? kWarps / a.batch : 1, part = warp % parts;
-    if (threadIdx.x < 16) {
-        first_of[threadIdx.x] = INT_MAX;
-        empty_of[threadIdx.x] = 0;
+    // `parts` warps a sequence, kEntries x 32 entries at a time: several where there are few long rows (at most 16)
+    constexpr int kWarps = kPlanThreads / 32, kEntries = 4;
+    const int parts = a.batch < kWarps && a.max_pages > 32 * kEntries ? kWarps / a.batch : 1, part = warp % parts;
+    if (parts > 1) {
+        if (threadIdx.x < 16) {
+            first_of[threadIdx.x] = INT_MAX;
+            empty_of[threadIdx.x] = 0;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     auto want_of = [&](int b) {
         const int L = a.lens[b], add = a.b[b];
         const int want = L >= 0 && add >= 0 ? pages_of((long long)L + add) : -1;
@@ -233,7 +232,8 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageArgs a)
                 first = min(first, k0 + e * 32 + lane);
                 ++empty;
             }
-            if (__reduce_add_sync(0xffffffffu, empty) > a.num_blocks) break;  // more than there are
+            // (looked for only where there is more to come)
+            if (k0 + parts * 32 * kEntries < want && __reduce_add_sync(0xffffffffu, empty) > a.num_blocks) break;
         }
         first = __reduce_min_sync(0xffffffffu, first);
         empty = __reduce_add_sync(0xffffffffu, empty);
