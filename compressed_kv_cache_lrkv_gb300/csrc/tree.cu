@@ -15,10 +15,11 @@
 //
 // Measured (a call in a stream of others): 8 heads of 64, r = 16, 1 x 4 drafted behind 256 tokens 14 us; 16 x 16 behind
 // 2,048 20 us; 32 heads of 128, r = 16, positional key, 24 x up to 26 behind 1 to 8,191 92 us; 32 heads, r = 32, 4 x 8
-// behind 16 to 32 K 100 us (475 MB read, 70 us at the copy rate); 128 heads, r = 16, 8 x up to 64 behind 8,192 326 to 334 us.
-// In the last no single part bounds the scan: a variant that issues the two products from two warps took 305 us, 269 of
-// them without the softmax and 290 with most products left out.  That variant is within 1% of this one (306 then) and
-// was not kept; more warps of rows (two threads a row, or a third group) were slower.
+// behind 16 to 32 K 100 us (475 MB read, 70 us at the copy rate); 128 heads, r = 16, 8 x up to 64 behind 8,192 332 us, 316
+// in bursts of a few ms (long context 95.6): a load of seconds runs at the power limit, with the SMs at 1.91 to 1.96 GHz.
+// No single part bounds the scan.  In bursts, 128 heads and long context: as it is 317 and 95.7; without the softmax 309
+// and 94.6; with a fraction of the score products and no maximum 284 and 90.6, of the value products 298 and 87.6, of
+// both 282 and 85.8.  More warps of rows (two threads a row, or a third group) were slower.
 #include "lrkv_internal.cuh"
 #include "tile_attn.cuh"
 #include "tree.h"
