@@ -283,13 +283,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t* k_empty = bars + 5;    // [3] P.V done with the page
     uint64_t* s_full = bars + 8;     // [3] partial S of tile g in TMEM buffer g % 3
     uint64_t* s_free = bars + 11;    // [3] P.V done with the P held in that S buffer
-    uint64_t* p_full = bars + 14;    // softmax wrote P (128 arrivals)
     uint64_t* o_done = bars + 15;    // [3] P.V of tile g (barrier g % 3) complete
     uint64_t* recv_full = bars + 18; // the peer's partial S is in this CTA's receive buffer (1 local arrival + 32 KiB)
     uint64_t* peer_free = bars + 19; // the peer has read what this CTA wrote into its buffer (4 remote arrivals)
     uint64_t* mma_drain = bars + 20;
     uint64_t* pv_drain = bars + 21;
     uint64_t* s_read = bars + 22;    // [3] the senders have read the partial S in that buffer (128 arrivals)
+    // [3] softmax wrote P into that buffer (128 arrivals).  One each: S_{g+3} is formed after P_g V_g, so a phase is seen
+    // before the next one ends, while two tiles' phases of one barrier may pass a P.V warp that waits for its code.
+    uint64_t* p_full = bars + 27;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
     volatile int* abort_flag = reinterpret_cast<int*>(bars + 26);
     auto B = [&](uint64_t* p) { return smem_u32(p); };
@@ -310,8 +312,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_init(B(s_free + i), 1);
             mbar_init(B(o_done + i), 1);
             mbar_init(B(s_read + i), 128);
+            mbar_init(B(p_full + i), 128);
         }
-        mbar_init(B(p_full), 128);
         mbar_init(B(recv_full), 1);
         mbar_init(B(peer_free), 4);
         mbar_init(B(mma_drain), 1);
@@ -427,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         auto pv = [&](int g, bool first, auto U) -> bool {
             constexpr int st = decltype(U)::value;  // ring stage = S buffer
             // P_g is in TMEM, and the senders are done with S_g (the buffer is freed after this P.V)
-            if (aborted() || !wait_all(B(p_full), g & 1, a.status) ||
+            if (aborted() || !wait_all(B(p_full + st), (g / kStages) & 1, a.status) ||
                 !wait_all(B(s_read + st), (g / kStages) & 1, a.status))
                 return false;
             tc_fence_after();
@@ -621,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 if (nvalid < kTok) fence_proxy_async_smem();  // cleared value rows before the tensor core reads them
                 tc_fence_before();
-                mbar_arrive(B(p_full));
+                mbar_arrive(B(p_full + st));
             }
             if (!ok) break;
             // ---- split epilogue: (m, l) and this CTA's 256 columns of the unnormalised O
