@@ -587,6 +587,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float muse = raise ? mnew : mref;
                 const float alpha = raise ? ((mref == -INFINITY) ? 0.f : ex2_approx(mref - mnew)) : 1.f;
                 const float nm = muse == -INFINITY ? -INFINITY : -muse;
+                // P is written over S_g: not before the senders have read it (they may still wait for the peer to
+                // take tile g-1 while the peer's part of tile g is already here)
+                if (!wait_all(B(s_read + st), (g / kStages) & 1, a.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
                 float r8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
