@@ -145,7 +145,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     uint64_t* qt_mma = bars + 1;
     uint64_t* qt_ready = bars + 2;
     uint64_t* s_full = bars + 3;    // [2]
-    uint64_t* p_full = bars + 5;
+    // p_full[j % 2]: P_j written.  One for each S buffer: S_{j+2} is formed after P_j . V_j, so the warp that waits for P_j
+    // sees its phase before the next one ends; tile after tile of one barrier could pass a warp that waits for its code.
+    uint64_t* p_full = bars + 5;    // [2]
     // o_done[j % 2]: P_j . V_j complete.  Softmax waits on it only before rescaling O (rare),
     // so it may skip phases; two barriers by tile parity keep that safe: o_done[j % 2] cannot
     // complete its next phase (P_{j+2} . V_{j+2}) before softmax has passed tile j + 2.
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             mbar_init(B(v_empty + i), 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(B(s_full + i), 1);
-        mbar_init(B(p_full), 128);
+        for (int i = 0; i < 2; ++i) mbar_init(B(p_full + i), 128);
         for (int i = 0; i < 2; ++i) mbar_init(B(o_done + i), 1);
         mbar_init(B(fin_done), 1);
         mbar_init(B(bvf_ready), 128);
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             const uint64_t dSV = mndesc128(S0 + OFF_V), dZV = mndesc32(S0 + OFF_V + V_Z);
             auto pv_tile = [&](int j, auto PAR) -> bool {
                 constexpr int vs = decltype(PAR)::value;  // value stage = S buffer = j % 2
-                if (aborted() || !wait_all(B(p_full), j & 1, a.status) ||
+                if (aborted() || !wait_all(B(p_full + vs), (j >> 1) & 1, a.status) ||
                     !wait_all(B(v_full + vs), (j >> 1) & 1, a.status))
                     return false;
                 tc_fence_after();
@@ -555,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             tmem_wait_st();
             fence_proxy_async_smem();  // zeroed value rows (if any) before the tensor core reads them
             tc_fence_before();
-            mbar_arrive(B(p_full));
+            mbar_arrive(B(p_full + (j & 1)));
         }
         if (ROPE) {
             // Every S MMA has completed (S_{nt-1} was read above), so key stage 0 is free:
